@@ -43,7 +43,12 @@
 extern "C" {
 #endif
 
-typedef enum { SPECDEC_F32 = 0, SPECDEC_BF16 = 1 } specdec_dtype;
+typedef enum {
+  SPECDEC_F32 = 0,
+  SPECDEC_BF16 = 1,
+  SPECDEC_F16 = 2, /* the cache calls: queries, keys, values and 16-bit pages */
+  SPECDEC_KV4 = 3  /* the cache calls: pages held in 4 bits                    */
+} specdec_dtype;
 
 /* return codes */
 #define SPECDEC_OK 0
@@ -62,6 +67,8 @@ typedef enum { SPECDEC_F32 = 0, SPECDEC_BF16 = 1 } specdec_dtype;
 #define SPECDEC_STATUS_BAD_TREE 32          /* parent not in [-1, i), or tree deeper than D   */
 #define SPECDEC_STATUS_BAD_TEMPERATURE 64   /* temperature NaN or infinite                    */
 #define SPECDEC_STATUS_TIMEOUT 128          /* a bounded wait inside a kernel gave up: not finished */
+#define SPECDEC_STATUS_BAD_CACHE 32         /* cache calls: a length or page out of range (the bit
+                                               with which a path that leaves the cache is reported) */
 #define SPECDEC_STATUS_ERROR_MASK 0xFF
 #define SPECDEC_STATUS_ZERO_Q 256           /* warning: q_i(x_i) == 0; accepted iff p_i(x_i) > 0 */
 #define SPECDEC_STATUS_ZERO_RESIDUAL 512    /* warning: residual mass 0 after rounding; drew from p */
@@ -361,6 +368,123 @@ int specdec_compact_kv(void* cache, int64_t row_bytes, int64_t slot_stride, int6
                        int32_t* out_status, void* stream);
 
 /* ------------------------------------------------------------------------------------
+ * The paged cache of the target's attention (SD 20.5, "Keeping the caches consistent after a
+ * rejection"): the calls that write it and attend over it, before the logits are verified.
+ *
+ * A sequence's tokens sit at logical slots 0, 1, ...; slot s of sequence b is entry
+ * s % page_size of page block_table[b * max_pages + s / page_size].  A slot holds kv_heads
+ * rows of head_dim values for keys and as many for values, at
+ *   k + page * page_stride + (s % page_size) * slot_stride + head * head_stride   (bytes),
+ * the same strides for v.  specdec_compact_kv moves slots of the same pages.
+ *   SPECDEC_BF16, SPECDEC_F16: a row is head_dim 16-bit values.
+ *   SPECDEC_KV4: a row is head_dim / 2 bytes of E2M1 codes, the even value in the low nibble;
+ *     k_scales / v_scales hold head_dim / 16 E4M3 bytes per row at their own strides, one for
+ *     each 16 values.  A value is code * scale * k_scale (v_scale for values).  k_scale and
+ *     v_scale are positive and finite; they are not read for 16-bit pages.
+ * Pointers and strides are multiples of 16 bytes (scales: of head_dim / 16 bytes); head_dim is
+ * 64 or 128; max_pages * page_size < 2^31 - 256.
+ *
+ * Lengths, for each call below: context_len[b] counts sequence b's tokens including the new
+ * ones of this call, query_len[b] <= n the new ones (NULL: n for every sequence); new token i
+ * is slot context_len[b] - query_len[b] + i.  Outputs for i >= query_len[b] are zeros.
+ * out_status[b] (optional) is SPECDEC_STATUS_BAD_CACHE for a length that does not fit (negative,
+ * query_len above n or above context_len, slots past max_pages) or a page outside
+ * [0, num_pages) among those the call uses for the sequence, else 0.
+ */
+typedef struct specdec_kv_pages {
+  void* k;
+  void* v;
+  void* k_scales; /* SPECDEC_KV4 only */
+  void* v_scales;
+  const int32_t* block_table; /* [B, max_pages], device */
+  int64_t page_stride, slot_stride, head_stride;
+  int64_t scale_page_stride, scale_slot_stride, scale_head_stride; /* SPECDEC_KV4 only */
+  int32_t num_pages, page_size, max_pages, kv_heads, head_dim;
+  int32_t format; /* SPECDEC_BF16, SPECDEC_F16 or SPECDEC_KV4 */
+  float k_scale, v_scale;
+} specdec_kv_pages;
+
+/* Norms of queries and keys for each head, the position rotation, and the write of keys and
+ * values to 16-bit pages, in one pass.
+ *
+ * For each head vector x of D = head_dim values:
+ *   y = x * weight / sqrt(mean(x^2) + eps)      (weight NULL: y = x)
+ *   (y_a, y_b) <- (y_a cos t - y_b sin t, y_b cos t + y_a sin t),  t = position * f_j,
+ * for the pairs (a, b) = (j, j + rot/2), or (2j, 2j + 1) with interleaved != 0, j < rot/2; values
+ * from rot on are not rotated.  The position is context_len[b] - query_len[b] + i, or + depth[i]
+ * for tree nodes (depth [n] int32, specdec_build_tree_mask's out_depth; NULL: i).
+ * turns [rot/2] uint64: f_j in 2^-64 turns for a position (f_j / (2 pi) * 2^64 for f_j in
+ * radians), so that position * f_j is exact modulo a turn at every position.
+ * Statistics, angles and products are fp32; every value is rounded once, at the end.
+ *
+ * q, k, v         [B, n, heads, D] of dtype (SPECDEC_BF16 or SPECDEC_F16); strides in elements
+ *                 of sequence, token and head in q_strides[3], k_strides[3], v_strides[3] (host
+ *                 arrays), the last dimension contiguous: views of a fused projection's output
+ * q_weight, k_weight [D] of dtype, or NULL
+ * out_q           [B, n, q_heads, D] contiguous
+ * out_k           [B, n, kv_heads, D] contiguous when pages is NULL (v is not used then); else
+ *                 NULL, and keys and values go to the pages, whose format is dtype
+ * A sequence in error leaves its pages alone; its out_q (and out_k) rows are NaN.
+ * 16 <= rot <= D, a multiple of 16; D is 64 or 128; B <= 65535; pointers and strides multiples of
+ * 16 bytes.  Two sequences must not write the same slot. */
+int specdec_rotate_qk(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                      const void* v, const int64_t* v_strides, specdec_dtype dtype, const void* q_weight,
+                      const void* k_weight, float eps, const uint64_t* turns, int rot, int interleaved,
+                      const int32_t* context_len, const int32_t* query_len, const int32_t* depth, int B, int n,
+                      int q_heads, int kv_heads, int head_dim, void* out_q, void* out_k,
+                      const specdec_kv_pages* pages, int32_t* out_status, void* stream);
+
+/* Keys and values [B, n, kv_heads, D] (strides as above) written to 4-bit pages.
+ * For each 16 values x, with y = x * (1 / k_scale) in fp32: scale = E4M3(max|y| / 6) (nearest
+ * even, saturated at 448), code = the E2M1 number nearest to y / scale (ties to the even
+ * code); a zero scale gives zeros.  A group with a value that is not finite stores the scale
+ * NaN and reads back as NaN.  A sequence in error is left alone.  B <= 65535. */
+int specdec_append_kv4(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                       specdec_dtype dtype, const int32_t* context_len, const int32_t* query_len, int B, int n,
+                       const specdec_kv_pages* pages, int32_t* out_status, void* stream);
+
+/* The values that 4-bit pages hold for the last query_len[b] tokens of each sequence:
+ * out_k, out_v [B, n, kv_heads, D] of dtype, contiguous, each rounded once.  A sequence in
+ * error gives NaN.  B <= 65535. */
+int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B, int n,
+                     const specdec_kv_pages* pages, specdec_dtype dtype, void* out_k, void* out_v,
+                     int32_t* out_status, void* stream);
+
+/* Attention of the new tokens over the cache, which holds their keys and values already
+ * (specdec_rotate_qk, specdec_append_kv4).
+ *
+ * With P = context_len[b] - query_len[b], query i sees slot s when
+ *   chain (tree_mask NULL):  s <= P + i
+ *   tree: s < P, or tree_mask[i * n + (s - P)] != 0 and s < context_len[b]
+ * and, with window > 0, pos(i) - pos(s) < window or pos(s) < sinks: the last `window` positions,
+ * itself among them, and the first `sinks`.  pos(s) = s before P, P + i for new token i, or
+ * P + depth[i] in a tree (depth in [0, n)).  tree_mask [n, n] uint8 and depth [n] int32 are
+ * shared by the batch: specdec_build_tree_mask's out_mask and out_depth for prefix_len 0.
+ *   out[b, i, h] = sum_s p_s v_s,  p = softmax over the visible s of scale * q . k_s,
+ * query head h with key head h / (q_heads / kv_heads).  Values and keys of slots that a query
+ * does not see do not touch its output, whatever they hold (NaN, infinities, stale pages).
+ *
+ * q            [B, n, q_heads, D] of dtype (SPECDEC_BF16 or SPECDEC_F16), q_strides as above
+ * pages        16-bit pages of the same dtype, or SPECDEC_KV4
+ * out          [B, n, q_heads, D] contiguous
+ * out_lse      [B, n, q_heads] fp32, optional: log of the sum of exp(scale * q . k_s)
+ * A query that sees nothing gives zeros and lse -inf; one that sees a slot on a page outside
+ * [0, num_pages) gives NaN, as does every query of a sequence whose lengths do not fit.  Pages
+ * that no query sees (behind a window) are not read, and their entries are not looked at.
+ * Scores, statistics and sums are fp32; the weights p are rounded to 16 bits (dtype, or fp16 for
+ * 4-bit pages) for the matrix products, the output once at the end.
+ * The workspace (specdec_attend_workspace_bytes) follows the rules at the top.  The split of the
+ * work follows the lengths on the device: the host reads none of them.
+ * window, sinks >= 0 (window 0: no window, sinks then has no effect); q_heads a multiple of
+ * kv_heads; n * (q_heads / kv_heads) < 2^24; B < 2^24. */
+size_t specdec_attend_workspace_bytes(int B, int n, int q_heads, int kv_heads, int head_dim);
+
+int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype, const specdec_kv_pages* pages,
+                   const int32_t* context_len, const int32_t* query_len, const uint8_t* tree_mask,
+                   const int32_t* depth, int B, int n, int q_heads, int window, int sinks, float scale, void* out,
+                   float* out_lse, int32_t* out_status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
  * Tree-attention mask and position ids (SD 20.5, box "Token tree and tree attention").
  *   out_mask          [N, P+N] uint8: row i is 1 on every prefix column j < P, on column
  *                     P+i and on column P+a for every ancestor a of node i; 0 elsewhere
@@ -397,7 +521,11 @@ int specdec_build_tree_mask(const int32_t* parents, int N, int prefix_len, uint8
 #define SPECDEC_KERNEL_GUMBEL 11       /* Gumbel-coupled verification                */
 #define SPECDEC_KERNEL_GUMBEL_DRAFT 12 /* the drafter's shared-noise sampler          */
 #define SPECDEC_KERNEL_KV_COMPACT 13   /* accepted-branch KV compaction              */
-#define SPECDEC_NUM_KERNELS 14
+#define SPECDEC_KERNEL_ROTATE_QK 14        /* norms, rotation and the page write          */
+#define SPECDEC_KERNEL_APPEND_KV4 15       /* the 4-bit page write                       */
+#define SPECDEC_KERNEL_READ_KV4 16         /* 4-bit pages read back                      */
+#define SPECDEC_KERNEL_ATTEND 17           /* attention over pages, its join included    */
+#define SPECDEC_NUM_KERNELS 18
 
 int specdec_profile_start(int max_launches);
 int specdec_profile_read(double* total_ms, int* launches, int n);

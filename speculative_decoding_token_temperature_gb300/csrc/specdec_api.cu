@@ -7,10 +7,12 @@
 #include <cstdio>
 #include <cstdlib>
 #include <cstring>
+#include <initializer_list>
 #include <vector>
 
 #include <cuda_runtime.h>
 
+#include "cache_ops.h"
 #include "specdec.h"
 #include "specdec_internal.h"
 
@@ -679,6 +681,227 @@ int specdec_compact_kv(void* cache, int64_t row_bytes, int64_t slot_stride, int6
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ProfScope prof(SPECDEC_KERNEL_KV_COMPACT, s);
   if (cudaError_t e = launch_kv_compact(P, s); e != cudaSuccess) return fail_cuda("KV compaction kernel", e);
+  return SPECDEC_OK;
+}
+
+namespace {
+
+bool valid_half(int t) { return t == SPECDEC_BF16 || t == SPECDEC_F16; }
+
+bool multiples(int64_t unit, std::initializer_list<int64_t> v) {
+  for (int64_t x : v)
+    if (x < 0 || x % unit != 0) return false;
+  return true;
+}
+bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+// Strides of a [B, n, heads, D] view, in elements: 16-byte rows.
+int check_view(const void* p, const int64_t* st, const char* what) {
+  if (!p || !st) return fail(SPECDEC_ERR_INVALID_ARG, what);
+  if (!aligned16(p) || !multiples(8, {st[0], st[1], st[2]}))
+    return fail(SPECDEC_ERR_UNSUPPORTED, "rows of queries, keys and values must start on 16 bytes (strides not negative)");
+  return SPECDEC_OK;
+}
+
+int check_pages(const specdec_kv_pages* pg, bool four, specdec_dtype dt, Pages* out) {
+  if (!pg) return fail(SPECDEC_ERR_INVALID_ARG, "pages is null");
+  if (pg->format != (four ? SPECDEC_KV4 : dt)) return fail(SPECDEC_ERR_INVALID_ARG, "the pages' format does not fit the call");
+  if (!pg->k || !pg->v || !pg->block_table || (four && (!pg->k_scales || !pg->v_scales)))
+    return fail(SPECDEC_ERR_INVALID_ARG, "a required pointer of the pages is null");
+  if (pg->num_pages <= 0 || pg->page_size <= 0 || pg->max_pages <= 0 || pg->kv_heads <= 0)
+    return fail(SPECDEC_ERR_INVALID_ARG, "num_pages, page_size, max_pages and kv_heads must be positive");
+  if (pg->head_dim != 64 && pg->head_dim != 128) return fail(SPECDEC_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (static_cast<int64_t>(pg->max_pages) * pg->page_size >= INT32_MAX - 256)
+    return fail(SPECDEC_ERR_UNSUPPORTED, "max_pages * page_size must be below 2^31 - 256");
+  if (!aligned16(pg->k) || !aligned16(pg->v) || !multiples(16, {pg->page_stride, pg->slot_stride, pg->head_stride}))
+    return fail(SPECDEC_ERR_UNSUPPORTED, "pages and their strides must be multiples of 16 bytes (not negative)");
+  if (four) {
+    const int64_t u = pg->head_dim / kGroup4;
+    if (!aligned_to(pg->k_scales, u) || !aligned_to(pg->v_scales, u) ||
+        !multiples(u, {pg->scale_page_stride, pg->scale_slot_stride, pg->scale_head_stride}))
+      return fail(SPECDEC_ERR_UNSUPPORTED, "scales and their strides must be multiples of head_dim / 16 bytes (not negative)");
+    if (!(pg->k_scale > 0.f && pg->k_scale <= 3.4e38f && pg->v_scale > 0.f && pg->v_scale <= 3.4e38f))
+      return fail(SPECDEC_ERR_INVALID_ARG, "k_scale and v_scale must be positive and finite");
+  }
+  Pages& o = *out;
+  o.k = static_cast<char*>(pg->k);
+  o.v = static_cast<char*>(pg->v);
+  o.k_scales = static_cast<char*>(pg->k_scales);
+  o.v_scales = static_cast<char*>(pg->v_scales);
+  o.page_stride = pg->page_stride;
+  o.slot_stride = pg->slot_stride;
+  o.head_stride = pg->head_stride;
+  o.scale_page_stride = pg->scale_page_stride;
+  o.scale_slot_stride = pg->scale_slot_stride;
+  o.scale_head_stride = pg->scale_head_stride;
+  o.table = pg->block_table;
+  o.num_pages = pg->num_pages;
+  o.page_size = pg->page_size;
+  o.max_pages = pg->max_pages;
+  o.kv_heads = pg->kv_heads;
+  o.head_dim = pg->head_dim;
+  o.k_scale = four ? pg->k_scale : 1.f;
+  o.v_scale = four ? pg->v_scale : 1.f;
+  return SPECDEC_OK;
+}
+
+}  // namespace
+
+int specdec_rotate_qk(const void* q, const int64_t* q_strides, const void* k, const int64_t* k_strides,
+                      const void* v, const int64_t* v_strides, specdec_dtype dtype, const void* q_weight,
+                      const void* k_weight, float eps, const uint64_t* turns, int rot, int interleaved,
+                      const int32_t* context_len, const int32_t* query_len, const int32_t* depth, int B, int n,
+                      int q_heads, int kv_heads, int head_dim, void* out_q, void* out_k,
+                      const specdec_kv_pages* pages, int32_t* out_status, void* stream) {
+  if (!valid_half(dtype)) return fail(SPECDEC_ERR_INVALID_ARG, "dtype must be SPECDEC_BF16 or SPECDEC_F16");
+  if (B <= 0 || n <= 0 || q_heads <= 0 || kv_heads <= 0) return fail(SPECDEC_ERR_INVALID_ARG, "sizes must be positive");
+  if (!turns || !context_len || !out_q) return fail(SPECDEC_ERR_INVALID_ARG, "a required pointer is null");
+  if ((pages == nullptr) == (out_k == nullptr)) return fail(SPECDEC_ERR_INVALID_ARG, "either pages or out_k");
+  if (!(eps >= 0.f && eps <= 3.4e38f)) return fail(SPECDEC_ERR_INVALID_ARG, "eps must be finite and not negative");
+  if (rot < 16 || rot > head_dim) return fail(SPECDEC_ERR_INVALID_ARG, "rot must be in [16, head_dim]");
+  if (head_dim != 64 && head_dim != 128) return fail(SPECDEC_ERR_UNSUPPORTED, "head_dim must be 64 or 128");
+  if (rot % 16 != 0) return fail(SPECDEC_ERR_UNSUPPORTED, "rot must be a multiple of 16");
+  if (B > 65535 || q_heads > (1 << 20) || kv_heads > (1 << 20)) return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, or too many heads");
+  if (int rc = check_view(q, q_strides, "q is null"); rc != SPECDEC_OK) return rc;
+  if (int rc = check_view(k, k_strides, "k is null"); rc != SPECDEC_OK) return rc;
+  if (pages)
+    if (int rc = check_view(v, v_strides, "v is null"); rc != SPECDEC_OK) return rc;
+  if (!aligned16(out_q) || (out_k && !aligned16(out_k)) || (q_weight && !aligned16(q_weight)) || (k_weight && !aligned16(k_weight)))
+    return fail(SPECDEC_ERR_UNSUPPORTED, "outputs and weights must be 16-byte aligned");
+  RotateParams P{};
+  if (pages) {
+    if (int rc = check_pages(pages, false, dtype, &P.pages); rc != SPECDEC_OK) return rc;
+    if (pages->kv_heads != kv_heads || pages->head_dim != head_dim)
+      return fail(SPECDEC_ERR_INVALID_ARG, "the pages' heads do not fit k");
+  }
+  P.q = q;
+  P.k = k;
+  P.v = v;
+  P.q_sb = q_strides[0]; P.q_st = q_strides[1]; P.q_sh = q_strides[2];
+  P.k_sb = k_strides[0]; P.k_st = k_strides[1]; P.k_sh = k_strides[2];
+  if (pages) {
+    P.v_sb = v_strides[0]; P.v_st = v_strides[1]; P.v_sh = v_strides[2];
+  }
+  P.q_weight = q_weight;
+  P.k_weight = k_weight;
+  P.turns = turns;
+  P.context_len = context_len;
+  P.query_len = query_len;
+  P.depth = depth;
+  P.B = B;
+  P.n = n;
+  P.Hq = q_heads;
+  P.Hkv = kv_heads;
+  P.D = head_dim;
+  P.rot = rot;
+  P.interleaved = interleaved;
+  P.eps = eps;
+  P.q_out = out_q;
+  P.k_out = out_k;
+  P.out_status = out_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope prof(SPECDEC_KERNEL_ROTATE_QK, s);
+  if (cudaError_t e = launch_rotate_qk(P, dtype, s); e != cudaSuccess) return fail_cuda("rotation kernel", e);
+  return SPECDEC_OK;
+}
+
+int specdec_append_kv4(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                       specdec_dtype dtype, const int32_t* context_len, const int32_t* query_len, int B, int n,
+                       const specdec_kv_pages* pages, int32_t* out_status, void* stream) {
+  if (!valid_half(dtype)) return fail(SPECDEC_ERR_INVALID_ARG, "dtype must be SPECDEC_BF16 or SPECDEC_F16");
+  if (B <= 0 || n <= 0 || !context_len) return fail(SPECDEC_ERR_INVALID_ARG, "B and n must be positive, context_len given");
+  Kv4Params P{};
+  if (int rc = check_view(k, k_strides, "k is null"); rc != SPECDEC_OK) return rc;
+  if (int rc = check_view(v, v_strides, "v is null"); rc != SPECDEC_OK) return rc;
+  if (int rc = check_pages(pages, true, dtype, &P.pages); rc != SPECDEC_OK) return rc;
+  if (B > 65535 || static_cast<int64_t>(n) * pages->kv_heads >= (1 << 26)) return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, or n * kv_heads above 2^26");
+  P.k = k;
+  P.v = v;
+  P.k_sb = k_strides[0]; P.k_st = k_strides[1]; P.k_sh = k_strides[2];
+  P.v_sb = v_strides[0]; P.v_st = v_strides[1]; P.v_sh = v_strides[2];
+  P.context_len = context_len;
+  P.query_len = query_len;
+  P.B = B;
+  P.n = n;
+  P.out_status = out_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope prof(SPECDEC_KERNEL_APPEND_KV4, s);
+  if (cudaError_t e = launch_append_kv4(P, dtype, s); e != cudaSuccess) return fail_cuda("4-bit page write kernel", e);
+  return SPECDEC_OK;
+}
+
+int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B, int n,
+                     const specdec_kv_pages* pages, specdec_dtype dtype, void* out_k, void* out_v,
+                     int32_t* out_status, void* stream) {
+  if (!valid_half(dtype)) return fail(SPECDEC_ERR_INVALID_ARG, "dtype must be SPECDEC_BF16 or SPECDEC_F16");
+  if (B <= 0 || n <= 0 || !context_len || !out_k || !out_v)
+    return fail(SPECDEC_ERR_INVALID_ARG, "B and n must be positive, the pointers given");
+  Kv4Params P{};
+  if (int rc = check_pages(pages, true, dtype, &P.pages); rc != SPECDEC_OK) return rc;
+  if (!aligned16(out_k) || !aligned16(out_v)) return fail(SPECDEC_ERR_UNSUPPORTED, "outputs must be 16-byte aligned");
+  if (B > 65535 || static_cast<int64_t>(n) * pages->kv_heads >= (1 << 26)) return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, or n * kv_heads above 2^26");
+  P.k_out = out_k;
+  P.v_out = out_v;
+  P.context_len = context_len;
+  P.query_len = query_len;
+  P.B = B;
+  P.n = n;
+  P.out_status = out_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope prof(SPECDEC_KERNEL_READ_KV4, s);
+  if (cudaError_t e = launch_read_kv4(P, dtype, s); e != cudaSuccess) return fail_cuda("4-bit page read kernel", e);
+  return SPECDEC_OK;
+}
+
+size_t specdec_attend_workspace_bytes(int B, int n, int q_heads, int kv_heads, int head_dim) {
+  if (B <= 0 || n <= 0 || q_heads <= 0 || kv_heads <= 0 || q_heads % kv_heads != 0 || (head_dim != 64 && head_dim != 128)) return 0;
+  return attend_workspace_bytes(n, q_heads / kv_heads, head_dim);
+}
+
+int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype, const specdec_kv_pages* pages,
+                   const int32_t* context_len, const int32_t* query_len, const uint8_t* tree_mask,
+                   const int32_t* depth, int B, int n, int q_heads, int window, int sinks, float scale, void* out,
+                   float* out_lse, int32_t* out_status, void* workspace, size_t workspace_bytes, void* stream) {
+  if (!valid_half(dtype)) return fail(SPECDEC_ERR_INVALID_ARG, "dtype must be SPECDEC_BF16 or SPECDEC_F16");
+  if (B <= 0 || n <= 0 || q_heads <= 0) return fail(SPECDEC_ERR_INVALID_ARG, "sizes must be positive");
+  if (window < 0 || sinks < 0) return fail(SPECDEC_ERR_INVALID_ARG, "window and sinks must not be negative");
+  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return fail(SPECDEC_ERR_INVALID_ARG, "scale must be finite");
+  if (!context_len || !out || !workspace) return fail(SPECDEC_ERR_INVALID_ARG, "a required pointer is null");
+  if (depth && !tree_mask) return fail(SPECDEC_ERR_INVALID_ARG, "depth without tree_mask");
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+    return fail(SPECDEC_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
+  if (int rc = check_view(q, q_strides, "q is null"); rc != SPECDEC_OK) return rc;
+  AttendParams P{};
+  const bool four = pages && pages->format == SPECDEC_KV4;
+  if (int rc = check_pages(pages, four, dtype, &P.pages); rc != SPECDEC_OK) return rc;
+  if (q_heads % pages->kv_heads != 0) return fail(SPECDEC_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
+  const int G = q_heads / pages->kv_heads;
+  if (B >= (1 << 24) || static_cast<int64_t>(n) * G >= (1 << 24)) return fail(SPECDEC_ERR_UNSUPPORTED, "B, or query rows of a key head, above 2^24");
+  if (!aligned16(out)) return fail(SPECDEC_ERR_UNSUPPORTED, "out must be 16-byte aligned");
+  if (workspace_bytes < attend_workspace_bytes(n, G, pages->head_dim))
+    return fail(SPECDEC_ERR_WORKSPACE, "workspace smaller than specdec_attend_workspace_bytes");
+  P.q = q;
+  P.q_sb = q_strides[0];
+  P.q_st = q_strides[1];
+  P.q_sh = q_strides[2];
+  P.context_len = context_len;
+  P.query_len = query_len;
+  P.tree_mask = tree_mask;
+  P.depth = depth;
+  P.B = B;
+  P.n = n;
+  P.Hq = q_heads;
+  P.G = G;
+  P.window = window;
+  P.sinks = sinks;
+  P.scale_log2 = scale * 1.4426950408889634f * P.pages.k_scale;
+  P.out = out;
+  P.lse = out_lse;
+  P.out_status = out_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope prof(SPECDEC_KERNEL_ATTEND, s);
+  if (cudaError_t e = launch_attend(P, dtype, four ? SPECDEC_KV4 : dtype, workspace, s); e != cudaSuccess)
+    return fail_cuda("attention kernels", e);
   return SPECDEC_OK;
 }
 
