@@ -582,6 +582,9 @@ int specdec_verify_chain_noalloc(const void* logits, specdec_dtype ldt, const fl
  *                                  to come back with SPECDEC_STATUS_TIMEOUT)
  *   SPECDEC_HOOK_QUEUE_WAIT_US     >= 1: the left-to-right kernel's bound on waits for
  *                                  queued work, in microseconds (0: one second)
+ *   SPECDEC_HOOK_ATTEND_KERNEL     1 or 2: attention over pages takes the kernel on warp-level
+ *                                  matrix instructions, or the tensor-memory kernel (16-bit
+ *                                  pages), whatever the number of rows
  * Returns SPECDEC_OK, or SPECDEC_ERR_INVALID_ARG for an unknown hook or value.
  */
 #define SPECDEC_HOOK_CHAIN_ALL_ROWS 0
@@ -589,7 +592,8 @@ int specdec_verify_chain_noalloc(const void* logits, specdec_dtype ldt, const fl
 #define SPECDEC_HOOK_TREE_CLUSTER 2
 #define SPECDEC_HOOK_CHAIN_DROP_DRAWS 3
 #define SPECDEC_HOOK_QUEUE_WAIT_US 4
-#define SPECDEC_NUM_HOOKS 5
+#define SPECDEC_HOOK_ATTEND_KERNEL 5
+#define SPECDEC_NUM_HOOKS 6
 
 int specdec_set_test_hook(int hook, int value);
 int specdec_get_test_hook(int hook);

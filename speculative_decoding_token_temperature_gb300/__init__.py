@@ -31,7 +31,7 @@ STATUS_TIMEOUT = 128
 TREE_WITHOUT_REPLACEMENT = 1  # specdec_verify_tree_recursive: children drawn without replacement
 
 # Test hooks of the library (specdec_set_test_hook): the library's own tests and sweeps.
-HOOK_CHAIN_ALL_ROWS, HOOK_BLOCK_TWO_PASS, HOOK_TREE_CLUSTER, HOOK_CHAIN_DROP_DRAWS, HOOK_QUEUE_WAIT_US = range(5)
+HOOK_CHAIN_ALL_ROWS, HOOK_BLOCK_TWO_PASS, HOOK_TREE_CLUSTER, HOOK_CHAIN_DROP_DRAWS, HOOK_QUEUE_WAIT_US, HOOK_ATTEND_KERNEL = range(6)
 
 OK, ERR_INVALID_ARG, ERR_UNSUPPORTED, ERR_CUDA, ERR_WORKSPACE = 0, 1, 2, 3, 4
 _ERR_NAMES = {1: "invalid argument", 2: "unsupported size", 3: "CUDA launch error",

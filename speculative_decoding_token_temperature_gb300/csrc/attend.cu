@@ -23,10 +23,8 @@
 // join their rows through shared memory once per segment.  Rows of the staged keys are padded
 // by 16 bytes, so the matrix loads meet no bank conflicts.
 
-#include <type_traits>
-
-#include "cache_device.cuh"
-#include "specdec_device.cuh"
+#include "attend_common.cuh"
+#include "specdec_internal.h"
 
 namespace specdec {
 
@@ -34,27 +32,7 @@ namespace {
 
 constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
-constexpr int kStep = 16;                 // slots of a step
-constexpr int kUnit = 8;                  // steps of a unit of the work split
-constexpr float kLn2 = 0.6931471805599453f;
 
-__device__ __forceinline__ uint32_t smem_addr(const void* p) {
-  return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-// 16 (or 8, 4) bytes to shared memory, zeros where `there` is false (src is not read then).
-template <int N>
-__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
-  const int n = there ? N : 0;
-  if constexpr (N == 16)
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-  else
-    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
-}
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
 __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -79,49 +57,6 @@ __device__ __forceinline__ void group_sync(int group) {
     __syncwarp();
   else
     asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(32 * WR) : "memory");
-}
-
-// ---- the work split ---------------------------------------------------------------------
-
-// The visible slots of an item as steps of 16: `sink_steps` from slot 0, then from step
-// `first_step` on, up to slot `end`.
-struct Range {
-  int sink_steps, first_step, steps, end;
-};
-__device__ __forceinline__ Range item_range(const AttendParams& P, const SeqLen& S, int row0, int rows) {
-  Range r{0, 0, 0, 0};
-  const int i0 = row0 / P.G, i1 = min((row0 + rows - 1) / P.G, S.nq - 1);
-  if (!S.ok || i0 > i1) return r;
-  const bool tree = P.tree_mask != nullptr;
-  r.end = tree ? S.len : S.first + i1 + 1;
-  int lo = 0;
-  if (P.window > 0) lo = max(0, (tree ? S.first : S.first + i0) - (P.window - 1));
-  r.sink_steps = (min(P.sinks, lo) + kStep - 1) / kStep;
-  r.first_step = lo / kStep;
-  if (r.sink_steps >= r.first_step) r.sink_steps = r.first_step = 0;
-  r.steps = r.sink_steps + (r.end + kStep - 1) / kStep - r.first_step;
-  return r;
-}
-// A node's depth; a tree of n nodes is at most n - 1 deep, which the tests of whole steps use.
-__device__ __forceinline__ int node_depth(const AttendParams& P, int i) {
-  return min(max(__ldg(P.depth + i), 0), P.n - 1);
-}
-template <int MR>
-__device__ __forceinline__ int tile_rows(const AttendParams& P, int rt) { return min(MR, P.n * P.G - rt * MR); }
-
-// Units of one key head's row tiles of a sequence: at least one each, so that every row is
-// written by somebody.
-template <int MR>
-__device__ __forceinline__ int item_units(const AttendParams& P, const SeqLen& S, int rt) {
-  const Range r = item_range(P, S, rt * MR, tile_rows<MR>(P, rt));
-  return max(1, (r.steps + kUnit - 1) / kUnit);
-}
-template <int MR>
-__device__ __forceinline__ int64_t sequence_units(const AttendParams& P, int b, int64_t slots) {
-  const SeqLen S = seq_len(P.context_len, P.query_len, b, P.n, slots);
-  int64_t u = 0;
-  for (int rt = 0; rt < P.row_tiles; ++rt) u += item_units<MR>(P, S, rt);
-  return u * P.pages.kv_heads;
 }
 
 // ---- one 16-bit or 4-bit step ------------------------------------------------------------
@@ -156,9 +91,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
   using M = typename std::conditional<FOUR, __half, T>::type;  // the matrix instructions' type
   constexpr int MR = Sh::MR, GROUPS = Sh::GROUPS, STAGES = Sh::STAGES, KT = D / 16, NT = D / 8;
   extern __shared__ __align__(128) char smem[];
-  __shared__ int64_t s_scan[kWarps];
-  __shared__ int64_t s_total, s_start;
-  __shared__ int s_seq;
+  __shared__ int64_t s_scan[kWarps + 2];
   const Pages& pg = P.pages;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
   const int group = warp / WR, wr = warp % WR;
@@ -168,63 +101,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
   uint32_t* const s_bad = reinterpret_cast<uint32_t*>(smem + Sh::kOffBad) + group * STAGES;
 
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // this CTA's range of units: a scan of the sequences' units, thread t taking a run of them
-  const int per = (P.B + kThreads - 1) / kThreads;
-  const int b_lo = min(P.B, tid * per), b_hi = min(P.B, b_lo + per);
-  int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += sequence_units<MR>(P, b, slots);
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-    if (lane >= o) incl += v;
-  }
-  if (lane == 31) s_scan[warp] = incl;
-  __syncthreads();
-  int64_t before = 0, total = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    if (w < warp) before += s_scan[w];
-    total += s_scan[w];
-  }
-  const int64_t quota = total / gridDim.x, extra = total % gridDim.x;
+  const Share share = scan_units<MR, kThreads>(P, slots, s_scan);
   const int64_t cta = blockIdx.x;
-  int64_t u = cta * quota + min(cta, extra);
-  const int64_t u_end = u + quota + (cta < extra ? 1 : 0);
-  int64_t lo = before + incl - mine;
-  if (u < u_end && u >= lo && u < lo + mine) {  // exactly one thread
-    int b = b_lo;
-    for (;; ++b) {
-      const int64_t n = sequence_units<MR>(P, b, slots);
-      if (u < lo + n) break;
-      lo += n;
-    }
-    s_seq = b;
-    s_start = lo;
-  }
   if (tid == 0) {
     P.split[cta] = make_int4(0, 0, 0, 0);
-    s_total = total;
+    P.gave_up[cta] = 0;
   }
-  __syncthreads();
-  if (u >= u_end) return;
-
-  int b = s_seq, rt = 0, h = 0;
-  SeqLen S = seq_len(P.context_len, P.query_len, b, P.n, slots);
-  int units = item_units<MR>(P, S, 0);
-  int64_t item = s_start;  // the first unit of item (b, rt, h)
-  while (u >= item + units) {
-    item += units;
-    if (++h == pg.kv_heads) {
-      h = 0;
-      ++rt;
-      units = item_units<MR>(P, S, rt);
-    }
-  }
+  if (share.u >= share.end) return;
+  Walk<MR> w(P, slots, share);
 
   while (true) {
     // ---- the segment [u, seg_end) of item (b, rt, h)
-    const int64_t seg_end = min(u_end, item + units);
+    const SeqLen S = w.S;
+    const int b = w.b, rt = w.rt, h = w.h;
+    const int64_t u = w.u, item = w.item, seg_end = w.seg_end();
     const int row0 = rt * MR, rows = tile_rows<MR>(P, rt);
     const Range R = item_range(P, S, row0, rows);
     const int t_lo = static_cast<int>(u - item) * kUnit;
@@ -235,15 +125,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
     const char* const ks_head = pg.k_scales + h * pg.scale_head_stride;
     const char* const vs_head = pg.v_scales + h * pg.scale_head_stride;
 
-    auto step_slot = [&](int t) { return (t < R.sink_steps ? t : t - R.sink_steps + R.first_step) * kStep; };
     // the table entry of this lane's slot of step t (lanes 16..31 repeat 0..15)
     auto entry = [&](int t) {
-      const int s = step_slot(t) + (lane & 15);
+      const int s = R.slot(t) + (lane & 15);
       return t < t_hi && s < R.end ? __ldg(table + s / pg.page_size) : 0;
     };
     auto prefetch = [&](int t, int stage, int page) {
       if (t < t_hi) {
-        const int s = step_slot(t) + (lane & 15);
+        const int s = R.slot(t) + (lane & 15);
         const bool bad = s < R.end && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
         const bool there = s < R.end && !bad;
         const int in_page = s % pg.page_size;
@@ -453,7 +342,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
       }
 
       // scale and mask; a slot on a page out of range gives NaN to the rows that see it
-      const int s0 = step_slot(t);
+      const int s0 = R.slot(t);
       bool whole = s0 + kStep <= R.end && bads == 0;
       if (tree) {
         whole = whole && s0 + kStep <= S.first;
@@ -669,22 +558,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
         }
       }
     __syncthreads();
-    const bool begins = u == item, ends = seg_end == item + units;
+    const bool begins = u == item, ends = seg_end == item + w.units;
     const int part = begins ? 1 : 0;  // a CTA has at most one part that goes on and one that began before
     for (int f = tid; f < MR * (D / 4); f += kThreads) {
       const int r = f / (D / 4), d = (f % (D / 4)) * 4;
       if (r >= rows) continue;
       float m = -kInf;
 #pragma unroll
-      for (int w = 0; w < GROUPS; ++w) m = fmaxf(m, s_ml[w * MR + r].x);
+      for (int k = 0; k < GROUPS; ++k) m = fmaxf(m, s_ml[k * MR + r].x);
       const float base = m == -kInf ? 0.f : m;
       float l = 0.f;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-      for (int w = 0; w < GROUPS; ++w) {
-        const float2 ml = s_ml[w * MR + r];
+      for (int k = 0; k < GROUPS; ++k) {
+        const float2 ml = s_ml[k * MR + r];
         const float a = ex2(ml.x - base);
-        const float4 x = *reinterpret_cast<const float4*>(s_o + (static_cast<size_t>(w) * MR + r) * D + d);
+        const float4 x = *reinterpret_cast<const float4*>(s_o + (static_cast<size_t>(k) * MR + r) * D + d);
         l += a * ml.y;
         acc.x += a * x.x; acc.y += a * x.y; acc.z += a * x.z; acc.w += a * x.w;
       }
@@ -693,13 +582,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
         const int64_t at = (static_cast<int64_t>(b) * P.n + i) * P.Hq + head;
         float inv = l == 0.f ? 0.f : pg.v_scale / l, lse = m * kLn2 + logf(l);
         if (l == 0.f || i >= S.nq) { lse = -kInf; inv = 0.f; }
-        uint2 w = make_uint2(Half16<T>::pack(acc.x * inv, acc.y * inv), Half16<T>::pack(acc.z * inv, acc.w * inv));
-        if (i >= S.nq) w = make_uint2(0u, 0u);
+        uint2 four = make_uint2(Half16<T>::pack(acc.x * inv, acc.y * inv), Half16<T>::pack(acc.z * inv, acc.w * inv));
+        if (i >= S.nq) four = make_uint2(0u, 0u);
         if (!S.ok) {
-          w = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+          four = make_uint2(0x7fff7fffu, 0x7fff7fffu);
           lse = __int_as_float(0x7fffffff);
         }
-        *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + at * D + d) = w;
+        *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + at * D + d) = four;
         if (d == 0 && P.lse) P.lse[at] = lse;
       } else {
         const int64_t at = (cta * 2 + part) * MR + r;
@@ -707,24 +596,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
         if (d == 0) P.part_ml[at] = make_float2(m, l);
       }
     }
-    if (begins && !ends && tid == 0) {  // the CTA that holds the item's last unit
-      const int64_t last = item + units - 1, wide = extra * (quota + 1);
-      const int64_t owner = last < wide ? last / (quota + 1) : extra + (last - wide) / quota;
-      P.split[cta] = make_int4(b, rt, h, static_cast<int>(owner - cta + 1));
-    }
-
-    u = seg_end;
-    if (u >= u_end) break;
-    item += units;
-    if (++h == pg.kv_heads) {
-      h = 0;
-      if (++rt == P.row_tiles) {
-        rt = 0;
-        ++b;
-        S = seq_len(P.context_len, P.query_len, b, P.n, slots);
-      }
-      units = item_units<MR>(P, S, rt);
-    }
+    if (begins && !ends && tid == 0) P.split[cta] = w.split(share);
+    if (!w.next()) break;
   }
 }
 
@@ -755,6 +628,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const Atte
     }
   }
   asm volatile("griddepcontrol.wait;" ::: "memory");
+  if (blockIdx.y == 0 && P.out_status) {  // a bounded wait gave up somewhere: nothing counts
+    int late = 0;
+    for (int k = threadIdx.x; k < gridDim.x; k += blockDim.x) late |= P.gave_up[k];
+    if (__syncthreads_or(late))
+      for (int b = cta + threadIdx.x * gridDim.x; b < P.B; b += gridDim.x * blockDim.x) P.out_status[b] |= SPECDEC_STATUS_TIMEOUT;
+  }
   const int4 it = P.split[cta];
   const int parts = it.w;
   if (parts == 0) return;
@@ -810,10 +689,7 @@ cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
   auto kernel = attend_kernel<T, D, FOUR, MT, WR>;
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes); e != cudaSuccess)
     return e;
-  if (cudaError_t e = launch_kernel(kernel, dim3(P.ctas), dim3(kThreads), Sh::kBytes, stream, 0, P); e != cudaSuccess)
-    return e;
-  return launch_kernel(attend_join_kernel<T, D>, dim3(P.ctas, Sh::MR / (2 * kJoinWarps)), dim3(32 * kJoinWarps), 0,
-                       stream, 1, P, int{Sh::MR});
+  return launch_kernel(kernel, dim3(P.ctas), dim3(kThreads), Sh::kBytes, stream, 0, P);
 }
 
 template <typename T, int D, bool FOUR>
@@ -838,19 +714,24 @@ int attend_sms() {
 }
 size_t round256(size_t x) { return (x + 255) / 256 * 256; }
 
-constexpr int kMaxCtas = 256;  // the workspace's size does not depend on the device
+constexpr int kMaxCtas = 160;  // the workspace's size does not depend on the device
 
 }  // namespace
 
 size_t attend_workspace_bytes(int n, int G, int D) {
-  const size_t mr = static_cast<size_t>(row_tile(static_cast<int64_t>(n) * G));
-  return round256(kMaxCtas * sizeof(int4)) + round256(kMaxCtas * 2 * mr * sizeof(float2)) +
+  // (any row tile that a rule or the test hook may choose for these rows)
+  const int64_t rows = static_cast<int64_t>(n) * G;
+  const size_t mr = rows <= 128 ? 128 : 256;
+  return round256(kMaxCtas * sizeof(int4)) + round256(kMaxCtas * sizeof(int)) + round256(kMaxCtas * 2 * mr * sizeof(float2)) +
          round256(kMaxCtas * 2 * mr * static_cast<size_t>(D) * sizeof(float));
 }
 
 cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format, void* workspace, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(P.n) * P.G;
-  const int mr = row_tile(rows);
+  const bool four = format == SPECDEC_KV4;
+  const int hook = test_hook(SPECDEC_HOOK_ATTEND_KERNEL);
+  const bool tc = !four && (hook == 0 ? rows > 64 : hook == 2);
+  const int mr = tc ? attend_tc_rows(rows) : row_tile(rows);
   P.row_tiles = static_cast<int>((rows + mr - 1) / mr);
   P.ctas = attend_sms();
   if (P.ctas <= 0) return cudaErrorInvalidDevice;
@@ -858,11 +739,22 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   char* ws = static_cast<char*>(workspace);
   P.split = reinterpret_cast<int4*>(ws);
   ws += round256(kMaxCtas * sizeof(int4));
+  P.gave_up = reinterpret_cast<int*>(ws);
+  ws += round256(kMaxCtas * sizeof(int));
   P.part_ml = reinterpret_cast<float2*>(ws);
   ws += round256(static_cast<size_t>(kMaxCtas) * 2 * mr * sizeof(float2));
   P.part_o = reinterpret_cast<float*>(ws);
-  const bool four = format == SPECDEC_KV4;
-  return dt == SPECDEC_BF16 ? launch_typed<__nv_bfloat16>(P, mr, four, stream) : launch_typed<__half>(P, mr, four, stream);
+  if (tc)
+    if (cudaError_t e = launch_attend_tc(P, dt, mr, stream); e != cudaSuccess) return e;
+  if (!tc)
+    if (cudaError_t e = dt == SPECDEC_BF16 ? launch_typed<__nv_bfloat16>(P, mr, four, stream)
+                                           : launch_typed<__half>(P, mr, four, stream);
+        e != cudaSuccess)
+      return e;
+  auto join = P.pages.head_dim == 64
+                  ? (dt == SPECDEC_BF16 ? attend_join_kernel<__nv_bfloat16, 64> : attend_join_kernel<__half, 64>)
+                  : (dt == SPECDEC_BF16 ? attend_join_kernel<__nv_bfloat16, 128> : attend_join_kernel<__half, 128>);
+  return launch_kernel(join, dim3(P.ctas, mr / (2 * kJoinWarps)), dim3(32 * kJoinWarps), 0, stream, 1, P, int{mr});
 }
 
 }  // namespace specdec

@@ -1,0 +1,180 @@
+// Pieces shared by the attention kernels: which slots an item sees, the split of the work over
+// the CTAs, and the asynchronous copies.
+#pragma once
+
+#include <type_traits>
+
+#include "cache_device.cuh"
+#include "specdec_device.cuh"
+
+namespace specdec {
+
+constexpr int kStep = 16;                 // slots of a step
+constexpr int kUnit = 8;                  // steps of a unit of the work split
+constexpr float kLn2 = 0.6931471805599453f;
+
+// 16 (or 8, 4) bytes to shared memory, zeros where `there` is false (src is not read then).
+template <int N>
+__device__ __forceinline__ void copy_async(uint32_t dst, const void* src, bool there) {
+  const int n = there ? N : 0;
+  if constexpr (N == 16)
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  else
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2, %3;" ::"r"(dst), "l"(src), "n"(N), "r"(n) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// ---- the work split ---------------------------------------------------------------------
+
+// The visible slots of an item as steps of 16: `sink_steps` from slot 0, then from step
+// `first_step` on, up to slot `end`.
+struct Range {
+  int sink_steps, first_step, steps, end;
+  int lo, sinks;  // no query of the item sees a slot in [sinks, lo)
+  __device__ __forceinline__ int slot(int step) const {
+    return (step < sink_steps ? step : step - sink_steps + first_step) * kStep;
+  }
+};
+__device__ __forceinline__ Range item_range(const AttendParams& P, const SeqLen& S, int row0, int rows) {
+  Range r{0, 0, 0, 0, 0, 0};
+  const int i0 = row0 / P.G, i1 = min((row0 + rows - 1) / P.G, S.nq - 1);
+  if (!S.ok || i0 > i1) return r;
+  const bool tree = P.tree_mask != nullptr;
+  r.end = tree ? S.len : S.first + i1 + 1;
+  int lo = 0;
+  if (P.window > 0) lo = max(0, (tree ? S.first : S.first + i0) - (P.window - 1));
+  r.lo = lo;
+  r.sinks = min(P.sinks, lo);
+  r.sink_steps = (r.sinks + kStep - 1) / kStep;
+  r.first_step = lo / kStep;
+  if (r.sink_steps >= r.first_step) r.sink_steps = r.first_step = 0;
+  r.steps = r.sink_steps + (r.end + kStep - 1) / kStep - r.first_step;
+  return r;
+}
+// A node's depth; a tree of n nodes is at most n - 1 deep, which the tests of whole steps use.
+__device__ __forceinline__ int node_depth(const AttendParams& P, int i) {
+  return min(max(__ldg(P.depth + i), 0), P.n - 1);
+}
+template <int MR>
+__device__ __forceinline__ int tile_rows(const AttendParams& P, int rt) { return min(MR, P.n * P.G - rt * MR); }
+
+// Units of one key head's row tiles of a sequence: at least one each, so that every row is
+// written by somebody.
+template <int MR>
+__device__ __forceinline__ int item_units(const AttendParams& P, const SeqLen& S, int rt) {
+  const Range r = item_range(P, S, rt * MR, tile_rows<MR>(P, rt));
+  return max(1, (r.steps + kUnit - 1) / kUnit);
+}
+template <int MR>
+__device__ __forceinline__ int64_t sequence_units(const AttendParams& P, int b, int64_t slots) {
+  const SeqLen S = seq_len(P.context_len, P.query_len, b, P.n, slots);
+  int64_t u = 0;
+  for (int rt = 0; rt < P.row_tiles; ++rt) u += item_units<MR>(P, S, rt);
+  return u * P.pages.kv_heads;
+}
+
+// A CTA's range of units and the item it starts in.  scan(): all threads of the CTA call it, with
+// shared memory for one int64_t per warp and four more.
+struct Share {
+  int64_t u, end;         // units [u, end) of all
+  int64_t quota, extra;   // every CTA has quota units, the first `extra` one more
+  int64_t item;           // first unit of item (b, rt, h)
+  int b;
+};
+template <int MR, int THREADS>
+__device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots, int64_t* sh) {
+  constexpr int WARPS = THREADS / 32;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int per = (P.B + THREADS - 1) / THREADS;  // thread t takes a run of sequences
+  const int b_lo = min(P.B, tid * per), b_hi = min(P.B, b_lo + per);
+  int64_t mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) mine += sequence_units<MR>(P, b, slots);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) sh[warp] = incl;
+  __syncthreads();
+  int64_t before = 0, total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += sh[w];
+    total += sh[w];
+  }
+  Share s;
+  s.quota = total / gridDim.x;
+  s.extra = total % gridDim.x;
+  const int64_t cta = blockIdx.x;
+  s.u = cta * s.quota + min(cta, s.extra);
+  s.end = s.u + s.quota + (cta < s.extra ? 1 : 0);
+  int64_t lo = before + incl - mine;
+  if (s.u < s.end && s.u >= lo && s.u < lo + mine) {  // exactly one thread
+    int b = b_lo;
+    for (;; ++b) {
+      const int64_t n = sequence_units<MR>(P, b, slots);
+      if (s.u < lo + n) break;
+      lo += n;
+    }
+    sh[WARPS] = b;
+    sh[WARPS + 1] = lo;
+  }
+  __syncthreads();
+  if (s.u < s.end) {
+    s.b = static_cast<int>(sh[WARPS]);
+    s.item = sh[WARPS + 1];
+  }
+  return s;
+}
+
+// Walks the items of a CTA's range.
+template <int MR>
+struct Walk {
+  const AttendParams& P;
+  int64_t slots, u, end, item;
+  int b, rt, h, units;
+  SeqLen S;
+  __device__ __forceinline__ Walk(const AttendParams& p, int64_t n, const Share& s)
+      : P(p), slots(n), u(s.u), end(s.end), item(s.item), b(s.b), rt(0), h(0) {
+    S = seq_len(P.context_len, P.query_len, b, P.n, slots);
+    units = item_units<MR>(P, S, 0);
+    while (u >= item + units) {
+      item += units;
+      if (++h == P.pages.kv_heads) {
+        h = 0;
+        ++rt;
+        units = item_units<MR>(P, S, rt);
+      }
+    }
+  }
+  __device__ __forceinline__ int64_t seg_end() const { return min(end, item + units); }
+  __device__ __forceinline__ bool next() {  // false: the range is done
+    u = seg_end();
+    if (u >= end) return false;
+    item += units;
+    if (++h == P.pages.kv_heads) {
+      h = 0;
+      if (++rt == P.row_tiles) {
+        rt = 0;
+        ++b;
+        S = seq_len(P.context_len, P.query_len, b, P.n, slots);
+      }
+      units = item_units<MR>(P, S, rt);
+    }
+    return true;
+  }
+  // The entry of the workspace's split table for a segment that begins an item and does not
+  // end it: the item and the number of CTAs that hold parts of it.
+  __device__ __forceinline__ int4 split(const Share& s) const {
+    const int64_t last = item + units - 1, wide = s.extra * (s.quota + 1);
+    const int64_t owner = last < wide ? last / (s.quota + 1) : s.extra + (last - wide) / s.quota;
+    return make_int4(b, rt, h, static_cast<int>(owner - blockIdx.x + 1));
+  }
+};
+
+}  // namespace specdec

@@ -65,10 +65,14 @@ struct AttendParams {
   int row_tiles;     // tiles of the n * G query rows that share a key head
   int ctas;
   int4* split;       // workspace [ctas]: the item whose first part a CTA left, and its parts
+  int* gave_up;      // workspace [ctas]: a bounded wait of the CTA ran out
   float2* part_ml;   // workspace [ctas, 2, rows]: (running maximum, sum) of a part
   float* part_o;     // workspace [ctas, 2, rows, D]: its unnormalised output
   Pages pages;
 };
+// The tensor-memory kernel for 16-bit pages: the rows of its tile, and its launch.
+int attend_tc_rows(int64_t rows);
+cudaError_t launch_attend_tc(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream);
 size_t attend_workspace_bytes(int n, int G, int D);
 cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format, void* workspace,
                           cudaStream_t stream);

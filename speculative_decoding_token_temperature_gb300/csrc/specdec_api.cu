@@ -971,6 +971,7 @@ int specdec_set_test_hook(int hook, int value) {
   if ((hook == SPECDEC_HOOK_CHAIN_ALL_ROWS || hook == SPECDEC_HOOK_BLOCK_TWO_PASS ||
        hook == SPECDEC_HOOK_CHAIN_DROP_DRAWS) && value > 1)
     return SPECDEC_ERR_INVALID_ARG;
+  if (hook == SPECDEC_HOOK_ATTEND_KERNEL && value > 2) return SPECDEC_ERR_INVALID_ARG;
   g_test_hooks[hook].store(value);
   return SPECDEC_OK;
 }

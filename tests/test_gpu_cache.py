@@ -34,6 +34,13 @@ def sd(built_library):
     return m
 
 
+@pytest.fixture(autouse=True, params=["rule", "warp", "tensor_memory"])
+def kernel(request, hooks):
+    """Every case through the kernel that the rule picks, and through each kernel."""
+    hooks(attend_kernel=("rule", "warp", "tensor_memory").index(request.param))
+    return request.param
+
+
 def _np(t):
     return t.detach().float().cpu().numpy().astype(np.float64)
 
