@@ -34,6 +34,11 @@ constexpr int kBadRing = 8;           // tiles whose out-of-range slots are reme
 constexpr float kSlack = 8.f;         // log2 of how far a weight may exceed 1
 static_assert(kTile == 128 && kCopyWarps * 32 == kTile, "one copy lane per slot");
 
+// What the row warps keep of an item.
+struct Item {
+  int b, h, row0, rows, t_lo, tiles, begins, ends, nq, first, ok, sink_steps, first_step, steps, end, more;
+};
+
 template <int D, bool TWO>
 struct TcShape {
   static constexpr int MR = TWO ? 256 : 128;
@@ -42,7 +47,8 @@ struct TcShape {
   static constexpr int kOffK = (TWO ? 2 : 1) * kTileBytes;
   static constexpr int kOffV = kOffK + RING * kTileBytes;
   static constexpr int kOffMl = kOffV + RING * kTileBytes;  // [2][128] (m, l) of the slots
-  static constexpr int kOffScan = kOffMl + 2 * 128 * 8;
+  static constexpr int kOffItem = kOffMl + 2 * 128 * 8;
+  static constexpr int kOffScan = kOffItem + 2 * sizeof(Item);
   static constexpr int kOffBad = kOffScan + (kTcThreads / 32 + 2) * 8;
   static constexpr int kOffBar = kOffBad + kBadRing * kCopyWarps * 4;
   static constexpr int kBars = 4 * RING + 2 + 2 + 2 + 1 + 1;
@@ -85,35 +91,34 @@ __device__ __forceinline__ void mma_commit(uint64_t* bar) {
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// 32 columns of this warp's 32 lanes; the wait is part of the load, so the values are there.
-__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[32]) {
+// 16 columns of this warp's 32 lanes.  The values are there after tmem_load_wait, which takes
+// them so that no use moves above it.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n"
-      "tcgen05.wait::ld.sync.aligned;"
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
-        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr)
       : "memory");
 }
-__device__ __forceinline__ void tmem_store(uint32_t addr, const uint32_t* r) {  // 32 columns
+__device__ __forceinline__ void tmem_load_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
-      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
 }
 __device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
-// Registers move from the warps that copy and issue to those that hold rows: 2 * 176 + 88 + 72 =
-// 4 * 128, what the CTA was launched with.
-template <int N> __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-template <int N> __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
 // A bounded wait: gives up after kMaxWaitNs, and at once when the CTA has given up elsewhere.
 __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
@@ -127,13 +132,6 @@ __device__ __forceinline__ void wait_for(uint64_t* bar, uint32_t parity, volatil
     }
   }
 }
-__device__ __forceinline__ bool test_for(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile("{\n.reg .pred p;\nmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\nselp.u32 %0, 1, 0, p;\n}"
-               : "=r"(ok) : "r"(smem_addr(bar)), "r"(parity) : "memory");
-  return ok != 0;
-}
-
 // Where the 16-byte piece `piece` of row `row` of a tile of 128 rows of D values lies: blocks
 // of 64 values, rows of 128 bytes, pieces swizzled by the row.
 template <int D>
@@ -141,10 +139,17 @@ __device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
   return (piece >> 3) * (kTile * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
 
-// One query row of an item and what it sees.
-struct Row {
-  int i, pos, hi, lo;  // chain: slots <= hi that are >= lo or among the sinks
-};
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Bits lo..hi-1 of a step's 16 slots, both clamped to 0..16.
+__device__ __forceinline__ uint32_t bits16(int lo, int hi) {
+  lo = min(max(lo, 0), kStep);
+  hi = min(max(hi, 0), kStep);
+  return hi > lo ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
+}
 
 template <typename T, int D, bool TWO>
 __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendParams P) {
@@ -172,9 +177,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
   asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     for (int r = 0; r < RING; ++r) {
-      mbar_init(k_full + r, kCopyWarps);
+      mbar_init(k_full + r, kTile + kCopyWarps);  // every copy lane's copies have landed; a warp's s_bad is written
       mbar_init(k_empty + r, 1);
-      mbar_init(v_full + r, kCopyWarps);
+      mbar_init(v_full + r, kTile);
       mbar_init(v_empty + r, 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -205,27 +210,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
   Walk<MR> w(P, slots, share);
 
   if (warp >= kRowWarps && warp < kRowWarps + kCopyWarps) {
-    fewer_registers<88>();
     // ---- copies: lane l of copy warp c brings slot 32 c + l of every tile
     const int cw = warp - kRowWarps;
-    int issued = 0, arrived = 0;  // groups: K of tile 0, V of tile 0, K of tile 1, ...
-    auto arrive_oldest = [&]() {
-      switch (issued - arrived) {  // copies in flight after the oldest
-        case 1: copy_wait<0>(); break;
-        case 2: copy_wait<1>(); break;
-        case 3: copy_wait<2>(); break;
-        case 4: copy_wait<3>(); break;
-        case 5: copy_wait<4>(); break;
-        case 6: copy_wait<5>(); break;
-        case 7: copy_wait<6>(); break;
-        default: copy_wait<7>(); break;
-      }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(((arrived & 1) ? v_full : k_full) + (arrived >> 1) % RING);
-      ++arrived;
-    };
-    static_assert(2 * RING <= 8, "arrive_oldest counts at most 8 groups in flight");
+    int tile = 0;
     do {
       const int rows = tile_rows<MR>(P, w.rt);
       const Range R = item_range(P, w.S, w.rt * MR, rows);
@@ -252,20 +239,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
           page = wanted(t + 1, s1) ? __ldg(table + s1 / pg.page_size) : 0;
         }
         const uint32_t present = __ballot_sync(0xffffffffu, want && !bad), bads = __ballot_sync(0xffffffffu, bad);
-        const int tile = issued >> 1, stage = tile % RING;
-        if (lane == 0) s_bad[(tile % kBadRing) * kCopyWarps + cw] = bads;
+        const int stage = tile % RING;
+        const uint32_t parity = ((tile / RING) & 1) ^ 1;  // the first round of a fresh barrier passes
 #pragma unroll
         for (int kv = 0; kv < 2; ++kv) {
-          uint64_t* const empty = (kv ? v_empty : k_empty) + stage;
-          const uint32_t parity = ((tile / RING) & 1) ^ 1;  // the first round of a fresh barrier passes
-          while (!__all_sync(0xffffffffu, test_for(empty, parity))) {
-            if (arrived < issued)
-              arrive_oldest();
-            else
-              wait_for(empty, parity, gave_up);
-            if (*gave_up) break;
-          }
+          wait_for((kv ? v_empty : k_empty) + stage, parity, gave_up);
           __syncwarp();
+          if (kv == 0 && lane == 0) {
+            s_bad[(tile % kBadRing) * kCopyWarps + cw] = bads;
+            mbar_arrive(k_full + stage);
+          }
           const char* const head = kv ? v_head : k_head;
           const uint32_t dst = smem_addr(smem + (kv ? Sh::kOffV : Sh::kOffK) + stage * Sh::kTileBytes);
           constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at a time
@@ -275,14 +258,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
             const int64_t o = __shfl_sync(0xffffffffu, off, row);
             copy_async<16>(dst + tile_offset<D>(cw * 32 + row, piece), head + o + piece * 16, (present >> row) & 1u);
           }
-          copy_commit();
-          ++issued;
+          // the barrier hears of it when this lane's copies so far have landed
+          asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr((kv ? v_full : k_full) + stage)) : "memory");
         }
+        ++tile;
       }
     } while (w.next());
-    while (arrived < issued) arrive_oldest();
+    copy_commit();
+    copy_wait<0>();
   } else if (warp >= kRowWarps + kCopyWarps) {
-    fewer_registers<72>();
     // ---- matrix instructions, from one thread
     if (warp == kRowWarps + kCopyWarps && lane == 0) {
       constexpr uint32_t id_s = instr_desc<T>(kTile, false), id_o = instr_desc<T>(D, true);
@@ -297,7 +281,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
         fence_after();
         auto issue_s = [&](int n) {
           const int slot = n & 1, tile = k_tile, stage = tile % RING;
-          if (!TWO || slot == 0) wait_for(k_full + stage, (tile / RING) & 1, gave_up);
+          if (!TWO || slot == 0) {
+            wait_for(k_full + stage, (tile / RING) & 1, gave_up);
+            fence_proxy_async_smem();  // the landed copies, before the matrix instructions read them
+          }
           fence_after();
           const uint32_t a = smem_addr(smem + (TWO ? slot * Sh::kTileBytes : 0));
           const uint32_t b = smem_addr(smem + Sh::kOffK + stage * Sh::kTileBytes);
@@ -316,7 +303,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
         if (jobs > 1) issue_s(1);
         for (int n = 0; n < jobs; ++n) {
           const int slot = n & 1, tile = v_tile, stage = tile % RING;
-          if (!TWO || slot == 0) wait_for(v_full + stage, (tile / RING) & 1, gave_up);
+          if (!TWO || slot == 0) {
+            wait_for(v_full + stage, (tile / RING) & 1, gave_up);
+            fence_proxy_async_smem();
+          }
           wait_for(p_full + slot, p_phase[slot], gave_up);
           p_phase[slot] ^= 1;
           fence_after();
@@ -338,33 +328,62 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
     }
     __syncwarp();
   } else {
-    more_registers<176>();
-    // ---- rows: thread = row of the slot's tile
+    // ---- rows: thread = row of the slot's tile.  What an item is stays in shared memory, so
+    // that the registers are free for a row of scores.
     const int slot = warp / 4, row = tid % 128;
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
     const uint32_t s_at = tmem + lanes + slot * 128, o_at = tmem + lanes + 256 + slot * 128;
     float2* const s_ml = reinterpret_cast<float2*>(smem + Sh::kOffMl);
+    volatile Item& it = *reinterpret_cast<volatile Item*>(smem + Sh::kOffItem + slot * sizeof(Item));
     uint32_t s_phase = 0, o_phase = 0;
     int tile_base = 0;  // tiles of earlier segments
-    do {
-      const SeqLen S = w.S;
-      const int row0 = w.rt * MR + (TWO ? slot * 128 : 0), item_rows = tile_rows<MR>(P, w.rt);
-      const int rows = min(128, item_rows - (TWO ? slot * 128 : 0));  // may be <= 0
-      const Range R = item_range(P, S, w.rt * MR, item_rows);
-      const int t_lo = static_cast<int>(w.u - w.item);
-      const int tiles = max(0, min(static_cast<int>(w.seg_end() - w.item), (R.steps + kUnit - 1) / kUnit) - t_lo);
+    bool more = true;
+    while (more) {
+      asm volatile("bar.sync %0, 128;" ::"r"(2 + slot) : "memory");  // the last item is done with
+      if (row == 0) {
+        const int item_rows = tile_rows<MR>(P, w.rt), row0 = w.rt * MR + (TWO ? slot * 128 : 0);
+        const Range R = item_range(P, w.S, w.rt * MR, item_rows);
+        const int t_lo = static_cast<int>(w.u - w.item);
+        it.b = w.b;
+        it.h = w.h;
+        it.row0 = row0;
+        it.rows = min(128, item_rows - (TWO ? slot * 128 : 0));  // may be <= 0
+        it.t_lo = t_lo;
+        it.tiles = max(0, min(static_cast<int>(w.seg_end() - w.item), (R.steps + kUnit - 1) / kUnit) - t_lo);
+        it.begins = w.u == w.item;
+        it.ends = w.seg_end() == w.item + w.units;
+        it.nq = w.S.nq;
+        it.first = w.S.first;
+        it.ok = w.S.ok;
+        it.sink_steps = R.sink_steps;
+        it.first_step = R.first_step;
+        it.steps = R.steps;
+        it.end = R.end;
+        if (it.begins && !it.ends && slot == 0) P.split[blockIdx.x] = w.split(share);
+        it.more = w.next();
+      }
+      asm volatile("bar.sync %0, 128;" ::"r"(2 + slot) : "memory");
+      more = it.more;
+      const int rows = it.rows, row0 = it.row0, tiles = it.tiles, t_lo = it.t_lo, first = it.first;
+      Range R;
+      R.sink_steps = it.sink_steps;
+      R.first_step = it.first_step;
+      R.steps = it.steps;
+      R.end = it.end;
       const bool tree = P.tree_mask != nullptr;
 
       // the query rows, zeros past the tile's: slot by slot, or together where both hold the same
       {
         constexpr int LOADERS = TWO ? 128 : 256;
         char* const dst = smem + (TWO ? slot * Sh::kTileBytes : 0);
+        const T* const q_item = static_cast<const T*>(P.q) + it.b * P.q_sb + it.h * P.G * P.q_sh;
+#pragma unroll 4
         for (int f = TWO ? row : tid; f < 128 * (D / 8); f += LOADERS) {
           const int r = f / (D / 8), piece = f % (D / 8);
           uint4 x = make_uint4(0, 0, 0, 0);
           if (r < rows)
-            x = *(reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + w.b * P.q_sb + ((row0 + r) / P.G) * P.q_st +
-                                                 (w.h * P.G + (row0 + r) % P.G) * P.q_sh) + piece);
+            x = __ldg(reinterpret_cast<const uint4*>(q_item + ((row0 + r) / P.G) * P.q_st + ((row0 + r) % P.G) * P.q_sh) + piece);
+          if (P.scale_log2 < 0.f) x = make_uint4(x.x ^ 0x80008000u, x.y ^ 0x80008000u, x.z ^ 0x80008000u, x.w ^ 0x80008000u);
           *reinterpret_cast<uint4*>(dst + tile_offset<D>(r, piece)) = x;
         }
         fence_proxy_async_smem();
@@ -373,49 +392,55 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
         if (lane == 0) mbar_arrive(q_full);
       }
 
-      Row me;
-      me.i = (row0 + row) / P.G;
-      me.pos = S.first + (P.depth && me.i < P.n ? node_depth(P, me.i) : me.i);
-      me.hi = min(S.first + me.i, R.end - 1);
-      me.lo = P.window > 0 ? max(0, me.pos - (P.window - 1)) : 0;
-      const int i0 = row0 / P.G, i1 = min((row0 + rows - 1) / P.G, S.nq - 1);
-      // every row of this slot's tile sees slots [s0, s0 + 16)
+      const int me = (row0 + row) / P.G;  // this row's query
+      const int my_pos = first + (P.depth && me < P.n ? node_depth(P, me) : me);
+      // every row of this slot's tile sees the 16 slots of a step
       auto whole_step = [&](int step) {
         const int s0 = R.slot(step);
-        bool ok = step < R.steps && s0 + kStep <= R.end;
-        if (tree) {
-          ok = ok && s0 + kStep <= S.first;
-          if (P.window > 0) ok = ok && (S.first + P.n - 1 - s0 < P.window || s0 + kStep <= P.sinks);
-        } else {
-          ok = ok && s0 + kStep - 1 <= S.first + i0;
-          if (P.window > 0) ok = ok && (S.first + i1 - s0 < P.window || s0 + kStep <= P.sinks);
-        }
+        bool ok = step < R.steps && s0 + kStep <= R.end && s0 + kStep <= (tree ? first : first + row0 / P.G + 1);
+        if (P.window > 0)
+          ok = ok && ((tree ? first + P.n - 1 : first + min((row0 + rows - 1) / P.G, it.nq - 1)) - s0 < P.window || s0 + kStep <= P.sinks);
         return ok;
       };
       // the same of a whole tile, from its first and last step (a few false answers at the sinks)
       auto whole_tile = [&](int step) {
-        const int first = R.slot(step), last = R.slot(step + kUnit - 1);
-        return step + kUnit <= R.steps && last + kStep <= R.end &&
-               last + kStep <= (tree ? S.first : S.first + i0 + 1) &&
-               (P.window == 0 || (tree ? S.first + P.n - 1 : S.first + i1) - first < P.window);
+        const int s0 = R.slot(step), last = R.slot(step + kUnit - 1);
+        return step + kUnit <= R.steps && last + kStep <= R.end && last + kStep <= (tree ? first : first + row0 / P.G + 1) &&
+               (P.window == 0 || (tree ? first + P.n - 1 : first + min((row0 + rows - 1) / P.G, it.nq - 1)) - s0 < P.window);
       };
-      auto sees = [&](int s) {
-        if (!tree) return s <= me.hi && (s >= me.lo || s < P.sinks);
-        const int j = s - S.first;
-        bool ok = s < R.end;
-        int pos = s;
-        if (j >= 0) {
-          ok = ok && me.i < P.n && __ldg(P.tree_mask + static_cast<int64_t>(me.i) * P.n + min(j, P.n - 1)) != 0;
-          if (P.depth) pos = S.first + node_depth(P, min(j, P.n - 1));
+      // which of the 16 slots of a step this row sees
+      auto sees16 = [&](int step) -> uint32_t {
+        if (step >= R.steps) return 0u;
+        const int s0 = R.slot(step);
+        uint32_t near = P.window > 0 ? bits16(my_pos - (P.window - 1) - s0, kStep) | bits16(0, P.sinks - s0) : 0xffffu;
+        if (!tree) return near & bits16(0, min(first + me, R.end - 1) + 1 - s0);
+        uint32_t see = near & bits16(0, min(first, R.end) - s0);
+        if (s0 + kStep > first && me < P.n) {
+          const uint8_t* const mask = P.tree_mask + static_cast<int64_t>(me) * P.n;
+          const uint32_t there = bits16(first - s0, R.end - s0);
+          uint32_t node = 0;
+#pragma unroll
+          for (int e = 0; e < kStep; ++e)
+            if ((there >> e) & 1u) node |= (__ldg(mask + (s0 + e - first)) != 0 ? 1u : 0u) << e;
+          if (P.window > 0 && P.depth) {
+            near = 0;
+#pragma unroll
+            for (int e = 0; e < kStep; ++e)
+              if ((there >> e) & 1u) {
+                const int pos = first + node_depth(P, s0 + e - first);
+                near |= (my_pos - pos < P.window || pos < P.sinks ? 1u : 0u) << e;
+              }
+          }
+          see |= near & node;
         }
-        return ok && (P.window == 0 || me.pos - pos < P.window || pos < P.sinks);
+        return see;
       };
 
       const bool active = (warp % 4) * 32 < rows;  // a warp without rows leaves its lanes as they are
-      const int scanners = min(128, (rows + 31) / 32 * 32);
-      // (a scale of 0 becomes the smallest one, so that a masked score stays infinite)
-      const float c = P.scale_log2 == 0.f ? 1.4e-45f : P.scale_log2;
-      const uint32_t hidden = __float_as_uint(c > 0.f ? -kInf : kInf);
+      // the sign of the scale is in the staged queries; a scale of 0 becomes the smallest one, so
+      // that a masked score stays infinite
+      const float c = P.scale_log2 == 0.f ? 1.4e-45f : fabsf(P.scale_log2);
+      constexpr uint32_t hidden = 0xff800000u;  // -inf
       float m = -kInf, l = 0.f;
       int jobs = 0;
       for (int t = TWO ? 0 : slot; t < tiles; t += TWO ? 1 : 2, ++jobs) {
@@ -424,128 +449,126 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
         s_phase ^= 1;
         __syncwarp();  // (lanes leave a wait apart; tensor-memory instructions want them together)
         fence_after();
-        if (active) {
-          const int step0 = (t_lo + t) * kUnit;
-          uint32_t partial = 0;  // chunks of 32 slots that not every row sees whole
-          uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
-          bool poisoned = false;  // the row sees a slot on a page out of range
+        const int step0 = (t_lo + t) * kUnit;
+        uint32_t partial = 0;  // chunks of 32 slots that not every row sees whole
+        uint32_t seen[4] = {~0u, ~0u, ~0u, ~0u};
+        bool poisoned = false;  // the row sees a slot on a page out of range
+        if (rows > 0) {
           const uint4 bads = *reinterpret_cast<const uint4*>(s_bad + (tile % kBadRing) * kCopyWarps);
           if ((bads.x | bads.y | bads.z | bads.w) != 0 || !whole_tile(step0)) {
             const uint32_t bad4[4] = {bads.x, bads.y, bads.z, bads.w};
 #pragma unroll
             for (int ch = 0; ch < 4; ++ch) {
-              if (bad4[ch] == 0 && whole_step(step0 + 2 * ch) && whole_step(step0 + 2 * ch + 1)) continue;
-              partial |= 1u << ch;
-              uint32_t see = 0;
-#pragma unroll 1
-              for (int e = 0; e < 32; ++e) {
-                const int step = step0 + 2 * ch + e / kStep;
-                if (step < R.steps && sees(R.slot(step) + e % kStep)) see |= 1u << e;
+              if (bad4[ch] != 0 || !whole_step(step0 + 2 * ch) || !whole_step(step0 + 2 * ch + 1)) {
+                partial |= 1u << ch;
+                if (active) seen[ch] = sees16(step0 + 2 * ch) | (sees16(step0 + 2 * ch + 1) << 16);
+                poisoned = poisoned || (seen[ch] & bad4[ch]) != 0;
               }
-              seen[ch] = see;
-              poisoned = poisoned || (see & bad4[ch]) != 0;
             }
           }
+        }
+        if (active) {
           __syncwarp();
-          auto load_scores = [&](int ch, uint32_t (&r)[32]) {
-            tmem_load(s_at + 32 * ch, r);
-            if ((partial >> ch) & 1u) {
+          auto mask_scores = [&](int ch, uint32_t (&r)[16]) {  // 16 scores: half of a chunk
+            if ((partial >> (ch >> 1)) & 1u) {
+              const uint32_t see = seen[ch >> 1] >> (16 * (ch & 1));
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = (seen[ch] >> e) & 1u ? r[e] : hidden;
+              for (int e = 0; e < 16; ++e) r[e] = (see >> e) & 1u ? r[e] : hidden;
             }
           };
-          uint32_t p[64];
-          float fresh = 0.f;
-          bool moved = m == -kInf;
-#pragma unroll 1
-          for (int pass = 0;; ++pass) {
-            if (__any_sync(0xffffffffu, moved)) {  // the reference moves to the row's maximum so far
-              float top = m;
+          uint32_t r[2][16];
+          float top = -kInf;
+          tmem_load(s_at, r[0]);
 #pragma unroll
-              for (int ch = 0; ch < 4; ++ch) {
-                uint32_t r[32];
-                load_scores(ch, r);
+          for (int ch = 0; ch < 8; ++ch) {
+            tmem_load_wait(r[ch & 1]);
+            if (ch < 7) tmem_load(s_at + 16 * (ch + 1), r[(ch + 1) & 1]);
+            mask_scores(ch, r[ch & 1]);
 #pragma unroll
-                for (int e = 0; e < 32; ++e) top = fmaxf(top, __uint_as_float(r[e]) * c);
-              }
-              const float alpha = m == top ? 1.f : ex2(m - (top == -kInf ? 0.f : top));
-              m = top;
-              l *= alpha;
-              if (jobs > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-#pragma unroll 1
-                for (int d = 0; d < D; d += 32) {
-                  uint32_t r[32];
-                  tmem_load(o_at + d, r);
-#pragma unroll
-                  for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * alpha);
-                  tmem_store(o_at + d, r);
-                }
-                tmem_store_wait();
-              }
-            }
-            const float base = m == -kInf ? 0.f : m;
-            float top = -kInf, sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch) {
-              uint32_t r[32];
-              load_scores(ch, r);
-#pragma unroll
-              for (int e = 0; e < 32; e += 2) {
-                const float x0 = fmaf(__uint_as_float(r[e]), c, -base), x1 = fmaf(__uint_as_float(r[e + 1]), c, -base);
-                top = fmaxf(top, fmaxf(x0, x1));
-                const float p0 = ex2(x0), p1 = ex2(x1);
-                sum[(e >> 1) & 1] += p0;
-                sum[2 + ((e >> 1) & 1)] += p1;
-                p[16 * ch + e / 2] = Half16<T>::pack(p0, p1);
-              }
-            }
-            fresh = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-            moved = top > kSlack;
-            // (after a move no score exceeds the reference: at most one more pass)
-            if (pass == 1 || !__any_sync(0xffffffffu, moved)) break;
+            for (int e = 0; e < 16; e += 2) top = max3(top, __uint_as_float(r[ch & 1][e]), __uint_as_float(r[ch & 1][e + 1]));
           }
-          if (poisoned) fresh = __int_as_float(0x7fffffff);
-          l += fresh;
-          if (partial) {
-            // 0 times a value that is not finite is not 0: where some row does not see a slot, such
-            // values are taken out of the staged tile; the rows that see them get them at the end
-            wait_for(v_full + tile % RING, (tile / RING) & 1, gave_up);
-            char* const vt = smem + Sh::kOffV + (tile % RING) * Sh::kTileBytes;
-            constexpr uint32_t em = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
-            bool found = false;
-            for (int f = row; f < kTile * (D / 8); f += scanners) {
-              const int r = f / (D / 8);
-              if (!((partial >> (r / 32)) & 1u)) continue;
-              uint4* const at = reinterpret_cast<uint4*>(vt + tile_offset<D>(r, f % (D / 8)));
+          top *= c;
+          if (__any_sync(0xffffffffu, top > m + kSlack)) {  // (also where m is still -inf)
+            top = fmaxf(m, top);
+            const float alpha = m == top ? 1.f : ex2(m - (top == -kInf ? 0.f : top));
+            m = top;
+            l *= alpha;
+            if (jobs > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll 1
+              for (int d = 0; d < D; d += 16) {
+                tmem_load(o_at + d, r[1]);
+                tmem_load_wait(r[1]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[1][e] = __float_as_uint(__uint_as_float(r[1][e]) * alpha);
+                tmem_store16(o_at + d, r[1]);
+              }
+            }
+          }
+          // the weights, 16 at a time; they overwrite scores that have been read: weights 16 ch ... are
+          // columns 8 ch ..., scores 16 ch ... columns 16 ch ...
+          const float base = m == -kInf ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          tmem_load(s_at, r[0]);
+#pragma unroll
+          for (int ch = 0; ch < 8; ++ch) {
+            tmem_load_wait(r[ch & 1]);
+            if (ch < 7) tmem_load(s_at + 16 * (ch + 1), r[(ch + 1) & 1]);
+            mask_scores(ch, r[ch & 1]);
+            uint32_t p[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float p0 = ex2(fmaf(__uint_as_float(r[ch & 1][e]), c, -base));
+              const float p1 = ex2(fmaf(__uint_as_float(r[ch & 1][e + 1]), c, -base));
+              sum[(e >> 1) & 1] += p0;
+              sum[2 + ((e >> 1) & 1)] += p1;
+              p[e / 2] = Half16<T>::pack(p0, p1);
+            }
+            tmem_store8(s_at + 8 * ch, p);
+          }
+          l += poisoned ? __int_as_float(0x7fffffff) : (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+        if (partial) {
+          // 0 times a value that is not finite is not 0: where some row does not see a slot, such
+          // values are taken out of the staged tile; the rows that see them get them at the end
+          wait_for(v_full + tile % RING, (tile / RING) & 1, gave_up);
+          char* const vt = smem + Sh::kOffV + (tile % RING) * Sh::kTileBytes;
+          constexpr uint32_t em = std::is_same<T, __half>::value ? 0x7c00u : 0x7f80u;
+          bool found = false;
+#pragma unroll 1
+          for (int ch = 0; ch < 4; ++ch) {
+            if (!((partial >> ch) & 1u)) continue;
+#pragma unroll 4
+            for (int f = row; f < 32 * (D / 8); f += 128) {
+              uint4* const at = reinterpret_cast<uint4*>(vt + tile_offset<D>(32 * ch + f / (D / 8), f % (D / 8)));
               uint32_t x[4] = {at->x, at->y, at->z, at->w};
               bool here = false;
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if ((x[e] & em) == em) { x[e] &= 0xffff0000u; here = true; }
-                if (((x[e] >> 16) & em) == em) { x[e] &= 0xffffu; here = true; }
-              }
+              for (int e = 0; e < 4; ++e) here = here || (x[e] & em) == em || (x[e] & (em << 16)) == em << 16;
               if (here) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  if ((x[e] & em) == em) x[e] &= 0xffff0000u;
+                  if ((x[e] & (em << 16)) == em << 16) x[e] &= 0xffffu;
+                }
                 *at = make_uint4(x[0], x[1], x[2], x[3]);
                 found = true;
               }
             }
-            if (found) {
-              *s_odd = 1;
-              fence_proxy_async_smem();
-            }
+          }
+          if (found) {
+            *s_odd = 1;
+            fence_proxy_async_smem();
           }
           __syncwarp();
-          tmem_store(s_at, p);
-          tmem_store(s_at + 32, p + 32);
-          tmem_store_wait();
         }
+        if (active) tmem_store_wait();
         fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full + slot);
       }
 
       // ---- the item's rows, or the part of them that this segment holds
-      const bool begins = w.u == w.item, ends = w.seg_end() == w.item + w.units;
+      const bool whole_item = it.begins && it.ends;
       const int other_jobs = TWO ? 0 : (slot == 0 ? tiles / 2 : (tiles + 1) / 2);
       float scale_own = 1.f, scale_other = 0.f;
       if (jobs > 0) {
@@ -561,54 +584,53 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
         const float top = fmaxf(m, other.x), base = top == -kInf ? 0.f : top;
         scale_own = ex2(m - base);
         scale_other = ex2(other.x - base);
-        l = slot == 0 ? l * scale_own + other.y * scale_other : other.y * scale_other + l * scale_own;
+        l = l * scale_own + other.y * scale_other;
         m = top;
       }
       fence_after();
-      const int i = me.i;
-      const bool mine = row < rows && i < P.n;
-      const int head = w.h * P.G + (row0 + row) % P.G;
-      const int64_t at = (static_cast<int64_t>(w.b) * P.n + i) * P.Hq + head;
-      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (begins ? 1 : 0)) * MR + (TWO ? slot * 128 : 0) + row;
-      const bool none = l == 0.f || i >= S.nq;
+      __syncwarp();
+      const bool mine = row < rows && me < P.n;
+      const int head = it.h * P.G + (row0 + row) % P.G;
+      const int64_t at = (static_cast<int64_t>(it.b) * P.n + me) * P.Hq + head;
+      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (it.begins ? 1 : 0)) * MR + (TWO ? slot * 128 : 0) + row;
+      const bool none = l == 0.f || me >= it.nq;
       const float inv = none ? 0.f : pg.v_scale / l;
       const bool odd = *s_odd != 0;
       if (active) {
         constexpr int COLS = TWO ? D : D / 2;
 #pragma unroll 1
-        for (int d0 = 0; d0 < COLS; d0 += 32) {
+        for (int d0 = 0; d0 < COLS; d0 += 16) {
           const int d = (TWO ? 0 : slot * COLS) + d0;
+          float acc[16];
+          uint32_t r[16];
           __syncwarp();
-          float acc[32];
 #pragma unroll
-          for (int e = 0; e < 32; ++e) acc[e] = 0.f;
+          for (int e = 0; e < 16; ++e) acc[e] = 0.f;
           if (jobs > 0) {
-            uint32_t r[32];
             tmem_load(o_at + d, r);
+            tmem_load_wait(r);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) acc[e] = __uint_as_float(r[e]) * scale_own;
+            for (int e = 0; e < 16; ++e) acc[e] = __uint_as_float(r[e]) * scale_own;
           }
           if (!TWO && other_jobs > 0) {
-            uint32_t r[32];
             tmem_load(o_at + (slot == 0 ? 128 : -128) + d, r);
+            tmem_load_wait(r);
 #pragma unroll
-            for (int e = 0; e < 32; ++e) acc[e] = fmaf(__uint_as_float(r[e]), scale_other, acc[e]);
+            for (int e = 0; e < 16; ++e) acc[e] = fmaf(__uint_as_float(r[e]), scale_other, acc[e]);
           }
           if (odd && mine) {  // rare: values that are not finite, for the rows that see them
-            const int32_t* table = pg.table + static_cast<int64_t>(w.b) * pg.max_pages;
+            const int32_t* table = pg.table + static_cast<int64_t>(it.b) * pg.max_pages;
 #pragma unroll 1
-            for (int ch = t_lo * 4; ch < (t_lo + tiles) * 4; ++ch) {
-              if (whole_step(2 * ch) && whole_step(2 * ch + 1)) continue;
-#pragma unroll 1
-              for (int e = 0; e < 32; ++e) {
-                const int step = 2 * ch + e / kStep, s = R.slot(step) + e % kStep;
-                if (step >= R.steps || s >= R.end || !sees(s)) continue;
+            for (int step = t_lo * kUnit; step < (t_lo + tiles) * kUnit; ++step) {
+              if (whole_step(step & ~1) && whole_step(step | 1)) continue;
+              for (uint32_t see = sees16(step); see != 0; see &= see - 1) {
+                const int s = R.slot(step) + __ffs(see) - 1;
                 const int page = __ldg(table + s / pg.page_size);
                 if (static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages)) continue;
                 const T* v = reinterpret_cast<const T*>(pg.v + page * pg.page_stride + (s % pg.page_size) * pg.slot_stride +
-                                                        w.h * pg.head_stride) + d;
+                                                        it.h * pg.head_stride) + d;
 #pragma unroll
-                for (int x = 0; x < 32; ++x) {
+                for (int x = 0; x < 16; ++x) {
                   const float f = static_cast<float>(v[x]);
                   if (!(fabsf(f) < kInf)) acc[x] += f;
                 }
@@ -616,34 +638,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) attend_tc_kernel(const AttendPa
             }
           }
           if (!mine) continue;
-          if (begins && ends) {
-            uint32_t out[16];
+          if (whole_item) {
+            uint32_t out[8];
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
+            for (int e = 0; e < 8; ++e) {
               out[e] = none ? 0u : Half16<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-              if (!S.ok) out[e] = 0x7fff7fffu;
+              if (!it.ok) out[e] = 0x7fff7fffu;
             }
             uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(P.out) + at * D + d);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_uint4(out[4 * e], out[4 * e + 1], out[4 * e + 2], out[4 * e + 3]);
+            dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+            dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
           } else {
             float4* dst = reinterpret_cast<float4*>(P.part_o + part * D + d);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) dst[e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
           }
         }
         if (mine && (TWO || slot == 0)) {
-          if (begins && ends) {
-            if (P.lse) P.lse[at] = !S.ok ? __int_as_float(0x7fffffff) : none ? -kInf : m * kLn2 + logf(l);
+          if (whole_item) {
+            if (P.lse) P.lse[at] = !it.ok ? __int_as_float(0x7fffffff) : none ? -kInf : m * kLn2 + logf(l);
           } else {
             P.part_ml[part] = make_float2(m, l);
           }
         }
       }
-      if (begins && !ends && tid == 0) P.split[blockIdx.x] = w.split(share);
       tile_base += tiles;
       fence_before();
-    } while (w.next());
+    }
   }
 
   fence_before();
