@@ -476,7 +476,7 @@ int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B
  * The workspace (specdec_attend_workspace_bytes) follows the rules at the top.  The split of the
  * work follows the lengths on the device: the host reads none of them.
  * window, sinks >= 0 (window 0: no window, sinks then has no effect); q_heads a multiple of
- * kv_heads; n * (q_heads / kv_heads) < 2^24; B < 2^24. */
+ * kv_heads, at most 65535 times; n * (q_heads / kv_heads) < 2^24; B < 2^24. */
 size_t specdec_attend_workspace_bytes(int B, int n, int q_heads, int kv_heads, int head_dim);
 
 int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype, const specdec_kv_pages* pages,
@@ -583,8 +583,8 @@ int specdec_verify_chain_noalloc(const void* logits, specdec_dtype ldt, const fl
  *   SPECDEC_HOOK_QUEUE_WAIT_US     >= 1: the left-to-right kernel's bound on waits for
  *                                  queued work, in microseconds (0: one second)
  *   SPECDEC_HOOK_ATTEND_KERNEL     1 or 2: attention over pages takes the kernel on warp-level
- *                                  matrix instructions, or the tensor-memory kernel (16-bit
- *                                  pages), whatever the number of rows
+ *                                  matrix instructions, or the tensor-memory kernel, whatever
+ *                                  the number of rows
  * Returns SPECDEC_OK, or SPECDEC_ERR_INVALID_ARG for an unknown hook or value.
  */
 #define SPECDEC_HOOK_CHAIN_ALL_ROWS 0

@@ -128,14 +128,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
     // the table entry of this lane's slot of step t (lanes 16..31 repeat 0..15)
     auto entry = [&](int t) {
       const int s = R.slot(t) + (lane & 15);
-      return t < t_hi && s < R.end ? __ldg(table + s / pg.page_size) : 0;
+      return t < t_hi && s < R.end ? __ldg(table + page_of(pg, s)) : 0;
     };
     auto prefetch = [&](int t, int stage, int page) {
       if (t < t_hi) {
         const int s = R.slot(t) + (lane & 15);
         const bool bad = s < R.end && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
         const bool there = s < R.end && !bad;
-        const int in_page = s % pg.page_size;
+        const int in_page = s - page_of(pg, s) * pg.page_size;
         const int64_t off = there ? page * pg.page_stride + in_page * pg.slot_stride : 0;
         const uint32_t bads = __ballot_sync(0xffffffffu, bad) & 0xffffu;
         const uint32_t present = __ballot_sync(0xffffffffu, there);
@@ -179,8 +179,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
       if constexpr (FOUR && !std::is_same<T, __half>::value) {
         float a = 0.f;
         if (r < rows) {
-          const T* src = static_cast<const T*>(P.q) + b * P.q_sb + ((row0 + r) / P.G) * P.q_st +
-                         (h * P.G + (row0 + r) % P.G) * P.q_sh;
+          const T* src = static_cast<const T*>(P.q) + b * P.q_sb + query_of(P, row0 + r) * P.q_st +
+                         (h * P.G + (row0 + r) - query_of(P, row0 + r) * P.G) * P.q_sh;
           for (int d = 2 * lane; d < D; d += 64) {
             const float2 f = Half16<T>::to_f32(*reinterpret_cast<const uint32_t*>(src + d));
             a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
@@ -207,8 +207,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
         const int d = FOUR ? (D / 4) * fc + 4 * t + (e >> 1) * 2 : 16 * t + 2 * fc + (e >> 1) * 8;
         uint32_t w = 0;
         if (r < rows) {
-          const T* src = static_cast<const T*>(P.q) + b * P.q_sb + ((row0 + r) / P.G) * P.q_st +
-                         (h * P.G + (row0 + r) % P.G) * P.q_sh;
+          const T* src = static_cast<const T*>(P.q) + b * P.q_sb + query_of(P, row0 + r) * P.q_st +
+                         (h * P.G + (row0 + r) - query_of(P, row0 + r) * P.G) * P.q_sh;
           w = *reinterpret_cast<const uint32_t*>(src + d);
           if constexpr (FOUR && !std::is_same<T, __half>::value) {
             const float2 v = Half16<T>::to_f32(w);
@@ -230,7 +230,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
 #pragma unroll
     for (int e = 0; e < 2 * MT; ++e) {
       const int r = 16 * (wr * MT + e / 2) + g + (e % 2) * 8;
-      q_i[e] = (row0 + r) / P.G;
+      q_i[e] = query_of(P, row0 + r);
       q_pos[e] = S.first + (P.depth && q_i[e] < P.n ? node_depth(P, q_i[e]) : q_i[e]);
       sc[e] = P.scale_log2 * s_rowscale[r];
       row_m[e] = -kInf;
@@ -247,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
 #pragma unroll
       for (int t = 0; t < KT; ++t) qf[t] = s_q[t * 32];
     }
-    const int i0 = row0 / P.G, i1 = min((row0 + rows - 1) / P.G, S.nq - 1);
+    const int i0 = query_of(P, row0), i1 = min(query_of(P, row0 + rows - 1), S.nq - 1);
     const bool tree = P.tree_mask != nullptr;
     auto sees = [&](int e, int s) {
       const int j = s - S.first;
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_kernel(const AttendParams 
         acc.x += a * x.x; acc.y += a * x.y; acc.z += a * x.z; acc.w += a * x.w;
       }
       if (begins && ends) {
-        const int i = (row0 + r) / P.G, head = h * P.G + (row0 + r) % P.G;
+        const int i = query_of(P, row0 + r), head = h * P.G + row0 + r - i * P.G;
         const int64_t at = (static_cast<int64_t>(b) * P.n + i) * P.Hq + head;
         float inv = l == 0.f ? 0.f : pg.v_scale / l, lse = m * kLn2 + logf(l);
         if (l == 0.f || i >= S.nq) { lse = -kInf; inv = 0.f; }
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const Atte
         acc[0] += a * x.x; acc[1] += a * x.y;
       }
     }
-    const int i = (row0 + r) / P.G, head = h * P.G + (row0 + r) % P.G;
+    const int i = query_of(P, row0 + r), head = h * P.G + row0 + r - i * P.G;
     const int64_t o_at = (static_cast<int64_t>(b) * P.n + i) * P.Hq + head;
     const bool none = l == 0.f || i >= S.nq;
     const float inv = none ? 0.f : pg.v_scale / l;
@@ -730,7 +730,7 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   const int64_t rows = static_cast<int64_t>(P.n) * P.G;
   const bool four = format == SPECDEC_KV4;
   const int hook = test_hook(SPECDEC_HOOK_ATTEND_KERNEL);
-  const bool tc = !four && (hook == 0 ? rows > 64 : hook == 2);
+  const bool tc = hook == 0 ? rows > 64 : hook == 2;
   const int mr = tc ? attend_tc_rows(rows) : row_tile(rows);
   P.row_tiles = static_cast<int>((rows + mr - 1) / mr);
   P.ctas = attend_sms();
@@ -745,7 +745,8 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   ws += round256(static_cast<size_t>(kMaxCtas) * 2 * mr * sizeof(float2));
   P.part_o = reinterpret_cast<float*>(ws);
   if (tc)
-    if (cudaError_t e = launch_attend_tc(P, dt, mr, stream); e != cudaSuccess) return e;
+    if (cudaError_t e = four ? launch_attend_tc4(P, dt, mr, stream) : launch_attend_tc(P, dt, mr, stream); e != cudaSuccess)
+      return e;
   if (!tc)
     if (cudaError_t e = dt == SPECDEC_BF16 ? launch_typed<__nv_bfloat16>(P, mr, four, stream)
                                            : launch_typed<__half>(P, mr, four, stream);

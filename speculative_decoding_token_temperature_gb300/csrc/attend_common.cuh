@@ -28,6 +28,11 @@ __device__ __forceinline__ void copy_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// A row's query: row / G as a product (exact for rows below 2^24 and G below 2^16).
+__device__ __forceinline__ int query_of(const AttendParams& P, int row) {
+  return static_cast<int>((static_cast<uint64_t>(row) * P.g_magic) >> 40);
+}
+
 // ---- the work split ---------------------------------------------------------------------
 
 // The visible slots of an item as steps of 16: `sink_steps` from slot 0, then from step
@@ -41,7 +46,7 @@ struct Range {
 };
 __device__ __forceinline__ Range item_range(const AttendParams& P, const SeqLen& S, int row0, int rows) {
   Range r{0, 0, 0, 0, 0, 0};
-  const int i0 = row0 / P.G, i1 = min((row0 + rows - 1) / P.G, S.nq - 1);
+  const int i0 = query_of(P, row0), i1 = min(query_of(P, row0 + rows - 1), S.nq - 1);
   if (!S.ok || i0 > i1) return r;
   const bool tree = P.tree_mask != nullptr;
   r.end = tree ? S.len : S.first + i1 + 1;
@@ -108,8 +113,13 @@ __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots
     total += sh[w];
   }
   Share s;
-  s.quota = total / gridDim.x;
-  s.extra = total % gridDim.x;
+  if (total >> 32 == 0) {
+    s.quota = static_cast<uint32_t>(total) / gridDim.x;
+    s.extra = static_cast<uint32_t>(total) % gridDim.x;
+  } else {
+    s.quota = total / gridDim.x;
+    s.extra = total % gridDim.x;
+  }
   const int64_t cta = blockIdx.x;
   s.u = cta * s.quota + min(cta, s.extra);
   s.end = s.u + s.quota + (cta < s.extra ? 1 : 0);

@@ -1,0 +1,876 @@
+// Attention over pages on the tensor cores with accumulators in tensor memory.
+//
+// The formula, the items and the split of the work are those of attend.cu.  A tile is 128 query
+// rows of one key head by 128 slots:
+//   S = Q K^T  (tcgen05.mma, Q and K from shared memory)  -> 128 columns of tensor memory
+//   P = 2^(c S - m)                                       -> back to tensor memory, 16 bits
+//   O += P V   (tcgen05.mma, P from tensor memory)        -> D columns of tensor memory
+// Two such streams ("slots" 0 and 1 of the CTA) take turns, so that one's exponentials run while
+// the other's products do: with more than 128 rows per key head they are two row tiles that share
+// every staged K and V tile; with fewer, both hold the same rows and take every other tile, and
+// their results join at the end.
+//
+// A row's reference m moves only when a tile exceeds it by more than 2^8: the weights then stay
+// below 256, where 16-bit rounding is relative and as good as below 1, and the accumulator is
+// rescaled once or twice per item instead of once per tile.  The sum l takes the unrounded weights,
+// in fp32.  Two threads hold a row, 64 columns each: the chain scores -> weights -> products of a
+// slot is what bounds a short tile, and this halves its longest link.
+//
+// Warps 0-15: rows (slot = warp / 8, columns = warp / 4 % 2, lanes = warp % 4).  Then the warps that
+// bring K and V: of 16-bit pages, 4 that copy rows asynchronously, 16 bytes at a time; of 4-bit
+// pages, 8 that read codes and write their fp16 values (exact: at most 6 significant bits).
+// Either way the tiles are 128-byte-swizzled and gathered row by row, so pages may have any size
+// and stride.  Then one warp whose first thread issues the matrix instructions, one that walks
+// the items ahead of everybody, and two that bring query rows.  The roles meet at mbarriers; every
+// wait is bounded.  Where one runs out, the walk publishes no further item, every role finishes the
+// item it is in (without waiting) and leaves; the row warps, which also meet at thread barriers, agree
+// at each item whether they go on.  The CTA reports it.
+#pragma once
+
+#include "attend_common.cuh"
+
+namespace specdec {
+
+namespace tc {
+
+constexpr int kRowWarps = 16;
+constexpr int kTile = kUnit * kStep;  // 128 slots
+constexpr int kBadRing = 8;           // tiles whose out-of-range slots are remembered
+constexpr int kItems = 4;             // items the walk may be ahead
+constexpr float kSlack = 8.f;         // log2 of how far a weight may exceed 1
+
+// What the roles need to know of an item, for the CTA's segment of it.
+struct Item {
+  int b, h, row0, rows;     // rows row0 .. row0 + rows - 1 of the key head
+  int t_lo, tiles;          // this segment's tiles
+  int begins, ends, last;   // of the item; last: the CTA's last item
+  int nq, first, ok;
+  int sink_steps, first_step, steps, end, lo, sinks;
+  int whole_lo[2], whole_hi[2];  // tiles that every row of a slot sees whole
+};
+
+template <int D, bool TWO, bool FOUR>
+struct Shape {
+  static constexpr int MR = TWO ? 256 : 128;
+  static constexpr int kCopyWarps = FOUR ? 8 : 4;
+  static constexpr int kMma = kRowWarps + kCopyWarps, kWalker = kMma + 1, kQuery = kMma + 2;
+  static constexpr int kThreads = 32 * (kRowWarps + kCopyWarps + 4);
+  static constexpr int kTileBytes = kTile * D * 2;
+  static constexpr int RK = D == 64 ? 4 : (TWO ? 2 : 3), RV = D == 64 ? 4 : 2;  // K tiles and V tiles staged
+  static constexpr int kOffK = (TWO ? 2 : 1) * kTileBytes;
+  static constexpr int kOffV = kOffK + RK * kTileBytes;
+  static constexpr int kOffMl = kOffV + RV * kTileBytes;      // [2][2][128] (m, l) of slots and halves
+  static constexpr int kOffQScale = kOffMl + 4 * 128 * 8;       // [2][MR] scales of query rows (4-bit pages)
+  static constexpr int kOffItem = kOffQScale + (FOUR ? 2 * MR * 4 : 0);
+  static constexpr int kOffScan = kOffItem + kItems * sizeof(Item);
+  static constexpr int kOffBad = (kOffScan + (kThreads / 32 + 2) * 8 + 15) / 16 * 16;
+  static constexpr int kOffBar = kOffBad + kBadRing * 16;
+  static constexpr int kBars = 2 * (RK + RV) + 2 + 2 + 2 + 2 + 2 * kItems + 1;
+  static constexpr int kOffMisc = kOffBar + kBars * 8;
+  static constexpr int kBytes = kOffMisc + 16;
+};
+
+// ---- tcgen05 -----------------------------------------------------------------------------
+
+// Shared-memory matrix descriptors: 128-byte swizzle.  The low word holds the address and the
+// leading stride, the high one the stride between groups of 8 rows (1024 bytes).
+__device__ __forceinline__ constexpr uint32_t desc_low(uint32_t addr, uint32_t lead) { return (addr >> 4) | ((lead >> 4) << 16); }
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+// Instruction descriptor: fp32 accumulator, 16-bit operands, M = 128.
+template <typename M>
+__device__ __forceinline__ constexpr uint32_t instr_desc(int n, bool b_mn_major) {
+  const uint32_t type = std::is_same<M, __nv_bfloat16>::value ? 1u : 0u;
+  return (1u << 4) | (type << 7) | (type << 10) | (b_mn_major ? 1u << 16 : 0u) | (static_cast<uint32_t>(n >> 3) << 17) |
+         ((128u >> 4) << 24);
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 da, db;\nmov.b64 da, {%1, %5};\nmov.b64 db, {%2, %5};\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate),
+      "r"(kDescHigh)
+      : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 db;\nmov.b64 db, {%2, %5};\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate),
+      "r"(kDescHigh)
+      : "memory");
+}
+// The barrier is arrived at when every matrix instruction issued so far is complete.
+__device__ __forceinline__ void mma_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+
+// 16 columns of this warp's 32 lanes.  The values are there after tmem_load_wait, which takes
+// them so that no use moves above it.
+__device__ __forceinline__ void tmem_load(uint32_t addr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_load_wait(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])::"memory");
+}
+__device__ __forceinline__ void tmem_store8(uint32_t addr, const uint32_t (&r)[8]) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(addr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void tmem_store16(uint32_t addr, const uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_store_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// A bounded wait: gives up after kMaxWaitNs, and at once when the CTA has given up elsewhere.
+__device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatile int* gave_up) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*gave_up) return false;
+    if (global_timer_ns() - t0 > kMaxWaitNs) {
+      *gave_up = 1;
+      return false;
+    }
+  }
+  return true;
+}
+// Whether all row threads say yes (the barrier of all of them).
+__device__ __forceinline__ bool rows_all(bool mine) {
+  uint32_t all;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.and.pred p, 1, 512, q;\nselp.u32 %0, 1, 0, p;\n}"
+               : "=r"(all) : "r"(mine ? 1u : 0u) : "memory");
+  return all != 0;
+}
+// Whether either warp of a pair (64 threads) says yes.
+__device__ __forceinline__ bool pair_any(int barrier, bool mine) {
+  uint32_t any;
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %2, 0;\nbarrier.cta.red.or.pred p, %1, 64, q;\nselp.u32 %0, 1, 0, p;\n}"
+               : "=r"(any) : "r"(barrier), "r"(mine ? 1u : 0u) : "memory");
+  return any != 0;
+}
+
+// Where the 16-byte piece `piece` of row `row` of a tile of 128 rows of D values lies: blocks
+// of 64 values, rows of 128 bytes, pieces swizzled by the row.
+__device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
+  return (piece >> 3) * (kTile * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float y;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+  return y;
+}
+// Bits lo..hi-1 of a step's 16 slots, both clamped to 0..16.
+__device__ __forceinline__ uint32_t bits16(int lo, int hi) {
+  lo = min(max(lo, 0), kStep);
+  hi = min(max(hi, 0), kStep);
+  return hi > lo ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
+}
+
+template <typename T, int D, bool TWO, bool FOUR>
+__global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_kernel(const AttendParams P) {
+  using Sh = Shape<D, TWO, FOUR>;
+  using M = typename std::conditional<FOUR, __half, T>::type;  // the matrix instructions' type
+  constexpr int MR = Sh::MR, RK = Sh::RK, RV = Sh::RV, KT = D / 16, THREADS = Sh::kThreads;
+  extern __shared__ __align__(1024) char smem[];
+  const Pages& pg = P.pages;
+  const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  uint32_t* const s_bad = reinterpret_cast<uint32_t*>(smem + Sh::kOffBad);
+  uint64_t* const k_full = reinterpret_cast<uint64_t*>(smem + Sh::kOffBar);
+  uint64_t* const k_empty = k_full + RK;
+  uint64_t* const v_full = k_empty + RK;
+  uint64_t* const v_empty = v_full + RV;
+  uint64_t* const s_full = v_empty + RV;  // [2]
+  uint64_t* const p_full = s_full + 2;      // [2]
+  uint64_t* const o_full = p_full + 2;      // [2]
+  uint64_t* const q_full = o_full + 2;
+  uint64_t* const q_empty = q_full + 1;
+  uint64_t* const it_full = q_empty + 1;    // [kItems]
+  uint64_t* const it_empty = it_full + kItems;
+  uint64_t* const done = it_empty + kItems;
+  uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(smem + Sh::kOffMisc);
+  volatile int* const gave_up = reinterpret_cast<int*>(smem + Sh::kOffMisc) + 1;
+  volatile int* const s_odd = reinterpret_cast<int*>(smem + Sh::kOffMisc) + 2;  // a masked value that is not finite
+  Item* const items = reinterpret_cast<Item*>(smem + Sh::kOffItem);
+  float* const s_qscale = reinterpret_cast<float*>(smem + Sh::kOffQScale);
+
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  if (tid == 0) {
+    // copied tiles: every copy lane's copies have landed, and a warp's part of s_bad is written
+    for (int r = 0; r < RK; ++r) {
+      mbar_init(k_full + r, FOUR ? Sh::kCopyWarps : kTile + Sh::kCopyWarps);
+      mbar_init(k_empty + r, 1);
+    }
+    for (int r = 0; r < RV; ++r) {
+      mbar_init(v_full + r, FOUR ? Sh::kCopyWarps : kTile);
+      mbar_init(v_empty + r, 1);
+    }
+    for (int s = 0; s < 2; ++s) {
+      mbar_init(s_full + s, 1);
+      mbar_init(p_full + s, kRowWarps / 2);
+      mbar_init(o_full + s, 1);
+    }
+    mbar_init(q_full, 2);
+    mbar_init(q_empty, 1);
+    for (int k = 0; k < kItems; ++k) {
+      mbar_init(it_full + k, 1);
+      mbar_init(it_empty + k, kRowWarps + Sh::kCopyWarps + 1 + 2);
+    }
+    mbar_init(done, 1);
+    mbar_fence_init();
+    *gave_up = 0;
+    *s_odd = 0;
+    P.split[blockIdx.x] = make_int4(0, 0, 0, 0);
+  }
+  const int64_t slots = static_cast<int64_t>(pg.max_pages) * pg.page_size;
+  const Share share = scan_units<MR, THREADS>(P, slots, reinterpret_cast<int64_t*>(smem + Sh::kOffScan));
+  if (share.u >= share.end) {  // nothing for this CTA
+    if (tid == 0) P.gave_up[blockIdx.x] = 0;
+    return;
+  }
+  if (warp == Sh::kMma) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(s_tmem)) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+  }
+  fence_before();
+  __syncthreads();
+  fence_after();
+  const uint32_t tmem = *s_tmem;  // columns: S of slots 0 and 1, then O of slots 0 and 1
+
+  if (warp == Sh::kWalker) {
+    // ---- the items, ahead of the others
+    if (lane == 0) {
+      Walk<MR> w(P, slots, share);
+      for (int n = 0;; ++n) {
+        if (!wait_for(it_empty + n % kItems, ((n / kItems) & 1) ^ 1, gave_up)) break;
+        volatile Item& it = items[n % kItems];
+        const int row0 = w.rt * MR, rows = tile_rows<MR>(P, w.rt);
+        const Range R = item_range(P, w.S, row0, rows);
+        const int t_lo = static_cast<int>(w.u - w.item);
+        const int t_hi = min(static_cast<int>(w.seg_end() - w.item), (R.steps + kUnit - 1) / kUnit);
+        const bool begins = w.u == w.item, ends = w.seg_end() == w.item + w.units;
+        it.b = w.b;
+        it.h = w.h;
+        it.row0 = row0;
+        it.rows = rows;
+        it.t_lo = t_lo;
+        it.tiles = max(0, t_hi - t_lo);
+        it.begins = begins;
+        it.ends = ends;
+        it.nq = w.S.nq;
+        it.first = w.S.first;
+        it.ok = w.S.ok;
+        it.sink_steps = R.sink_steps;
+        it.first_step = R.first_step;
+        it.steps = R.steps;
+        it.end = R.end;
+        it.lo = R.lo;
+        it.sinks = R.sinks;
+        for (int slot = 0; slot < 2; ++slot) {
+          // tile t (past the sinks) is slots 128 t - 16 off ...: it ends before `limit`, and its first slot
+          // is inside the last row's window
+          const int r_lo = row0 + (TWO ? slot * 128 : 0), r_hi = min(row0 + rows, r_lo + 128) - 1;
+          const bool tree = P.tree_mask != nullptr;
+          const int limit = min(R.end, tree ? w.S.first : w.S.first + query_of(P, min(r_lo, row0 + rows - 1)) + 1);
+          const int last = tree ? w.S.first + P.n - 1 : w.S.first + min(query_of(P, max(r_hi, 0)), w.S.nq - 1);
+          const int from = P.window > 0 ? max(0, last - (P.window - 1)) : 0;
+          const int off = R.sink_steps - R.first_step;
+          const int lo = max(R.sink_steps, (from + kStep - 1) / kStep + off);
+          const int hi = limit / kStep + off;  // steps before hi end before the limit
+          it.whole_lo[slot] = (lo + kUnit - 1) / kUnit;
+          it.whole_hi[slot] = hi < 0 ? 0 : hi / kUnit;
+        }
+        if (begins && !ends) P.split[blockIdx.x] = w.split(share);
+        const bool more = w.next();
+        it.last = more ? 0 : 1;
+        mbar_arrive(it_full + n % kItems);
+        if (!more) break;
+      }
+    }
+    __syncwarp();
+  } else if (warp >= kRowWarps && warp < kRowWarps + Sh::kCopyWarps) {
+    // ---- K and V
+    const int cw = warp - kRowWarps;
+    int tile = 0;
+    for (int n = 0;; ++n) {
+      if (!__all_sync(0xffffffffu, wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up))) break;
+      const Item it = items[n % kItems];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(it_empty + n % kItems);
+      Range R;
+      R.sink_steps = it.sink_steps;
+      R.first_step = it.first_step;
+      const int t_lo = it.t_lo, t_hi = it.t_lo + it.tiles;
+      const int32_t* table = pg.table + static_cast<int64_t>(it.b) * pg.max_pages;
+      const char* const k_head = pg.k + it.h * pg.head_stride;
+      const char* const v_head = pg.v + it.h * pg.head_stride;
+      // this lane's slot of a tile: lane l of 4 copy warps slot 32 c + l, of 8 warps slot 16 c + l % 16
+      const int step_in_tile = FOUR ? cw : cw * 2 + lane / kStep;
+      auto slot_of = [&](int t) { return R.slot(t * kUnit + step_in_tile) + lane % kStep; };
+      auto wanted = [&](int t, int s) {  // a slot that some query of the item sees
+        return t < t_hi && t * kUnit + step_in_tile < it.steps && s < it.end && (s >= it.lo || s < it.sinks);
+      };
+      auto entry = [&](int t) {
+        const int s = slot_of(t);
+        return wanted(t, s) ? __ldg(table + page_of(pg, s)) : 0;
+      };
+      if constexpr (!FOUR) {
+        int page = entry(t_lo);
+        for (int t = t_lo; t < t_hi; ++t, ++tile) {
+          const int s = slot_of(t);
+          const bool want = wanted(t, s);
+          const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
+          const int64_t off = want && !bad ? page * pg.page_stride + (s - page_of(pg, s) * pg.page_size) * pg.slot_stride : 0;
+          page = entry(t + 1);
+          const uint32_t present = __ballot_sync(0xffffffffu, want && !bad), bads = __ballot_sync(0xffffffffu, bad);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int stage = tile % (kv ? RV : RK);
+            const uint32_t parity = ((tile / (kv ? RV : RK)) & 1) ^ 1;  // the first round of a fresh barrier passes
+            wait_for((kv ? v_empty : k_empty) + stage, parity, gave_up);
+            __syncwarp();
+            if (kv == 0 && lane == 0) {
+              s_bad[(tile % kBadRing) * 4 + cw] = bads;
+              mbar_arrive(k_full + stage);
+            }
+            const char* const head = kv ? v_head : k_head;
+            const uint32_t dst = smem_addr(smem + (kv ? Sh::kOffV : Sh::kOffK) + stage * Sh::kTileBytes);
+            constexpr int CH = D / 8, RPI = 32 / CH;  // 16-byte pieces of a row, rows at a time
+#pragma unroll 8
+            for (int j = 0; j < 32 / RPI; ++j) {
+              const int row = j * RPI + lane / CH, piece = lane % CH;
+              const int64_t o = __shfl_sync(0xffffffffu, off, row);
+              copy_async<16>(dst + tile_offset(cw * 32 + row, piece), head + o + piece * 16, (present >> row) & 1u);
+            }
+            // the barrier hears of it when this lane's copies so far have landed
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr((kv ? v_full : k_full) + stage)) : "memory");
+          }
+        }
+      } else {
+        // lane l: half l / 16 of slot 16 c + l % 16, D/2 values: D/16 words of codes and D/32 scales
+        constexpr int W = D / 16, G2 = D / 64;
+        const int half = lane / 16;
+        const char* const ks_head = pg.k_scales + it.h * pg.scale_head_stride;
+        const char* const vs_head = pg.v_scales + it.h * pg.scale_head_stride;
+        uint4 code[2][W / 4];
+        uint32_t scale[2];
+        uint32_t bads = 0;
+        auto load = [&](int t, int page) {
+          const int s = slot_of(t);
+          const bool want = wanted(t, s);
+          const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
+          bads = __ballot_sync(0xffffffffu, bad) & 0xffffu;
+          const int in_page = s - page_of(pg, s) * pg.page_size;
+          const int64_t off = page * pg.page_stride + in_page * pg.slot_stride + half * (W * 4);
+          const int64_t soff = page * pg.scale_page_stride + in_page * pg.scale_slot_stride + half * (2 * G2);
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+#pragma unroll
+            for (int x = 0; x < W / 4; ++x)
+              code[kv][x] = want && !bad ? __ldg(reinterpret_cast<const uint4*>((kv ? v_head : k_head) + off) + x) : make_uint4(0, 0, 0, 0);
+            const char* const sp = (kv ? vs_head : ks_head) + soff;
+            scale[kv] = !(want && !bad) ? 0u : G2 == 2 ? __ldg(reinterpret_cast<const uint32_t*>(sp)) : __ldg(reinterpret_cast<const uint16_t*>(sp));
+          }
+        };
+        int page = entry(t_lo);
+        if (t_lo < t_hi) {
+          load(t_lo, page);
+          page = entry(t_lo + 1);
+        }
+        for (int t = t_lo; t < t_hi; ++t, ++tile) {
+          const uint32_t bads_now = bads;
+          uint4 now[2][W / 4];
+          uint32_t scale_now[2] = {scale[0], scale[1]};
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv)
+#pragma unroll
+            for (int x = 0; x < W / 4; ++x) now[kv][x] = code[kv][x];
+          if (t + 1 < t_hi) {
+            load(t + 1, page);
+            page = entry(t + 2);
+          }
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int stage = tile % (kv ? RV : RK);
+            wait_for((kv ? v_empty : k_empty) + stage, ((tile / (kv ? RV : RK)) & 1) ^ 1, gave_up);
+            __syncwarp();
+            char* const dst = smem + (kv ? Sh::kOffV : Sh::kOffK) + stage * Sh::kTileBytes;
+            const int row = cw * 16 + lane % 16;
+#pragma unroll
+            for (int x = 0; x < W; ++x) {
+              const uint4 c4 = now[kv][x / 4];
+              const uint32_t word = x % 4 == 0 ? c4.x : x % 4 == 1 ? c4.y : x % 4 == 2 ? c4.z : c4.w;
+              uint32_t f0, f1, f2, f3;
+              e2m1x8_to_f16(word, f0, f1, f2, f3);
+              const uint32_t s2 = e4m3x2_to_f16(((scale_now[kv] >> (8 * (x / 2))) & 0xffu) * 0x101u);
+              *reinterpret_cast<uint4*>(dst + tile_offset(row, half * W + x)) =
+                  make_uint4(mul_f16x2(f0, s2), mul_f16x2(f1, s2), mul_f16x2(f2, s2), mul_f16x2(f3, s2));
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (kv == 0) reinterpret_cast<uint16_t*>(s_bad)[(tile % kBadRing) * 8 + cw] = static_cast<uint16_t>(bads_now);
+              mbar_arrive((kv ? v_full : k_full) + stage);
+            }
+          }
+        }
+      }
+      if (it.last) break;
+    }
+    copy_commit();
+    copy_wait<0>();
+  } else if (warp == Sh::kMma) {
+    // ---- matrix instructions, from one thread
+    if (lane == 0) {
+      constexpr uint32_t id_s = instr_desc<M>(kTile, false), id_o = instr_desc<M>(D, true);
+      int k_tile = 0, v_tile = 0;
+      uint32_t p_phase[2] = {0, 0};
+      for (int n = 0;; ++n) {
+        if (!wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up)) break;
+        const int tiles = items[n % kItems].tiles;
+        const bool last = items[n % kItems].last != 0;
+        mbar_arrive(it_empty + n % kItems);
+        const int jobs = TWO ? 2 * tiles : tiles;
+        wait_for(q_full, n & 1, gave_up);
+        fence_after();
+        auto issue_s = [&](int j) {
+          const int slot = j & 1, stage = k_tile % RK;
+          if (!TWO || slot == 0) {
+            wait_for(k_full + stage, (k_tile / RK) & 1, gave_up);
+            fence_proxy_async_smem();  // the landed copies, before the matrix instructions read them
+          }
+          fence_after();
+          const uint32_t a = desc_low(smem_addr(smem + (TWO ? slot * Sh::kTileBytes : 0)), 16);
+          const uint32_t b = desc_low(smem_addr(smem + Sh::kOffK + stage * Sh::kTileBytes), 16);
+          const uint32_t d = tmem + slot * 128;
+#pragma unroll
+          for (int k = 0; k < KT; ++k) {
+            const uint32_t o = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
+            mma_ss(d, a + o, b + o, id_s, k > 0 ? 1u : 0u);
+          }
+          mma_commit(s_full + slot);
+          if (!TWO || slot == 1) {
+            mma_commit(k_empty + stage);
+            ++k_tile;
+          }
+          if (j == jobs - 1) mma_commit(q_empty);
+        };
+        if (jobs == 0) mma_commit(q_empty);
+        if (jobs > 0) issue_s(0);
+        if (jobs > 1) issue_s(1);
+        for (int j = 0; j < jobs; ++j) {
+          const int slot = j & 1, stage = v_tile % RV;
+          if (!TWO || slot == 0) {
+            wait_for(v_full + stage, (v_tile / RV) & 1, gave_up);
+            fence_proxy_async_smem();
+          }
+          wait_for(p_full + slot, p_phase[slot], gave_up);
+          p_phase[slot] ^= 1;
+          fence_after();
+          const uint32_t b = desc_low(smem_addr(smem + Sh::kOffV + stage * Sh::kTileBytes), kTile * 128);
+          const uint32_t p = tmem + slot * 128, d = tmem + 256 + slot * 128;
+#pragma unroll
+          for (int k = 0; k < kTile / 16; ++k)  // weights of slots 64.. are in columns 64..
+            mma_ts(d, p + (k & 3) * 8 + (k >> 2) * 64, b + k * (2048 >> 4), id_o, (j >= 2 || k > 0) ? 1u : 0u);
+          if (!TWO || slot == 1) {
+            mma_commit(v_empty + stage);
+            ++v_tile;
+          }
+          if (j + 2 >= jobs) mma_commit(o_full + slot);
+          if (j + 2 < jobs) issue_s(j + 2);
+        }
+        if (last) break;
+      }
+      mma_commit(done);
+      if (!mbar_wait(done, 0)) *gave_up = 1;
+    }
+    __syncwarp();
+  } else if (warp >= Sh::kQuery) {
+    // ---- query rows
+    const int t2 = tid - Sh::kQuery * 32;
+    for (int n = 0;; ++n) {
+      if (!__all_sync(0xffffffffu, wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up))) break;
+      const int b = items[n % kItems].b, h = items[n % kItems].h, row0 = items[n % kItems].row0, rows = items[n % kItems].rows;
+      const bool last = items[n % kItems].last != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(it_empty + n % kItems);
+      wait_for(q_empty, (n & 1) ^ 1, gave_up);
+      __syncwarp();
+      const T* const q_item = static_cast<const T*>(P.q) + b * P.q_sb + h * P.G * P.q_sh;
+      constexpr int CH = D / 8, AT = 64 / CH;  // lanes of a row, rows at a time
+      const int piece = t2 % CH;
+      // (rows past the item's keep what was there: they only reach rows of S that nobody reads)
+#pragma unroll 4
+      for (int r = t2 / CH; r < (rows + AT - 1) / AT * AT; r += AT) {
+        uint4 x = make_uint4(0, 0, 0, 0);
+        if (r < rows) {
+          const int i = query_of(P, row0 + r);
+          x = __ldg(reinterpret_cast<const uint4*>(q_item + i * P.q_st + (row0 + r - i * P.G) * P.q_sh) + piece);
+        }
+        uint32_t y[4] = {x.x, x.y, x.z, x.w};
+        if constexpr (FOUR && !std::is_same<T, __half>::value) {
+          // bf16 queries over 4-bit pages: q / 2^(exponent of the row's largest value) is within
+          // (-2, 2), and fp16 then holds it to 2^-25 of that value
+          float a = 0.f;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = Half16<T>::to_f32(y[e]);
+            a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+          }
+#pragma unroll
+          for (int o = CH / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+          const int e8 = (__float_as_int(a) >> 23) & 0xff;
+          const float up = (e8 == 0 || e8 == 0xff) ? 1.f : __int_as_float(e8 << 23);
+          if (piece == 0 && r < MR) s_qscale[(n & 1) * MR + r] = up;
+          const float down = 1.f / up;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float2 f = Half16<T>::to_f32(y[e]);
+            y[e] = Half16<__half>::pack(f.x * down, f.y * down);
+          }
+        }
+        if (P.scale_log2 < 0.f) {  // the scale's sign goes into the queries
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] ^= 0x80008000u;
+        }
+        if (r < MR)
+          *reinterpret_cast<uint4*>(smem + (TWO ? r / 128 * Sh::kTileBytes : 0) + tile_offset(r % 128, piece)) =
+              make_uint4(y[0], y[1], y[2], y[3]);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(q_full);
+      if (last) break;
+    }
+  } else {
+    // ---- rows: threads 128 half + row of a slot hold columns 64 half ... of the slot's row
+    const int slot = warp / 8, half = (warp / 4) % 2, row = tid % 128;
+    const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
+    const uint32_t s_at = tmem + lanes + slot * 128 + half * 64, o_at = tmem + lanes + 256 + slot * 128;
+    const int pair = 2 + slot * 4 + warp % 4;  // named barrier of the two warps that share rows
+    float2* const s_ml = reinterpret_cast<float2*>(smem + Sh::kOffMl);
+    uint32_t s_phase = 0, o_phase = 0;
+    int tile_base = 0;  // tiles of earlier items
+    for (int n = 0;; ++n) {
+      // (all row threads are also done with the last item's accumulators and (m, l) here)
+      if (!rows_all(wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up))) break;
+      const volatile Item& it = items[n % kItems];
+      const int row0 = it.row0 + (TWO ? slot * 128 : 0), rows = min(128, it.rows - (TWO ? slot * 128 : 0));  // may be <= 0
+      const int tiles = it.tiles, t_lo = it.t_lo, first = it.first, end = it.end;
+      const int me = query_of(P, row0 + row);  // this row's query
+      const int my_pos = first + (P.depth && me < P.n ? node_depth(P, me) : me);
+      const bool tree = P.tree_mask != nullptr;
+      auto slot_at = [&](int step) { return (step < it.sink_steps ? step : step - it.sink_steps + it.first_step) * kStep; };
+      // which of the 16 slots of a step this row sees
+      auto sees16 = [&](int step) -> uint32_t {
+        if (step >= it.steps) return 0u;
+        const int s0 = slot_at(step);
+        uint32_t near = P.window > 0 ? bits16(my_pos - (P.window - 1) - s0, kStep) | bits16(0, P.sinks - s0) : 0xffffu;
+        if (!tree) return near & bits16(0, min(first + me, end - 1) + 1 - s0);
+        uint32_t see = near & bits16(0, min(first, end) - s0);
+        if (s0 + kStep > first && me < P.n) {
+          const uint8_t* const mask = P.tree_mask + static_cast<int64_t>(me) * P.n;
+          const uint32_t there = bits16(first - s0, end - s0);
+          uint32_t node = 0;
+#pragma unroll
+          for (int e = 0; e < kStep; ++e)
+            if ((there >> e) & 1u) node |= (__ldg(mask + (s0 + e - first)) != 0 ? 1u : 0u) << e;
+          if (P.window > 0 && P.depth) {
+            near = 0;
+#pragma unroll 1
+            for (int e = 0; e < kStep; ++e)
+              if ((there >> e) & 1u) {
+                const int pos = first + node_depth(P, s0 + e - first);
+                near |= (my_pos - pos < P.window || pos < P.sinks ? 1u : 0u) << e;
+              }
+          }
+          see |= near & node;
+        }
+        return see;
+      };
+
+      const bool active = (warp % 4) * 32 < rows;  // a warp without rows leaves its lanes as they are
+      // (a scale of 0 becomes the smallest one, so that a masked score stays infinite; the sign is in
+      // the staged queries)
+      float c = P.scale_log2 == 0.f ? 1.4e-45f : fabsf(P.scale_log2);
+      constexpr uint32_t hidden = 0xff800000u;  // -inf
+      float m = -kInf, l = 0.f;
+      int jobs = 0;
+      for (int t = TWO ? 0 : slot; t < tiles; t += TWO ? 1 : 2, ++jobs) {
+        const int tile = tile_base + t;
+        wait_for(s_full + slot, s_phase, gave_up);
+        s_phase ^= 1;
+        __syncwarp();  // (lanes leave a wait apart; tensor-memory instructions want them together)
+        fence_after();
+        if (FOUR && !std::is_same<T, __half>::value && jobs == 0) c *= s_qscale[(n & 1) * MR + (TWO ? slot * 128 : 0) + row];
+        bool partial = false;  // some row may not see some slot, or a page is out of range
+        uint32_t seen[2] = {~0u, ~0u};
+        bool poisoned = false;  // the row sees a slot on a page out of range
+        if (rows > 0) {
+          const uint4 bads = *reinterpret_cast<const uint4*>(s_bad + (tile % kBadRing) * 4);
+          partial = t_lo + t < it.whole_lo[slot] || t_lo + t >= it.whole_hi[slot] || (bads.x | bads.y | bads.z | bads.w) != 0;
+          if (partial && active) {
+            const int step0 = (t_lo + t) * kUnit + half * (kUnit / 2);
+#pragma unroll 1
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t see = sees16(step0 + x) << (16 * (x & 1)), keep = 0xffff0000u >> (16 * (x & 1));
+              if (x < 2) seen[0] = (seen[0] & keep) | see;
+              else seen[1] = (seen[1] & keep) | see;
+            }
+            poisoned = ((seen[0] & (half ? bads.z : bads.x)) | (seen[1] & (half ? bads.w : bads.y))) != 0;
+          }
+        }
+        if (active) {
+          __syncwarp();
+          auto mask_scores = [&](int ch, uint32_t (&r)[16]) {
+            if (partial) {
+              const uint32_t see = seen[ch >> 1] >> (16 * (ch & 1));
+#pragma unroll
+              for (int e = 0; e < 16; ++e) r[e] = (see >> e) & 1u ? r[e] : hidden;
+            }
+          };
+          uint32_t r[2][16];
+          float top = -kInf;
+          tmem_load(s_at, r[0]);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            tmem_load_wait(r[ch & 1]);
+            if (ch < 3) tmem_load(s_at + 16 * (ch + 1), r[(ch + 1) & 1]);
+            mask_scores(ch, r[ch & 1]);
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) top = max3(top, __uint_as_float(r[ch & 1][e]), __uint_as_float(r[ch & 1][e + 1]));
+          }
+          top *= c;
+          if (pair_any(pair, top > m + kSlack)) {  // (also where m is still -inf) the reference moves
+            s_ml[(slot * 2 + half) * 128 + row].x = top;
+            asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+            top = fmaxf(fmaxf(m, top), s_ml[(slot * 2 + (half ^ 1)) * 128 + row].x);
+            const float alpha = m == top ? 1.f : ex2(m - (top == -kInf ? 0.f : top));
+            m = top;
+            l *= alpha;
+            if (jobs > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {  // each half rescales half of the accumulator
+#pragma unroll 1
+              for (int d = half * (D / 2); d < (half + 1) * (D / 2); d += 16) {
+                tmem_load(o_at + d, r[1]);
+                tmem_load_wait(r[1]);
+#pragma unroll
+                for (int e = 0; e < 16; ++e) r[1][e] = __float_as_uint(__uint_as_float(r[1][e]) * alpha);
+                tmem_store16(o_at + d, r[1]);
+              }
+            }
+          }
+          // the weights, 16 at a time; they overwrite scores that this thread has read: weights 16 ch ... go
+          // to columns 8 ch ..., scores 16 ch ... are in columns 16 ch ...
+          const float base = m == -kInf ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          tmem_load(s_at, r[0]);
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            tmem_load_wait(r[ch & 1]);
+            if (ch < 3) tmem_load(s_at + 16 * (ch + 1), r[(ch + 1) & 1]);
+            mask_scores(ch, r[ch & 1]);
+            uint32_t p[8];
+#pragma unroll
+            for (int e = 0; e < 16; e += 2) {
+              const float p0 = ex2(fmaf(__uint_as_float(r[ch & 1][e]), c, -base));
+              const float p1 = ex2(fmaf(__uint_as_float(r[ch & 1][e + 1]), c, -base));
+              sum[(e >> 1) & 1] += p0;
+              sum[2 + ((e >> 1) & 1)] += p1;
+              p[e / 2] = Half16<M>::pack(p0, p1);
+            }
+            tmem_store8(s_at + 8 * ch, p);
+          }
+          l += poisoned ? __int_as_float(0x7fffffff) : (sum[0] + sum[1]) + (sum[2] + sum[3]);
+        }
+        if (partial) {
+          // 0 times a value that is not finite is not 0: where some row does not see a slot, such
+          // values are taken out of the staged tile; the rows that see them get them at the end
+          wait_for(v_full + tile % RV, (tile / RV) & 1, gave_up);
+          char* const vt = smem + Sh::kOffV + (tile % RV) * Sh::kTileBytes;
+          constexpr uint32_t em = std::is_same<M, __half>::value ? 0x7c00u : 0x7f80u;
+          bool found = false;
+#pragma unroll 2
+          for (int f = (warp % 8) * 32 + lane; f < kTile * (D / 8); f += 256) {
+            uint4* const at = reinterpret_cast<uint4*>(vt + f * 16);
+            uint32_t x[4] = {at->x, at->y, at->z, at->w};
+            bool here = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) here = here || (x[e] & em) == em || (x[e] & (em << 16)) == em << 16;
+            if (here) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                if ((x[e] & em) == em) x[e] &= 0xffff0000u;
+                if ((x[e] & (em << 16)) == em << 16) x[e] &= 0xffffu;
+              }
+              *at = make_uint4(x[0], x[1], x[2], x[3]);
+              found = true;
+            }
+          }
+          if (found) {
+            *s_odd = 1;
+            fence_proxy_async_smem();
+          }
+          __syncwarp();
+        }
+        if (active) tmem_store_wait();
+        fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full + slot);
+      }
+
+      // ---- the item's rows, or the part of them that this segment holds
+      if (jobs > 0) {
+        wait_for(o_full + slot, o_phase, gave_up);
+        o_phase ^= 1;
+        fence_after();
+      }
+      s_ml[(slot * 2 + half) * 128 + row] = make_float2(m, l);
+      fence_before();
+      // the halves of a row meet, and where both slots hold the same rows, the slots too
+      if constexpr (TWO)
+        asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
+      else
+        asm volatile("bar.sync 1, 512;" ::: "memory");
+      fence_after();
+      l = s_ml[slot * 256 + row].y + s_ml[slot * 256 + 128 + row].y;
+      float scale_own = 1.f, scale_other = 0.f;
+      const int other_jobs = TWO ? 0 : (slot == 0 ? tiles / 2 : (tiles + 1) / 2);
+      if constexpr (!TWO) {
+        const int o = (slot ^ 1) * 256 + row;
+        const float other = s_ml[o].x, other_l = s_ml[o].y + s_ml[o + 128].y;
+        const float top = fmaxf(m, other), base = top == -kInf ? 0.f : top;
+        scale_own = ex2(m - base);
+        scale_other = ex2(other - base);
+        l = l * scale_own + other_l * scale_other;
+        m = top;
+      }
+      __syncwarp();
+      const bool mine = row < rows && me < P.n;
+      const bool whole_item = it.begins && it.ends;
+      const int head = it.h * P.G + row0 + row - me * P.G;
+      const int64_t at = (static_cast<int64_t>(it.b) * P.n + me) * P.Hq + head;
+      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (it.begins ? 1 : 0)) * MR + (TWO ? slot * 128 : 0) + row;
+      const bool none = l == 0.f || me >= it.nq;
+      const float inv = none ? 0.f : pg.v_scale / l;
+      constexpr int COLS = TWO ? D / 2 : D / 4;  // of this thread
+      const int d_lo = TWO ? half * COLS : (slot * 2 + half) * COLS;
+      if (active) {
+#pragma unroll 1
+        for (int d = d_lo; d < d_lo + COLS; d += 16) {
+          float acc[16];
+          uint32_t r[16];
+          __syncwarp();
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+          if (jobs > 0) {
+            tmem_load(o_at + d, r);
+            tmem_load_wait(r);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] = __uint_as_float(r[e]) * scale_own;
+          }
+          if (!TWO && other_jobs > 0) {
+            tmem_load(o_at + (slot == 0 ? 128 : -128) + d, r);
+            tmem_load_wait(r);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] = fmaf(__uint_as_float(r[e]), scale_other, acc[e]);
+          }
+          if (*s_odd != 0 && mine) {  // rare: values that are not finite, for the rows that see them
+            const int32_t* table = pg.table + static_cast<int64_t>(it.b) * pg.max_pages;
+#pragma unroll 1
+            for (int step = t_lo * kUnit; step < (t_lo + tiles) * kUnit; ++step) {
+              if (step / kUnit >= it.whole_lo[slot] && step / kUnit < it.whole_hi[slot]) continue;
+              for (uint32_t see = sees16(step); see != 0; see &= see - 1) {
+                const int s = slot_at(step) + __ffs(see) - 1;
+                const int page = __ldg(table + page_of(pg, s)), in_page = s - page_of(pg, s) * pg.page_size;
+                if (static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages)) continue;
+                if constexpr (FOUR) {  // only a group's scale can be NaN
+                  const uint8_t sb = *reinterpret_cast<const uint8_t*>(pg.v_scales + page * pg.scale_page_stride + in_page * pg.scale_slot_stride +
+                                                                       it.h * pg.scale_head_stride + d / kGroup4);
+                  if ((sb & 0x7f) == 0x7f) {
+#pragma unroll
+                    for (int x = 0; x < 16; ++x) acc[x] = __int_as_float(0x7fffffff);
+                  }
+                } else {
+                  const T* v = reinterpret_cast<const T*>(pg.v + page * pg.page_stride + in_page * pg.slot_stride + it.h * pg.head_stride) + d;
+#pragma unroll
+                  for (int x = 0; x < 16; ++x) {
+                    const float f = static_cast<float>(v[x]);
+                    if (!(fabsf(f) < kInf)) acc[x] += f;
+                  }
+                }
+              }
+            }
+          }
+          if (!mine) continue;
+          if (whole_item) {
+            uint32_t out[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              out[e] = none ? 0u : Half16<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+              if (!it.ok) out[e] = 0x7fff7fffu;
+            }
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(P.out) + at * D + d);
+            dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+            dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+          } else {
+            float4* dst = reinterpret_cast<float4*>(P.part_o + part * D + d);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dst[e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
+          }
+        }
+        if (mine && d_lo == 0) {
+          if (whole_item) {
+            if (P.lse) P.lse[at] = !it.ok ? __int_as_float(0x7fffffff) : none ? -kInf : m * kLn2 + logf(l);
+          } else {
+            P.part_ml[part] = make_float2(m, l);
+          }
+        }
+      }
+      tile_base += tiles;
+      fence_before();
+      const bool last = it.last != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(it_empty + n % kItems);
+      if (last) break;
+    }
+  }
+
+  fence_before();
+  __syncthreads();
+  fence_after();
+  if (warp == Sh::kMma)
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+  if (tid == 0) P.gave_up[blockIdx.x] = *gave_up;
+}
+
+template <typename T, int D, bool TWO, bool FOUR>
+cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
+  using Sh = Shape<D, TWO, FOUR>;
+  auto kernel = attend_tc_kernel<T, D, TWO, FOUR>;
+  static_assert(Sh::kBytes <= 227 * 1024, "shared memory of a CTA");
+  if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes); e != cudaSuccess)
+    return e;
+  return launch_kernel(kernel, dim3(P.ctas), dim3(Sh::kThreads), Sh::kBytes, stream, 0, P);
+}
+
+template <typename T, bool FOUR>
+cudaError_t launch_typed(const AttendParams& P, int mr, cudaStream_t stream) {
+  if (P.pages.head_dim == 64)
+    return mr == 256 ? launch_shape<T, 64, true, FOUR>(P, stream) : launch_shape<T, 64, false, FOUR>(P, stream);
+  return mr == 256 ? launch_shape<T, 128, true, FOUR>(P, stream) : launch_shape<T, 128, false, FOUR>(P, stream);
+}
+
+}  // namespace tc
+
+}  // namespace specdec

@@ -48,6 +48,11 @@ __device__ __forceinline__ SeqLen seq_len(const int32_t* context_len, const int3
   return s;
 }
 
+// The page of a slot: slot / page_size as the high half of a product (exact for slots below 2^31).
+__device__ __forceinline__ int page_of(const Pages& pg, int slot) {
+  return pg.page_magic == 0 ? slot : static_cast<int>(__umul64hi(static_cast<uint64_t>(slot), pg.page_magic));
+}
+
 // Eight 4-bit values (E2M1, the low nibble first) of a word as four fp16 pairs.
 __device__ __forceinline__ void e2m1x8_to_f16(uint32_t w, uint32_t& a, uint32_t& b, uint32_t& c, uint32_t& d) {
   asm("{\n.reg .b8 x0, x1, x2, x3;\n"

@@ -22,6 +22,7 @@ struct Pages {
   int num_pages, page_size, max_pages;
   int kv_heads, head_dim;
   float k_scale, v_scale;
+  uint64_t page_magic;   // 2^64 / page_size, rounded up (0 for pages of one slot)
 };
 
 struct RotateParams {
@@ -62,6 +63,7 @@ struct AttendParams {
   void* out;         // [B, n, Hq, D]
   float* lse;        // [B, n, Hq] or nullptr
   int32_t* out_status;
+  uint64_t g_magic;  // 2^40 / G, rounded up: n * G < 2^24 rows
   int row_tiles;     // tiles of the n * G query rows that share a key head
   int ctas;
   int4* split;       // workspace [ctas]: the item whose first part a CTA left, and its parts
@@ -70,9 +72,10 @@ struct AttendParams {
   float* part_o;     // workspace [ctas, 2, rows, D]: its unnormalised output
   Pages pages;
 };
-// The tensor-memory kernel for 16-bit pages: the rows of its tile, and its launch.
+// The tensor-memory kernel: the rows of its tile, and its launches for 16-bit and 4-bit pages.
 int attend_tc_rows(int64_t rows);
 cudaError_t launch_attend_tc(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream);
+cudaError_t launch_attend_tc4(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream);
 size_t attend_workspace_bytes(int n, int G, int D);
 cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format, void* workspace,
                           cudaStream_t stream);

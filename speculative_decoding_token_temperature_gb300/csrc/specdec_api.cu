@@ -737,6 +737,7 @@ int check_pages(const specdec_kv_pages* pg, bool four, specdec_dtype dt, Pages* 
   o.table = pg->block_table;
   o.num_pages = pg->num_pages;
   o.page_size = pg->page_size;
+  o.page_magic = pg->page_size == 1 ? 0 : ~uint64_t{0} / static_cast<uint64_t>(pg->page_size) + 1;
   o.max_pages = pg->max_pages;
   o.kv_heads = pg->kv_heads;
   o.head_dim = pg->head_dim;
@@ -876,7 +877,8 @@ int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype,
   if (int rc = check_pages(pages, four, dtype, &P.pages); rc != SPECDEC_OK) return rc;
   if (q_heads % pages->kv_heads != 0) return fail(SPECDEC_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
   const int G = q_heads / pages->kv_heads;
-  if (B >= (1 << 24) || static_cast<int64_t>(n) * G >= (1 << 24)) return fail(SPECDEC_ERR_UNSUPPORTED, "B, or query rows of a key head, above 2^24");
+  if (B >= (1 << 24) || static_cast<int64_t>(n) * G >= (1 << 24) || G >= (1 << 16))
+    return fail(SPECDEC_ERR_UNSUPPORTED, "B, or query rows of a key head, above 2^24, or more than 65535 query heads to a key head");
   if (!aligned16(out)) return fail(SPECDEC_ERR_UNSUPPORTED, "out must be 16-byte aligned");
   if (workspace_bytes < attend_workspace_bytes(n, G, pages->head_dim))
     return fail(SPECDEC_ERR_WORKSPACE, "workspace smaller than specdec_attend_workspace_bytes");
@@ -892,6 +894,7 @@ int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype,
   P.n = n;
   P.Hq = q_heads;
   P.G = G;
+  P.g_magic = ((uint64_t{1} << 40) + static_cast<uint64_t>(G) - 1) / static_cast<uint64_t>(G);
   P.window = window;
   P.sinks = sinks;
   P.scale_log2 = scale * 1.4426950408889634f * P.pages.k_scale;
