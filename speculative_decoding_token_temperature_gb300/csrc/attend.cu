@@ -730,7 +730,7 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   const int64_t rows = static_cast<int64_t>(P.n) * P.G;
   const bool four = format == SPECDEC_KV4;
   const int hook = test_hook(SPECDEC_HOOK_ATTEND_KERNEL);
-  const bool tc = hook == 0 ? rows > 64 : hook == 2;
+  const bool tc = hook == 0 ? rows > 16 : hook == 2;
   const int mr = tc ? attend_tc_rows(rows) : row_tile(rows);
   P.row_tiles = static_cast<int>((rows + mr - 1) / mr);
   P.ctas = attend_sms();

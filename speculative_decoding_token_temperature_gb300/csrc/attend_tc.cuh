@@ -56,11 +56,15 @@ struct Shape {
   static constexpr int kMma = kRowWarps + kCopyWarps, kWalker = kMma + 1, kQuery = kMma + 2;
   static constexpr int kThreads = 32 * (kRowWarps + kCopyWarps + 4);
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int RK = D == 64 ? 4 : (TWO ? 2 : 3), RV = D == 64 ? 4 : 2;  // K tiles and V tiles staged
+  static constexpr int RK = D == 64 ? 4 : (TWO || FOUR ? 2 : 3), RV = D == 64 ? 4 : 2;  // K tiles and V tiles staged
+  // 4-bit pages: codes and scales of 16 slots, copied ahead by each warp for itself
+  static constexpr int kRawSide = 16 * (D / 2), kRawBytes = 2 * kRawSide + 2 * D;
+  static constexpr int RAW = FOUR ? (TWO && D == 128 ? 1 : 3) : 0;
   static constexpr int kOffK = (TWO ? 2 : 1) * kTileBytes;
   static constexpr int kOffV = kOffK + RK * kTileBytes;
   static constexpr int kOffMl = kOffV + RV * kTileBytes;      // [2][2][128] (m, l) of slots and halves
-  static constexpr int kOffQScale = kOffMl + 4 * 128 * 8;       // [2][MR] scales of query rows (4-bit pages)
+  static constexpr int kOffRaw = kOffMl + 4 * 128 * 8;
+  static constexpr int kOffQScale = kOffRaw + RAW * kCopyWarps * kRawBytes;  // [2][MR] scales of query rows (4-bit pages)
   static constexpr int kOffItem = kOffQScale + (FOUR ? 2 * MR * 4 : 0);
   static constexpr int kOffScan = kOffItem + kItems * sizeof(Item);
   static constexpr int kOffBad = (kOffScan + (kThreads / 32 + 2) * 8 + 15) / 16 * 16;
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
       mbar_init(p_full + s, kRowWarps / 2);
       mbar_init(o_full + s, 1);
     }
-    mbar_init(q_full, 2);
+    mbar_init(q_full, 64);
     mbar_init(q_empty, 1);
     for (int k = 0; k < kItems; ++k) {
       mbar_init(it_full + k, 1);
@@ -358,62 +362,88 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
           }
         }
       } else {
-        // lane l: half l / 16 of slot 16 c + l % 16, D/2 values: D/16 words of codes and D/32 scales
-        constexpr int W = D / 16, G2 = D / 64;
+        // lane l converts half l / 16 of slot 16 c + l % 16: D/2 values, D/16 words of codes, D/32 scales
+        constexpr int W = D / 16, RAW = Sh::RAW, CPR = D / 32;  // CPR: 16-byte pieces of a row of codes
         const int half = lane / 16;
         const char* const ks_head = pg.k_scales + it.h * pg.scale_head_stride;
         const char* const vs_head = pg.v_scales + it.h * pg.scale_head_stride;
-        uint4 code[2][W / 4];
-        uint32_t scale[2];
-        uint32_t bads = 0;
-        auto load = [&](int t, int page) {
-          const int s = slot_of(t);
-          const bool want = wanted(t, s);
-          const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
-          bads = __ballot_sync(0xffffffffu, bad) & 0xffffu;
-          const int in_page = s - page_of(pg, s) * pg.page_size;
-          const int64_t off = page * pg.page_stride + in_page * pg.slot_stride + half * (W * 4);
-          const int64_t soff = page * pg.scale_page_stride + in_page * pg.scale_slot_stride + half * (2 * G2);
+        char* const raw = smem + Sh::kOffRaw + cw * RAW * Sh::kRawBytes;
+        uint32_t bad_ring[RAW];  // of the tiles copied ahead
+        auto copy = [&](int t, int stage, int page) -> uint32_t {
+          uint32_t bads = 0;
+          if (t < t_hi) {
+            const int s = slot_of(t);
+            const bool want = wanted(t, s);
+            const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
+            const bool there = want && !bad;
+            bads = __ballot_sync(0xffffffffu, bad) & 0xffffu;
+            const uint32_t present = __ballot_sync(0xffffffffu, there);
+            const int in_page = s - page_of(pg, s) * pg.page_size;
+            const int64_t off = there ? page * pg.page_stride + in_page * pg.slot_stride : 0;
+            const int64_t soff = there ? page * pg.scale_page_stride + in_page * pg.scale_slot_stride : 0;
+            const uint32_t dst = smem_addr(raw + stage * Sh::kRawBytes);
 #pragma unroll
-          for (int kv = 0; kv < 2; ++kv) {
-#pragma unroll
-            for (int x = 0; x < W / 4; ++x)
-              code[kv][x] = want && !bad ? __ldg(reinterpret_cast<const uint4*>((kv ? v_head : k_head) + off) + x) : make_uint4(0, 0, 0, 0);
-            const char* const sp = (kv ? vs_head : ks_head) + soff;
-            scale[kv] = !(want && !bad) ? 0u : G2 == 2 ? __ldg(reinterpret_cast<const uint32_t*>(sp)) : __ldg(reinterpret_cast<const uint16_t*>(sp));
+            for (int j = 0; j < 16 * CPR / 32; ++j) {
+              const int f = j * 32 + lane, row = f / CPR;
+              const int64_t o = __shfl_sync(0xffffffffu, off, row) + (f % CPR) * 16;
+              copy_async<16>(dst + f * 16, k_head + o, (present >> row) & 1u);
+              copy_async<16>(dst + Sh::kRawSide + f * 16, v_head + o, (present >> row) & 1u);
+            }
+            copy_async<D / 16>(dst + 2 * Sh::kRawSide + (half ? D : 0) + (lane % 16) * (D / 16), (half ? vs_head : ks_head) + soff, there);
           }
+          copy_commit();
+          return bads;
         };
         int page = entry(t_lo);
-        if (t_lo < t_hi) {
-          load(t_lo, page);
-          page = entry(t_lo + 1);
+#pragma unroll
+        for (int k = 0; k < RAW; ++k) {
+          const int now = page;
+          page = entry(t_lo + k + 1);
+          bad_ring[k] = copy(t_lo + k, k, now);
         }
+        int stage = 0;
         for (int t = t_lo; t < t_hi; ++t, ++tile) {
-          const uint32_t bads_now = bads;
-          uint4 now[2][W / 4];
-          uint32_t scale_now[2] = {scale[0], scale[1]};
-#pragma unroll
-          for (int kv = 0; kv < 2; ++kv)
-#pragma unroll
-            for (int x = 0; x < W / 4; ++x) now[kv][x] = code[kv][x];
-          if (t + 1 < t_hi) {
-            load(t + 1, page);
-            page = entry(t + 2);
-          }
+          copy_wait<RAW - 1>();
+          __syncwarp();
+          const char* const src = raw + stage * Sh::kRawBytes;
+          uint32_t word[2][W], scale[2];
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const int stage = tile % (kv ? RV : RK);
-            wait_for((kv ? v_empty : k_empty) + stage, ((tile / (kv ? RV : RK)) & 1) ^ 1, gave_up);
+            const uint4* const cp = reinterpret_cast<const uint4*>(src + kv * Sh::kRawSide + (lane % 16) * (D / 2) + half * (D / 4));
+#pragma unroll
+            for (int x = 0; x < W / 4; ++x) {
+              const uint4 c4 = cp[x];
+              word[kv][4 * x] = c4.x;
+              word[kv][4 * x + 1] = c4.y;
+              word[kv][4 * x + 2] = c4.z;
+              word[kv][4 * x + 3] = c4.w;
+            }
+            const char* const sp = src + 2 * Sh::kRawSide + kv * D + (lane % 16) * (D / 16) + half * (D / 32);
+            scale[kv] = D == 128 ? *reinterpret_cast<const uint32_t*>(sp) : *reinterpret_cast<const uint16_t*>(sp);
+          }
+          const uint32_t bads_now = bad_ring[0];
+          __syncwarp();
+          {
+            const int now = page;
+            page = entry(t + RAW + 1);
+            const uint32_t next = copy(t + RAW, stage, now);
+#pragma unroll
+            for (int k = 0; k + 1 < RAW; ++k) bad_ring[k] = bad_ring[k + 1];
+            bad_ring[RAW - 1] = next;
+          }
+          stage = stage + 1 == RAW ? 0 : stage + 1;
+          const int row = cw * 16 + lane % 16;
+#pragma unroll
+          for (int kv = 0; kv < 2; ++kv) {
+            const int st = tile % (kv ? RV : RK);
+            wait_for((kv ? v_empty : k_empty) + st, ((tile / (kv ? RV : RK)) & 1) ^ 1, gave_up);
             __syncwarp();
-            char* const dst = smem + (kv ? Sh::kOffV : Sh::kOffK) + stage * Sh::kTileBytes;
-            const int row = cw * 16 + lane % 16;
+            char* const dst = smem + (kv ? Sh::kOffV : Sh::kOffK) + st * Sh::kTileBytes;
 #pragma unroll
             for (int x = 0; x < W; ++x) {
-              const uint4 c4 = now[kv][x / 4];
-              const uint32_t word = x % 4 == 0 ? c4.x : x % 4 == 1 ? c4.y : x % 4 == 2 ? c4.z : c4.w;
               uint32_t f0, f1, f2, f3;
-              e2m1x8_to_f16(word, f0, f1, f2, f3);
-              const uint32_t s2 = e4m3x2_to_f16(((scale_now[kv] >> (8 * (x / 2))) & 0xffu) * 0x101u);
+              e2m1x8_to_f16(word[kv][x], f0, f1, f2, f3);
+              const uint32_t s2 = e4m3x2_to_f16(((scale[kv] >> (8 * (x / 2))) & 0xffu) * 0x101u);
               *reinterpret_cast<uint4*>(dst + tile_offset(row, half * W + x)) =
                   make_uint4(mul_f16x2(f0, s2), mul_f16x2(f1, s2), mul_f16x2(f2, s2), mul_f16x2(f3, s2));
             }
@@ -421,10 +451,12 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
             __syncwarp();
             if (lane == 0) {
               if (kv == 0) reinterpret_cast<uint16_t*>(s_bad)[(tile % kBadRing) * 8 + cw] = static_cast<uint16_t>(bads_now);
-              mbar_arrive((kv ? v_full : k_full) + stage);
+              mbar_arrive((kv ? v_full : k_full) + st);
             }
           }
         }
+        copy_wait<0>();
+        __syncwarp();
       }
       if (it.last) break;
     }
@@ -443,6 +475,7 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
         mbar_arrive(it_empty + n % kItems);
         const int jobs = TWO ? 2 * tiles : tiles;
         wait_for(q_full, n & 1, gave_up);
+        fence_proxy_async_smem();
         fence_after();
         auto issue_s = [&](int j) {
           const int slot = j & 1, stage = k_tile % RK;
@@ -510,49 +543,62 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
       const T* const q_item = static_cast<const T*>(P.q) + b * P.q_sb + h * P.G * P.q_sh;
       constexpr int CH = D / 8, AT = 64 / CH;  // lanes of a row, rows at a time
       const int piece = t2 % CH;
+      auto source = [&](int r) {
+        const int i = query_of(P, row0 + r);
+        return reinterpret_cast<const uint4*>(q_item + i * P.q_st + (row0 + r - i * P.G) * P.q_sh) + piece;
+      };
+      auto target = [&](int r) { return smem + (TWO ? r / 128 * Sh::kTileBytes : 0) + tile_offset(r % 128, piece); };
       // (rows past the item's keep what was there: they only reach rows of S that nobody reads)
+      if (!FOUR && P.scale_log2 >= 0.f) {  // as they are
 #pragma unroll 4
-      for (int r = t2 / CH; r < (rows + AT - 1) / AT * AT; r += AT) {
-        uint4 x = make_uint4(0, 0, 0, 0);
-        if (r < rows) {
-          const int i = query_of(P, row0 + r);
-          x = __ldg(reinterpret_cast<const uint4*>(q_item + i * P.q_st + (row0 + r - i * P.G) * P.q_sh) + piece);
-        }
-        uint32_t y[4] = {x.x, x.y, x.z, x.w};
-        if constexpr (FOUR && !std::is_same<T, __half>::value) {
-          // bf16 queries over 4-bit pages: q / 2^(exponent of the row's largest value) is within
-          // (-2, 2), and fp16 then holds it to 2^-25 of that value
-          float a = 0.f;
+        for (int r = t2 / CH; r < rows; r += AT) copy_async<16>(smem_addr(target(r)), source(r), true);
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(q_full)) : "memory");
+      } else {
+        constexpr int AHEAD = 4;
+        for (int r0 = t2 / CH; r0 - t2 / CH < rows; r0 += AHEAD * AT) {
+          uint4 x[AHEAD];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = Half16<T>::to_f32(y[e]);
-            a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+          for (int k = 0; k < AHEAD; ++k)
+            x[k] = r0 + k * AT < rows ? __ldg(source(r0 + k * AT)) : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int k = 0; k < AHEAD; ++k) {
+            const int r = r0 + k * AT;
+            uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
+            if constexpr (FOUR && !std::is_same<T, __half>::value) {
+              // bf16 queries over 4-bit pages: q / 2^(exponent of the row's largest value) is within
+              // (-2, 2), and fp16 then holds it to 2^-25 of that value
+              float a = 0.f;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = Half16<T>::to_f32(y[e]);
+                a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
+              }
+#pragma unroll
+              for (int o = CH / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
+              const int e8 = (__float_as_int(a) >> 23) & 0xff;
+              const float up = (e8 == 0 || e8 == 0xff) ? 1.f : __int_as_float(e8 << 23);
+              if (piece == 0 && r < rows) s_qscale[(n & 1) * MR + r] = up;
+              const float down = 1.f / up;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float2 f = Half16<T>::to_f32(y[e]);
+                y[e] = Half16<__half>::pack(f.x * down, f.y * down);
+              }
+            }
+            if (P.scale_log2 < 0.f) {  // the scale's sign goes into the queries
+#pragma unroll
+              for (int e = 0; e < 4; ++e) y[e] ^= 0x80008000u;
+            }
+            if (r < rows) *reinterpret_cast<uint4*>(target(r)) = make_uint4(y[0], y[1], y[2], y[3]);
           }
-#pragma unroll
-          for (int o = CH / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
-          const int e8 = (__float_as_int(a) >> 23) & 0xff;
-          const float up = (e8 == 0 || e8 == 0xff) ? 1.f : __int_as_float(e8 << 23);
-          if (piece == 0 && r < MR) s_qscale[(n & 1) * MR + r] = up;
-          const float down = 1.f / up;
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const float2 f = Half16<T>::to_f32(y[e]);
-            y[e] = Half16<__half>::pack(f.x * down, f.y * down);
-          }
         }
-        if (P.scale_log2 < 0.f) {  // the scale's sign goes into the queries
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[e] ^= 0x80008000u;
-        }
-        if (r < MR)
-          *reinterpret_cast<uint4*>(smem + (TWO ? r / 128 * Sh::kTileBytes : 0) + tile_offset(r % 128, piece)) =
-              make_uint4(y[0], y[1], y[2], y[3]);
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
       }
-      fence_proxy_async_smem();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(q_full);
       if (last) break;
     }
+    copy_commit();
+    copy_wait<0>();
   } else {
     // ---- rows: threads 128 half + row of a slot hold columns 64 half ... of the slot's row
     const int slot = warp / 8, half = (warp / 4) % 2, row = tid % 128;
@@ -568,6 +614,7 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
       const volatile Item& it = items[n % kItems];
       const int row0 = it.row0 + (TWO ? slot * 128 : 0), rows = min(128, it.rows - (TWO ? slot * 128 : 0));  // may be <= 0
       const int tiles = it.tiles, t_lo = it.t_lo, first = it.first, end = it.end;
+      const int whole_lo = it.whole_lo[slot], whole_hi = it.whole_hi[slot];
       const int me = query_of(P, row0 + row);  // this row's query
       const int my_pos = first + (P.depth && me < P.n ? node_depth(P, me) : me);
       const bool tree = P.tree_mask != nullptr;
@@ -609,17 +656,17 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
       int jobs = 0;
       for (int t = TWO ? 0 : slot; t < tiles; t += TWO ? 1 : 2, ++jobs) {
         const int tile = tile_base + t;
+        bool partial = rows > 0 && (t_lo + t < whole_lo || t_lo + t >= whole_hi);  // some row may not see some slot
         wait_for(s_full + slot, s_phase, gave_up);
         s_phase ^= 1;
         __syncwarp();  // (lanes leave a wait apart; tensor-memory instructions want them together)
         fence_after();
         if (FOUR && !std::is_same<T, __half>::value && jobs == 0) c *= s_qscale[(n & 1) * MR + (TWO ? slot * 128 : 0) + row];
-        bool partial = false;  // some row may not see some slot, or a page is out of range
         uint32_t seen[2] = {~0u, ~0u};
         bool poisoned = false;  // the row sees a slot on a page out of range
         if (rows > 0) {
           const uint4 bads = *reinterpret_cast<const uint4*>(s_bad + (tile % kBadRing) * 4);
-          partial = t_lo + t < it.whole_lo[slot] || t_lo + t >= it.whole_hi[slot] || (bads.x | bads.y | bads.z | bads.w) != 0;
+          partial = partial || (bads.x | bads.y | bads.z | bads.w) != 0;
           if (partial && active) {
             const int step0 = (t_lo + t) * kUnit + half * (kUnit / 2);
 #pragma unroll 1
@@ -673,7 +720,9 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
           // the weights, 16 at a time; they overwrite scores that this thread has read: weights 16 ch ... go
           // to columns 8 ch ..., scores 16 ch ... are in columns 16 ch ...
           const float base = m == -kInf ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          // (two at a time: packed fp32 products and sums, rounded as the scalar ones)
+          const unsigned long long c2 = f2pack(c, c), base2 = f2pack(-base, -base);
+          unsigned long long sum2[2] = {0ull, 0ull};
           tmem_load(s_at, r[0]);
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) {
@@ -683,15 +732,17 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
             uint32_t p[8];
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
-              const float p0 = ex2(fmaf(__uint_as_float(r[ch & 1][e]), c, -base));
-              const float p1 = ex2(fmaf(__uint_as_float(r[ch & 1][e + 1]), c, -base));
-              sum[(e >> 1) & 1] += p0;
-              sum[2 + ((e >> 1) & 1)] += p1;
+              float x0, x1;
+              f2unpack(f2fma(f2pack(__uint_as_float(r[ch & 1][e]), __uint_as_float(r[ch & 1][e + 1])), c2, base2), x0, x1);
+              const float p0 = ex2(x0), p1 = ex2(x1);
+              sum2[(e >> 1) & 1] = f2add(sum2[(e >> 1) & 1], f2pack(p0, p1));
               p[e / 2] = Half16<M>::pack(p0, p1);
             }
             tmem_store8(s_at + 8 * ch, p);
           }
-          l += poisoned ? __int_as_float(0x7fffffff) : (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          float s0, s1;
+          f2unpack(f2add(sum2[0], sum2[1]), s0, s1);
+          l += poisoned ? __int_as_float(0x7fffffff) : s0 + s1;
         }
         if (partial) {
           // 0 times a value that is not finite is not 0: where some row does not see a slot, such
