@@ -2,7 +2,8 @@
 
 Each .cu translation unit is compiled in parallel to an object, then linked into one
 shared library next to this file.  The CUDA runtime is linked statically, so loading
-the library (e.g. to list its symbols) does not need a GPU.
+the library (e.g. to list its symbols) does not need a GPU.  The host compiler builds
+`_cache_calls.so`, the Python side of the cache calls, beside it.
 """
 from __future__ import annotations
 
@@ -11,7 +12,11 @@ import hashlib
 import os
 import shutil
 import subprocess
+import sys
+import sysconfig
 from pathlib import Path
+
+import torch
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
@@ -19,6 +24,7 @@ CSRC = PKG / "csrc"
 INCLUDE = ROOT / "include"
 LIB_NAME = "libspecdec.so"
 LIB_PATH = PKG / LIB_NAME
+CALLS_PATH = PKG / "_cache_calls.so"
 BUILD_DIR = PKG / "_build"
 
 ARCH_FLAGS = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -45,14 +51,28 @@ def _fingerprint() -> str:
             h.update(p.read_bytes())
     h.update(" ".join(ARCH_FLAGS + NVCC_FLAGS).encode())
     h.update(os.uname().machine.encode())
+    h.update((torch.__version__ + sys.version).encode())
     return h.hexdigest()
+
+
+def _calls_command(out: Path) -> list:
+    """The host compiler's command for the Python side of the cache calls (csrc/cache_calls.cpp),
+    a CPython module on torch's C++ tensors, linked against the library next to it."""
+    cuda = Path(_nvcc()).resolve().parents[1]
+    root = Path(torch.__file__).resolve().parent
+    lib = root / "lib"
+    inc = [sysconfig.get_paths()["include"], root / "include", root / "include" / "torch" / "csrc" / "api" / "include",
+           cuda / "include", INCLUDE]
+    return (["g++", "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+             *(f"-I{i}" for i in inc), str(CSRC / "cache_calls.cpp"), "-o", str(out), f"-L{lib}", "-lc10", "-lc10_cuda",
+             "-ltorch_cpu", "-ltorch_python", "-ltorch", f"-Wl,-rpath,{lib}"])
 
 
 def build(verbose: bool = False, force: bool = False, extra_flags=None) -> Path:
     """Compile every .cu under csrc/ and link libspecdec.so (skipped when up to date)."""
     stamp = BUILD_DIR / "stamp"
     fp = _fingerprint()
-    if not force and LIB_PATH.exists() and stamp.exists() and stamp.read_text() == fp:
+    if not force and LIB_PATH.exists() and CALLS_PATH.exists() and stamp.exists() and stamp.read_text() == fp:
         return LIB_PATH
     BUILD_DIR.mkdir(exist_ok=True)
     nvcc = _nvcc()
@@ -68,14 +88,32 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> Path:
             print(r.stdout, r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
+    calls_obj = BUILD_DIR / "cache_calls.o"
+
+    def compile_calls():
+        cmd = _calls_command(calls_obj)
+        cmd = [c for c in cmd if c != "-shared" and not c.startswith(("-l", "-L", "-Wl"))] + ["-c"]
+        r = subprocess.run(cmd, capture_output=True, text=True)
+        if r.returncode != 0:
+            raise RuntimeError(f"g++ failed for cache_calls.cpp:\n{r.stderr}")
+
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1)) + 1) as ex:
+        calls = ex.submit(compile_calls)
         objs = list(ex.map(compile_one, _sources()))
+        calls.result()
     tmp = LIB_PATH.with_suffix(".so.tmp")
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", str(tmp), *map(str, objs)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    tmp = CALLS_PATH.with_suffix(".so.tmp")
+    cmd = [str(calls_obj) if c == str(CSRC / "cache_calls.cpp") else c for c in _calls_command(tmp)]
+    cmd += [f"-L{PKG}", "-lspecdec", "-Wl,-rpath,$ORIGIN"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"link of {CALLS_PATH.name} failed:\n{r.stderr}")
+    os.replace(tmp, CALLS_PATH)
     stamp.write_text(fp)
     return LIB_PATH
 
