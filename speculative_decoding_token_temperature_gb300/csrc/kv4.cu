@@ -62,11 +62,29 @@ __device__ __forceinline__ bool sequence_fits(const SeqLen& S, const Pages& pg, 
   int bad = S.ok ? 0 : 1;
   if (S.ok && S.nq > 0) {
     const int32_t* table = pg.table + static_cast<int64_t>(b) * pg.max_pages;
-    const int p0 = S.first / pg.page_size, p1 = (S.len - 1) / pg.page_size;
+    const int p0 = page_of(pg, S.first), p1 = page_of(pg, S.len - 1);
     for (int p = p0 + threadIdx.x; p <= p1; p += blockDim.x)
       bad |= static_cast<unsigned>(__ldg(table + p)) >= static_cast<unsigned>(pg.num_pages);
   }
   return !__syncthreads_or(bad);
+}
+
+// The group of a thread: token i, K or V, head h, group g of the head.
+struct Group {
+  int i, h, g;
+  bool is_v;
+};
+__device__ __forceinline__ Group group_of(const Pages& pg) {
+  const int shift = pg.head_dim == 128 ? 3 : 2;  // log2 of the groups of a head
+  const unsigned at = blockIdx.x * kKv4Threads + threadIdx.x, per_token = 2u * pg.kv_heads << shift;
+  Group r;
+  r.i = static_cast<int>(at / per_token);
+  unsigned k = at - r.i * per_token;
+  r.is_v = k >= per_token / 2;
+  if (r.is_v) k -= per_token / 2;
+  r.h = static_cast<int>(k >> shift);
+  r.g = static_cast<int>(k & ((1u << shift) - 1));
+  return r;
 }
 
 // grid (chunks of a sequence's groups, B); the groups of a token: Hkv * D/16 of K, then of V
@@ -74,21 +92,21 @@ template <typename T>
 __global__ void __launch_bounds__(kKv4Threads) append_kv4_kernel(const Kv4Params P) {
   const Pages& pg = P.pages;
   const int b = blockIdx.y;
+  const Group at = group_of(pg);
+  uint4 a = make_uint4(0, 0, 0, 0), c = a;
+  if (at.i < P.n) {  // (before the lengths and pages are there)
+    const T* src = static_cast<const T*>(at.is_v ? P.v : P.k) +
+                   (at.is_v ? b * P.v_sb + at.i * P.v_st + at.h * P.v_sh : b * P.k_sb + at.i * P.k_st + at.h * P.k_sh) + at.g * kGroup4;
+    a = __ldg(reinterpret_cast<const uint4*>(src));
+    c = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+  }
   const SeqLen S = seq_len(P.context_len, P.query_len, b, P.n, static_cast<int64_t>(pg.max_pages) * pg.page_size);
   const bool fits = sequence_fits(S, pg, b);
   if (blockIdx.x == 0 && threadIdx.x == 0 && P.out_status) P.out_status[b] = fits ? 0 : SPECDEC_STATUS_BAD_CACHE;
-  if (!fits) return;
-  const int gd = pg.head_dim / kGroup4, per_token = 2 * pg.kv_heads * gd;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kKv4Threads + threadIdx.x;
-  const int i = static_cast<int>(at / per_token);
-  if (i >= S.nq) return;
-  int r = static_cast<int>(at % per_token);
-  const bool is_v = r >= per_token / 2;
-  if (is_v) r -= per_token / 2;
-  const int h = r / gd, g = r % gd;
-  const T* src = static_cast<const T*>(is_v ? P.v : P.k) +
-                 (is_v ? b * P.v_sb + i * P.v_st + h * P.v_sh : b * P.k_sb + i * P.k_st + h * P.k_sh) + g * kGroup4;
-  const uint4 a = __ldg(reinterpret_cast<const uint4*>(src)), c = __ldg(reinterpret_cast<const uint4*>(src) + 1);
+  if (!fits || at.i >= S.nq) return;
+  const int slot = S.first + at.i, logical = page_of(pg, slot);
+  const int64_t page = __ldg(pg.table + static_cast<int64_t>(b) * pg.max_pages + logical);
+  const int off = slot - logical * pg.page_size;
   const uint32_t in[8] = {a.x, a.y, a.z, a.w, c.x, c.y, c.z, c.w};
   float x[16];
 #pragma unroll
@@ -98,15 +116,12 @@ __global__ void __launch_bounds__(kKv4Threads) append_kv4_kernel(const Kv4Params
     x[2 * e + 1] = f.y;
   }
   uint8_t scale;
-  const uint2 codes = quantise(x, 1.f / (is_v ? pg.v_scale : pg.k_scale), scale);
-  const int slot = S.first + i;
-  const int64_t page = __ldg(pg.table + static_cast<int64_t>(b) * pg.max_pages + slot / pg.page_size);
-  const int off = slot % pg.page_size;
-  char* dst = (is_v ? pg.v : pg.k) + page * pg.page_stride + off * pg.slot_stride + h * pg.head_stride;
-  char* sdst = (is_v ? pg.v_scales : pg.k_scales) + page * pg.scale_page_stride + off * pg.scale_slot_stride +
-               h * pg.scale_head_stride;
-  reinterpret_cast<uint2*>(dst)[g] = codes;
-  reinterpret_cast<uint8_t*>(sdst)[g] = scale;
+  const uint2 codes = quantise(x, 1.f / (at.is_v ? pg.v_scale : pg.k_scale), scale);
+  char* dst = (at.is_v ? pg.v : pg.k) + page * pg.page_stride + off * pg.slot_stride + at.h * pg.head_stride;
+  char* sdst = (at.is_v ? pg.v_scales : pg.k_scales) + page * pg.scale_page_stride + off * pg.scale_slot_stride +
+               at.h * pg.scale_head_stride;
+  reinterpret_cast<uint2*>(dst)[at.g] = codes;
+  reinterpret_cast<uint8_t*>(sdst)[at.g] = scale;
 }
 
 // The same groups read back: 8 bytes of codes and a scale in, 16 values out.
@@ -117,29 +132,23 @@ __global__ void __launch_bounds__(kKv4Threads) read_kv4_kernel(const Kv4Params P
   const SeqLen S = seq_len(P.context_len, P.query_len, b, P.n, static_cast<int64_t>(pg.max_pages) * pg.page_size);
   const bool fits = sequence_fits(S, pg, b);
   if (blockIdx.x == 0 && threadIdx.x == 0 && P.out_status) P.out_status[b] = fits ? 0 : SPECDEC_STATUS_BAD_CACHE;
-  const int gd = pg.head_dim / kGroup4, per_token = 2 * pg.kv_heads * gd;
-  const int64_t at = static_cast<int64_t>(blockIdx.x) * kKv4Threads + threadIdx.x;
-  const int i = static_cast<int>(at / per_token);
-  if (i >= P.n) return;
-  int r = static_cast<int>(at % per_token);
-  const bool is_v = r >= per_token / 2;
-  if (is_v) r -= per_token / 2;
-  const int h = r / gd, g = r % gd;
+  const Group at = group_of(pg);
+  if (at.i >= P.n) return;
   uint32_t out[8];
-  if (!fits || i >= S.nq) {  // NaN for a sequence in error, zeros for tokens it does not have
+  if (!fits || at.i >= S.nq) {  // NaN for a sequence in error, zeros for tokens it does not have
 #pragma unroll
     for (int e = 0; e < 8; ++e) out[e] = fits ? 0u : 0x7fff7fffu;
   } else {
-    const int slot = S.first + i;
-    const int64_t page = __ldg(pg.table + static_cast<int64_t>(b) * pg.max_pages + slot / pg.page_size);
-    const int off = slot % pg.page_size;
-    const char* src = (is_v ? pg.v : pg.k) + page * pg.page_stride + off * pg.slot_stride + h * pg.head_stride;
-    const char* ssrc = (is_v ? pg.v_scales : pg.k_scales) + page * pg.scale_page_stride + off * pg.scale_slot_stride +
-                       h * pg.scale_head_stride;
-    const uint2 codes = reinterpret_cast<const uint2*>(src)[g];
-    const uint32_t sb = reinterpret_cast<const uint8_t*>(ssrc)[g];
+    const int slot = S.first + at.i, logical = page_of(pg, slot);
+    const int64_t page = __ldg(pg.table + static_cast<int64_t>(b) * pg.max_pages + logical);
+    const int off = slot - logical * pg.page_size;
+    const char* src = (at.is_v ? pg.v : pg.k) + page * pg.page_stride + off * pg.slot_stride + at.h * pg.head_stride;
+    const char* ssrc = (at.is_v ? pg.v_scales : pg.k_scales) + page * pg.scale_page_stride + off * pg.scale_slot_stride +
+                       at.h * pg.scale_head_stride;
+    const uint2 codes = reinterpret_cast<const uint2*>(src)[at.g];
+    const uint32_t sb = reinterpret_cast<const uint8_t*>(ssrc)[at.g];
     const float s = __half2float(__ushort_as_half(static_cast<unsigned short>(e4m3x2_to_f16(sb) & 0xffffu)));
-    const float t = is_v ? pg.v_scale : pg.k_scale;
+    const float t = at.is_v ? pg.v_scale : pg.k_scale;
     uint32_t f[8];
     e2m1x8_to_f16(codes.x, f[0], f[1], f[2], f[3]);
     e2m1x8_to_f16(codes.y, f[4], f[5], f[6], f[7]);
@@ -149,8 +158,8 @@ __global__ void __launch_bounds__(kKv4Threads) read_kv4_kernel(const Kv4Params P
       out[e] = Half16<T>::pack(v.x * s * t, v.y * s * t);  // v * s is exact
     }
   }
-  T* dst = static_cast<T*>(is_v ? P.v_out : P.k_out) +
-           ((static_cast<int64_t>(b) * P.n + i) * pg.kv_heads + h) * pg.head_dim + g * kGroup4;
+  T* dst = static_cast<T*>(at.is_v ? P.v_out : P.k_out) +
+           ((static_cast<int64_t>(b) * P.n + at.i) * pg.kv_heads + at.h) * pg.head_dim + at.g * kGroup4;
   reinterpret_cast<uint4*>(dst)[0] = make_uint4(out[0], out[1], out[2], out[3]);
   reinterpret_cast<uint4*>(dst)[1] = make_uint4(out[4], out[5], out[6], out[7]);
 }

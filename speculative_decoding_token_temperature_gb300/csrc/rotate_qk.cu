@@ -8,10 +8,11 @@
 // bits become a float of at most half a turn in magnitude (error 2^-25 turns), which sincospi
 // takes.  Statistics and rotation are in fp32; each value is rounded once, at the store.
 //
-// One CTA per token: its rot/2 angles are computed once, into shared memory, and used by all
-// heads.  A head's row is D/8 lanes of 16 bytes; a lane's row loads are issued before the
-// angles, so the two latencies overlap.  The kernel is bound by HBM on prompts and by the
-// chain length -> page -> store for a few tokens.
+// D/8 lanes hold a head's row, 8 values each: two pieces of 4 whose values pair up, so that the
+// rotation needs no exchange, and a lane's 4 pairs are the same for every head, so that its sines,
+// cosines and weights stay in registers.  A warp's rows are a token's heads; 1 to 8 warps share a
+// token, the more the fewer tokens there are: a few tokens are bound by latency and want the rows
+// side by side, prompts by instructions and want the angles computed once.
 
 #include "cache_device.cuh"
 #include "specdec_device.cuh"
@@ -21,157 +22,190 @@ namespace specdec {
 namespace {
 
 constexpr int kRotateThreads = 256;
-constexpr int kRowsAhead = 4;  // rows a lane group loads before it waits for the angles
+constexpr int kRotateWarps = kRotateThreads / 32;
+constexpr int kRowsAhead = 4;  // rows a lane group loads before it works on the first
 
-template <typename T, int D>
-__global__ void __launch_bounds__(kRotateThreads) rotate_qk_kernel(const RotateParams P) {
-  constexpr int LPH = D / 8;  // lanes of a head
-  constexpr int SLOTS = kRotateThreads / LPH;
-  __shared__ float2 s_cs[D / 2];
-  const int b = blockIdx.y, i = blockIdx.x;
-  const int tid = threadIdx.x, slot = tid / LPH, l = tid % LPH;
+template <typename T, int D, bool INTERLEAVED>
+__global__ void __launch_bounds__(kRotateThreads) rotate_qk_kernel(const RotateParams P, int warps_per_token) {
+  constexpr int LPH = D / 8;     // lanes of a head
+  constexpr int RPW = 32 / LPH;  // rows a warp takes at a time
+  const int b = blockIdx.y, warp = threadIdx.x / 32, lane = threadIdx.x % 32, l = lane % LPH;
+  const int i = blockIdx.x * (kRotateWarps / warps_per_token) + warp / warps_per_token;
+  if (i >= P.n) return;
   const Pages& pg = P.pages;
   const bool paged = P.k_out == nullptr;
-  const int heads = P.Hq + P.Hkv + (paged ? P.Hkv : 0);
+  const int rotated = P.Hq + P.Hkv, heads = rotated + (paged ? P.Hkv : 0);
+  const int r_first = (warp % warps_per_token) * RPW + lane / LPH, r_step = warps_per_token * RPW;
 
-  auto src_row = [&](int r) -> const T* {
+  // this lane's two pieces of 4 values: the halves of 4 pairs, or values that are not rotated
+  const int pairs = P.rot / 8;  // lanes with rotated values (interleaved: the same count)
+  const bool turned = l < pairs;
+  const int pa = INTERLEAVED ? 2 * l : turned ? l : 2 * l, pb = INTERLEAVED ? 2 * l + 1 : turned ? l + pairs : 2 * l + 1;
+  auto row_of = [&](int r) -> const T* {
     if (r < P.Hq) return static_cast<const T*>(P.q) + b * P.q_sb + i * P.q_st + r * P.q_sh;
-    if (r < P.Hq + P.Hkv) return static_cast<const T*>(P.k) + b * P.k_sb + i * P.k_st + (r - P.Hq) * P.k_sh;
-    return static_cast<const T*>(P.v) + b * P.v_sb + i * P.v_st + (r - P.Hq - P.Hkv) * P.v_sh;
+    if (r < rotated) return static_cast<const T*>(P.k) + b * P.k_sb + i * P.k_st + (r - P.Hq) * P.k_sh;
+    return static_cast<const T*>(P.v) + b * P.v_sb + i * P.v_st + (r - rotated) * P.v_sh;
   };
-  uint4 rows[kRowsAhead];
+  uint2 ra[kRowsAhead], rb[kRowsAhead];
+  auto load = [&](int r0) {
 #pragma unroll
-  for (int u = 0; u < kRowsAhead; ++u) {
-    const int r = slot + u * SLOTS;
-    if (r < heads) rows[u] = __ldg(reinterpret_cast<const uint4*>(src_row(r)) + l);
-  }
+    for (int u = 0; u < kRowsAhead; ++u) {
+      const int r = r0 + u * r_step;
+      if (r < heads) {
+        const uint2* const src = reinterpret_cast<const uint2*>(row_of(r));
+        ra[u] = __ldg(src + pa);
+        rb[u] = __ldg(src + pb);
+      } else {
+        ra[u] = rb[u] = make_uint2(0u, 0u);
+      }
+    }
+  };
+  load(r_first);
 
   const SeqLen S = seq_len(P.context_len, P.query_len, b, P.n,
                            paged ? static_cast<int64_t>(pg.max_pages) * pg.page_size : INT32_MAX);
   const int32_t* table = pg.table + static_cast<int64_t>(b) * pg.max_pages;
-  // a sequence with a bad length or page is left alone as a whole: every CTA looks at all of
+  // a sequence with a bad length or page is left alone as a whole: every warp looks at all of
   // its new tokens' pages
-  int bad = S.ok ? 0 : 1;
+  bool bad = !S.ok;
   if (S.ok && paged && S.nq > 0) {
-    const int p0 = S.first / pg.page_size, p1 = (S.len - 1) / pg.page_size;
-    for (int p = p0 + tid; p <= p1; p += kRotateThreads)
-      bad |= static_cast<unsigned>(__ldg(table + p)) >= static_cast<unsigned>(pg.num_pages);
+    const int p0 = page_of(pg, S.first), p1 = page_of(pg, S.len - 1);
+    for (int p = p0 + lane; p <= p1; p += 32)
+      bad = bad || static_cast<unsigned>(__ldg(table + p)) >= static_cast<unsigned>(pg.num_pages);
   }
-  if (tid < P.rot / 2) {
-    const int64_t pos = static_cast<int64_t>(S.first) + (P.depth ? __ldg(P.depth + i) : i);
-    const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(P.turns + tid);
-    const float half_turns = static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f;
-    float s, c;
-    sincospif(half_turns, &s, &c);
-    s_cs[tid] = make_float2(c, s);
-  }
-  bad = __syncthreads_or(bad);
-  if (i == 0 && tid == 0 && P.out_status) P.out_status[b] = bad ? SPECDEC_STATUS_BAD_CACHE : 0;
+  bad = __any_sync(0xffffffffu, bad);
+  if (i == 0 && warp % warps_per_token == 0 && lane == 0 && P.out_status) P.out_status[b] = bad ? SPECDEC_STATUS_BAD_CACHE : 0;
   const bool live = !bad && i < S.nq;
+
+  float cs[4], sn[4];
+  if (turned) {
+    const int64_t pos = static_cast<int64_t>(S.first) + (P.depth ? __ldg(P.depth + i) : i);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const uint64_t turn = static_cast<uint64_t>(pos) * __ldg(P.turns + 4 * l + e);
+      sincospif(static_cast<float>(static_cast<int32_t>(turn >> 32)) * 0x1p-31f, &sn[e], &cs[e]);
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      cs[e] = 1.f;
+      sn[e] = 0.f;
+    }
+  }
+  uint2 wq[2] = {}, wk[2] = {};
+  if (P.q_weight) {
+    wq[0] = __ldg(static_cast<const uint2*>(P.q_weight) + pa);
+    wq[1] = __ldg(static_cast<const uint2*>(P.q_weight) + pb);
+  }
+  if (P.k_weight) {
+    wk[0] = __ldg(static_cast<const uint2*>(P.k_weight) + pa);
+    wk[1] = __ldg(static_cast<const uint2*>(P.k_weight) + pb);
+  }
   int64_t page_off = 0;
   if (paged && live) {
-    const int at = S.first + i;
-    page_off = static_cast<int64_t>(__ldg(table + at / pg.page_size)) * pg.page_stride +
-               static_cast<int64_t>(at % pg.page_size) * pg.slot_stride;
+    const int at = S.first + i, page = page_of(pg, at);
+    page_off = static_cast<int64_t>(__ldg(table + page)) * pg.page_stride + static_cast<int64_t>(at - page * pg.page_size) * pg.slot_stride;
   }
-  const int half = P.rot / 16;  // lanes that hold the first half of the rotated values
+  const int64_t token = static_cast<int64_t>(b) * P.n + i;
 
-  for (int r0 = slot; r0 - slot < heads; r0 += kRowsAhead * SLOTS) {
-    if (r0 != slot) {
-#pragma unroll
-      for (int u = 0; u < kRowsAhead; ++u) {
-        const int r = r0 + u * SLOTS;
-        if (r < heads) rows[u] = __ldg(reinterpret_cast<const uint4*>(src_row(r)) + l);
-      }
-    }
+  // (lane groups of a warp share the loop, so that all lanes meet at the exchanges)
+  for (int r0 = r_first; r0 - lane / LPH < heads; r0 += kRowsAhead * r_step) {
+    uint2 xa[kRowsAhead], xb[kRowsAhead];
 #pragma unroll
     for (int u = 0; u < kRowsAhead; ++u) {
-      const int r = r0 + u * SLOTS;  // lane groups of one warp may differ here: no early exit
-      const bool is_q = r < P.Hq, is_v = r >= P.Hq + P.Hkv;
-      const uint32_t in[4] = {rows[u].x, rows[u].y, rows[u].z, rows[u].w};
-      float x[8];
+      xa[u] = ra[u];
+      xb[u] = rb[u];
+    }
+    load(r0 + kRowsAhead * r_step);
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const float2 f = Half16<T>::to_f32(r < heads ? in[e] : 0u);
-        x[2 * e] = f.x;
-        x[2 * e + 1] = f.y;
+    for (int u = 0; u < kRowsAhead; ++u) {
+      const int r = r0 + u * r_step;
+      if (r - lane / LPH >= heads) break;  // the whole warp
+      const bool is_q = r < P.Hq;
+      float x[8];
+      {
+        const float2 a0 = Half16<T>::to_f32(xa[u].x), a1 = Half16<T>::to_f32(xa[u].y);
+        const float2 b0 = Half16<T>::to_f32(xb[u].x), b1 = Half16<T>::to_f32(xb[u].y);
+        x[0] = a0.x; x[1] = a0.y; x[2] = a1.x; x[3] = a1.y;
+        x[4] = b0.x; x[5] = b0.y; x[6] = b1.x; x[7] = b1.y;
       }
-      const void* w = is_q ? P.q_weight : P.k_weight;
       float ss = 0.f;
 #pragma unroll
       for (int e = 0; e < 8; ++e) ss += x[e] * x[e];
 #pragma unroll
       for (int o = LPH / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-      if (w != nullptr) {
+      if ((is_q ? P.q_weight : P.k_weight) != nullptr) {
         const float inv = rsqrtf(ss * (1.f / D) + P.eps);
-        const uint4 wv = __ldg(static_cast<const uint4*>(w) + l);
-        const uint32_t ww[4] = {wv.x, wv.y, wv.z, wv.w};
+        const uint2 w0 = is_q ? wq[0] : wk[0], w1 = is_q ? wq[1] : wk[1];
+        const float2 f0 = Half16<T>::to_f32(w0.x), f1 = Half16<T>::to_f32(w0.y), f2 = Half16<T>::to_f32(w1.x), f3 = Half16<T>::to_f32(w1.y);
+        const float wf[8] = {f0.x, f0.y, f1.x, f1.y, f2.x, f2.y, f3.x, f3.y};
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[e] = x[e] * inv * wf[e];
+      }
+      uint2 ya, yb;
+      if constexpr (INTERLEAVED) {  // pairs (x0, x1), (x2, x3), ...
+        float y[8];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          const float2 f = Half16<T>::to_f32(ww[e]);
-          x[2 * e] = x[2 * e] * inv * f.x;
-          x[2 * e + 1] = x[2 * e + 1] * inv * f.y;
+          y[2 * e] = x[2 * e] * cs[e] - x[2 * e + 1] * sn[e];
+          y[2 * e + 1] = x[2 * e + 1] * cs[e] + x[2 * e] * sn[e];
         }
-      }
-      float y[8];
-      if (P.interleaved) {
+        ya = make_uint2(Half16<T>::pack(y[0], y[1]), Half16<T>::pack(y[2], y[3]));
+        yb = make_uint2(Half16<T>::pack(y[4], y[5]), Half16<T>::pack(y[6], y[7]));
+      } else {  // pairs (x0, x4), (x1, x5), ...
+        float y[8];
 #pragma unroll
-        for (int e = 0; e < 8; e += 2) {
-          const int j = (8 * l + e) / 2;
-          const float2 cs = 2 * j < P.rot ? s_cs[j] : make_float2(1.f, 0.f);
-          y[e] = x[e] * cs.x - x[e + 1] * cs.y;
-          y[e + 1] = x[e + 1] * cs.x + x[e] * cs.y;
+        for (int e = 0; e < 4; ++e) {
+          y[e] = x[e] * cs[e] - x[e + 4] * sn[e];
+          y[e + 4] = x[e + 4] * cs[e] + x[e] * sn[e];
         }
-      } else {
-        const bool lo = l < half, turned = l < 2 * half;
-        const int from = (tid & 31 & ~(LPH - 1)) + (lo ? l + half : turned ? l - half : l);
+        if (!turned) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float other = __shfl_sync(0xffffffffu, x[e], from);
-          const float2 cs = turned ? s_cs[(lo ? l : l - half) * 8 + e] : make_float2(1.f, 0.f);
-          y[e] = lo ? x[e] * cs.x - other * cs.y : x[e] * cs.x + other * cs.y;
-          if (!turned) y[e] = x[e];
+          for (int e = 0; e < 8; ++e) y[e] = x[e];
         }
+        ya = make_uint2(Half16<T>::pack(y[0], y[1]), Half16<T>::pack(y[2], y[3]));
+        yb = make_uint2(Half16<T>::pack(y[4], y[5]), Half16<T>::pack(y[6], y[7]));
       }
       if (r >= heads) continue;
-      uint4 out = rows[u];
-      if (!is_v) {
-        out.x = Half16<T>::pack(y[0], y[1]);
-        out.y = Half16<T>::pack(y[2], y[3]);
-        out.z = Half16<T>::pack(y[4], y[5]);
-        out.w = Half16<T>::pack(y[6], y[7]);
-        // a new token that does not exist gives zeros, a sequence in error NaN
-        if (!live) {
-          const uint32_t f = bad ? 0x7fff7fffu : 0u;
-          out = make_uint4(f, f, f, f);
-        }
+      if (r >= rotated) {  // values go as they are
+        ya = xa[u];
+        yb = xb[u];
+      } else if (!live) {  // a new token that does not exist gives zeros, a sequence in error NaN
+        const uint32_t f = bad ? 0x7fff7fffu : 0u;
+        ya = yb = make_uint2(f, f);
       }
-      const int64_t token = static_cast<int64_t>(b) * P.n + i;
+      uint2* dst;
       if (is_q) {
-        reinterpret_cast<uint4*>(static_cast<T*>(P.q_out) + (token * P.Hq + r) * D)[l] = out;
+        dst = reinterpret_cast<uint2*>(static_cast<T*>(P.q_out) + (token * P.Hq + r) * D);
       } else if (!paged) {
-        reinterpret_cast<uint4*>(static_cast<T*>(P.k_out) + (token * P.Hkv + (r - P.Hq)) * D)[l] = out;
-      } else if (live) {
-        char* base = is_v ? pg.v : pg.k;
-        const int h = is_v ? r - P.Hq - P.Hkv : r - P.Hq;
-        reinterpret_cast<uint4*>(base + page_off + h * pg.head_stride)[l] = out;
+        dst = reinterpret_cast<uint2*>(static_cast<T*>(P.k_out) + (token * P.Hkv + (r - P.Hq)) * D);
+      } else {
+        if (!live) continue;
+        dst = reinterpret_cast<uint2*>((r < rotated ? pg.k : pg.v) + page_off + (r < rotated ? r - P.Hq : r - rotated) * pg.head_stride);
       }
+      dst[pa] = ya;
+      dst[pb] = yb;
     }
   }
 }
 
-template <typename T>
+template <typename T, int D>
 cudaError_t launch_typed(const RotateParams& P, cudaStream_t stream) {
-  const dim3 grid(static_cast<unsigned>(P.n), static_cast<unsigned>(P.B));
+  // warps that share a token: enough warps to fill the GPU (152 SMs of 48 warps and more)
+  const int64_t tokens = static_cast<int64_t>(P.B) * P.n;
+  const int wpt = tokens < 1024 ? 8 : tokens < 2048 ? 4 : tokens < 16384 ? 2 : 1;
+  const int per_cta = kRotateWarps / wpt;
+  const dim3 grid(static_cast<unsigned>((P.n + per_cta - 1) / per_cta), static_cast<unsigned>(P.B));
   const dim3 block(kRotateThreads);
-  if (P.D == 64) return launch_kernel(rotate_qk_kernel<T, 64>, grid, block, 0, stream, 0, P);
-  return launch_kernel(rotate_qk_kernel<T, 128>, grid, block, 0, stream, 0, P);
+  return P.interleaved ? launch_kernel(rotate_qk_kernel<T, D, true>, grid, block, 0, stream, 0, P, int{wpt})
+                       : launch_kernel(rotate_qk_kernel<T, D, false>, grid, block, 0, stream, 0, P, int{wpt});
 }
 
 }  // namespace
 
 cudaError_t launch_rotate_qk(const RotateParams& P, specdec_dtype dt, cudaStream_t stream) {
-  return dt == SPECDEC_BF16 ? launch_typed<__nv_bfloat16>(P, stream) : launch_typed<__half>(P, stream);
+  if (P.D == 64) return dt == SPECDEC_BF16 ? launch_typed<__nv_bfloat16, 64>(P, stream) : launch_typed<__half, 64>(P, stream);
+  return dt == SPECDEC_BF16 ? launch_typed<__nv_bfloat16, 128>(P, stream) : launch_typed<__half, 128>(P, stream);
 }
 
 }  // namespace specdec
