@@ -74,30 +74,44 @@ __device__ __forceinline__ int item_units(const AttendParams& P, const SeqLen& S
   const Range r = item_range(P, S, rt * MR, tile_rows<MR>(P, rt));
   return max(1, (r.steps + kUnit - 1) / kUnit);
 }
-template <int MR>
-__device__ __forceinline__ int64_t sequence_units(const AttendParams& P, int b, int64_t slots) {
-  const SeqLen S = seq_len(P.context_len, P.query_len, b, P.n, slots);
-  int64_t u = 0;
-  for (int rt = 0; rt < P.row_tiles; ++rt) u += item_units<MR>(P, S, rt);
-  return u * P.pages.kv_heads;
-}
-
 // A CTA's range of units and the item it starts in.  scan(): all threads of the CTA call it, with
-// shared memory for one int64_t per warp and four more.
+// shared memory for one int64_t per warp and two more.
 struct Share {
   int64_t u, end;         // units [u, end) of all
   int64_t quota, extra;   // every CTA has quota units, the first `extra` one more
-  int64_t item;           // first unit of item (b, rt, h)
-  int b;
+  int64_t first;          // first unit of the key heads' items of (b, rt)
+  int b, rt;
 };
 template <int MR, int THREADS>
 __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots, int64_t* sh) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
-  const int per = (P.B + THREADS - 1) / THREADS;  // thread t takes a run of sequences
-  const int b_lo = min(P.B, tid * per), b_hi = min(P.B, b_lo + per);
+  // row tile rt of sequence b is number b * row_tiles + rt; thread t takes a run of them
+  const int64_t all = static_cast<int64_t>(P.B) * P.row_tiles, per = (all + THREADS - 1) / THREADS;
+  const int64_t lo_tile = min(all, tid * per), hi_tile = min(all, lo_tile + per);
+  int b0 = 0, rt0 = 0;
+  if (lo_tile < hi_tile) {
+    b0 = P.row_tiles == 1 ? static_cast<int>(lo_tile) : static_cast<int>(lo_tile / P.row_tiles);
+    rt0 = static_cast<int>(lo_tile - static_cast<int64_t>(b0) * P.row_tiles);
+  }
+  // calls f(b, rt, units) for the run until it says stop
+  auto each = [&](auto&& f) {
+    int b = b0, rt = rt0;
+    SeqLen S{};
+    for (int64_t k = lo_tile; k < hi_tile; ++k) {
+      if (k == lo_tile || rt == 0) S = seq_len(P.context_len, P.query_len, b, P.n, slots);
+      if (!f(b, rt, static_cast<int64_t>(item_units<MR>(P, S, rt)) * P.pages.kv_heads)) return;
+      if (++rt == P.row_tiles) {
+        rt = 0;
+        ++b;
+      }
+    }
+  };
   int64_t mine = 0;
-  for (int b = b_lo; b < b_hi; ++b) mine += sequence_units<MR>(P, b, slots);
+  each([&](int, int, int64_t n) {
+    mine += n;
+    return true;
+  });
   int64_t incl = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -124,20 +138,21 @@ __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots
   s.u = cta * s.quota + min(cta, s.extra);
   s.end = s.u + s.quota + (cta < s.extra ? 1 : 0);
   int64_t lo = before + incl - mine;
-  if (s.u < s.end && s.u >= lo && s.u < lo + mine) {  // exactly one thread
-    int b = b_lo;
-    for (;; ++b) {
-      const int64_t n = sequence_units<MR>(P, b, slots);
-      if (s.u < lo + n) break;
+  if (s.u < s.end && s.u >= lo && s.u < lo + mine)  // exactly one thread
+    each([&](int b, int rt, int64_t n) {
+      if (s.u < lo + n) {
+        sh[WARPS] = (static_cast<int64_t>(b) << 32) | rt;
+        sh[WARPS + 1] = lo;
+        return false;
+      }
       lo += n;
-    }
-    sh[WARPS] = b;
-    sh[WARPS + 1] = lo;
-  }
+      return true;
+    });
   __syncthreads();
   if (s.u < s.end) {
-    s.b = static_cast<int>(sh[WARPS]);
-    s.item = sh[WARPS + 1];
+    s.b = static_cast<int>(sh[WARPS] >> 32);
+    s.rt = static_cast<int>(sh[WARPS] & 0xffffffff);
+    s.first = sh[WARPS + 1];
   }
   return s;
 }
@@ -150,17 +165,12 @@ struct Walk {
   int b, rt, h, units;
   SeqLen S;
   __device__ __forceinline__ Walk(const AttendParams& p, int64_t n, const Share& s)
-      : P(p), slots(n), u(s.u), end(s.end), item(s.item), b(s.b), rt(0), h(0) {
+      : P(p), slots(n), u(s.u), end(s.end), b(s.b), rt(s.rt) {
     S = seq_len(P.context_len, P.query_len, b, P.n, slots);
-    units = item_units<MR>(P, S, 0);
-    while (u >= item + units) {
-      item += units;
-      if (++h == P.pages.kv_heads) {
-        h = 0;
-        ++rt;
-        units = item_units<MR>(P, S, rt);
-      }
-    }
+    units = item_units<MR>(P, S, rt);
+    const int64_t at = u - s.first;
+    h = at >> 32 == 0 ? static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(units)) : static_cast<int>(at / units);
+    item = s.first + static_cast<int64_t>(h) * units;
   }
   __device__ __forceinline__ int64_t seg_end() const { return min(end, item + units); }
   __device__ __forceinline__ bool next() {  // false: the range is done

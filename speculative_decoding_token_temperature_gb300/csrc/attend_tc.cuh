@@ -72,6 +72,14 @@ struct Shape {
   static constexpr int kBars = 2 * (RK + RV) + 2 + 2 + 2 + 2 + 2 * kItems + 1;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kBytes = kOffMisc + 16;
+
+  // Tensor memory's 512 columns: S of slots 0 and 1, then O.  With D = 64 there is room for the
+  // weights beside the scores, and a slot's next scores need not wait for its products (AHEAD); with
+  // D = 128 the weights of a slot take the place of its scores, each half's of its own.
+  static constexpr bool AHEAD = D == 64;
+  static constexpr int kHalfP = AHEAD ? 32 : 64;  // columns between the weights of a tile's halves
+  __host__ __device__ static constexpr int o_column(int slot) { return 256 + slot * D; }
+  __host__ __device__ static constexpr int p_column(int slot) { return AHEAD ? 384 + slot * 64 : slot * 128; }
 };
 
 // ---- tcgen05 -----------------------------------------------------------------------------
@@ -187,6 +195,7 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
   using Sh = Shape<D, TWO, FOUR>;
   using M = typename std::conditional<FOUR, __half, T>::type;  // the matrix instructions' type
   constexpr int MR = Sh::MR, RK = Sh::RK, RV = Sh::RV, KT = D / 16, THREADS = Sh::kThreads;
+  constexpr bool AHEAD = Sh::AHEAD;
   extern __shared__ __align__(1024) char smem[];
   const Pages& pg = P.pages;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -504,24 +513,25 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
         if (jobs > 1) issue_s(1);
         for (int j = 0; j < jobs; ++j) {
           const int slot = j & 1, stage = v_tile % RV;
+          wait_for(p_full + slot, p_phase[slot], gave_up);
+          p_phase[slot] ^= 1;
+          if (AHEAD && j + 2 < jobs) issue_s(j + 2);
           if (!TWO || slot == 0) {
             wait_for(v_full + stage, (v_tile / RV) & 1, gave_up);
             fence_proxy_async_smem();
           }
-          wait_for(p_full + slot, p_phase[slot], gave_up);
-          p_phase[slot] ^= 1;
           fence_after();
           const uint32_t b = desc_low(smem_addr(smem + Sh::kOffV + stage * Sh::kTileBytes), kTile * 128);
-          const uint32_t p = tmem + slot * 128, d = tmem + 256 + slot * 128;
+          const uint32_t p = tmem + Sh::p_column(slot), d = tmem + Sh::o_column(slot);
 #pragma unroll
-          for (int k = 0; k < kTile / 16; ++k)  // weights of slots 64.. are in columns 64..
-            mma_ts(d, p + (k & 3) * 8 + (k >> 2) * 64, b + k * (2048 >> 4), id_o, (j >= 2 || k > 0) ? 1u : 0u);
+          for (int k = 0; k < kTile / 16; ++k)
+            mma_ts(d, p + (k & 3) * 8 + (k >> 2) * Sh::kHalfP, b + k * (2048 >> 4), id_o, (j >= 2 || k > 0) ? 1u : 0u);
           if (!TWO || slot == 1) {
             mma_commit(v_empty + stage);
             ++v_tile;
           }
-          if (j + 2 >= jobs) mma_commit(o_full + slot);
-          if (j + 2 < jobs) issue_s(j + 2);
+          if (AHEAD || j + 2 >= jobs) mma_commit(o_full + slot);
+          if (!AHEAD && j + 2 < jobs) issue_s(j + 2);
         }
         if (last) break;
       }
@@ -603,7 +613,8 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
     // ---- rows: threads 128 half + row of a slot hold columns 64 half ... of the slot's row
     const int slot = warp / 8, half = (warp / 4) % 2, row = tid % 128;
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + slot * 128 + half * 64, o_at = tmem + lanes + 256 + slot * 128;
+    const uint32_t s_at = tmem + lanes + slot * 128 + half * 64, o_at = tmem + lanes + Sh::o_column(slot);
+    const uint32_t p_at = tmem + lanes + Sh::p_column(slot) + half * Sh::kHalfP;
     const int pair = 2 + slot * 4 + warp % 4;  // named barrier of the two warps that share rows
     float2* const s_ml = reinterpret_cast<float2*>(smem + Sh::kOffMl);
     uint32_t s_phase = 0, o_phase = 0;
@@ -678,17 +689,17 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
             poisoned = ((seen[0] & (half ? bads.z : bads.x)) | (seen[1] & (half ? bads.w : bads.y))) != 0;
           }
         }
+        uint32_t r[2][16];
+        float top = -kInf;
+        auto mask_scores = [&](int ch, uint32_t (&r)[16]) {
+          if (partial) {
+            const uint32_t see = seen[ch >> 1] >> (16 * (ch & 1));
+#pragma unroll
+            for (int e = 0; e < 16; ++e) r[e] = (see >> e) & 1u ? r[e] : hidden;
+          }
+        };
         if (active) {
           __syncwarp();
-          auto mask_scores = [&](int ch, uint32_t (&r)[16]) {
-            if (partial) {
-              const uint32_t see = seen[ch >> 1] >> (16 * (ch & 1));
-#pragma unroll
-              for (int e = 0; e < 16; ++e) r[e] = (see >> e) & 1u ? r[e] : hidden;
-            }
-          };
-          uint32_t r[2][16];
-          float top = -kInf;
           tmem_load(s_at, r[0]);
 #pragma unroll
           for (int ch = 0; ch < 4; ++ch) {
@@ -699,6 +710,14 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
             for (int e = 0; e < 16; e += 2) top = max3(top, __uint_as_float(r[ch & 1][e]), __uint_as_float(r[ch & 1][e + 1]));
           }
           top *= c;
+        }
+        if (AHEAD && jobs > 0) {  // the last products have read their weights and added to the accumulator
+          wait_for(o_full + slot, o_phase, gave_up);
+          o_phase ^= 1;
+          __syncwarp();
+          fence_after();
+        }
+        if (active) {
           if (pair_any(pair, top > m + kSlack)) {  // (also where m is still -inf) the reference moves
             s_ml[(slot * 2 + half) * 128 + row].x = top;
             asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
@@ -717,8 +736,8 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
               }
             }
           }
-          // the weights, 16 at a time; they overwrite scores that this thread has read: weights 16 ch ... go
-          // to columns 8 ch ..., scores 16 ch ... are in columns 16 ch ...
+          // the weights, 16 at a time; where they overwrite scores, this thread has read them: weights 16 ch ...
+          // go to columns 8 ch ..., scores 16 ch ... are in columns 16 ch ...
           const float base = m == -kInf ? 0.f : m;
           // (two at a time: packed fp32 products and sums, rounded as the scalar ones)
           const unsigned long long c2 = f2pack(c, c), base2 = f2pack(-base, -base);
@@ -738,7 +757,7 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
               sum2[(e >> 1) & 1] = f2add(sum2[(e >> 1) & 1], f2pack(p0, p1));
               p[e / 2] = Half16<M>::pack(p0, p1);
             }
-            tmem_store8(s_at + 8 * ch, p);
+            tmem_store8(p_at + 8 * ch, p);
           }
           float s0, s1;
           f2unpack(f2add(sum2[0], sum2[1]), s0, s1);
@@ -831,7 +850,7 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
             for (int e = 0; e < 16; ++e) acc[e] = __uint_as_float(r[e]) * scale_own;
           }
           if (!TWO && other_jobs > 0) {
-            tmem_load(o_at + (slot == 0 ? 128 : -128) + d, r);
+            tmem_load(tmem + lanes + Sh::o_column(slot ^ 1) + d, r);
             tmem_load_wait(r);
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[e] = fmaf(__uint_as_float(r[e]), scale_other, acc[e]);
