@@ -158,6 +158,12 @@ __device__ __forceinline__ bool wait_for(uint64_t* bar, uint32_t parity, volatil
   }
   return true;
 }
+// One lane of the warp (the same one every time).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t yes;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(yes)::"memory");
+  return yes != 0;
+}
 // Whether all row threads say yes (the barrier of all of them).
 __device__ __forceinline__ bool rows_all(bool mine) {
   uint32_t all;
@@ -472,69 +478,79 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
     copy_commit();
     copy_wait<0>();
   } else if (warp == Sh::kMma) {
-    // ---- matrix instructions, from one thread
-    if (lane == 0) {
-      constexpr uint32_t id_s = instr_desc<M>(kTile, false), id_o = instr_desc<M>(D, true);
-      int k_tile = 0, v_tile = 0;
-      uint32_t p_phase[2] = {0, 0};
-      for (int n = 0;; ++n) {
-        if (!wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up)) break;
-        const int tiles = items[n % kItems].tiles;
-        const bool last = items[n % kItems].last != 0;
-        mbar_arrive(it_empty + n % kItems);
-        const int jobs = TWO ? 2 * tiles : tiles;
-        wait_for(q_full, n & 1, gave_up);
-        fence_proxy_async_smem();
+    // ---- matrix instructions, from one elected thread.  The whole warp runs the loops, on values that
+    // are the same in all lanes: the operands' descriptors then live in uniform registers, as the
+    // instructions take them (from a thread's own registers each one cost about 80 clocks to issue).
+    constexpr uint32_t id_s = instr_desc<M>(kTile, false), id_o = instr_desc<M>(D, true);
+    const bool leader = elect_one();
+    const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
+    int k_tile = 0, v_tile = 0;
+    uint32_t p_phase = 0;  // bit s: slot s
+    for (int n = 0;; ++n) {
+      if (!__all_sync(0xffffffffu, wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up))) break;
+      const int tiles = __shfl_sync(0xffffffffu, items[n % kItems].tiles, 0);
+      const int last = __shfl_sync(0xffffffffu, items[n % kItems].last, 0);
+      if (leader) mbar_arrive(it_empty + n % kItems);
+      const int jobs = TWO ? 2 * tiles : tiles;
+      wait_for(q_full, n & 1, gave_up);
+      __syncwarp();
+      fence_proxy_async_smem();
+      fence_after();
+      auto issue_s = [&](int j) {
+        const int slot = j & 1, stage = k_tile % RK;
+        if (!TWO || slot == 0) {
+          wait_for(k_full + stage, (k_tile / RK) & 1, gave_up);
+          __syncwarp();
+          fence_proxy_async_smem();  // the landed copies, before the matrix instructions read them
+        }
         fence_after();
-        auto issue_s = [&](int j) {
-          const int slot = j & 1, stage = k_tile % RK;
-          if (!TWO || slot == 0) {
-            wait_for(k_full + stage, (k_tile / RK) & 1, gave_up);
-            fence_proxy_async_smem();  // the landed copies, before the matrix instructions read them
-          }
-          fence_after();
-          const uint32_t a = desc_low(smem_addr(smem + (TWO ? slot * Sh::kTileBytes : 0)), 16);
-          const uint32_t b = desc_low(smem_addr(smem + Sh::kOffK + stage * Sh::kTileBytes), 16);
-          const uint32_t d = tmem + slot * 128;
+        const uint32_t a = desc_low(smem_addr(smem + (TWO ? slot * Sh::kTileBytes : 0)), 16);
+        const uint32_t b = desc_low(smem_addr(smem + Sh::kOffK + stage * Sh::kTileBytes), 16);
+        const uint32_t d = base + slot * 128;
+        if (leader) {
 #pragma unroll
           for (int k = 0; k < KT; ++k) {
             const uint32_t o = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
             mma_ss(d, a + o, b + o, id_s, k > 0 ? 1u : 0u);
           }
           mma_commit(s_full + slot);
-          if (!TWO || slot == 1) {
-            mma_commit(k_empty + stage);
-            ++k_tile;
-          }
+          if (!TWO || slot == 1) mma_commit(k_empty + stage);
           if (j == jobs - 1) mma_commit(q_empty);
-        };
-        if (jobs == 0) mma_commit(q_empty);
-        if (jobs > 0) issue_s(0);
-        if (jobs > 1) issue_s(1);
-        for (int j = 0; j < jobs; ++j) {
-          const int slot = j & 1, stage = v_tile % RV;
-          wait_for(p_full + slot, p_phase[slot], gave_up);
-          p_phase[slot] ^= 1;
-          if (AHEAD && j + 2 < jobs) issue_s(j + 2);
-          if (!TWO || slot == 0) {
-            wait_for(v_full + stage, (v_tile / RV) & 1, gave_up);
-            fence_proxy_async_smem();
-          }
-          fence_after();
-          const uint32_t b = desc_low(smem_addr(smem + Sh::kOffV + stage * Sh::kTileBytes), kTile * 128);
-          const uint32_t p = tmem + Sh::p_column(slot), d = tmem + Sh::o_column(slot);
+        }
+        if (!TWO || slot == 1) ++k_tile;
+        __syncwarp();
+      };
+      if (jobs == 0 && leader) mma_commit(q_empty);
+      if (jobs > 0) issue_s(0);
+      if (jobs > 1) issue_s(1);
+      for (int j = 0; j < jobs; ++j) {
+        const int slot = j & 1, stage = v_tile % RV;
+        wait_for(p_full + slot, (p_phase >> slot) & 1, gave_up);
+        __syncwarp();
+        p_phase ^= 1u << slot;
+        if (AHEAD && j + 2 < jobs) issue_s(j + 2);
+        if (!TWO || slot == 0) {
+          wait_for(v_full + stage, (v_tile / RV) & 1, gave_up);
+          __syncwarp();
+          fence_proxy_async_smem();
+        }
+        fence_after();
+        const uint32_t b = desc_low(smem_addr(smem + Sh::kOffV + stage * Sh::kTileBytes), kTile * 128);
+        const uint32_t p = base + Sh::p_column(slot), d = base + Sh::o_column(slot);
+        if (leader) {
 #pragma unroll
           for (int k = 0; k < kTile / 16; ++k)
             mma_ts(d, p + (k & 3) * 8 + (k >> 2) * Sh::kHalfP, b + k * (2048 >> 4), id_o, (j >= 2 || k > 0) ? 1u : 0u);
-          if (!TWO || slot == 1) {
-            mma_commit(v_empty + stage);
-            ++v_tile;
-          }
+          if (!TWO || slot == 1) mma_commit(v_empty + stage);
           if (AHEAD || j + 2 >= jobs) mma_commit(o_full + slot);
-          if (!AHEAD && j + 2 < jobs) issue_s(j + 2);
         }
-        if (last) break;
+        if (!TWO || slot == 1) ++v_tile;
+        __syncwarp();
+        if (!AHEAD && j + 2 < jobs) issue_s(j + 2);
       }
+      if (last) break;
+    }
+    if (leader) {
       mma_commit(done);
       if (!mbar_wait(done, 0)) *gave_up = 1;
     }
