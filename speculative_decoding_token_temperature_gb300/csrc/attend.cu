@@ -84,7 +84,9 @@ __global__ void __launch_bounds__(32 * Stage<D, FOUR>::WARPS, 1) attend_kernel(c
   char* const stages = smem + warp * STAGES * St::kBytes;
   float* const s_rowscale = reinterpret_cast<float*>(smem + St::kOffScale);
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+  // (the launch may overlap the end of the kernel before it: nothing above touches global memory)
+  grid_dependency_wait();
+  grid_launch_dependents();
   const Share share = scan_units<MR, THREADS>(P, slots, s_scan);
   const int64_t cta = blockIdx.x;
   if (tid == 0) {
@@ -564,6 +566,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const Atte
   const Pages& pg = P.pages;
   const int64_t slots = static_cast<int64_t>(pg.max_pages) * pg.page_size;
   const int cta = blockIdx.x;
+  grid_launch_dependents();
   if (blockIdx.y == 0 && P.out_status) {  // a bad length, or a page that a query sees out of range
     for (int b = cta; b < P.B; b += gridDim.x) {
       const SeqLen S = seq_len(P.context_len, P.query_len, b, P.n, slots);
@@ -580,7 +583,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const Atte
       if (threadIdx.x == 0) P.out_status[b] = bad ? SPECDEC_STATUS_BAD_CACHE : 0;
     }
   }
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_dependency_wait();
   if (blockIdx.y == 0 && P.out_status) {  // a bounded wait gave up somewhere: nothing counts
     int late = 0;
     for (int k = threadIdx.x; k < gridDim.x; k += blockDim.x) late |= P.gave_up[k];
@@ -639,7 +642,7 @@ cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
   static_assert(St::kSmem <= 227 * 1024 - 1024, "shared memory of a CTA");
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, St::kSmem); e != cudaSuccess)
     return e;
-  return launch_kernel(kernel, dim3(P.ctas), dim3(32 * St::WARPS), St::kSmem, stream, 0, P);
+  return launch_kernel(kernel, dim3(P.ctas), dim3(32 * St::WARPS), St::kSmem, stream, 1, P);
 }
 
 template <typename T>

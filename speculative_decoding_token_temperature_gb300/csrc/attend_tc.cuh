@@ -224,7 +224,6 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
   Item* const items = reinterpret_cast<Item*>(smem + Sh::kOffItem);
   float* const s_qscale = reinterpret_cast<float*>(smem + Sh::kOffQScale);
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if (tid == 0) {
     // copied tiles: every copy lane's copies have landed, and a warp's part of s_bad is written
     for (int r = 0; r < RK; ++r) {
@@ -250,8 +249,11 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
     mbar_fence_init();
     *gave_up = 0;
     *s_odd = 0;
-    P.split[blockIdx.x] = make_int4(0, 0, 0, 0);
   }
+  // (the launch may overlap the end of the kernel before it: nothing above touches global memory)
+  grid_dependency_wait();
+  grid_launch_dependents();
+  if (tid == 0) P.split[blockIdx.x] = make_int4(0, 0, 0, 0);
   const int64_t slots = static_cast<int64_t>(pg.max_pages) * pg.page_size;
   const Share share = scan_units<MR, THREADS>(P, slots, reinterpret_cast<int64_t*>(smem + Sh::kOffScan));
   if (share.u >= share.end) {  // nothing for this CTA
@@ -688,25 +690,24 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
         s_phase ^= 1;
         __syncwarp();  // (lanes leave a wait apart; tensor-memory instructions want them together)
         fence_after();
+        uint32_t r[2][16];
+        float top = -kInf;
+        const uint4 bads = *reinterpret_cast<const uint4*>(s_bad + (tile % kBadRing) * 4);
         if (FOUR && !std::is_same<T, __half>::value && jobs == 0) c *= s_qscale[(n & 1) * MR + (TWO ? slot * 128 : 0) + row];
         uint32_t seen[2] = {~0u, ~0u};
         bool poisoned = false;  // the row sees a slot on a page out of range
-        if (rows > 0) {
-          const uint4 bads = *reinterpret_cast<const uint4*>(s_bad + (tile % kBadRing) * 4);
-          partial = partial || (bads.x | bads.y | bads.z | bads.w) != 0;
-          if (partial && active) {
-            const int step0 = (t_lo + t) * kUnit + half * (kUnit / 2);
+        partial = partial || (rows > 0 && (bads.x | bads.y | bads.z | bads.w) != 0);
+        if (partial && active) {
+          const int step0 = (t_lo + t) * kUnit + half * (kUnit / 2);
 #pragma unroll 1
-            for (int x = 0; x < 4; ++x) {
-              const uint32_t see = sees16(step0 + x) << (16 * (x & 1)), keep = 0xffff0000u >> (16 * (x & 1));
-              if (x < 2) seen[0] = (seen[0] & keep) | see;
-              else seen[1] = (seen[1] & keep) | see;
-            }
-            poisoned = ((seen[0] & (half ? bads.z : bads.x)) | (seen[1] & (half ? bads.w : bads.y))) != 0;
+          for (int x = 0; x < 4; ++x) {
+            const uint32_t see = sees16(step0 + x) << (16 * (x & 1)), keep = 0xffff0000u >> (16 * (x & 1));
+            if (x < 2) seen[0] = (seen[0] & keep) | see;
+            else seen[1] = (seen[1] & keep) | see;
           }
+          poisoned = ((seen[0] & (half ? bads.z : bads.x)) | (seen[1] & (half ? bads.w : bads.y))) != 0;
+          __syncwarp();
         }
-        uint32_t r[2][16];
-        float top = -kInf;
         auto mask_scores = [&](int ch, uint32_t (&r)[16]) {
           if (partial) {
             const uint32_t see = seen[ch >> 1] >> (16 * (ch & 1));
@@ -715,15 +716,17 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
           }
         };
         if (active) {
-          __syncwarp();
-          tmem_load(s_at, r[0]);
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            tmem_load_wait(r[ch & 1]);
-            if (ch < 3) tmem_load(s_at + 16 * (ch + 1), r[(ch + 1) & 1]);
-            mask_scores(ch, r[ch & 1]);
+          for (int h2 = 0; h2 < 2; ++h2) {  // 32 columns at a time
+            tmem_load(s_at + 32 * h2, r[0]);
+            tmem_load(s_at + 32 * h2 + 16, r[1]);
 #pragma unroll
-            for (int e = 0; e < 16; e += 2) top = max3(top, __uint_as_float(r[ch & 1][e]), __uint_as_float(r[ch & 1][e + 1]));
+            for (int x = 0; x < 2; ++x) {
+              tmem_load_wait(r[x]);
+              mask_scores(2 * h2 + x, r[x]);
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) top = max3(top, __uint_as_float(r[x][e]), __uint_as_float(r[x][e + 1]));
+            }
           }
           top *= c;
         }
@@ -947,7 +950,7 @@ cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
   static_assert(Sh::kBytes <= 227 * 1024, "shared memory of a CTA");
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes); e != cudaSuccess)
     return e;
-  return launch_kernel(kernel, dim3(P.ctas), dim3(Sh::kThreads), Sh::kBytes, stream, 0, P);
+  return launch_kernel(kernel, dim3(P.ctas), dim3(Sh::kThreads), Sh::kBytes, stream, 1, P);
 }
 
 template <typename T, bool FOUR>
