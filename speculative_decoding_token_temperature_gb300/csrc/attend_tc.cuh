@@ -35,7 +35,7 @@ namespace tc {
 
 constexpr int kRowWarps = 16;
 constexpr int kTile = kUnit * kStep;  // 128 slots
-constexpr int kBadRing = 8;           // tiles whose out-of-range slots are remembered
+constexpr int kBadRing = 16;          // tiles whose out-of-range slots are remembered
 constexpr int kItems = 4;             // items the walk may be ahead
 constexpr float kSlack = 8.f;         // log2 of how far a weight may exceed 1
 
@@ -57,19 +57,19 @@ struct Shape {
   static constexpr int kThreads = 32 * (kRowWarps + kCopyWarps + 4);
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int RK = D == 64 ? 4 : (TWO || FOUR ? 2 : 3), RV = D == 64 ? 4 : 2;  // K tiles and V tiles staged
-  // 4-bit pages: codes and scales of 16 slots, copied ahead by each warp for itself
-  static constexpr int kRawSide = 16 * (D / 2), kRawBytes = 2 * kRawSide + 2 * D;
+  // 4-bit pages: a tile's codes and scales (of K, then of V), copied ahead of their conversion
+  static constexpr int kRawCodes = kTile * (D / 2), kRawScales = kTile * (D / 16), kRawBytes = 2 * (kRawCodes + kRawScales);
   static constexpr int RAW = FOUR ? (TWO && D == 128 ? 1 : 3) : 0;
   static constexpr int kOffK = (TWO ? 2 : 1) * kTileBytes;
   static constexpr int kOffV = kOffK + RK * kTileBytes;
   static constexpr int kOffMl = kOffV + RV * kTileBytes;      // [2][2][128] (m, l) of slots and halves
   static constexpr int kOffRaw = kOffMl + 4 * 128 * 8;
-  static constexpr int kOffQScale = kOffRaw + RAW * kCopyWarps * kRawBytes;  // [2][MR] scales of query rows (4-bit pages)
+  static constexpr int kOffQScale = kOffRaw + RAW * kRawBytes;  // [2][MR] scales of query rows (4-bit pages)
   static constexpr int kOffItem = kOffQScale + (FOUR ? 2 * MR * 4 : 0);
   static constexpr int kOffScan = kOffItem + kItems * sizeof(Item);
   static constexpr int kOffBad = (kOffScan + (kThreads / 32 + 2) * 8 + 15) / 16 * 16;
   static constexpr int kOffBar = kOffBad + kBadRing * 16;
-  static constexpr int kBars = 2 * (RK + RV) + 2 + 2 + 2 + 2 + 2 * kItems + 1;
+  static constexpr int kBars = 2 * (RK + RV + RAW) + 2 + 2 + 2 + 2 + 2 * kItems + 1;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kBytes = kOffMisc + 16;
 
@@ -218,6 +218,8 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
   uint64_t* const it_full = q_empty + 1;    // [kItems]
   uint64_t* const it_empty = it_full + kItems;
   uint64_t* const done = it_empty + kItems;
+  uint64_t* const raw_full = done + 1;      // [RAW], 4-bit pages
+  uint64_t* const raw_empty = raw_full + Sh::RAW;
   uint32_t* const s_tmem = reinterpret_cast<uint32_t*>(smem + Sh::kOffMisc);
   volatile int* const gave_up = reinterpret_cast<int*>(smem + Sh::kOffMisc) + 1;
   volatile int* const s_odd = reinterpret_cast<int*>(smem + Sh::kOffMisc) + 2;  // a masked value that is not finite
@@ -246,6 +248,10 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
       mbar_init(it_empty + k, kRowWarps + Sh::kCopyWarps + 1 + 2);
     }
     mbar_init(done, 1);
+    for (int r = 0; r < Sh::RAW; ++r) {
+      mbar_init(raw_full + r, 64 + 2);  // every lane's copies, and the two parts of s_bad
+      mbar_init(raw_empty + r, Sh::kCopyWarps);
+    }
     mbar_fence_init();
     *gave_up = 0;
     *s_odd = 0;
@@ -380,76 +386,30 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
         }
       } else {
         // lane l converts half l / 16 of slot 16 c + l % 16: D/2 values, D/16 words of codes, D/32 scales
-        constexpr int W = D / 16, RAW = Sh::RAW, CPR = D / 32;  // CPR: 16-byte pieces of a row of codes
-        const int half = lane / 16;
-        const char* const ks_head = pg.k_scales + it.h * pg.scale_head_stride;
-        const char* const vs_head = pg.v_scales + it.h * pg.scale_head_stride;
-        char* const raw = smem + Sh::kOffRaw + cw * RAW * Sh::kRawBytes;
-        uint32_t bad_ring[RAW];  // of the tiles copied ahead
-        auto copy = [&](int t, int stage, int page) -> uint32_t {
-          uint32_t bads = 0;
-          if (t < t_hi) {
-            const int s = slot_of(t);
-            const bool want = wanted(t, s);
-            const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
-            const bool there = want && !bad;
-            bads = __ballot_sync(0xffffffffu, bad) & 0xffffu;
-            const uint32_t present = __ballot_sync(0xffffffffu, there);
-            const int in_page = s - page_of(pg, s) * pg.page_size;
-            const int64_t off = there ? page * pg.page_stride + in_page * pg.slot_stride : 0;
-            const int64_t soff = there ? page * pg.scale_page_stride + in_page * pg.scale_slot_stride : 0;
-            const uint32_t dst = smem_addr(raw + stage * Sh::kRawBytes);
-#pragma unroll
-            for (int j = 0; j < 16 * CPR / 32; ++j) {
-              const int f = j * 32 + lane, row = f / CPR;
-              const int64_t o = __shfl_sync(0xffffffffu, off, row) + (f % CPR) * 16;
-              copy_async<16>(dst + f * 16, k_head + o, (present >> row) & 1u);
-              copy_async<16>(dst + Sh::kRawSide + f * 16, v_head + o, (present >> row) & 1u);
-            }
-            copy_async<D / 16>(dst + 2 * Sh::kRawSide + (half ? D : 0) + (lane % 16) * (D / 16), (half ? vs_head : ks_head) + soff, there);
-          }
-          copy_commit();
-          return bads;
-        };
-        int page = entry(t_lo);
-#pragma unroll
-        for (int k = 0; k < RAW; ++k) {
-          const int now = page;
-          page = entry(t_lo + k + 1);
-          bad_ring[k] = copy(t_lo + k, k, now);
-        }
-        int stage = 0;
+        constexpr int W = D / 16, RAW = Sh::RAW;
+        const int half = lane / 16, row = cw * 16 + lane % 16;
         for (int t = t_lo; t < t_hi; ++t, ++tile) {
-          copy_wait<RAW - 1>();
+          const int rs = tile % RAW;
+          wait_for(raw_full + rs, (tile / RAW) & 1, gave_up);
           __syncwarp();
-          const char* const src = raw + stage * Sh::kRawBytes;
+          const char* const src = smem + Sh::kOffRaw + rs * Sh::kRawBytes;
           uint32_t word[2][W], scale[2];
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const uint4* const cp = reinterpret_cast<const uint4*>(src + kv * Sh::kRawSide + (lane % 16) * (D / 2) + half * (D / 4));
+            const uint4* const cp = reinterpret_cast<const uint4*>(src + kv * Sh::kRawCodes + row * (D / 2) + half * (D / 4));
 #pragma unroll
-            for (int x = 0; x < W / 4; ++x) {
-              const uint4 c4 = cp[x];
-              word[kv][4 * x] = c4.x;
-              word[kv][4 * x + 1] = c4.y;
-              word[kv][4 * x + 2] = c4.z;
-              word[kv][4 * x + 3] = c4.w;
+            for (int y = 0; y < W / 4; ++y) {
+              const uint4 c4 = cp[y];
+              word[kv][4 * y] = c4.x;
+              word[kv][4 * y + 1] = c4.y;
+              word[kv][4 * y + 2] = c4.z;
+              word[kv][4 * y + 3] = c4.w;
             }
-            const char* const sp = src + 2 * Sh::kRawSide + kv * D + (lane % 16) * (D / 16) + half * (D / 32);
+            const char* const sp = src + 2 * Sh::kRawCodes + kv * Sh::kRawScales + row * (D / 16) + half * (D / 32);
             scale[kv] = D == 128 ? *reinterpret_cast<const uint32_t*>(sp) : *reinterpret_cast<const uint16_t*>(sp);
           }
-          const uint32_t bads_now = bad_ring[0];
           __syncwarp();
-          {
-            const int now = page;
-            page = entry(t + RAW + 1);
-            const uint32_t next = copy(t + RAW, stage, now);
-#pragma unroll
-            for (int k = 0; k + 1 < RAW; ++k) bad_ring[k] = bad_ring[k + 1];
-            bad_ring[RAW - 1] = next;
-          }
-          stage = stage + 1 == RAW ? 0 : stage + 1;
-          const int row = cw * 16 + lane % 16;
+          if (lane == 0) mbar_arrive(raw_empty + rs);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
             const int st = tile % (kv ? RV : RK);
@@ -457,23 +417,18 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
             __syncwarp();
             char* const dst = smem + (kv ? Sh::kOffV : Sh::kOffK) + st * Sh::kTileBytes;
 #pragma unroll
-            for (int x = 0; x < W; ++x) {
+            for (int y = 0; y < W; ++y) {
               uint32_t f0, f1, f2, f3;
-              e2m1x8_to_f16(word[kv][x], f0, f1, f2, f3);
-              const uint32_t s2 = e4m3x2_to_f16(((scale[kv] >> (8 * (x / 2))) & 0xffu) * 0x101u);
-              *reinterpret_cast<uint4*>(dst + tile_offset(row, half * W + x)) =
+              e2m1x8_to_f16(word[kv][y], f0, f1, f2, f3);
+              const uint32_t s2 = e4m3x2_to_f16(__byte_perm(scale[kv], 0, 0x11 * (y / 2)));
+              *reinterpret_cast<uint4*>(dst + tile_offset(row, half * W + y)) =
                   make_uint4(mul_f16x2(f0, s2), mul_f16x2(f1, s2), mul_f16x2(f2, s2), mul_f16x2(f3, s2));
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
-              if (kv == 0) reinterpret_cast<uint16_t*>(s_bad)[(tile % kBadRing) * 8 + cw] = static_cast<uint16_t>(bads_now);
-              mbar_arrive((kv ? v_full : k_full) + st);
-            }
+            if (lane == 0) mbar_arrive((kv ? v_full : k_full) + st);
           }
         }
-        copy_wait<0>();
-        __syncwarp();
       }
       if (it.last) break;
     }
@@ -558,14 +513,74 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
     }
     __syncwarp();
   } else if (warp >= Sh::kQuery) {
-    // ---- query rows
+    // ---- query rows, and the codes and scales of 4-bit pages
     const int t2 = tid - Sh::kQuery * 32;
+    int raw_tile = 0;
     for (int n = 0;; ++n) {
       if (!__all_sync(0xffffffffu, wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up))) break;
-      const int b = items[n % kItems].b, h = items[n % kItems].h, row0 = items[n % kItems].row0, rows = items[n % kItems].rows;
-      const bool last = items[n % kItems].last != 0;
+      const Item it = items[n % kItems];
+      const int b = it.b, h = it.h, row0 = it.row0, rows = it.rows;
+      const bool last = it.last != 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(it_empty + n % kItems);
+      // warp w of the two brings slots 64 w ... of a tile; lane l looks up slots l and 32 + l of them
+      int raw_t = it.t_lo;
+      auto copy_raw = [&](int until) {
+        if constexpr (FOUR) {
+          constexpr int RAW = Sh::RAW, CPR = D / 32;  // CPR: 16-byte pieces of a row of codes
+          Range R;
+          R.sink_steps = it.sink_steps;
+          R.first_step = it.first_step;
+          const int32_t* const table = pg.table + static_cast<int64_t>(b) * pg.max_pages;
+          const char* const k_head = pg.k + h * pg.head_stride;
+          const char* const v_head = pg.v + h * pg.head_stride;
+          const char* const ks_head = pg.k_scales + h * pg.scale_head_stride;
+          const char* const vs_head = pg.v_scales + h * pg.scale_head_stride;
+          const int w2 = t2 / 32;
+#pragma unroll 1
+          for (; raw_t < until; ++raw_t, ++raw_tile) {
+            int64_t off[2], soff[2];
+            uint32_t present[2];
+            const int rs = raw_tile % RAW;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const int step = raw_t * kUnit + w2 * 4 + x * 2 + lane / kStep, s = R.slot(step) + lane % kStep;
+              const bool want = step < it.steps && s < it.end && (s >= it.lo || s < it.sinks);
+              const int logical = page_of(pg, want ? s : 0), in_page = (want ? s : 0) - logical * pg.page_size;
+              const int page = want ? __ldg(table + logical) : 0;
+              const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
+              const uint32_t bads = __ballot_sync(0xffffffffu, bad);
+              present[x] = __ballot_sync(0xffffffffu, want && !bad);
+              off[x] = want && !bad ? page * pg.page_stride + in_page * pg.slot_stride : 0;
+              soff[x] = want && !bad ? page * pg.scale_page_stride + in_page * pg.scale_slot_stride : 0;
+              if (lane == 0) s_bad[(raw_tile % kBadRing) * 4 + w2 * 2 + x] = bads;
+            }
+            wait_for(raw_empty + rs, ((raw_tile / RAW) & 1) ^ 1, gave_up);
+            __syncwarp();
+            if (lane == 0) mbar_arrive(raw_full + rs);
+            const uint32_t dst = smem_addr(smem + Sh::kOffRaw + rs * Sh::kRawBytes);
+#pragma unroll
+            for (int j = 0; j < 64 * CPR / 32; ++j) {
+              const int f = j * 32 + lane, row = f / CPR;  // row of the warp's 64
+              const int x = j * 32 / CPR / 32;
+              const int64_t o = __shfl_sync(0xffffffffu, off[x], row % 32) + (f % CPR) * 16;
+              const bool there = (present[x] >> (row % 32)) & 1u;
+              copy_async<16>(dst + w2 * (64 * CPR * 16) + f * 16, k_head + o, there);
+              copy_async<16>(dst + Sh::kRawCodes + w2 * (64 * CPR * 16) + f * 16, v_head + o, there);
+            }
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              const uint32_t sd = dst + 2 * Sh::kRawCodes + (w2 * 64 + x * 32 + lane) * (D / 16);
+              const bool there = (present[x] >> lane) & 1u;
+              copy_async<D / 16>(sd, ks_head + soff[x], there);
+              copy_async<D / 16>(sd + Sh::kRawScales, vs_head + soff[x], there);
+            }
+            asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(raw_full + rs)) : "memory");
+          }
+        }
+      };
+      // the first tiles may come before the last item's queries are done with
+      copy_raw(it.t_lo + min(it.tiles, Sh::RAW));
       wait_for(q_empty, (n & 1) ^ 1, gave_up);
       __syncwarp();
       const T* const q_item = static_cast<const T*>(P.q) + b * P.q_sb + h * P.G * P.q_sh;
@@ -623,6 +638,7 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
         fence_proxy_async_smem();
         mbar_arrive(q_full);
       }
+      copy_raw(it.t_lo + it.tiles);
       if (last) break;
     }
     copy_commit();
