@@ -18,10 +18,10 @@
 //
 // Warps 0-15: rows (slot = warp / 8, columns = warp / 4 % 2, lanes = warp % 4).  Then the warps that
 // bring K and V: of 16-bit pages, 4 that copy rows asynchronously, 16 bytes at a time; of 4-bit
-// pages, 8 that read codes and write their fp16 values (exact: at most 6 significant bits).
+// pages, 8 that turn copied codes into their fp16 values (exact: at most 6 significant bits).
 // Either way the tiles are 128-byte-swizzled and gathered row by row, so pages may have any size
-// and stride.  Then one warp whose first thread issues the matrix instructions, one that walks
-// the items ahead of everybody, and two that bring query rows.  The roles meet at mbarriers; every
+// and stride.  One warp issues the matrix instructions, one walks the items ahead of everybody, and
+// two bring query rows and, of 4-bit pages, the codes and scales.  The roles meet at mbarriers; every
 // wait is bounded.  Where one runs out, the walk publishes no further item, every role finishes the
 // item it is in (without waiting) and leaves; the row warps, which also meet at thread barriers, agree
 // at each item whether they go on.  The CTA reports it.
@@ -53,12 +53,22 @@ template <int D, bool TWO, bool FOUR>
 struct Shape {
   static constexpr int MR = TWO ? 256 : 128;
   static constexpr int kCopyWarps = FOUR ? 8 : 4;
-  static constexpr int kMma = kRowWarps + kCopyWarps, kWalker = kMma + 1, kQuery = kMma + 2;
   static constexpr int kThreads = 32 * (kRowWarps + kCopyWarps + 4);
+  // Who is who among the warps from 16 on.  With at most 32 rows the row warps that have any are 0, 4, 8
+  // and 12, all on the first of an SM's four schedulers (warp % 4): the busy warps of the other roles
+  // keep off it.
+  static constexpr int kWalker = FOUR ? 16 : 20, kMma = FOUR ? 27 : 23, kQuery0 = FOUR ? 20 : 21, kQuery1 = FOUR ? 24 : 22;
+  // 16-bit pages: 16 .. 19; 4-bit pages: 17, 18, 19, 21, 22, 23, 25, 26
+  __device__ static constexpr int copy_index(int warp) {
+    const int k = warp - kRowWarps;
+    return FOUR ? (k % 4 == 0 || k > 10 || k < 0 ? -1 : k / 4 * 3 + k % 4 - 1) : (k >= 0 && k < 4 ? k : -1);
+  }
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int RK = D == 64 ? 4 : (TWO || FOUR ? 2 : 3), RV = D == 64 ? 4 : 2;  // K tiles and V tiles staged
   // 4-bit pages: a tile's codes and scales (of K, then of V), copied ahead of their conversion
   static constexpr int kRawCodes = kTile * (D / 2), kRawScales = kTile * (D / 16), kRawBytes = 2 * (kRawCodes + kRawScales);
+  // where the 16-byte piece of a row of codes lies: turned by the row, so that 8 rows meet no bank conflict
+  __device__ static constexpr int raw_piece(int row, int piece) { return piece ^ ((row >> (D == 128 ? 1 : 2)) & (D / 32 - 1)); }
   static constexpr int RAW = FOUR ? (TWO && D == 128 ? 1 : 3) : 0;
   static constexpr int kOffK = (TWO ? 2 : 1) * kTileBytes;
   static constexpr int kOffV = kOffK + RK * kTileBytes;
@@ -326,9 +336,9 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
       }
     }
     __syncwarp();
-  } else if (warp >= kRowWarps && warp < kRowWarps + Sh::kCopyWarps) {
+  } else if (Sh::copy_index(warp) >= 0) {
     // ---- K and V
-    const int cw = warp - kRowWarps;
+    const int cw = Sh::copy_index(warp);
     int tile = 0;
     for (int n = 0;; ++n) {
       if (!__all_sync(0xffffffffu, wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up))) break;
@@ -396,10 +406,10 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
           uint32_t word[2][W], scale[2];
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
-            const uint4* const cp = reinterpret_cast<const uint4*>(src + kv * Sh::kRawCodes + row * (D / 2) + half * (D / 4));
+            const uint4* const cp = reinterpret_cast<const uint4*>(src + kv * Sh::kRawCodes + row * (D / 2));
 #pragma unroll
             for (int y = 0; y < W / 4; ++y) {
-              const uint4 c4 = cp[y];
+              const uint4 c4 = cp[Sh::raw_piece(row, half * (W / 4) + y)];
               word[kv][4 * y] = c4.x;
               word[kv][4 * y + 1] = c4.y;
               word[kv][4 * y + 2] = c4.z;
@@ -512,9 +522,9 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
       if (!mbar_wait(done, 0)) *gave_up = 1;
     }
     __syncwarp();
-  } else if (warp >= Sh::kQuery) {
+  } else if (warp == Sh::kQuery0 || warp == Sh::kQuery1) {
     // ---- query rows, and the codes and scales of 4-bit pages
-    const int t2 = tid - Sh::kQuery * 32;
+    const int t2 = (warp == Sh::kQuery0 ? 0 : 32) + lane;
     int raw_tile = 0;
     for (int n = 0;; ++n) {
       if (!__all_sync(0xffffffffu, wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up))) break;
@@ -565,8 +575,9 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
               const int x = j * 32 / CPR / 32;
               const int64_t o = __shfl_sync(0xffffffffu, off[x], row % 32) + (f % CPR) * 16;
               const bool there = (present[x] >> (row % 32)) & 1u;
-              copy_async<16>(dst + w2 * (64 * CPR * 16) + f * 16, k_head + o, there);
-              copy_async<16>(dst + Sh::kRawCodes + w2 * (64 * CPR * 16) + f * 16, v_head + o, there);
+              const uint32_t to = dst + (w2 * 64 + row) * (D / 2) + Sh::raw_piece(row, f % CPR) * 16;
+              copy_async<16>(to, k_head + o, there);
+              copy_async<16>(to + Sh::kRawCodes, v_head + o, there);
             }
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
