@@ -49,9 +49,13 @@ struct Item {
   int whole_lo[2], whole_hi[2];  // tiles that every row of a slot sees whole
 };
 
-template <int D, bool TWO, bool FOUR>
+// Row tiles: 32 rows, each in the four quarters of tensor memory's lanes, or 128, or two of 128.
+enum Rows { kQuad, kOne, kTwo };
+
+template <int D, Rows ROWS, bool FOUR>
 struct Shape {
-  static constexpr int MR = TWO ? 256 : 128;
+  static constexpr bool TWO = ROWS == kTwo, QUAD = ROWS == kQuad;
+  static constexpr int MR = QUAD ? 32 : TWO ? 256 : 128;
   static constexpr int kCopyWarps = FOUR ? 8 : 4;
   static constexpr int kThreads = 32 * (kRowWarps + kCopyWarps + 4);
   // Who is who among the warps from 16 on.  With at most 32 rows the row warps that have any are 0, 4, 8
@@ -69,13 +73,14 @@ struct Shape {
   static constexpr int kRawCodes = kTile * (D / 2), kRawScales = kTile * (D / 16), kRawBytes = 2 * (kRawCodes + kRawScales);
   // where the 16-byte piece of a row of codes lies: turned by the row, so that 8 rows meet no bank conflict
   __device__ static constexpr int raw_piece(int row, int piece) { return piece ^ ((row >> (D == 128 ? 1 : 2)) & (D / 32 - 1)); }
-  static constexpr int RAW = FOUR ? (TWO && D == 128 ? 1 : 3) : 0;
+  static constexpr int RAW = !FOUR ? 0 : D == 64 ? 3 : TWO ? 1 : QUAD ? 2 : 3;
   static constexpr int kOffK = (TWO ? 2 : 1) * kTileBytes;
   static constexpr int kOffV = kOffK + RK * kTileBytes;
   static constexpr int kOffMl = kOffV + RV * kTileBytes;      // [2][2][128] (m, l) of slots and halves
   static constexpr int kOffRaw = kOffMl + 4 * 128 * 8;
   static constexpr int kOffQScale = kOffRaw + RAW * kRawBytes;  // [2][MR] scales of query rows (4-bit pages)
-  static constexpr int kOffItem = kOffQScale + (FOUR ? 2 * MR * 4 : 0);
+  static constexpr int kOffSum = kOffQScale + (FOUR ? 2 * MR * 4 : 0);  // [4][4][32][8] accumulators on their way, [32] 1 / l
+  static constexpr int kOffItem = kOffSum + (QUAD ? 4 * 4 * 32 * 8 * 4 + 32 * 4 : 0);
   static constexpr int kOffScan = kOffItem + kItems * sizeof(Item);
   static constexpr int kOffBad = (kOffScan + (kThreads / 32 + 2) * 8 + 15) / 16 * 16;
   static constexpr int kOffBar = kOffBad + kBadRing * 16;
@@ -206,12 +211,12 @@ __device__ __forceinline__ uint32_t bits16(int lo, int hi) {
   return hi > lo ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
 }
 
-template <typename T, int D, bool TWO, bool FOUR>
-__global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_kernel(const AttendParams P) {
-  using Sh = Shape<D, TWO, FOUR>;
+template <typename T, int D, Rows ROWS, bool FOUR>
+__global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_kernel(const AttendParams P) {
+  using Sh = Shape<D, ROWS, FOUR>;
   using M = typename std::conditional<FOUR, __half, T>::type;  // the matrix instructions' type
   constexpr int MR = Sh::MR, RK = Sh::RK, RV = Sh::RV, KT = D / 16, THREADS = Sh::kThreads;
-  constexpr bool AHEAD = Sh::AHEAD;
+  constexpr bool AHEAD = Sh::AHEAD, TWO = Sh::TWO, QUAD = Sh::QUAD;
   extern __shared__ __align__(1024) char smem[];
   const Pages& pg = P.pages;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -605,7 +610,10 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
       // (rows past the item's keep what was there: they only reach rows of S that nobody reads)
       if (!FOUR && P.scale_log2 >= 0.f) {  // as they are
 #pragma unroll 4
-        for (int r = t2 / CH; r < rows; r += AT) copy_async<16>(smem_addr(target(r)), source(r), true);
+        for (int r = t2 / CH; r < rows; r += AT) {
+#pragma unroll
+          for (int q = 0; q < (QUAD ? 4 : 1); ++q) copy_async<16>(smem_addr(target(r + 32 * q)), source(r), true);
+        }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(q_full)) : "memory");
       } else {
         constexpr int AHEAD = 4;
@@ -643,7 +651,11 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
 #pragma unroll
               for (int e = 0; e < 4; ++e) y[e] ^= 0x80008000u;
             }
-            if (r < rows) *reinterpret_cast<uint4*>(target(r)) = make_uint4(y[0], y[1], y[2], y[3]);
+            if (r < rows) {
+#pragma unroll
+              for (int q = 0; q < (QUAD ? 4 : 1); ++q)
+                *reinterpret_cast<uint4*>(target(r + 32 * q)) = make_uint4(y[0], y[1], y[2], y[3]);
+            }
           }
         }
         fence_proxy_async_smem();
@@ -655,11 +667,15 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
     copy_commit();
     copy_wait<0>();
   } else {
-    // ---- rows: threads 128 half + row of a slot hold columns 64 half ... of the slot's row
-    const int slot = warp / 8, half = (warp / 4) % 2, row = tid % 128;
+    // ---- rows: threads 128 half + row of a slot hold columns 64 half ... of the slot's row.  With 32 rows
+    // (QUAD) every row is in each quarter of the lanes; quarter q holds its slots 32 q ..., 16 for
+    // each half, with weights of 0 for the others', and accumulates them apart, under a reference of
+    // its own: all threads then have a part of every tile.
+    const int slot = warp / 8, half = (warp / 4) % 2, quarter = warp % 4;
+    const int spot = tid % 128, row = QUAD ? lane : spot;  // spot: the lane of tensor memory
     const uint32_t lanes = static_cast<uint32_t>((warp % 4) * 32) << 16;
-    const uint32_t s_at = tmem + lanes + slot * 128 + half * 64, o_at = tmem + lanes + Sh::o_column(slot);
-    const uint32_t p_at = tmem + lanes + Sh::p_column(slot) + half * Sh::kHalfP;
+    const uint32_t s_at = tmem + lanes + slot * 128 + (QUAD ? quarter * 32 + half * 16 : half * 64), o_at = tmem + lanes + Sh::o_column(slot);
+    const uint32_t p_at = tmem + lanes + Sh::p_column(slot) + (QUAD ? half * 8 : half * Sh::kHalfP);
     const int pair = 2 + slot * 4 + warp % 4;  // named barrier of the two warps that share rows
     float2* const s_ml = reinterpret_cast<float2*>(smem + Sh::kOffMl);
     uint32_t s_phase = 0, o_phase = 0;
@@ -703,7 +719,7 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
         return see;
       };
 
-      const bool active = (warp % 4) * 32 < rows;  // a warp without rows leaves its lanes as they are
+      const bool active = QUAD || quarter * 32 < rows;  // a warp without rows leaves its lanes as they are
       // (a scale of 0 becomes the smallest one, so that a masked score stays infinite; the sign is in
       // the staged queries)
       float c = P.scale_log2 == 0.f ? 1.4e-45f : fabsf(P.scale_log2);
@@ -724,7 +740,12 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
         uint32_t seen[2] = {~0u, ~0u};
         bool poisoned = false;  // the row sees a slot on a page out of range
         partial = partial || (rows > 0 && (bads.x | bads.y | bads.z | bads.w) != 0);
-        if (partial && active) {
+        if (QUAD && partial) {
+          seen[0] = sees16((t_lo + t) * kUnit + 2 * quarter + half);
+          const uint32_t mine = quarter == 0 ? bads.x : quarter == 1 ? bads.y : quarter == 2 ? bads.z : bads.w;
+          poisoned = (seen[0] & (mine >> (16 * half))) != 0;
+          __syncwarp();
+        } else if (partial && active) {
           const int step0 = (t_lo + t) * kUnit + half * (kUnit / 2);
 #pragma unroll 1
           for (int x = 0; x < 4; ++x) {
@@ -742,7 +763,14 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
             for (int e = 0; e < 16; ++e) r[e] = (see >> e) & 1u ? r[e] : hidden;
           }
         };
-        if (active) {
+        if constexpr (QUAD) {
+          tmem_load(s_at, r[0]);
+          tmem_load_wait(r[0]);
+          mask_scores(0, r[0]);
+#pragma unroll
+          for (int e = 0; e < 16; e += 2) top = max3(top, __uint_as_float(r[0][e]), __uint_as_float(r[0][e + 1]));
+          top *= c;
+        } else if (active) {
 #pragma unroll
           for (int h2 = 0; h2 < 2; ++h2) {  // 32 columns at a time
             tmem_load(s_at + 32 * h2, r[0]);
@@ -765,9 +793,9 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
         }
         if (active) {
           if (pair_any(pair, top > m + kSlack)) {  // (also where m is still -inf) the reference moves
-            s_ml[(slot * 2 + half) * 128 + row].x = top;
+            s_ml[(slot * 2 + half) * 128 + spot].x = top;
             asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-            top = fmaxf(fmaxf(m, top), s_ml[(slot * 2 + (half ^ 1)) * 128 + row].x);
+            top = fmaxf(fmaxf(m, top), s_ml[(slot * 2 + (half ^ 1)) * 128 + spot].x);
             const float alpha = m == top ? 1.f : ex2(m - (top == -kInf ? 0.f : top));
             m = top;
             l *= alpha;
@@ -788,12 +816,14 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
           // (two at a time: packed fp32 products and sums, rounded as the scalar ones)
           const unsigned long long c2 = f2pack(c, c), base2 = f2pack(-base, -base);
           unsigned long long sum2[2] = {0ull, 0ull};
-          tmem_load(s_at, r[0]);
+          if constexpr (!QUAD) tmem_load(s_at, r[0]);
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            tmem_load_wait(r[ch & 1]);
-            if (ch < 3) tmem_load(s_at + 16 * (ch + 1), r[(ch + 1) & 1]);
-            mask_scores(ch, r[ch & 1]);
+          for (int ch = 0; ch < (QUAD ? 1 : 4); ++ch) {
+            if constexpr (!QUAD) {
+              tmem_load_wait(r[ch & 1]);
+              if (ch < 3) tmem_load(s_at + 16 * (ch + 1), r[(ch + 1) & 1]);
+              mask_scores(ch, r[ch & 1]);
+            }
             uint32_t p[8];
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
@@ -803,7 +833,17 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
               sum2[(e >> 1) & 1] = f2add(sum2[(e >> 1) & 1], f2pack(p0, p1));
               p[e / 2] = Half16<M>::pack(p0, p1);
             }
-            tmem_store8(p_at + 8 * ch, p);
+            if constexpr (QUAD) {  // (both halves have read their scores: the pair met above)
+              const uint32_t none[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const uint32_t at = p_at + (q & 1) * 16 + (q >> 1) * Sh::kHalfP;
+                if (q == quarter) tmem_store8(at, p);
+                else tmem_store8(at, none);
+              }
+            } else {
+              tmem_store8(p_at + 8 * ch, p);
+            }
           }
           float s0, s1;
           f2unpack(f2add(sum2[0], sum2[1]), s0, s1);
@@ -851,7 +891,7 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
         o_phase ^= 1;
         fence_after();
       }
-      s_ml[(slot * 2 + half) * 128 + row] = make_float2(m, l);
+      s_ml[(slot * 2 + half) * 128 + spot] = make_float2(m, l);
       fence_before();
       // the halves of a row meet, and where both slots hold the same rows, the slots too
       if constexpr (TWO)
@@ -859,9 +899,125 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
       else
         asm volatile("bar.sync 1, 512;" ::: "memory");
       fence_after();
+      const bool whole_item = it.begins && it.ends;
+      const int64_t token = static_cast<int64_t>(it.b) * P.n;
+      const int64_t part0 = (static_cast<int64_t>(blockIdx.x) * 2 + (it.begins ? 1 : 0)) * MR;
+      // 16 values d ... of this row's products with values that are not finite (rare)
+      auto add_odd = [&](int d, float (&acc)[16]) {
+        const int32_t* table = pg.table + static_cast<int64_t>(it.b) * pg.max_pages;
+#pragma unroll 1
+        for (int step = t_lo * kUnit; step < (t_lo + tiles) * kUnit; ++step) {
+          if (step / kUnit >= whole_lo && step / kUnit < whole_hi) continue;
+          for (uint32_t see = sees16(step); see != 0; see &= see - 1) {
+            const int s = slot_at(step) + __ffs(see) - 1;
+            const int page = __ldg(table + page_of(pg, s)), in_page = s - page_of(pg, s) * pg.page_size;
+            if (static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages)) continue;
+            if constexpr (FOUR) {  // only a group's scale can be NaN
+              const uint8_t sb = *reinterpret_cast<const uint8_t*>(pg.v_scales + page * pg.scale_page_stride + in_page * pg.scale_slot_stride +
+                                                                   it.h * pg.scale_head_stride + d / kGroup4);
+              if ((sb & 0x7f) == 0x7f) {
+#pragma unroll
+                for (int x = 0; x < 16; ++x) acc[x] = __int_as_float(0x7fffffff);
+              }
+            } else {
+              const T* v = reinterpret_cast<const T*>(pg.v + page * pg.page_stride + in_page * pg.slot_stride + it.h * pg.head_stride) + d;
+#pragma unroll
+              for (int x = 0; x < 16; ++x) {
+                const float f = static_cast<float>(v[x]);
+                if (!(fabsf(f) < kInf)) acc[x] += f;
+              }
+            }
+          }
+        }
+      };
+      // a row's slots that had tiles (what the others' accumulators hold says nothing)
+      const bool had0 = TWO ? jobs > 0 : tiles > 0, had1 = TWO ? jobs > 0 : tiles > 1;
+      if constexpr (QUAD) {
+        // eight sums of every row: join them over slots here, over quarters in shared memory
+        float mm[2][4], top = -kInf;
+#pragma unroll
+        for (int x = 0; x < 8; ++x) {
+          mm[x / 4][x % 4] = s_ml[x / 4 * 256 + x % 4 * 32 + lane].x;
+          top = fmaxf(top, mm[x / 4][x % 4]);
+        }
+        const float base = top == -kInf ? 0.f : top;
+        float* const s_sum = reinterpret_cast<float*>(smem + Sh::kOffSum);
+        float* const s_inv = s_sum + 4 * 4 * 32 * 8;
+        if (warp == 0) {
+          float sum = 0.f;
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const float2* const at = s_ml + x / 4 * 256 + x % 4 * 32 + lane;
+            sum += ex2(mm[x / 4][x % 4] - base) * (at[0].y + at[128].y);
+          }
+          const bool none = sum == 0.f || me >= it.nq;
+          s_inv[lane] = none ? 0.f : pg.v_scale / sum;
+          if (row < rows && me < P.n) {
+            if (whole_item) {
+              if (P.lse)
+                P.lse[(token + me) * P.Hq + it.h * P.G + row0 + row - me * P.G] =
+                    !it.ok ? __int_as_float(0x7fffffff) : none ? -kInf : top * kLn2 + logf(sum);
+            } else {
+              P.part_ml[part0 + row] = make_float2(top, sum);
+            }
+          }
+        }
+        const int group = slot * 2 + half;
+        const float scale0 = had0 ? ex2(s_ml[quarter * 32 + lane].x - base) : 0.f, scale1 = had1 ? ex2(s_ml[256 + quarter * 32 + lane].x - base) : 0.f;
+        // afterwards: thread 128 g + 4 row + k sums values 2 k, 2 k + 1 of the 8 of group g
+        const int sum_row = spot / 4, sum_me = query_of(P, row0 + sum_row);
+        const int sum_head = it.h * P.G + row0 + sum_row - sum_me * P.G;
+        const bool writes = sum_row < rows && sum_me < P.n;
+#pragma unroll 1
+        for (int d = 0; d < D / 4; d += 16) {
+          float acc[16];
+          uint32_t x[16];
+          const uint32_t at = tmem + lanes + group * (D / 4) + d;
+#pragma unroll
+          for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+          if (had0) {
+            tmem_load(at + Sh::o_column(0), x);
+            tmem_load_wait(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] = __uint_as_float(x[e]) * scale0;
+          }
+          if (had1) {
+            tmem_load(at + Sh::o_column(1), x);
+            tmem_load_wait(x);
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[e] = fmaf(__uint_as_float(x[e]), scale1, acc[e]);
+          }
+          if (*s_odd != 0 && quarter == 0 && row < rows && me < P.n) add_odd(group * (D / 4) + d, acc);
+#pragma unroll
+          for (int u = 0; u < 2; ++u) {
+            float4* const to = reinterpret_cast<float4*>(s_sum + ((quarter * 4 + group) * 32 + lane) * 8);
+            to[0] = make_float4(acc[8 * u], acc[8 * u + 1], acc[8 * u + 2], acc[8 * u + 3]);
+            to[1] = make_float4(acc[8 * u + 4], acc[8 * u + 5], acc[8 * u + 6], acc[8 * u + 7]);
+            asm volatile("bar.sync 1, 512;" ::: "memory");
+            const float* const from = s_sum + (group * 32 + sum_row) * 8 + (spot % 4) * 2;
+            float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const float2 y = *reinterpret_cast<const float2*>(from + q * (4 * 32 * 8));
+              v.x += y.x;
+              v.y += y.y;
+            }
+            const int column = group * (D / 4) + d + 8 * u + (spot % 4) * 2;
+            if (writes) {
+              if (whole_item) {
+                const float inv = s_inv[sum_row];
+                const uint32_t two = inv == 0.f ? 0u : Half16<T>::pack(v.x * inv, v.y * inv);
+                *reinterpret_cast<uint32_t*>(static_cast<T*>(P.out) + ((token + sum_me) * P.Hq + sum_head) * D + column) = it.ok ? two : 0x7fff7fffu;
+              } else {
+                *reinterpret_cast<float2*>(P.part_o + (part0 + sum_row) * D + column) = v;
+              }
+            }
+            asm volatile("bar.sync 1, 512;" ::: "memory");
+          }
+        }
+      } else {
       l = s_ml[slot * 256 + row].y + s_ml[slot * 256 + 128 + row].y;
       float scale_own = 1.f, scale_other = 0.f;
-      const int other_jobs = TWO ? 0 : (slot == 0 ? tiles / 2 : (tiles + 1) / 2);
       if constexpr (!TWO) {
         const int o = (slot ^ 1) * 256 + row;
         const float other = s_ml[o].x, other_l = s_ml[o].y + s_ml[o + 128].y;
@@ -873,10 +1029,8 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
       }
       __syncwarp();
       const bool mine = row < rows && me < P.n;
-      const bool whole_item = it.begins && it.ends;
-      const int head = it.h * P.G + row0 + row - me * P.G;
-      const int64_t at = (static_cast<int64_t>(it.b) * P.n + me) * P.Hq + head;
-      const int64_t part = (static_cast<int64_t>(blockIdx.x) * 2 + (it.begins ? 1 : 0)) * MR + (TWO ? slot * 128 : 0) + row;
+      const int64_t at = (token + me) * P.Hq + it.h * P.G + row0 + row - me * P.G;
+      const int64_t part = part0 + (TWO ? slot * 128 : 0) + row;
       const bool none = l == 0.f || me >= it.nq;
       const float inv = none ? 0.f : pg.v_scale / l;
       constexpr int COLS = TWO ? D / 2 : D / 4;  // of this thread
@@ -895,39 +1049,13 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[e] = __uint_as_float(r[e]) * scale_own;
           }
-          if (!TWO && other_jobs > 0) {
+          if (!TWO && (slot == 0 ? had1 : had0)) {
             tmem_load(tmem + lanes + Sh::o_column(slot ^ 1) + d, r);
             tmem_load_wait(r);
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[e] = fmaf(__uint_as_float(r[e]), scale_other, acc[e]);
           }
-          if (*s_odd != 0 && mine) {  // rare: values that are not finite, for the rows that see them
-            const int32_t* table = pg.table + static_cast<int64_t>(it.b) * pg.max_pages;
-#pragma unroll 1
-            for (int step = t_lo * kUnit; step < (t_lo + tiles) * kUnit; ++step) {
-              if (step / kUnit >= it.whole_lo[slot] && step / kUnit < it.whole_hi[slot]) continue;
-              for (uint32_t see = sees16(step); see != 0; see &= see - 1) {
-                const int s = slot_at(step) + __ffs(see) - 1;
-                const int page = __ldg(table + page_of(pg, s)), in_page = s - page_of(pg, s) * pg.page_size;
-                if (static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages)) continue;
-                if constexpr (FOUR) {  // only a group's scale can be NaN
-                  const uint8_t sb = *reinterpret_cast<const uint8_t*>(pg.v_scales + page * pg.scale_page_stride + in_page * pg.scale_slot_stride +
-                                                                       it.h * pg.scale_head_stride + d / kGroup4);
-                  if ((sb & 0x7f) == 0x7f) {
-#pragma unroll
-                    for (int x = 0; x < 16; ++x) acc[x] = __int_as_float(0x7fffffff);
-                  }
-                } else {
-                  const T* v = reinterpret_cast<const T*>(pg.v + page * pg.page_stride + in_page * pg.slot_stride + it.h * pg.head_stride) + d;
-#pragma unroll
-                  for (int x = 0; x < 16; ++x) {
-                    const float f = static_cast<float>(v[x]);
-                    if (!(fabsf(f) < kInf)) acc[x] += f;
-                  }
-                }
-              }
-            }
-          }
+          if (*s_odd != 0 && mine) add_odd(d, acc);
           if (!mine) continue;
           if (whole_item) {
             uint32_t out[8];
@@ -953,6 +1081,7 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
           }
         }
       }
+      }
       tile_base += tiles;
       fence_before();
       const bool last = it.last != 0;
@@ -970,21 +1099,26 @@ __global__ void __launch_bounds__(Shape<D, TWO, FOUR>::kThreads, 1) attend_tc_ke
   if (tid == 0) P.gave_up[blockIdx.x] = *gave_up;
 }
 
-template <typename T, int D, bool TWO, bool FOUR>
+template <typename T, int D, Rows ROWS, bool FOUR>
 cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
-  using Sh = Shape<D, TWO, FOUR>;
-  auto kernel = attend_tc_kernel<T, D, TWO, FOUR>;
+  using Sh = Shape<D, ROWS, FOUR>;
+  auto kernel = attend_tc_kernel<T, D, ROWS, FOUR>;
   static_assert(Sh::kBytes <= 227 * 1024, "shared memory of a CTA");
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes); e != cudaSuccess)
     return e;
   return launch_kernel(kernel, dim3(P.ctas), dim3(Sh::kThreads), Sh::kBytes, stream, 1, P);
 }
 
+template <typename T, int D, bool FOUR>
+cudaError_t launch_rows(const AttendParams& P, int mr, cudaStream_t stream) {
+  return mr == 32    ? launch_shape<T, D, kQuad, FOUR>(P, stream)
+         : mr == 128 ? launch_shape<T, D, kOne, FOUR>(P, stream)
+                     : launch_shape<T, D, kTwo, FOUR>(P, stream);
+}
+
 template <typename T, bool FOUR>
 cudaError_t launch_typed(const AttendParams& P, int mr, cudaStream_t stream) {
-  if (P.pages.head_dim == 64)
-    return mr == 256 ? launch_shape<T, 64, true, FOUR>(P, stream) : launch_shape<T, 64, false, FOUR>(P, stream);
-  return mr == 256 ? launch_shape<T, 128, true, FOUR>(P, stream) : launch_shape<T, 128, false, FOUR>(P, stream);
+  return P.pages.head_dim == 64 ? launch_rows<T, 64, FOUR>(P, mr, stream) : launch_rows<T, 128, FOUR>(P, mr, stream);
 }
 
 }  // namespace tc
