@@ -538,15 +538,30 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
       const bool last = it.last != 0;
       __syncwarp();
       if (lane == 0) mbar_arrive(it_empty + n % kItems);
-      // warp w of the two brings slots 64 w ... of a tile; lane l looks up slots l and 32 + l of them
+      // warp w of the two brings slots 64 w ... of a tile; lane l looks up slots l and 32 + l of them, a
+      // tile ahead
       int raw_t = it.t_lo;
+      const int raw_end = it.t_lo + it.tiles;
+      Range R;
+      R.sink_steps = it.sink_steps;
+      R.first_step = it.first_step;
+      const int32_t* const table = pg.table + static_cast<int64_t>(b) * pg.max_pages;
+      auto raw_slot = [&](int t, int x) {  // -1: no query of the item sees it
+        const int step = t * kUnit + t2 / 32 * 4 + x * 2 + lane / kStep, s = R.slot(step) + lane % kStep;
+        return t < raw_end && step < it.steps && s < it.end && (s >= it.lo || s < it.sinks) ? s : -1;
+      };
+      int raw_page[2] = {0, 0};
+      auto raw_lookup = [&](int t) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int s = raw_slot(t, x);
+          raw_page[x] = s >= 0 ? __ldg(table + page_of(pg, s)) : 0;
+        }
+      };
+      if constexpr (FOUR) raw_lookup(raw_t);
       auto copy_raw = [&](int until) {
         if constexpr (FOUR) {
           constexpr int RAW = Sh::RAW, CPR = D / 32;  // CPR: 16-byte pieces of a row of codes
-          Range R;
-          R.sink_steps = it.sink_steps;
-          R.first_step = it.first_step;
-          const int32_t* const table = pg.table + static_cast<int64_t>(b) * pg.max_pages;
           const char* const k_head = pg.k + h * pg.head_stride;
           const char* const v_head = pg.v + h * pg.head_stride;
           const char* const ks_head = pg.k_scales + h * pg.scale_head_stride;
@@ -559,17 +574,17 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
             const int rs = raw_tile % RAW;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const int step = raw_t * kUnit + w2 * 4 + x * 2 + lane / kStep, s = R.slot(step) + lane % kStep;
-              const bool want = step < it.steps && s < it.end && (s >= it.lo || s < it.sinks);
-              const int logical = page_of(pg, want ? s : 0), in_page = (want ? s : 0) - logical * pg.page_size;
-              const int page = want ? __ldg(table + logical) : 0;
-              const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
+              const int s = raw_slot(raw_t, x), page = raw_page[x];
+              const bool bad = s >= 0 && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
+              const bool there = s >= 0 && !bad;
+              const int in_page = there ? s - page_of(pg, s) * pg.page_size : 0;
               const uint32_t bads = __ballot_sync(0xffffffffu, bad);
-              present[x] = __ballot_sync(0xffffffffu, want && !bad);
-              off[x] = want && !bad ? page * pg.page_stride + in_page * pg.slot_stride : 0;
-              soff[x] = want && !bad ? page * pg.scale_page_stride + in_page * pg.scale_slot_stride : 0;
+              present[x] = __ballot_sync(0xffffffffu, there);
+              off[x] = there ? page * pg.page_stride + in_page * pg.slot_stride : 0;
+              soff[x] = there ? page * pg.scale_page_stride + in_page * pg.scale_slot_stride : 0;
               if (lane == 0) s_bad[(raw_tile % kBadRing) * 4 + w2 * 2 + x] = bads;
             }
+            raw_lookup(raw_t + 1);
             wait_for(raw_empty + rs, ((raw_tile / RAW) & 1) ^ 1, gave_up);
             __syncwarp();
             if (lane == 0) mbar_arrive(raw_full + rs);
