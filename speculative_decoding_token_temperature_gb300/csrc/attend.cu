@@ -23,6 +23,8 @@
 // join their rows through shared memory once per segment.  Rows of the staged keys are padded
 // by 16 bytes, so the matrix loads meet no bank conflicts.
 
+#include <algorithm>
+
 #include "attend_common.cuh"
 #include "specdec_internal.h"
 
@@ -30,7 +32,13 @@ namespace specdec {
 
 namespace {
 
-constexpr int kRows = 16;  // rows of a tile
+constexpr int kRows = 16;     // rows of a tile
+// Calls with at most this many query rows to a key head take the kernel here, others the
+// tensor-memory kernel.  Measured on either side (B requests of n tokens, 32 query and 8 key heads of
+// 128, us here / there): 4 rows, B=1, 900 slots 12.8 / 16.2; B=32, 8000 slots 122 / 120; 16 rows
+// 15.7 / 16.3 and 127 / 123; 32 rows, B=32, 8000 slots 223 / 126.  4-bit pages: 4 rows 16.1 / 17.7 and
+// 108 / 107, 16 rows 19.7 / 17.8 and 120 / 107.
+constexpr int kWarpRows = 8;
 
 __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -675,7 +683,7 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   const int64_t rows = static_cast<int64_t>(P.n) * P.G;
   const bool four = format == SPECDEC_KV4;
   const int hook = test_hook(SPECDEC_HOOK_ATTEND_KERNEL);
-  const bool tc = hook == 0 ? rows > kRows : hook == 2;
+  const bool tc = hook == 0 ? rows > kWarpRows : hook == 2;
   const int mr = tc ? attend_tc_rows(rows) : kRows;
   P.row_tiles = static_cast<int>((rows + mr - 1) / mr);
   P.ctas = attend_sms();
@@ -700,7 +708,10 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   auto join = P.pages.head_dim == 64
                   ? (dt == SPECDEC_BF16 ? attend_join_kernel<__nv_bfloat16, 64> : attend_join_kernel<__half, 64>)
                   : (dt == SPECDEC_BF16 ? attend_join_kernel<__nv_bfloat16, 128> : attend_join_kernel<__half, 128>);
-  return launch_kernel(join, dim3(P.ctas, mr / (2 * kJoinWarps)), dim3(32 * kJoinWarps), 0, stream, 1, P, int{mr});
+  // a warp a row, as far as 16 blocks to an item go
+  const int64_t item_rows = rows < mr ? rows : mr;
+  const int blocks = static_cast<int>(std::min<int64_t>((item_rows + kJoinWarps - 1) / kJoinWarps, 16));
+  return launch_kernel(join, dim3(P.ctas, blocks), dim3(32 * kJoinWarps), 0, stream, 1, P, int{mr});
 }
 
 }  // namespace specdec
