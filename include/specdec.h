@@ -462,7 +462,8 @@ int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B
  * shared by the batch: specdec_build_tree_mask's out_mask and out_depth for prefix_len 0.
  *   out[b, i, h] = sum_s p_s v_s,  p = softmax over the visible s of scale * q . k_s,
  * query head h with key head h / (q_heads / kv_heads).  Values and keys of slots that a query
- * does not see do not touch its output, whatever they hold (NaN, infinities, stale pages).
+ * does not see do not touch its output, whatever they hold (NaN, infinities, stale pages); an
+ * output that does depend on a value that is not finite is not finite (an infinity or NaN).
  *
  * q            [B, n, q_heads, D] of dtype (SPECDEC_BF16 or SPECDEC_F16), q_strides as above
  * pages        16-bit pages of the same dtype, or SPECDEC_KV4
@@ -473,6 +474,8 @@ int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B
  * that no query sees (behind a window) are not read, and their entries are not looked at.
  * Scores, statistics and sums are fp32; the weights p are rounded to 16 bits (dtype, or fp16 for
  * 4-bit pages) for the matrix products, the output once at the end.
+ * Every wait inside the kernels is bounded (one second); a call in which one runs out reports
+ * SPECDEC_STATUS_TIMEOUT for every sequence, and its outputs do not count.
  * The workspace (specdec_attend_workspace_bytes) follows the rules at the top.  The split of the
  * work follows the lengths on the device: the host reads none of them.
  * window, sinks >= 0 (window 0: no window, sinks then has no effect); q_heads a multiple of

@@ -6,9 +6,8 @@
 // grows; parts of a row computed apart join as O = sum 2^(m_a - m) O_a, l likewise.
 //
 // The n * G query rows that share a key head are one matrix (row r: query r / G, head r % G),
-// so a cached key is read once for all of them.  Row tiles of 16, 32 or 64 rows go through
-// m16n8k16 matrix instructions.  Below about 64 rows per key head the cache's bytes bound the
-// call: 4 D flop per row and slot against 4 D bytes.
+// so a cached key is read once for all of them: 4 D flop per row and slot against 4 D bytes.  Up to a
+// hundred rows or so the cache's bytes bound the call, beyond that the exponentials and products.
 //
 // Work split: an item is (sequence, row tile, key head); its visible slots, the first `sinks`
 // and the window, make steps of 16 and units of 8 steps.  Every CTA takes an equal, contiguous
@@ -17,11 +16,15 @@
 // workspace, which a second kernel, started while the first one runs, joins in a fixed order:
 // the result depends on the number of CTAs only.
 //
-// In a CTA, 8 warps: WR of them share a stream of keys and split the tile's rows, and 8 / WR
-// such groups take every (8 / WR)-th step of a segment.  Each group copies its own steps ahead
-// with 16-byte asynchronous copies, several stages deep, with no CTA-wide barrier; the groups
-// join their rows through shared memory once per segment.  Rows of the staged keys are padded
-// by 16 bytes, so the matrix loads meet no bank conflicts.
+// Two kernels do the first part.  The one here is for a few rows (kWarpRows): m16n8k16 matrix
+// instructions, each of 8 warps with a stream of slots of its own (every 8th step of a segment) and all
+// 16 rows of the tile, copied ahead with 16-byte asynchronous copies three stages deep; no barrier
+// until the warps join their rows through shared memory, once per segment.  It comes up faster than
+// the tensor-memory kernel (attend_tc.cuh), which takes all other calls, and reaches the same share of
+// HBM bandwidth on 16-bit pages: B=32, 8 key heads, 8000 slots at most, one token of 32 heads of 128
+// in 122 us, 5.4 TB/s, 0.79 of the measured copy rate.  Over 4-bit pages it is bound by the conversion of
+// codes (a conversion and a product for every two values, at 64 lanes a clock and SM): the same in
+// 108 us, 1.7 TB/s.
 
 #include <algorithm>
 

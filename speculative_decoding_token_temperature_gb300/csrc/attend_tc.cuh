@@ -1031,71 +1031,71 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
           }
         }
       } else {
-      l = s_ml[slot * 256 + row].y + s_ml[slot * 256 + 128 + row].y;
-      float scale_own = 1.f, scale_other = 0.f;
-      if constexpr (!TWO) {
-        const int o = (slot ^ 1) * 256 + row;
-        const float other = s_ml[o].x, other_l = s_ml[o].y + s_ml[o + 128].y;
-        const float top = fmaxf(m, other), base = top == -kInf ? 0.f : top;
-        scale_own = ex2(m - base);
-        scale_other = ex2(other - base);
-        l = l * scale_own + other_l * scale_other;
-        m = top;
-      }
-      __syncwarp();
-      const bool mine = row < rows && me < P.n;
-      const int64_t at = (token + me) * P.Hq + it.h * P.G + row0 + row - me * P.G;
-      const int64_t part = part0 + (TWO ? slot * 128 : 0) + row;
-      const bool none = l == 0.f || me >= it.nq;
-      const float inv = none ? 0.f : pg.v_scale / l;
-      constexpr int COLS = TWO ? D / 2 : D / 4;  // of this thread
-      const int d_lo = TWO ? half * COLS : (slot * 2 + half) * COLS;
-      if (active) {
+        l = s_ml[slot * 256 + row].y + s_ml[slot * 256 + 128 + row].y;
+        float scale_own = 1.f, scale_other = 0.f;
+        if constexpr (!TWO) {
+          const int o = (slot ^ 1) * 256 + row;
+          const float other = s_ml[o].x, other_l = s_ml[o].y + s_ml[o + 128].y;
+          const float top = fmaxf(m, other), base = top == -kInf ? 0.f : top;
+          scale_own = ex2(m - base);
+          scale_other = ex2(other - base);
+          l = l * scale_own + other_l * scale_other;
+          m = top;
+        }
+        __syncwarp();
+        const bool mine = row < rows && me < P.n;
+        const int64_t at = (token + me) * P.Hq + it.h * P.G + row0 + row - me * P.G;
+        const int64_t part = part0 + (TWO ? slot * 128 : 0) + row;
+        const bool none = l == 0.f || me >= it.nq;
+        const float inv = none ? 0.f : pg.v_scale / l;
+        constexpr int COLS = TWO ? D / 2 : D / 4;  // of this thread
+        const int d_lo = TWO ? half * COLS : (slot * 2 + half) * COLS;
+        if (active) {
 #pragma unroll 1
-        for (int d = d_lo; d < d_lo + COLS; d += 16) {
-          float acc[16];
-          uint32_t r[16];
-          __syncwarp();
+          for (int d = d_lo; d < d_lo + COLS; d += 16) {
+            float acc[16];
+            uint32_t r[16];
+            __syncwarp();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) acc[e] = 0.f;
-          if (jobs > 0) {
-            tmem_load(o_at + d, r);
-            tmem_load_wait(r);
+            for (int e = 0; e < 16; ++e) acc[e] = 0.f;
+            if (jobs > 0) {
+              tmem_load(o_at + d, r);
+              tmem_load_wait(r);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) acc[e] = __uint_as_float(r[e]) * scale_own;
-          }
-          if (!TWO && (slot == 0 ? had1 : had0)) {
-            tmem_load(tmem + lanes + Sh::o_column(slot ^ 1) + d, r);
-            tmem_load_wait(r);
-#pragma unroll
-            for (int e = 0; e < 16; ++e) acc[e] = fmaf(__uint_as_float(r[e]), scale_other, acc[e]);
-          }
-          if (*s_odd != 0 && mine) add_odd(d, acc);
-          if (!mine) continue;
-          if (whole_item) {
-            uint32_t out[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              out[e] = none ? 0u : Half16<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-              if (!it.ok) out[e] = 0x7fff7fffu;
+              for (int e = 0; e < 16; ++e) acc[e] = __uint_as_float(r[e]) * scale_own;
             }
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(P.out) + at * D + d);
-            dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
-            dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
-          } else {
-            float4* dst = reinterpret_cast<float4*>(P.part_o + part * D + d);
+            if (!TWO && (slot == 0 ? had1 : had0)) {
+              tmem_load(tmem + lanes + Sh::o_column(slot ^ 1) + d, r);
+              tmem_load_wait(r);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
+              for (int e = 0; e < 16; ++e) acc[e] = fmaf(__uint_as_float(r[e]), scale_other, acc[e]);
+            }
+            if (*s_odd != 0 && mine) add_odd(d, acc);
+            if (!mine) continue;
+            if (whole_item) {
+              uint32_t out[8];
+#pragma unroll
+              for (int e = 0; e < 8; ++e) {
+                out[e] = none ? 0u : Half16<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+                if (!it.ok) out[e] = 0x7fff7fffu;
+              }
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(P.out) + at * D + d);
+              dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
+              dst[1] = make_uint4(out[4], out[5], out[6], out[7]);
+            } else {
+              float4* dst = reinterpret_cast<float4*>(P.part_o + part * D + d);
+#pragma unroll
+              for (int e = 0; e < 4; ++e) dst[e] = make_float4(acc[4 * e], acc[4 * e + 1], acc[4 * e + 2], acc[4 * e + 3]);
+            }
+          }
+          if (mine && d_lo == 0) {
+            if (whole_item) {
+              if (P.lse) P.lse[at] = !it.ok ? __int_as_float(0x7fffffff) : none ? -kInf : m * kLn2 + logf(l);
+            } else {
+              P.part_ml[part] = make_float2(m, l);
+            }
           }
         }
-        if (mine && d_lo == 0) {
-          if (whole_item) {
-            if (P.lse) P.lse[at] = !it.ok ? __int_as_float(0x7fffffff) : none ? -kInf : m * kLn2 + logf(l);
-          } else {
-            P.part_ml[part] = make_float2(m, l);
-          }
-        }
-      }
       }
       tile_base += tiles;
       fence_before();

@@ -72,7 +72,7 @@ def test_four_bit_pages_are_checked(sd, change, code):
 @pytest.mark.parametrize("change,code", [
     (dict(q=None), 1), (dict(st=None), 1), (dict(dt=0), 1), (dict(dt=3), 1), (dict(B=0), 1), (dict(n=0), 1), (dict(hq=0), 1),
     (dict(window=-1), 1), (dict(sinks=-2), 1), (dict(scale=math.nan), 1), (dict(scale=math.inf), 1), (dict(lens=None), 1),
-    (dict(out=None), 1), (dict(ws=None), 1), (dict(wsb=16), 4), (dict(hq=12), 1), (dict(n=1 << 23), 2),
+    (dict(out=None), 1), (dict(ws=None), 1), (dict(wsb=16), 4), (dict(hq=12), 1), (dict(n=1 << 23), 2), (dict(hq=8 << 16), 2),
     (dict(st=(ctypes.c_int64 * 3)(4, 8, 8)), 2), (dict(st=(ctypes.c_int64 * 3)(8, -8, 8)), 2),
 ])
 def test_attend_refuses_bad_arguments(sd, change, code):
@@ -153,3 +153,10 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(sd):
 def test_rotation_turns_are_exact_counts(sd):
     t = sd.rotation_turns([2 * math.pi * 0.25, 2 * math.pi * 0.75, 2 * math.pi * 1.25, 0.0])
     assert t.tolist() == [1 << 62, -(1 << 62), 1 << 62, 0]
+
+
+def test_kernel_hook_values(sd):
+    assert sd.load_library().specdec_set_test_hook(sd.HOOK_ATTEND_KERNEL, 3) == sd.ERR_INVALID_ARG
+    with sd.test_hooks(attend_kernel=2):
+        assert sd.get_test_hook(sd.HOOK_ATTEND_KERNEL) == 2
+    assert sd.get_test_hook(sd.HOOK_ATTEND_KERNEL) == 0

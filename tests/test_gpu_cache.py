@@ -151,6 +151,17 @@ def test_chain_over_ragged_lengths(sd, four, dtype, hq, hkv, D, n):
 
 
 @pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("hq,n", [(1, 8), (1, 9), (1, 16), (1, 32), (1, 33), (3, 43), (1, 129), (2, 128), (1, 257), (5, 77)])
+def test_row_tiles(sd, four, D, hq, n):
+    """Query rows of a key head at and around the row tiles' borders (8, 32, 128, 256 rows), over one
+    tile of 128 slots, two and several."""
+    lens = [n, n + 100, n + 128, n + 500]
+    c = Cache(len(lens), max(lens), 16, 1, D, torch.float16, four, seed=n)
+    _run(sd, c, _q(len(lens), n, hq, D, torch.float16), lens, torch.float16, D)
+
+
+@pytest.mark.parametrize("four", [False, True])
 @pytest.mark.parametrize("page", [1, 7, 24, 64, 500])
 def test_pages_that_end_inside_a_step(sd, four, page):
     lens = [1, 6, 8, 63, 65, 333]
@@ -339,6 +350,25 @@ def test_same_inputs_give_the_same_bits_and_streams(sd):
         b = sd.attend(q, c.k, c.v, c.table, L, with_lse=True, stream=side)
         side.synchronize()
         assert all(torch.equal(a[x], b[x]) for x in a)
+
+
+def test_two_streams_at_a_time(sd):
+    """Calls on two streams, whose launches and workspaces may overlap, give what one gives."""
+    cases = []
+    for seed, n, L in ((1, 8, 3000), (2, 40, 2000)):
+        c = Cache(4, L, 16, 2, 128, torch.bfloat16, seed=seed)
+        cases.append((c, _q(4, n, 8, 128, torch.bfloat16, seed=seed), _i32([L, L // 2, n, L - 7])))
+    want = [sd.attend(q, c.k, c.v, c.table, lens, with_lse=True) for c, q, lens in cases]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(6):
+        for i, (c, q, lens) in enumerate(cases):
+            got[i].append(sd.attend(q, c.k, c.v, c.table, lens, with_lse=True, stream=streams[i]))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for r in got[i]:
+            assert all(torch.equal(r[x], want[i][x]) for x in r)
 
 
 def test_captured_in_a_graph(sd):
