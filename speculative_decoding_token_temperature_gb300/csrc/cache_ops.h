@@ -43,6 +43,7 @@ cudaError_t launch_rotate_qk(const RotateParams& P, specdec_dtype dt, cudaStream
 struct Kv4Params {
   const void *k, *v;  // append: [B, n, Hkv, D] inputs, strides in elements
   int64_t k_sb, k_st, k_sh, v_sb, v_st, v_sh;
+  float k_inv, v_inv;   // append: 1 / the tensor-wide scales, rounded to fp32
   void *k_out, *v_out;  // read: [B, n, Hkv, D] outputs
   const int32_t *context_len, *query_len;
   int B, n;

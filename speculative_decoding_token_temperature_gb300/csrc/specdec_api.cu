@@ -820,6 +820,8 @@ int specdec_append_kv4(const void* k, const int64_t* k_strides, const void* v, c
   P.v = v;
   P.k_sb = k_strides[0]; P.k_st = k_strides[1]; P.k_sh = k_strides[2];
   P.v_sb = v_strides[0]; P.v_st = v_strides[1]; P.v_sh = v_strides[2];
+  P.k_inv = 1.f / pages->k_scale;
+  P.v_inv = 1.f / pages->v_scale;
   P.context_len = context_len;
   P.query_len = query_len;
   P.B = B;

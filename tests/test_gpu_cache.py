@@ -528,6 +528,31 @@ def test_four_bit_codes_scales_and_values(sd, dtype, D, hkv, page):
         assert torch.equal(x[keep], y[keep])
 
 
+def test_four_bit_signs_of_zero_and_quotients_next_to_ties(sd):
+    """The codes are those of the IEEE quotient: -0 keeps its sign, and values a step of the type on
+    either side of a tie go to either side of it."""
+    n, hkv, D, dtype = 64, 2, 64, torch.float16
+    k, v = _q(1, n, hkv, D, dtype, std=3.0), torch.zeros(1, n, hkv, D, device=DEV, dtype=dtype)
+    k[0, :, :, 1::5], v[0, :, :, ::2] = -0.0, -0.0
+    ties = torch.tensor([.25, .75, 1.25, 1.75, 2.5, 3.5, 5.0], dtype=torch.float64)
+    steps = torch.nextafter(ties.to(dtype), torch.tensor(float("inf"), dtype=dtype)), torch.nextafter(ties.to(dtype), torch.tensor(0.0, dtype=dtype))
+    for i in range(n):
+        m = 6 * (1 + (i % 8) / 8) * 2.0 ** (i // 8 - 6)  # each mantissa of the scale
+        v[0, i, 0, :16] = torch.cat([torch.tensor([m, -m], dtype=torch.float64), *(x.double() * m / 6 for x in steps)]).to(dtype).to(DEV)
+    c = Cache(1, n, 16, hkv, D, dtype, True)
+    sd.append_kv4(k, v, c.k, c.v, c.table, _i32([n]), **c.kw)
+    torch.cuda.synchronize()
+    for x, codes, scales, ts in ((k, c.k, c.ks, c.kw["k_scale"]), (v, c.v, c.vs, c.kw["v_scale"])):
+        for i in range(n):
+            pg, off = int(c.host_table[0, i // 16]), i % 16
+            for h in range(hkv):
+                row = x[0, i, h].float().cpu().numpy()
+                want = [co.quantise_group(row[g:g + 16], ts) for g in range(0, D, 16)]
+                nib = np.concatenate([w[0] for w in want])
+                assert scales[pg, off, h].tolist() == [w[1] for w in want], (i, h)
+                assert codes[pg, off, h].tolist() == (nib[0::2] | (nib[1::2] << 4)).tolist(), (i, h)
+
+
 def test_four_bit_bad_sequences(sd):
     c = Cache(3, 40, 16, 2, 64, torch.bfloat16, True)
     t = c.table.clone()
