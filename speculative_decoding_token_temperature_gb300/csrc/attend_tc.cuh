@@ -624,10 +624,21 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
       auto target = [&](int r) { return smem + (TWO ? r / 128 * Sh::kTileBytes : 0) + tile_offset(r % 128, piece); };
       // (rows past the item's keep what was there: they only reach rows of S that nobody reads)
       if (!FOUR && P.scale_log2 >= 0.f) {  // as they are
-#pragma unroll 4
+        const int di = query_of(P, AT), dg = AT - di * P.G;
+        const int64_t on = di * P.q_st + dg * P.q_sh, wrap = P.q_st - P.G * P.q_sh;
+        const int i0 = query_of(P, row0 + t2 / CH);
+        int g = row0 + t2 / CH - i0 * P.G;
+        const T* from = q_item + i0 * P.q_st + g * P.q_sh + piece * 8;
+#pragma unroll 8
         for (int r = t2 / CH; r < rows; r += AT) {
 #pragma unroll
-          for (int q = 0; q < (QUAD ? 4 : 1); ++q) copy_async<16>(smem_addr(target(r + 32 * q)), source(r), true);
+          for (int q = 0; q < (QUAD ? 4 : 1); ++q) copy_async<16>(smem_addr(target(r + 32 * q)), from, true);
+          from += on;
+          g += dg;
+          if (g >= P.G) {
+            g -= P.G;
+            from += wrap;
+          }
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(q_full)) : "memory");
       } else {
@@ -1002,7 +1013,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
 #pragma unroll
             for (int e = 0; e < 16; ++e) acc[e] = fmaf(__uint_as_float(x[e]), scale1, acc[e]);
           }
-          if (*s_odd != 0 && quarter == 0 && row < rows && me < P.n) add_odd(group * (D / 4) + d, acc);
+          if (__builtin_expect(*s_odd != 0, 0) && quarter == 0 && row < rows && me < P.n) add_odd(group * (D / 4) + d, acc);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
             float4* const to = reinterpret_cast<float4*>(s_sum + ((quarter * 4 + group) * 32 + lane) * 8);
@@ -1070,7 +1081,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
 #pragma unroll
               for (int e = 0; e < 16; ++e) acc[e] = fmaf(__uint_as_float(r[e]), scale_other, acc[e]);
             }
-            if (*s_odd != 0 && mine) add_odd(d, acc);
+            if (__builtin_expect(*s_odd != 0, 0) && mine) add_odd(d, acc);
             if (!mine) continue;
             if (whole_item) {
               uint32_t out[8];
