@@ -210,6 +210,11 @@ __device__ __forceinline__ uint32_t bits16(int lo, int hi) {
   hi = min(max(hi, 0), kStep);
   return hi > lo ? ((1u << hi) - 1u) & ~((1u << lo) - 1u) : 0u;
 }
+// Bits lo..hi-1 of 64 slots, both clamped to 0..64.
+__device__ __forceinline__ uint64_t bits64(int lo, int hi) {
+  const uint64_t below = hi >= 64 ? ~0ull : (1ull << max(hi, 0)) - 1;
+  return lo >= 64 ? 0ull : below & (~0ull << max(lo, 0));
+}
 
 template <typename T, int D, Rows ROWS, bool FOUR>
 __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_kernel(const AttendParams P) {
@@ -772,12 +777,20 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
           poisoned = (seen[0] & (mine >> (16 * half))) != 0;
           __syncwarp();
         } else if (partial && active) {
-          const int step0 = (t_lo + t) * kUnit + half * (kUnit / 2);
+          const int step0 = (t_lo + t) * kUnit + half * (kUnit / 2), s0 = slot_at(step0);
+          if ((step0 >= it.sink_steps || step0 + 4 <= it.sink_steps) && !(tree && s0 + 64 > first)) {
+            // 64 slots in a row, and no tree node among them
+            const uint64_t near = P.window > 0 ? bits64(my_pos - (P.window - 1) - s0, 64) | bits64(0, P.sinks - s0) : ~0ull;
+            const uint64_t see = near & bits64(0, (tree ? min(first, end) : min(first + me, end - 1) + 1) - s0);
+            seen[0] = static_cast<uint32_t>(see);
+            seen[1] = static_cast<uint32_t>(see >> 32);
+          } else {
 #pragma unroll 1
-          for (int x = 0; x < 4; ++x) {
-            const uint32_t see = sees16(step0 + x) << (16 * (x & 1)), keep = 0xffff0000u >> (16 * (x & 1));
-            if (x < 2) seen[0] = (seen[0] & keep) | see;
-            else seen[1] = (seen[1] & keep) | see;
+            for (int x = 0; x < 4; ++x) {
+              const uint32_t see = sees16(step0 + x) << (16 * (x & 1)), keep = 0xffff0000u >> (16 * (x & 1));
+              if (x < 2) seen[0] = (seen[0] & keep) | see;
+              else seen[1] = (seen[1] & keep) | see;
+            }
           }
           poisoned = ((seen[0] & (half ? bads.z : bads.x)) | (seen[1] & (half ? bads.w : bads.y))) != 0;
           __syncwarp();
@@ -882,13 +895,12 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
           char* const vt = smem + Sh::kOffV + (tile % RV) * Sh::kTileBytes;
           constexpr uint32_t em = std::is_same<M, __half>::value ? 0x7c00u : 0x7f80u;
           bool found = false;
-#pragma unroll 2
+#pragma unroll 4
           for (int f = (warp % 8) * 32 + lane; f < kTile * (D / 8); f += 256) {
             uint4* const at = reinterpret_cast<uint4*>(vt + f * 16);
             uint32_t x[4] = {at->x, at->y, at->z, at->w};
-            bool here = false;
-#pragma unroll
-            for (int e = 0; e < 4; ++e) here = here || (x[e] & em) == em || (x[e] & (em << 16)) == em << 16;
+            const uint32_t top2 = __vmaxu2(__vmaxu2(x[0] & 0x7fff7fffu, x[1] & 0x7fff7fffu), __vmaxu2(x[2] & 0x7fff7fffu, x[3] & 0x7fff7fffu));
+            const bool here = (top2 & 0xffffu) >= em || top2 >= em << 16;
             if (here) {
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
