@@ -58,14 +58,17 @@ struct Shape {
   static constexpr int MR = QUAD ? 32 : TWO ? 256 : 128;
   static constexpr int kCopyWarps = FOUR ? 8 : 4;
   static constexpr int kThreads = 32 * (kRowWarps + kCopyWarps + 4);
-  // Who is who among the warps from 16 on.  With at most 32 rows the row warps that have any are 0, 4, 8
-  // and 12, all on the first of an SM's four schedulers (warp % 4): the busy warps of the other roles
-  // keep off it.
-  static constexpr int kWalker = FOUR ? 16 : 20, kMma = FOUR ? 27 : 23, kQuery0 = FOUR ? 20 : 21, kQuery1 = FOUR ? 24 : 22;
-  // 16-bit pages: 16 .. 19; 4-bit pages: 17, 18, 19, 21, 22, 23, 25, 26
+  // Who is who among the warps from 16 on.  16-bit pages: 16 .. 19 copy.  4-bit pages: 16 .. 23 convert, two
+  // on each of an SM's four schedulers (warp % 4); with at most 32 rows, where a tile's copies are the
+  // longer way, they keep off the scheduler of the two warps that copy.  (B=16, 16000 slots, D=128, us for
+  // 32, 64 and 256 rows: 103, 120 and 266 two on each, 99, 127 and 279 on three schedulers.)
+  static constexpr bool THREE = FOUR && QUAD;
+  static constexpr int kWalker = THREE ? 16 : FOUR ? 24 : 20, kMma = FOUR ? 27 : 23;
+  static constexpr int kQuery0 = THREE ? 20 : FOUR ? 25 : 21, kQuery1 = THREE ? 24 : FOUR ? 26 : 22;
   __device__ static constexpr int copy_index(int warp) {
     const int k = warp - kRowWarps;
-    return FOUR ? (k % 4 == 0 || k > 10 || k < 0 ? -1 : k / 4 * 3 + k % 4 - 1) : (k >= 0 && k < 4 ? k : -1);
+    if (THREE) return k % 4 == 0 || k > 10 || k < 0 ? -1 : k / 4 * 3 + k % 4 - 1;  // 17, 18, 19, 21, 22, 23, 25, 26
+    return k >= 0 && k < kCopyWarps ? k : -1;
   }
   static constexpr int kTileBytes = kTile * D * 2;
   static constexpr int RK = D == 64 ? 4 : (TWO || FOUR ? 2 : 3), RV = D == 64 ? 4 : 2;  // K tiles and V tiles staged
