@@ -549,21 +549,21 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
       // warp w of the two brings slots 64 w ... of a tile; lane l looks up slots l and 32 + l of them, a
       // tile ahead
       int raw_t = it.t_lo;
-      const int raw_end = it.t_lo + it.tiles;
       Range R;
       R.sink_steps = it.sink_steps;
       R.first_step = it.first_step;
       const int32_t* const table = pg.table + static_cast<int64_t>(b) * pg.max_pages;
-      auto raw_slot = [&](int t, int x) {  // -1: no query of the item sees it
-        const int step = t * kUnit + t2 / 32 * 4 + x * 2 + lane / kStep, s = R.slot(step) + lane % kStep;
-        return t < raw_end && step < it.steps && s < it.end && (s >= it.lo || s < it.sinks) ? s : -1;
-      };
-      int raw_page[2] = {0, 0};
+      int raw_page[2] = {0, 0}, raw_in[2] = {-1, -1};  // page, slot of the page (-1: no query of the item sees it)
       auto raw_lookup = [&](int t) {
 #pragma unroll
         for (int x = 0; x < 2; ++x) {
-          const int s = raw_slot(t, x);
-          raw_page[x] = s >= 0 ? __ldg(table + page_of(pg, s)) : 0;
+          const int s = R.slot(t * kUnit + t2 / 32 * 4 + x * 2 + lane / kStep) + lane % kStep;
+          raw_in[x] = -1;
+          if (s < it.end && (s >= it.lo || s < it.sinks)) {
+            const int logical = page_of(pg, s);
+            raw_page[x] = __ldg(table + logical);
+            raw_in[x] = s - logical * pg.page_size;
+          }
         }
       };
       if constexpr (FOUR) raw_lookup(raw_t);
@@ -582,10 +582,9 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
             const int rs = raw_tile % RAW;
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              const int s = raw_slot(raw_t, x), page = raw_page[x];
-              const bool bad = s >= 0 && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
-              const bool there = s >= 0 && !bad;
-              const int in_page = there ? s - page_of(pg, s) * pg.page_size : 0;
+              const int page = raw_page[x], in_page = raw_in[x];
+              const bool bad = in_page >= 0 && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
+              const bool there = in_page >= 0 && !bad;
               const uint32_t bads = __ballot_sync(0xffffffffu, bad);
               present[x] = __ballot_sync(0xffffffffu, there);
               off[x] = there ? page * pg.page_stride + in_page * pg.slot_stride : 0;
