@@ -11,7 +11,7 @@
 //
 // Work split: an item is (sequence, row tile, key head); its visible slots, the first `sinks`
 // and the window, make steps of 16 and units of 8 steps.  Every CTA takes an equal, contiguous
-// range of all units, whatever the sequences' lengths, found by a scan over the lengths on the
+// range of all units (an item counting for a few more, kItemUnits), whatever the sequences' lengths, found by a scan over the lengths on the
 // device (the host never reads them).  An item cut by a range border leaves parts in the
 // workspace, which a second kernel, started while the first one runs, joins in a fixed order:
 // the result depends on the number of CTAs only.
@@ -42,6 +42,13 @@ constexpr int kRows = 16;     // rows of a tile
 // 15.7 / 16.3 and 127 / 123; 32 rows, B=32, 8000 slots 223 / 126.  4-bit pages: 4 rows 16.1 / 17.7 and
 // 108 / 107, 16 rows 19.7 / 17.8 and 120 / 107.
 constexpr int kWarpRows = 8;
+// What an item counts for in the split besides its units: its queries' way in, its last tile's and its
+// rows' way out take about as long.  Only where there are at least as many items as CTAs: with fewer,
+// most segments end inside an item anyway.  0, 3, 4 and 8 measured (16 bits, 32 query and 8 key heads of
+// 128, us): B=64, 600 slots, one token 46.5, 40.6, 40.6, 42.3; B=32, 2000 slots, 24 tokens 58.4, 52.4,
+// 52.2, 55.3; B=64, 4000 slots, 8 tokens 127, 122, 123, 129; 24 trees of 64 nodes, 12000 slots 217, 205,
+// 200, 200; 4-bit pages, B=64, 4000 slots, 24 tokens 184, 171, 163, 151.
+constexpr int kItemUnits = 4;
 
 __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -88,7 +95,7 @@ __global__ void __launch_bounds__(32 * Stage<D, FOUR>::WARPS, 1) attend_kernel(c
   constexpr int MR = kRows, WARPS = St::WARPS, SUB = St::SUB, SLOTS = SUB * kStep, STAGES = St::STAGES, THREADS = 32 * WARPS;
   constexpr int KT = D / 16, NT = D / 8;
   extern __shared__ __align__(128) char smem[];
-  __shared__ int64_t s_scan[WARPS + 2];
+  __shared__ int64_t s_scan[WARPS + 3];
   const Pages& pg = P.pages;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
   const int64_t slots = static_cast<int64_t>(pg.max_pages) * pg.page_size;
@@ -524,7 +531,7 @@ __global__ void __launch_bounds__(32 * Stage<D, FOUR>::WARPS, 1) attend_kernel(c
       }
     }
     __syncthreads();
-    const bool begins = w.u == w.item, ends = w.seg_end() == w.item + w.units;
+    const bool begins = w.u == w.item, ends = w.ends();
     const int part = begins ? 1 : 0;  // a CTA has at most one part that goes on and one that began before
     for (int f = tid; f < MR * (D / 4); f += THREADS) {
       const int r = f / (D / 4), d = (f % (D / 4)) * 4;
@@ -692,6 +699,7 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   P.ctas = attend_sms();
   if (P.ctas <= 0) return cudaErrorInvalidDevice;
   if (P.ctas > kMaxCtas) P.ctas = kMaxCtas;
+  P.item_units = static_cast<int64_t>(P.B) * P.row_tiles * P.pages.kv_heads >= P.ctas ? kItemUnits : 0;
   char* ws = static_cast<char*>(workspace);
   P.split = reinterpret_cast<int4*>(ws);
   ws += round256(kMaxCtas * sizeof(int4));

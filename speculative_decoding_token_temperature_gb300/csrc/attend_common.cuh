@@ -68,14 +68,16 @@ template <int MR>
 __device__ __forceinline__ int tile_rows(const AttendParams& P, int rt) { return min(MR, P.n * P.G - rt * MR); }
 
 // Units of one key head's row tiles of a sequence: at least one each, so that every row is
-// written by somebody.
+// written by somebody, and P.item_units more that stand for the time an item takes besides its
+// slots.  They come last, hold no work, and no cut falls among them: a border there counts as the
+// item's end.
 template <int MR>
 __device__ __forceinline__ int item_units(const AttendParams& P, const SeqLen& S, int rt) {
   const Range r = item_range(P, S, rt * MR, tile_rows<MR>(P, rt));
-  return max(1, (r.steps + kUnit - 1) / kUnit);
+  return max(1, (r.steps + kUnit - 1) / kUnit) + P.item_units;
 }
 // A CTA's range of units and the item it starts in.  scan(): all threads of the CTA call it, with
-// shared memory for one int64_t per warp and two more.
+// shared memory for one int64_t per warp and three more.
 struct Share {
   int64_t u, end;         // units [u, end) of all
   int64_t quota, extra;   // every CTA has quota units, the first `extra` one more
@@ -100,7 +102,7 @@ __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots
     SeqLen S{};
     for (int64_t k = lo_tile; k < hi_tile; ++k) {
       if (k == lo_tile || rt == 0) S = seq_len(P.context_len, P.query_len, b, P.n, slots);
-      if (!f(b, rt, static_cast<int64_t>(item_units<MR>(P, S, rt)) * P.pages.kv_heads)) return;
+      if (!f(b, rt, item_units<MR>(P, S, rt))) return;
       if (++rt == P.row_tiles) {
         rt = 0;
         ++b;
@@ -108,8 +110,8 @@ __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots
     }
   };
   int64_t mine = 0;
-  each([&](int, int, int64_t n) {
-    mine += n;
+  each([&](int, int, int units) {
+    mine += static_cast<int64_t>(units) * P.pages.kv_heads;
     return true;
   });
   int64_t incl = mine;
@@ -139,10 +141,14 @@ __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots
   s.end = s.u + s.quota + (cta < s.extra ? 1 : 0);
   int64_t lo = before + incl - mine;
   if (s.u < s.end && s.u >= lo && s.u < lo + mine)  // exactly one thread
-    each([&](int b, int rt, int64_t n) {
+    each([&](int b, int rt, int units) {
+      const int64_t n = static_cast<int64_t>(units) * P.pages.kv_heads;
       if (s.u < lo + n) {
+        const int64_t at = s.u - lo;
+        const int left = units - static_cast<int>(at >> 32 == 0 ? static_cast<uint32_t>(at) % static_cast<uint32_t>(units) : at % units);
         sh[WARPS] = (static_cast<int64_t>(b) << 32) | rt;
         sh[WARPS + 1] = lo;
+        sh[WARPS + 2] = s.u + (left <= P.item_units ? left : 0);
         return false;
       }
       lo += n;
@@ -153,6 +159,7 @@ __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots
     s.b = static_cast<int>(sh[WARPS] >> 32);
     s.rt = static_cast<int>(sh[WARPS] & 0xffffffff);
     s.first = sh[WARPS + 1];
+    s.u = sh[WARPS + 2];
   }
   return s;
 }
@@ -171,27 +178,30 @@ struct Walk {
     const int64_t at = u - s.first;
     h = at >> 32 == 0 ? static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(units)) : static_cast<int>(at / units);
     item = s.first + static_cast<int64_t>(h) * units;
+    if (h == P.pages.kv_heads) turn();
+  }
+  __device__ __forceinline__ void turn() {  // to the next row tile's items
+    h = 0;
+    if (++rt == P.row_tiles) {
+      rt = 0;
+      ++b;
+      S = seq_len(P.context_len, P.query_len, b, P.n, slots);
+    }
+    units = item_units<MR>(P, S, rt);
   }
   __device__ __forceinline__ int64_t seg_end() const { return min(end, item + units); }
+  __device__ __forceinline__ bool ends() const { return seg_end() >= item + units - P.item_units; }  // the item, in this segment
   __device__ __forceinline__ bool next() {  // false: the range is done
     u = seg_end();
     if (u >= end) return false;
     item += units;
-    if (++h == P.pages.kv_heads) {
-      h = 0;
-      if (++rt == P.row_tiles) {
-        rt = 0;
-        ++b;
-        S = seq_len(P.context_len, P.query_len, b, P.n, slots);
-      }
-      units = item_units<MR>(P, S, rt);
-    }
+    if (++h == P.pages.kv_heads) turn();
     return true;
   }
   // The entry of the workspace's split table for a segment that begins an item and does not
   // end it: the item and the number of CTAs that hold parts of it.
   __device__ __forceinline__ int4 split(const Share& s) const {
-    const int64_t last = item + units - 1, wide = s.extra * (s.quota + 1);
+    const int64_t last = item + units - P.item_units - 1, wide = s.extra * (s.quota + 1);
     const int64_t owner = last < wide ? last / (s.quota + 1) : s.extra + (last - wide) / s.quota;
     return make_int4(b, rt, h, static_cast<int>(owner - blockIdx.x + 1));
   }

@@ -85,7 +85,7 @@ struct Shape {
   static constexpr int kOffSum = kOffQScale + (FOUR ? 2 * MR * 4 : 0);  // [4][4][32][8] accumulators on their way, [32] 1 / l
   static constexpr int kOffItem = kOffSum + (QUAD ? 4 * 4 * 32 * 8 * 4 + 32 * 4 : 0);
   static constexpr int kOffScan = kOffItem + kItems * sizeof(Item);
-  static constexpr int kOffBad = (kOffScan + (kThreads / 32 + 2) * 8 + 15) / 16 * 16;
+  static constexpr int kOffBad = (kOffScan + (kThreads / 32 + 3) * 8 + 15) / 16 * 16;
   static constexpr int kOffBar = kOffBad + kBadRing * 16;
   static constexpr int kBars = 2 * (RK + RV + RAW) + 2 + 2 + 2 + 2 + 2 * kItems + 1;
   static constexpr int kOffMisc = kOffBar + kBars * 8;
@@ -309,7 +309,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
         const Range R = item_range(P, w.S, row0, rows);
         const int t_lo = static_cast<int>(w.u - w.item);
         const int t_hi = min(static_cast<int>(w.seg_end() - w.item), (R.steps + kUnit - 1) / kUnit);
-        const bool begins = w.u == w.item, ends = w.seg_end() == w.item + w.units;
+        const bool begins = w.u == w.item, ends = w.ends();
         it.b = w.b;
         it.h = w.h;
         it.row0 = row0;
