@@ -11,10 +11,10 @@
 //
 // Work split: an item is (sequence, row tile, key head); its visible slots, the first `sinks`
 // and the window, make steps of 16 and units of 8 steps.  Every CTA takes an equal, contiguous
-// range of all units (an item counting for a few more, kItemUnits), whatever the sequences' lengths, found by a scan over the lengths on the
-// device (the host never reads them).  An item cut by a range border leaves parts in the
-// workspace, which a second kernel, started while the first one runs, joins in a fixed order:
-// the result depends on the number of CTAs only.
+// range of all units (an item counting for a few more, kItemUnits), whatever the sequences' lengths,
+// found by a scan over the lengths on the device (the host never reads them).  An item cut by a range
+// border leaves parts in the workspace, which a second kernel, started while the first one runs, joins in
+// a fixed order: the result depends on the number of CTAs only.
 //
 // Two kernels do the first part.  The one here is for a few rows (kWarpRows): m16n8k16 matrix
 // instructions, each of 8 warps with a stream of slots of its own (every 8th step of a segment) and all
@@ -22,9 +22,9 @@
 // until the warps join their rows through shared memory, once per segment.  It comes up faster than
 // the tensor-memory kernel (attend_tc.cuh), which takes all other calls, and reaches the same share of
 // HBM bandwidth on 16-bit pages: B=32, 8 key heads, 8000 slots at most, one token of 32 heads of 128
-// in 122 us, 5.4 TB/s, 0.79 of the measured copy rate.  Over 4-bit pages it is bound by the conversion of
+// in 117 us, 5.6 TB/s, 0.83 of the measured copy rate.  Over 4-bit pages it is bound by the conversion of
 // codes (a conversion and a product for every two values, at 64 lanes a clock and SM): the same in
-// 108 us, 1.7 TB/s.
+// 99 us, 1.9 TB/s.
 
 #include <algorithm>
 
@@ -36,11 +36,13 @@ namespace specdec {
 namespace {
 
 constexpr int kRows = 16;     // rows of a tile
-// Calls with at most this many query rows to a key head take the kernel here, others the
-// tensor-memory kernel.  Measured on either side (B requests of n tokens, 32 query and 8 key heads of
-// 128, us here / there): 4 rows, B=1, 900 slots 12.8 / 16.2; B=32, 8000 slots 122 / 120; 16 rows
-// 15.7 / 16.3 and 127 / 123; 32 rows, B=32, 8000 slots 223 / 126.  4-bit pages: 4 rows 16.1 / 17.7 and
-// 108 / 107, 16 rows 19.7 / 17.8 and 120 / 107.
+// Calls with at most this many query rows to a key head take the kernel here, unless heads of 128 make at
+// least an item for every CTA; others the tensor-memory kernel.  Measured on either side (B requests of
+// n tokens, 32 query and 8 key heads, us here / there).  128 values: 4 rows, B=1, 900 slots 13.1 / 14.8;
+// B=16, 4000 slots 43.0 / 43.6; B=64, 600 slots 40.6 / 38.2; B=32, 8000 slots 116.5 / 115; 32 rows 210 /
+// 118.  4-bit pages: 4 rows, B=1, 900 slots 16.2 / 17.4; B=64, 600 slots 46.9 / 43.6; B=32, 8000 slots
+// 99 / 95; 32 rows 191 / 97.  64 values: 4 rows, B=4, 4000 slots 17.3 / 18.8; B=32, 8000 slots 68.4 / 68.2;
+// 4-bit pages 19.3 / 21.3 and 68.2 / 70.7; 16 rows, B=32, 8000 slots 68.8 / 68.4 and 72.3 / 70.6.
 constexpr int kWarpRows = 8;
 // What an item counts for in the split besides its units: its queries' way in, its last tile's and its
 // rows' way out take about as long.  Only where there are at least as many items as CTAs: with fewer,
@@ -693,12 +695,13 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   const int64_t rows = static_cast<int64_t>(P.n) * P.G;
   const bool four = format == SPECDEC_KV4;
   const int hook = test_hook(SPECDEC_HOOK_ATTEND_KERNEL);
-  const bool tc = hook == 0 ? rows > kWarpRows : hook == 2;
-  const int mr = tc ? attend_tc_rows(rows) : kRows;
-  P.row_tiles = static_cast<int>((rows + mr - 1) / mr);
   P.ctas = attend_sms();
   if (P.ctas <= 0) return cudaErrorInvalidDevice;
   if (P.ctas > kMaxCtas) P.ctas = kMaxCtas;
+  const bool items = P.pages.head_dim == 128 && static_cast<int64_t>(P.B) * P.pages.kv_heads >= P.ctas;
+  const bool tc = hook == 0 ? rows > kWarpRows || items : hook == 2;
+  const int mr = tc ? attend_tc_rows(rows) : kRows;
+  P.row_tiles = static_cast<int>((rows + mr - 1) / mr);
   P.item_units = static_cast<int64_t>(P.B) * P.row_tiles * P.pages.kv_heads >= P.ctas ? kItemUnits : 0;
   char* ws = static_cast<char*>(workspace);
   P.split = reinterpret_cast<int4*>(ws);

@@ -1004,10 +1004,15 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
         }
         const int group = slot * 2 + half;
         const float scale0 = had0 ? ex2(s_ml[quarter * 32 + lane].x - base) : 0.f, scale1 = had1 ? ex2(s_ml[256 + quarter * 32 + lane].x - base) : 0.f;
-        // afterwards: thread 128 g + 4 row + k sums values 2 k, 2 k + 1 of the 8 of group g
-        const int sum_row = spot / 4, sum_me = query_of(P, row0 + sum_row);
+        // `per` of a thread's D / 4 values at a time go through shared memory, as many as there is room for
+        // with this many rows; thread 128 g + t of group g then sums two of a row's.  (16-byte pieces turned
+        // by the row: 8 lanes meet no bank conflict.)
+        const int per = rows <= 8 && D == 128 ? 32 : rows <= 16 ? 16 : 8, turn = per / 4 - 1;
+        const int sum_row = 2 * spot / per, sum_me = query_of(P, row0 + sum_row), sum_at = 2 * spot % per;
         const int sum_head = it.h * P.G + row0 + sum_row - sum_me * P.G;
         const bool writes = sum_row < rows && sum_me < P.n;
+        const float* const from = s_sum + group * 256 + sum_row * per + ((sum_at / 4) ^ (sum_row & turn)) * 4 + sum_at % 4;
+        float* const to = s_sum + (quarter * 4 + group) * 256 + lane * per;
 #pragma unroll 1
         for (int d = 0; d < D / 4; d += 16) {
           float acc[16];
@@ -1030,11 +1035,13 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
           if (__builtin_expect(*s_odd != 0, 0) && quarter == 0 && row < rows && me < P.n) add_odd(group * (D / 4) + d, acc);
 #pragma unroll
           for (int u = 0; u < 2; ++u) {
-            float4* const to = reinterpret_cast<float4*>(s_sum + ((quarter * 4 + group) * 32 + lane) * 8);
-            to[0] = make_float4(acc[8 * u], acc[8 * u + 1], acc[8 * u + 2], acc[8 * u + 3]);
-            to[1] = make_float4(acc[8 * u + 4], acc[8 * u + 5], acc[8 * u + 6], acc[8 * u + 7]);
+            const int piece = (d + 8 * u) % per / 4;
+            if (lane * per < 256) {
+              *reinterpret_cast<float4*>(to + (piece ^ (lane & turn)) * 4) = make_float4(acc[8 * u], acc[8 * u + 1], acc[8 * u + 2], acc[8 * u + 3]);
+              *reinterpret_cast<float4*>(to + ((piece + 1) ^ (lane & turn)) * 4) = make_float4(acc[8 * u + 4], acc[8 * u + 5], acc[8 * u + 6], acc[8 * u + 7]);
+            }
+            if ((d + 8 * u + 8) % per != 0) continue;
             asm volatile("bar.sync 1, 512;" ::: "memory");
-            const float* const from = s_sum + (group * 32 + sum_row) * 8 + (spot % 4) * 2;
             float2 v = make_float2(0.f, 0.f);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -1042,7 +1049,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
               v.x += y.x;
               v.y += y.y;
             }
-            const int column = group * (D / 4) + d + 8 * u + (spot % 4) * 2;
+            const int column = group * (D / 4) + d + 8 * u + 8 - per + sum_at;
             if (writes) {
               if (whole_item) {
                 const float inv = s_inv[sum_row];
