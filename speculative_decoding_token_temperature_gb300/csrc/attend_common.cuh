@@ -76,18 +76,21 @@ __device__ __forceinline__ int item_units(const AttendParams& P, const SeqLen& S
   const Range r = item_range(P, S, rt * MR, tile_rows<MR>(P, rt));
   return max(1, (r.steps + kUnit - 1) / kUnit) + P.item_units;
 }
-// A CTA's range of units and the item it starts in.  scan(): all threads of the CTA call it, with
+// The CTAs make P.tracks rows of as many, each with its share of the key heads: CTA c is number
+// c / tracks of row c % tracks.  (One row, or one for each key head: the heads of a sequence are then read
+// side by side.)  A CTA's range of its row's units and the item it starts in.  scan(): all threads of the CTA call it, with
 // shared memory for one int64_t per warp and three more.
 struct Share {
   int64_t u, end;         // units [u, end) of all
   int64_t quota, extra;   // every CTA has quota units, the first `extra` one more
   int64_t first;          // first unit of the key heads' items of (b, rt)
-  int b, rt;
+  int b, rt, track, id;
 };
 template <int MR, int THREADS>
 __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots, int64_t* sh) {
   constexpr int WARPS = THREADS / 32;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
+  const int heads = P.tracks == 1 ? P.pages.kv_heads : 1, ctas = gridDim.x / P.tracks;
   // row tile rt of sequence b is number b * row_tiles + rt; thread t takes a run of them
   const int64_t all = static_cast<int64_t>(P.B) * P.row_tiles, per = (all + THREADS - 1) / THREADS;
   const int64_t lo_tile = min(all, tid * per), hi_tile = min(all, lo_tile + per);
@@ -111,7 +114,7 @@ __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots
   };
   int64_t mine = 0;
   each([&](int, int, int units) {
-    mine += static_cast<int64_t>(units) * P.pages.kv_heads;
+    mine += static_cast<int64_t>(units) * heads;
     return true;
   });
   int64_t incl = mine;
@@ -130,19 +133,21 @@ __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots
   }
   Share s;
   if (total >> 32 == 0) {
-    s.quota = static_cast<uint32_t>(total) / gridDim.x;
-    s.extra = static_cast<uint32_t>(total) % gridDim.x;
+    s.quota = static_cast<uint32_t>(total) / ctas;
+    s.extra = static_cast<uint32_t>(total) % ctas;
   } else {
-    s.quota = total / gridDim.x;
-    s.extra = total % gridDim.x;
+    s.quota = total / ctas;
+    s.extra = total % ctas;
   }
-  const int64_t cta = blockIdx.x;
+  s.id = blockIdx.x / P.tracks;
+  s.track = blockIdx.x - s.id * P.tracks;
+  const int64_t cta = s.id;
   s.u = cta * s.quota + min(cta, s.extra);
-  s.end = s.u + s.quota + (cta < s.extra ? 1 : 0);
+  s.end = s.id < ctas ? s.u + s.quota + (cta < s.extra ? 1 : 0) : s.u;
   int64_t lo = before + incl - mine;
   if (s.u < s.end && s.u >= lo && s.u < lo + mine)  // exactly one thread
     each([&](int b, int rt, int units) {
-      const int64_t n = static_cast<int64_t>(units) * P.pages.kv_heads;
+      const int64_t n = static_cast<int64_t>(units) * heads;
       if (s.u < lo + n) {
         const int64_t at = s.u - lo;
         const int left = units - static_cast<int>(at >> 32 == 0 ? static_cast<uint32_t>(at) % static_cast<uint32_t>(units) : at % units);
@@ -169,19 +174,22 @@ template <int MR>
 struct Walk {
   const AttendParams& P;
   int64_t slots, u, end, item;
-  int b, rt, h, units;
+  int b, rt, h, h_lo, h_hi, units;  // h_lo .. h_hi - 1: the row's key heads
   SeqLen S;
   __device__ __forceinline__ Walk(const AttendParams& p, int64_t n, const Share& s)
       : P(p), slots(n), u(s.u), end(s.end), b(s.b), rt(s.rt) {
     S = seq_len(P.context_len, P.query_len, b, P.n, slots);
     units = item_units<MR>(P, S, rt);
+    h_lo = s.track;
+    h_hi = P.tracks == 1 ? P.pages.kv_heads : h_lo + 1;
     const int64_t at = u - s.first;
-    h = at >> 32 == 0 ? static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(units)) : static_cast<int>(at / units);
-    item = s.first + static_cast<int64_t>(h) * units;
-    if (h == P.pages.kv_heads) turn();
+    const int k = at >> 32 == 0 ? static_cast<int>(static_cast<uint32_t>(at) / static_cast<uint32_t>(units)) : static_cast<int>(at / units);
+    item = s.first + static_cast<int64_t>(k) * units;
+    h = h_lo + k;
+    if (h == h_hi) turn();
   }
   __device__ __forceinline__ void turn() {  // to the next row tile's items
-    h = 0;
+    h = h_lo;
     if (++rt == P.row_tiles) {
       rt = 0;
       ++b;
@@ -195,7 +203,7 @@ struct Walk {
     u = seg_end();
     if (u >= end) return false;
     item += units;
-    if (++h == P.pages.kv_heads) turn();
+    if (++h == h_hi) turn();
     return true;
   }
   // The entry of the workspace's split table for a segment that begins an item and does not
@@ -203,7 +211,7 @@ struct Walk {
   __device__ __forceinline__ int4 split(const Share& s) const {
     const int64_t last = item + units - P.item_units - 1, wide = s.extra * (s.quota + 1);
     const int64_t owner = last < wide ? last / (s.quota + 1) : s.extra + (last - wide) / s.quota;
-    return make_int4(b, rt, h, static_cast<int>(owner - blockIdx.x + 1));
+    return make_int4(b, rt, h, static_cast<int>(owner - s.id + 1));
   }
 };
 

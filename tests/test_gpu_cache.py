@@ -291,6 +291,15 @@ def test_many_short_sequences(sd):
     _run(sd, c, _q(700, 2, 2, 64, torch.bfloat16), lens, torch.bfloat16, 64, nq=nq)
 
 
+@pytest.mark.parametrize("four", [False, True])
+@pytest.mark.parametrize("hkv,G,n,D", [(19, 2, 3, 64), (20, 1, 5, 64), (161, 1, 2, 64), (40, 1, 2, 128)])
+def test_key_heads_that_do_or_do_not_divide_the_gpu(sd, four, hkv, G, n, D):
+    lens = [700, 0, 33, 260, 129]
+    dtype = torch.bfloat16
+    c = Cache(len(lens), max(lens), 16, hkv, D, dtype, four)
+    _run(sd, c, _q(len(lens), n, hkv * G, D, dtype), lens, dtype, D, nq=[min(n, L) for L in lens])
+
+
 def test_prompt_chunks(sd):
     for four in (False, True):
         c = Cache(2, 700, 32, 1, 64, torch.bfloat16, four)
