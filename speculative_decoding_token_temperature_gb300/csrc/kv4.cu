@@ -11,7 +11,11 @@
 // A CTA takes some tokens of a sequence and up to 256 of a token's columns (16 values to write, 8 to
 // read); a thread keeps its column for kSteps tokens, so that what is left to do for each is the work on
 // its values: the tokens' places in the pages stand in shared memory, and a thread adds its column's.
-// Bound by instructions.  y / s is the IEEE quotient from one reciprocal per group: with r = RN(1/s) and
+// 8180 tokens of 8 key heads of 128 in fp16 are written in 14.7 us (42.9 MB, 2.9 TB/s) and read back in
+// 12.5 us (43 %, then 54 % of the issue slots): bound by instructions, and by the ramp of so short a
+// kernel.  One group a thread with its place worked out for each took 19.7 and 14.0 us; four tokens a
+// thread against two 25.2 and 29.4 us for the pair, eight 25.3.  Few tokens are bound by latency: 512
+// tokens take 6.5 us a call.  y / s is the IEEE quotient from one reciprocal per group: with r = RN(1/s) and
 // q = RN(y r), RN(q + RN(y - q s) r) is the correct rounding of y / s (P. Markstein, "Computation of
 // elementary functions on the IBM RISC System/6000 processor", 1990; s has 4 significant bits, and all
 // significands of y and s agree): 3 operations for each value.

@@ -12,7 +12,9 @@
 // rotation needs no exchange, and a lane's 4 pairs are the same for every head, so that its sines,
 // cosines and weights stay in registers.  A warp's rows are a token's heads; 1 to 8 warps share a
 // token, the more the fewer tokens there are: a few tokens are bound by latency and want the rows
-// side by side, prompts by instructions and want the angles computed once.
+// side by side, prompts by instructions and want the angles computed once.  8193 tokens of 28 query and
+// 4 key heads of 128 in bf16 (151 MB read and written) take 32.3 us, 4.7 TB/s: 52 % of the issue slots,
+// 41 % of HBM (most of what is written stays in L2).
 
 #include "cache_device.cuh"
 #include "specdec_device.cuh"
@@ -196,6 +198,8 @@ template <typename T, int D>
 cudaError_t launch_typed(const RotateParams& P, cudaStream_t stream) {
   // warps that share a token: enough warps to fill the GPU (152 SMs of 48 warps and more)
   const int64_t tokens = static_cast<int64_t>(P.B) * P.n;
+  // (8193 tokens of 36 heads: 36 us with one warp a token, 45.6 with two, 51.8 with four; a few hundred
+  // tokens are latency, and one warp would go through all the heads by itself)
   const int wpt = tokens < 1024 ? 8 : tokens < 2048 ? 4 : tokens < 4096 ? 2 : 1;
   const int per_cta = kRotateWarps / wpt;
   const dim3 grid(static_cast<unsigned>((P.n + per_cta - 1) / per_cta), static_cast<unsigned>(P.B));
