@@ -381,24 +381,24 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
       const int32_t* table = pg.table + static_cast<int64_t>(it.b) * pg.max_pages;
       const char* const k_head = pg.k + it.h * pg.head_stride;
       const char* const v_head = pg.v + it.h * pg.head_stride;
-      // this lane's slot of a tile: lane l of 4 copy warps slot 32 c + l, of 8 warps slot 16 c + l % 16
-      const int step_in_tile = FOUR ? cw : cw * 2 + lane / kStep;
-      auto slot_of = [&](int t) { return R.slot(t * kUnit + step_in_tile) + lane % kStep; };
-      auto wanted = [&](int t, int s) {  // a slot that some query of the item sees
-        return t < t_hi && t * kUnit + step_in_tile < it.steps && s < it.end && (s >= it.lo || s < it.sinks);
-      };
-      auto entry = [&](int t) {
-        const int s = slot_of(t);
-        return wanted(t, s) ? __ldg(table + page_of(pg, s)) : 0;
-      };
       if constexpr (!FOUR) {
-        int page = entry(t_lo);
+        // lane l of warp c brings slot 32 c + l of a tile; its page is looked up a tile ahead
+        int page = 0, in_page = -1;  // slot of the page (-1: no query of the item sees it)
+        auto look_up = [&](int t) {
+          const int s = R.slot(t * kUnit + cw * 2 + lane / kStep) + lane % kStep;
+          in_page = -1;
+          if (s < it.end && (s >= it.lo || s < it.sinks)) {
+            const int logical = page_of(pg, s);
+            page = __ldg(table + logical);
+            in_page = s - logical * pg.page_size;
+          }
+        };
+        look_up(t_lo);
         for (int t = t_lo; t < t_hi; ++t, ++tile) {
-          const int s = slot_of(t);
-          const bool want = wanted(t, s);
+          const bool want = in_page >= 0;
           const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
-          const int64_t off = want && !bad ? page * pg.page_stride + (s - page_of(pg, s) * pg.page_size) * pg.slot_stride : 0;
-          page = entry(t + 1);
+          const int64_t off = want && !bad ? page * pg.page_stride + in_page * pg.slot_stride : 0;
+          look_up(t + 1);
           const uint32_t present = __ballot_sync(0xffffffffu, want && !bad), bads = __ballot_sync(0xffffffffu, bad);
 #pragma unroll
           for (int kv = 0; kv < 2; ++kv) {
