@@ -38,19 +38,12 @@ namespace {
 constexpr int kRows = 16;     // rows of a tile
 // Calls with at most this many query rows to a key head take the kernel here, unless heads of 128 make at
 // least an item for every CTA; others the tensor-memory kernel.  Measured on either side (B requests of
-// n tokens, 32 query and 8 key heads, us here / there).  128 values: 4 rows, B=1, 900 slots 13.1 / 14.8;
-// B=16, 4000 slots 43.0 / 43.6; B=64, 600 slots 40.6 / 38.2; B=32, 8000 slots 116.5 / 115; 32 rows 210 /
+// n tokens, 32 query and 8 key heads, us here / there).  128 values: 4 rows, B=1, 900 slots 13.1 / 15.0;
+// B=16, 4000 slots 38.8 / 43.8; B=64, 600 slots 40.1 / 36.2; B=32, 8000 slots 116 / 114; 32 rows 210 /
 // 118.  4-bit pages: 4 rows, B=1, 900 slots 16.2 / 17.4; B=64, 600 slots 46.9 / 43.6; B=32, 8000 slots
-// 99 / 95; 32 rows 191 / 97.  64 values: 4 rows, B=4, 4000 slots 17.3 / 18.8; B=32, 8000 slots 68.4 / 68.2;
-// 4-bit pages 19.3 / 21.3 and 68.2 / 70.7; 16 rows, B=32, 8000 slots 68.8 / 68.4 and 72.3 / 70.6.
+// 99 / 95; 32 rows 191 / 97.  64 values: 4 rows, B=4, 4000 slots 15.0 / 16.4; B=32, 8000 slots 67.8 / 68.3;
+// 4-bit pages 15.5 / 19.6 and 68.2 / 70.7; 16 rows, B=32, 8000 slots 68.8 / 68.4 and 72.3 / 70.6.
 constexpr int kWarpRows = 8;
-// What an item counts for in the split besides its units: its queries' way in, its last tile's and its
-// rows' way out take about as long.  Only where there are at least as many items as CTAs: with fewer,
-// most segments end inside an item anyway.  0, 3, 4 and 8 measured (16 bits, 32 query and 8 key heads of
-// 128, us): B=64, 600 slots, one token 46.5, 40.6, 40.6, 42.3; B=32, 2000 slots, 24 tokens 58.4, 52.4,
-// 52.2, 55.3; B=64, 4000 slots, 8 tokens 127, 122, 123, 129; 24 trees of 64 nodes, 12000 slots 217, 205,
-// 200, 200; 4-bit pages, B=64, 4000 slots, 24 tokens 184, 171, 163, 151.
-constexpr int kItemUnits = 4;
 
 __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -706,7 +699,6 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   // lie side by side, and are then read at about the same time (4-bit decode of 64 requests of 16000
   // slots: 1857 MB of DRAM reads and 313 us in one row, 740 MB, the cache's bytes, and 304 us in eight; a prompt chunk 55, 52; 24 requests of 300 slots 26.1, 24.1).
   P.tracks = P.pages.kv_heads <= P.ctas && (P.ctas % P.pages.kv_heads) * 16 <= P.ctas ? P.pages.kv_heads : 1;
-  P.item_units = static_cast<int64_t>(P.B) * P.row_tiles * P.pages.kv_heads >= P.ctas ? kItemUnits : 0;
   char* ws = static_cast<char*>(workspace);
   P.split = reinterpret_cast<int4*>(ws);
   ws += round256(kMaxCtas * sizeof(int4));

@@ -11,6 +11,14 @@ namespace specdec {
 
 constexpr int kStep = 16;                 // slots of a step
 constexpr int kUnit = 8;                  // steps of a unit of the work split
+// What an item counts for in the split besides its units: its queries' way in, its last tile's and its
+// rows' way out take about as long.  0, 3, 4 and 8 measured (16 bits, 32 query and 8 key heads of 128, us):
+// B=64, 600 slots, one token 46.5, 40.6, 40.6, 42.3; B=32, 2000 slots, 24 tokens 58.4, 52.4, 52.2, 55.3;
+// B=64, 4000 slots, 8 tokens 127, 122, 123, 129; 24 trees of 64 nodes, 12000 slots 217, 205, 200, 200; 4-bit
+// pages, B=64, 4000 slots, 24 tokens 184, 171, 163, 151.  Fewer items than CTAs, 0 and 4: B=1, a prompt of
+// 1024 tokens 47.2, 42.2; B=2, 64 nodes over 5000 slots 58.7, 48.4; B=16, one token, 4000 slots 43.5, 39.5;
+// B=1, one token, 2400 slots (a unit for each CTA) 16.0, 17.0, 32000 slots 36.7, 37.3.
+constexpr int kItemUnits = 4;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // 16 (or 8, 4) bytes to shared memory, zeros where `there` is false (src is not read then).
@@ -68,13 +76,12 @@ template <int MR>
 __device__ __forceinline__ int tile_rows(const AttendParams& P, int rt) { return min(MR, P.n * P.G - rt * MR); }
 
 // Units of one key head's row tiles of a sequence: at least one each, so that every row is
-// written by somebody, and P.item_units more that stand for the time an item takes besides its
-// slots.  They come last, hold no work, and no cut falls among them: a border there counts as the
-// item's end.
+// written by somebody, and kItemUnits more.  Those come last, hold no work, and no cut falls
+// among them: a border there counts as the item's end.
 template <int MR>
 __device__ __forceinline__ int item_units(const AttendParams& P, const SeqLen& S, int rt) {
   const Range r = item_range(P, S, rt * MR, tile_rows<MR>(P, rt));
-  return max(1, (r.steps + kUnit - 1) / kUnit) + P.item_units;
+  return max(1, (r.steps + kUnit - 1) / kUnit) + kItemUnits;
 }
 // The CTAs make P.tracks rows of as many, each with its share of the key heads: CTA c is number
 // c / tracks of row c % tracks.  (One row, or one for each key head: the heads of a sequence are then read
@@ -153,7 +160,7 @@ __device__ __forceinline__ Share scan_units(const AttendParams& P, int64_t slots
         const int left = units - static_cast<int>(at >> 32 == 0 ? static_cast<uint32_t>(at) % static_cast<uint32_t>(units) : at % units);
         sh[WARPS] = (static_cast<int64_t>(b) << 32) | rt;
         sh[WARPS + 1] = lo;
-        sh[WARPS + 2] = s.u + (left <= P.item_units ? left : 0);
+        sh[WARPS + 2] = s.u + (left <= kItemUnits ? left : 0);
         return false;
       }
       lo += n;
@@ -198,7 +205,7 @@ struct Walk {
     units = item_units<MR>(P, S, rt);
   }
   __device__ __forceinline__ int64_t seg_end() const { return min(end, item + units); }
-  __device__ __forceinline__ bool ends() const { return seg_end() >= item + units - P.item_units; }  // the item, in this segment
+  __device__ __forceinline__ bool ends() const { return seg_end() >= item + units - kItemUnits; }  // the item, in this segment
   __device__ __forceinline__ bool next() {  // false: the range is done
     u = seg_end();
     if (u >= end) return false;
@@ -209,7 +216,7 @@ struct Walk {
   // The entry of the workspace's split table for a segment that begins an item and does not
   // end it: the item and the number of CTAs that hold parts of it.
   __device__ __forceinline__ int4 split(const Share& s) const {
-    const int64_t last = item + units - P.item_units - 1, wide = s.extra * (s.quota + 1);
+    const int64_t last = item + units - kItemUnits - 1, wide = s.extra * (s.quota + 1);
     const int64_t owner = last < wide ? last / (s.quota + 1) : s.extra + (last - wide) / s.quota;
     return make_int4(b, rt, h, static_cast<int>(owner - s.id + 1));
   }

@@ -67,7 +67,6 @@ struct AttendParams {
   uint64_t g_magic;  // 2^40 / G, rounded up: n * G < 2^24 rows
   int row_tiles;     // tiles of the n * G query rows that share a key head
   int tracks;        // rows of CTAs: 1, or a key head each
-  int item_units;    // units that an item counts for besides its slots
   int ctas;
   int4* split;       // workspace [ctas]: the item whose first part a CTA left, and its parts
   int* gave_up;      // workspace [ctas]: a bounded wait of the CTA ran out
