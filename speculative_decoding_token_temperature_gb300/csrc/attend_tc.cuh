@@ -28,7 +28,7 @@
 //
 // Measured (32 query and 8 key heads of 128, key bytes against the copy rate, products against the
 // matrix rate):
-//  - 64 requests, 8 tokens, up to 8190 slots in 16 bits (32 rows to a key head): 225 us, 6.0 TB/s, 0.88 of
+//  - 64 requests, 8 tokens, up to 8190 slots in 16 bits (32 rows to a key head): 222 us, 6.1 TB/s, 0.90 of
 //    the measured copy rate; HBM bounds it.
 //  - 24 trees of 64 nodes, up to 12000 slots (256 rows): 200 us, 3.8 TB/s and 0.94 PFLOP/s, 0.56 of the
 //    measured copy and 0.49 of the matrix rate.  A pair of 128-by-128 tiles takes about 4200 clocks against 2050 of products: the chain scores,
@@ -39,7 +39,7 @@
 //    cache's bytes.  A tile takes about 2400 clocks: its codes' conversion 790 at 64 lanes a clock, but
 //    with the copies in and the stores of the values (shared memory is busy for about 1500) the converting
 //    warps need 2000.
-//  - 35 rows, a window of 1024 slots, 96 requests: 59 us, 3.6 TB/s: an item is 9 tiles, and its first,
+//  - 35 rows, a window of 1024 slots, 96 requests: 60 us, 3.5 TB/s: an item is 9 tiles, and its first,
 //    partial tile, the way out of its rows and the next one's queries cost about 4 more.
 #pragma once
 
