@@ -63,6 +63,7 @@ struct Item {
   int nq, first, ok;
   int sink_steps, first_step, steps, end, lo, sinks;
   int whole_lo[2], whole_hi[2];  // tiles that every row of a slot sees whole
+  int clean_lo, clean_hi;        // tiles that every row of the item sees whole: others' values are scanned
 };
 
 // Row tiles: 32 rows, each in the four quarters of tensor memory's lanes, or 128, or two of 128.
@@ -343,6 +344,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
         it.end = R.end;
         it.lo = R.lo;
         it.sinks = R.sinks;
+        int clean_lo = 0, clean_hi = INT32_MAX;
         for (int slot = 0; slot < 2; ++slot) {
           // tile t (past the sinks) is slots 128 t - 16 off ...: it ends before `limit`, and its first slot
           // is inside the last row's window
@@ -354,9 +356,16 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
           const int off = R.sink_steps - R.first_step;
           const int lo = max(R.sink_steps, (from + kStep - 1) / kStep + off);
           const int hi = limit / kStep + off;  // steps before hi end before the limit
-          it.whole_lo[slot] = (lo + kUnit - 1) / kUnit;
-          it.whole_hi[slot] = hi < 0 ? 0 : hi / kUnit;
+          const int whole_lo = (lo + kUnit - 1) / kUnit, whole_hi = hi < 0 ? 0 : hi / kUnit;
+          it.whole_lo[slot] = whole_lo;
+          it.whole_hi[slot] = whole_hi;
+          if (slot == 0 || (TWO && r_lo < row0 + rows)) {
+            clean_lo = max(clean_lo, whole_lo);
+            clean_hi = min(clean_hi, whole_hi);
+          }
         }
+        it.clean_lo = clean_lo;
+        it.clean_hi = clean_hi;
         if (begins && !ends) P.split[blockIdx.x] = w.split(share);
         const bool more = w.next();
         it.last = more ? 0 : 1;
@@ -906,9 +915,11 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
           f2unpack(f2add(sum2[0], sum2[1]), s0, s1);
           l += poisoned ? __int_as_float(0x7fffffff) : s0 + s1;
         }
-        if (partial) {
-          // 0 times a value that is not finite is not 0: where some row does not see a slot, such
-          // values are taken out of the staged tile; the rows that see them get them at the end
+        // 0 times a value that is not finite is not 0: where some row does not see a slot, such
+        // values are taken out of the staged tile; the rows that see them get them at the end.  Two row
+        // tiles share the staged tile: the first one's warps scan it where either is partial, for their
+        // product comes before the second's.
+        if (TWO ? slot == 0 && (partial || t_lo + t < it.clean_lo || t_lo + t >= it.clean_hi) : partial) {
           wait_for(v_full + tile % RV, (tile / RV) & 1, gave_up);
           char* const vt = smem + Sh::kOffV + (tile % RV) * Sh::kTileBytes;
           constexpr uint32_t em = std::is_same<M, __half>::value ? 0x7c00u : 0x7f80u;
@@ -963,7 +974,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
         const int32_t* table = pg.table + static_cast<int64_t>(it.b) * pg.max_pages;
 #pragma unroll 1
         for (int step = t_lo * kUnit; step < (t_lo + tiles) * kUnit; ++step) {
-          if (step / kUnit >= whole_lo && step / kUnit < whole_hi) continue;
+          if (step / kUnit >= it.clean_lo && step / kUnit < it.clean_hi) continue;  // not scanned
           for (uint32_t see = sees16(step); see != 0; see &= see - 1) {
             const int s = slot_at(step) + __ffs(see) - 1;
             const int page = __ldg(table + page_of(pg, s)), in_page = s - page_of(pg, s) * pg.page_size;
