@@ -778,9 +778,10 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
       };
 
       const bool active = QUAD || quarter * 32 < rows;  // a warp without rows leaves its lanes as they are
-      // (a scale of 0 becomes the smallest one, so that a masked score stays infinite; the sign is in
-      // the staged queries)
-      float c = P.scale_log2 == 0.f ? 1.4e-45f : fabsf(P.scale_log2);
+      // (never 0, not by underflow either, so that a masked score stays infinite; the sign is in the
+      // staged queries)
+      constexpr float kLeast = 1.4e-45f;
+      float c = fmaxf(fabsf(P.scale_log2), kLeast);
       constexpr uint32_t hidden = 0xff800000u;  // -inf
       float m = -kInf, l = 0.f;
       int jobs = 0;
@@ -794,7 +795,8 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
         uint32_t r[2][16];
         float top = -kInf;
         const uint4 bads = *reinterpret_cast<const uint4*>(s_bad + (tile % kBadRing) * 4);
-        if (FOUR && !std::is_same<T, __half>::value && jobs == 0) c *= s_qscale[(n & 1) * MR + (TWO ? slot * 128 : 0) + row];
+        if (FOUR && !std::is_same<T, __half>::value && jobs == 0)
+          c = fmaxf(c * s_qscale[(n & 1) * MR + (TWO ? slot * 128 : 0) + row], kLeast);
         uint32_t seen[2] = {~0u, ~0u};
         bool poisoned = false;  // the row sees a slot on a page out of range
         partial = partial || (rows > 0 && (bads.x | bads.y | bads.z | bads.w) != 0);

@@ -68,3 +68,13 @@ def test_odd_values_under_two_row_tiles(sd, four, D, dtype, n, window, sinks):
         torch.cuda.synchronize()
         assert not r["status"].any()
         _same_places(r, c, q, lens, dtype, D, window=window, sinks=sinks)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [2, 7, 20, 40])
+@pytest.mark.parametrize("scale", [0.0, 1e-44, -1e-44, 1e-38])
+def test_scales_next_to_zero_over_four_bit_pages(sd, kernel, D, n, scale):
+    """bf16 queries below 1, whose rows carry a power of two below 1 of their own: its product with the scale
+    may vanish, and masked slots stay masked."""
+    c = base.Cache(2, 300, 16, 1, D, BF16, True)
+    base._run(sd, c, base._q(2, n, 4, D, BF16, std=0.1), [n, 299], BF16, D, scale=scale)
