@@ -463,7 +463,9 @@ int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B
  *   out[b, i, h] = sum_s p_s v_s,  p = softmax over the visible s of scale * q . k_s,
  * query head h with key head h / (q_heads / kv_heads).  Values and keys of slots that a query
  * does not see do not touch its output, whatever they hold (NaN, infinities, stale pages); an
- * output that does depend on a value that is not finite is not finite (an infinity or NaN).
+ * output that does depend on a value that is not finite is not finite (an infinity or NaN).  A
+ * visible score of -inf (an infinite key) has the weight 0; a row whose visible scores are all -inf, or
+ * one of them +inf, gives NaN and lse NaN.
  *
  * q            [B, n, q_heads, D] of dtype (SPECDEC_BF16 or SPECDEC_F16), q_strides as above
  * pages        16-bit pages of the same dtype, or SPECDEC_KV4

@@ -552,7 +552,7 @@ __global__ void __launch_bounds__(32 * Stage<D, FOUR>::WARPS, 1) attend_kernel(c
         if (l == 0.f || i >= S.nq) { lse = -kInf; inv = 0.f; }
         uint2 four = make_uint2(Half16<T>::pack(acc.x * inv, acc.y * inv), Half16<T>::pack(acc.z * inv, acc.w * inv));
         if (i >= S.nq) four = make_uint2(0u, 0u);
-        if (!S.ok) {
+        if (!S.ok || (l == 0.f && sees_some(P, S.first, S.nq, i))) {
           four = make_uint2(0x7fff7fffu, 0x7fff7fffu);
           lse = __int_as_float(0x7fffffff);
         }
@@ -634,15 +634,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps) attend_join_kernel(const Atte
     }
     const int i = query_of(P, row0 + r), head = h * P.G + row0 + r - i * P.G;
     const int64_t o_at = (static_cast<int64_t>(b) * P.n + i) * P.Hq + head;
-    const bool none = l == 0.f || i >= S.nq;
+    const bool none = l == 0.f || i >= S.nq, undefined = l == 0.f && sees_some(P, S.first, S.nq, i);
     const float inv = none ? 0.f : pg.v_scale / l;
     uint32_t w[E / 2];
 #pragma unroll
-    for (int e = 0; e < E / 2; ++e) w[e] = none ? 0u : Half16<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+    for (int e = 0; e < E / 2; ++e) {
+      w[e] = none ? 0u : Half16<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
+      if (undefined) w[e] = 0x7fff7fffu;
+    }
     uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<T*>(P.out) + o_at * D) + lane * (E / 2);
 #pragma unroll
     for (int e = 0; e < E / 2; ++e) dst[e] = w[e];
-    if (lane == 0 && P.lse) P.lse[o_at] = none ? -kInf : m * kLn2 + logf(l);
+    if (lane == 0 && P.lse) P.lse[o_at] = undefined ? __int_as_float(0x7fffffff) : none ? -kInf : m * kLn2 + logf(l);
   }
 }
 

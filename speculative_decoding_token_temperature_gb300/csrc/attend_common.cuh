@@ -72,6 +72,20 @@ __device__ __forceinline__ Range item_range(const AttendParams& P, const SeqLen&
 __device__ __forceinline__ int node_depth(const AttendParams& P, int i) {
   return min(max(__ldg(P.depth + i), 0), P.n - 1);
 }
+// Whether query i of a sequence whose lengths fit sees any slot: tells a row whose visible scores are
+// all -inf (its softmax has no value: NaN) from one that sees nothing (zeros).  Asked where a row's
+// weights sum to 0.
+__device__ __forceinline__ bool sees_some(const AttendParams& P, int first, int nq, int i) {
+  if (i >= nq) return false;
+  if (P.tree_mask == nullptr) return true;  // itself
+  auto position = [&](int j) { return first + (P.depth ? node_depth(P, j) : j); };
+  const int pos = position(i);
+  auto near = [&](int p) { return P.window == 0 || pos - p < P.window || p < P.sinks; };
+  if (first > 0 && (near(first - 1) || near(0))) return true;  // the last slot before the tree, or the first one
+  for (int j = 0; j < nq; ++j)
+    if (__ldg(P.tree_mask + static_cast<int64_t>(i) * P.n + j) != 0 && near(position(j))) return true;
+  return false;
+}
 template <int MR>
 __device__ __forceinline__ int tile_rows(const AttendParams& P, int rt) { return min(MR, P.n * P.G - rt * MR); }
 

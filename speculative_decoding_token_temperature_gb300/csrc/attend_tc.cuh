@@ -1020,12 +1020,13 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
             sum += ex2(mm[x / 4][x % 4] - base) * (at[0].y + at[128].y);
           }
           const bool none = sum == 0.f || me >= it.nq;
-          s_inv[lane] = none ? 0.f : pg.v_scale / sum;
+          const bool undefined = !it.ok || (whole_item && sum == 0.f && sees_some(P, first, it.nq, me));
+          s_inv[lane] = undefined ? __int_as_float(0x7fffffff) : none ? 0.f : pg.v_scale / sum;
           if (row < rows && me < P.n) {
             if (whole_item) {
               if (P.lse)
                 P.lse[(token + me) * P.Hq + it.h * P.G + row0 + row - me * P.G] =
-                    !it.ok ? __int_as_float(0x7fffffff) : none ? -kInf : top * kLn2 + logf(sum);
+                    undefined ? __int_as_float(0x7fffffff) : none ? -kInf : top * kLn2 + logf(sum);
             } else {
               P.part_ml[part0 + row] = make_float2(top, sum);
             }
@@ -1082,8 +1083,8 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
             if (writes) {
               if (whole_item) {
                 const float inv = s_inv[sum_row];
-                const uint32_t two = inv == 0.f ? 0u : Half16<T>::pack(v.x * inv, v.y * inv);
-                *reinterpret_cast<uint32_t*>(static_cast<T*>(P.out) + ((token + sum_me) * P.Hq + sum_head) * D + column) = it.ok ? two : 0x7fff7fffu;
+                *reinterpret_cast<uint32_t*>(static_cast<T*>(P.out) + ((token + sum_me) * P.Hq + sum_head) * D + column) =
+                    inv == 0.f ? 0u : Half16<T>::pack(v.x * inv, v.y * inv);
               } else {
                 *reinterpret_cast<float2*>(P.part_o + (part0 + sum_row) * D + column) = v;
               }
@@ -1108,6 +1109,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
         const int64_t at = (token + me) * P.Hq + it.h * P.G + row0 + row - me * P.G;
         const int64_t part = part0 + (TWO ? slot * 128 : 0) + row;
         const bool none = l == 0.f || me >= it.nq;
+        const bool undefined = !it.ok || (mine && whole_item && l == 0.f && sees_some(P, first, it.nq, me));
         const float inv = none ? 0.f : pg.v_scale / l;
         constexpr int COLS = TWO ? D / 2 : D / 4;  // of this thread
         const int d_lo = TWO ? half * COLS : (slot * 2 + half) * COLS;
@@ -1138,7 +1140,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
 #pragma unroll
               for (int e = 0; e < 8; ++e) {
                 out[e] = none ? 0u : Half16<T>::pack(acc[2 * e] * inv, acc[2 * e + 1] * inv);
-                if (!it.ok) out[e] = 0x7fff7fffu;
+                if (undefined) out[e] = 0x7fff7fffu;
               }
               uint4* dst = reinterpret_cast<uint4*>(static_cast<T*>(P.out) + at * D + d);
               dst[0] = make_uint4(out[0], out[1], out[2], out[3]);
@@ -1151,7 +1153,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
           }
           if (mine && d_lo == 0) {
             if (whole_item) {
-              if (P.lse) P.lse[at] = !it.ok ? __int_as_float(0x7fffffff) : none ? -kInf : m * kLn2 + logf(l);
+              if (P.lse) P.lse[at] = undefined ? __int_as_float(0x7fffffff) : none ? -kInf : m * kLn2 + logf(l);
             } else {
               P.part_ml[part] = make_float2(m, l);
             }

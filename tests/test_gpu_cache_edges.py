@@ -78,3 +78,63 @@ def test_scales_next_to_zero_over_four_bit_pages(sd, kernel, D, n, scale):
     may vanish, and masked slots stay masked."""
     c = base.Cache(2, 300, 16, 1, D, BF16, True)
     base._run(sd, c, base._q(2, n, 4, D, BF16, std=0.1), [n, 299], BF16, D, scale=scale)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("n", [1, 7, 20, 40])
+def test_scores_of_minus_infinity(sd, kernel, dtype, n):
+    """A visible score of -inf among finite ones has the weight 0; where all of a row's are -inf (or one is
+    +inf) the softmax has no value, and the row is NaN."""
+    D, page = 64, 16
+    lens = [n + 200, n + 5, n + 150]
+    c = base.Cache(3, max(lens), page, 1, D, dtype)
+    q = base._q(3, n, 4, D, dtype).abs() + 0.5
+
+    def key(b, slot, value):
+        c.k[int(c.host_table[b, slot // page]), slot % page, :, 3] = value
+
+    low = {0: [5, 130, lens[0] - 1], 1: list(range(6)), 2: []}
+    for b, slots in low.items():
+        for s in slots:
+            key(b, s, float("-inf"))
+    key(2, lens[2] - 1, float("inf"))
+    r = sd.attend(q, c.k, c.v, c.table, base._i32(lens), with_lse=True)
+    torch.cuda.synchronize()
+    assert not r["status"].any()
+    for b, L in enumerate(lens):
+        sees = co.visible(n, n, L, 0, 0)
+        sees[:, low[b]] = False  # what is left of the softmax
+        some = sees.any(1)
+        if b == 2:
+            some = some & ~sees[:, L - 1]
+        k, v = c.rows(b, L)
+        want = co.attend(base._np(q[b, some]), k, v, sees[some], D ** -0.5)
+        base._check(r["out"][b, some], r["lse"][b, some], want, dtype, False, D, f"b={b}")
+        assert torch.isnan(r["out"][b, ~some]).all() and torch.isnan(r["lse"][b, ~some]).all(), b
+        assert b == 0 or not some.all()
+
+
+def test_all_scores_of_minus_infinity_in_parts_and_beside_empty_rows(sd, kernel):
+    D = 128
+    c = base.Cache(1, 5000, 64, 1, D, BF16)
+    c.k[..., 0] = float("-inf")
+    q = base._q(1, 1, 2, D, BF16).abs() + 0.5
+    r = sd.attend(q, c.k, c.v, c.table, base._i32([5000]), with_lse=True)  # parts of many CTAs
+    torch.cuda.synchronize()
+    assert torch.isnan(r["out"]).all() and torch.isnan(r["lse"]).all()
+    # a tree's rows that see no slot stay zeros: by the mask, or for a sequence that is shorter
+    n = 5
+    mask = np.tril(np.ones((n, n), np.uint8))
+    mask[1] = 0
+    q = base._q(1, n, 2, D, BF16).abs() + 0.5
+    kw = dict(query_len=base._i32([4]), tree_mask=torch.tensor(mask, device=DEV), with_lse=True)
+    depth = dict(depth=base._i32([0, 1, 1, 2, 2]))
+    for extra, first, empty in (({}, 0, (1, 4)), ({}, 3, (4,)), (dict(window=1, **depth), 3, (1, 4)), (dict(window=2), 3, (1, 4)),
+                                (dict(window=2, sinks=1), 3, (4,))):
+        r = sd.attend(q, c.k, c.v, c.table, base._i32([first + 4]), **kw, **extra)
+        torch.cuda.synchronize()
+        for i in range(n):
+            if i in empty:
+                assert not r["out"][0, i].any() and torch.isneginf(r["lse"][0, i]).all(), (extra, first, i)
+            else:
+                assert torch.isnan(r["out"][0, i]).all() and torch.isnan(r["lse"][0, i]).all(), (extra, first, i)
