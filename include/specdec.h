@@ -475,7 +475,8 @@ int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B
  * [0, num_pages) gives NaN, as does every query of a sequence whose lengths do not fit.  Pages
  * that no query sees (behind a window) are not read, and their entries are not looked at.
  * Scores, statistics and sums are fp32; the weights p are rounded to 16 bits (dtype, or fp16 for
- * 4-bit pages) for the matrix products, the output once at the end.
+ * 4-bit pages; in fp16 to 2^-32 of the row's largest where that is more) for the matrix products,
+ * the output once at the end.
  * Every wait inside the kernels is bounded (one second); a call in which one runs out reports
  * SPECDEC_STATUS_TIMEOUT for every sequence, and its outputs do not count.
  * The workspace (specdec_attend_workspace_bytes) follows the rules at the top.  The split of the

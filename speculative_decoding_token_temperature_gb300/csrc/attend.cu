@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(32 * Stage<D, FOUR>::WARPS, 1) attend_kernel(c
           for (int n = 0; n < 2 * SUB; ++n) m = fmaxf(m, fmaxf(s_acc[n][2 * x], s_acc[n][2 * x + 1]));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          const float now = fmaxf(row_m[x], m);
+          const float now = fmaxf(row_m[x], m - kBelow<M>);
           const float base = now == -kInf ? 0.f : now;
           alpha[x] = ex2(row_m[x] - base);
           row_m[x] = now;
@@ -370,8 +370,9 @@ __global__ void __launch_bounds__(32 * Stage<D, FOUR>::WARPS, 1) attend_kernel(c
             }
           row_l[x] = row_l[x] * alpha[x] + sum;  // this lane's keys; joined at the end
         }
-        // P in the matrix type: a rounding of 2^-9 (bf16) or 2^-12 (fp16) of each weight, as
-        // large as that of the output itself; l keeps the unrounded weights
+        // P in the matrix type: a rounding of 2^-8 (bf16) or 2^-11 (fp16) of each weight, as large as
+        // that of the output itself (fp16 below 2^-21 of the row's largest weight: 2^-32 of that
+        // one); l keeps the unrounded weights
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
           p[u] = make_uint4(Half16<M>::pack(pe[2 * u][0], pe[2 * u][1]), Half16<M>::pack(pe[2 * u][2], pe[2 * u][3]),

@@ -20,6 +20,12 @@ constexpr int kUnit = 8;                  // steps of a unit of the work split
 // B=1, one token, 2400 slots (a unit for each CTA) 16.0, 17.0, 32000 slots 36.7, 37.3.
 constexpr int kItemUnits = 4;
 constexpr float kLn2 = 0.6931471805599453f;
+// A row's weights are 2^(s - m), m its reference.  In fp16 they keep their 11 bits down to 2^-14 and vanish
+// below 2^-25, so there the reference stays 7 below the largest score: the weights reach 2^7 (2^15 where the
+// reference lags), what vanishes is below 2^-32 of the largest, and many small weights beside a large one
+// count in the product with V as they do in the sum.  (Sums, products and lse follow the reference.)
+template <typename M>
+constexpr float kBelow = std::is_same<M, __half>::value ? 7.f : 0.f;
 
 // 16 (or 8, 4) bytes to shared memory, zeros where `there` is false (src is not read then).
 template <int N>

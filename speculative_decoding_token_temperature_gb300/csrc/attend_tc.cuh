@@ -10,10 +10,10 @@
 // every staged K and V tile; with fewer, both hold the same rows and take every other tile, and
 // their results join at the end.
 //
-// A row's reference m moves only when a tile exceeds it by more than 2^8: the weights then stay
-// below 256, where 16-bit rounding is relative and as good as below 1, and the accumulator is
-// rescaled once or twice per item instead of once per tile.  The sum l takes the unrounded weights,
-// in fp32.  Two threads hold a row, 64 columns each: the chain scores -> weights -> products of a
+// A row's reference m moves only when a tile exceeds what it was set for by more than 2^8: the weights
+// then stay below 2^8 (2^15 in fp16, whose reference is 7 lower, kBelow), where 16-bit rounding is relative,
+// and the accumulator is rescaled once or twice per item instead of once per tile.  The sum l takes the
+// unrounded weights, in fp32.  Two threads hold a row, 64 columns each: the chain scores -> weights -> products of a
 // slot is what bounds a short tile, and this halves its longest link.
 //
 // Warps 0-15: rows (slot = warp / 8, columns = warp / 4 % 2, lanes = warp % 4).  Then the warps that
@@ -53,7 +53,7 @@ constexpr int kRowWarps = 16;
 constexpr int kTile = kUnit * kStep;  // 128 slots
 constexpr int kBadRing = 16;          // tiles whose out-of-range slots are remembered
 constexpr int kItems = 4;             // items the walk may be ahead
-constexpr float kSlack = 8.f;         // log2 of how far a weight may exceed 1
+constexpr float kSlack = 8.f;         // log2 of how far a tile may exceed what the reference was set for
 
 // What the roles need to know of an item, for the CTA's segment of it.
 struct Item {
@@ -860,10 +860,10 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
           fence_after();
         }
         if (active) {
-          if (pair_any(pair, top > m + kSlack)) {  // (also where m is still -inf) the reference moves
+          if (pair_any(pair, top - m > kSlack + kBelow<M>)) {  // (also where m is still -inf) the reference moves
             s_ml[(slot * 2 + half) * 128 + spot].x = top;
             asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
-            top = fmaxf(fmaxf(m, top), s_ml[(slot * 2 + (half ^ 1)) * 128 + spot].x);
+            top = fmaxf(m, fmaxf(top, s_ml[(slot * 2 + (half ^ 1)) * 128 + spot].x) - kBelow<M>);
             const float alpha = m == top ? 1.f : ex2(m - (top == -kInf ? 0.f : top));
             m = top;
             l *= alpha;

@@ -138,3 +138,36 @@ def test_all_scores_of_minus_infinity_in_parts_and_beside_empty_rows(sd, kernel)
                 assert not r["out"][0, i].any() and torch.isneginf(r["lse"][0, i]).all(), (extra, first, i)
             else:
                 assert torch.isnan(r["out"][0, i]).all() and torch.isnan(r["lse"][0, i]).all(), (extra, first, i)
+
+
+@pytest.mark.parametrize("dtype,four", [(F16, False), (F16, True), (BF16, True)])
+@pytest.mark.parametrize("n,hq", [(1, 2), (4, 4), (12, 4), (40, 4)])
+def test_many_small_weights_beside_a_large_one(sd, kernel, dtype, four, n, hq):
+    """A first slot 26 bits above 2000 equal ones, its value 0: the output is theirs alone.  A weight is
+    rounded in fp16 relative to a reference of 2^7 or more, so to 2^-25 2^-7 of the row's largest.
+    (160 requests share the pages, so that an item's tiles stay on a CTA.)"""
+    D, B = 64, 160
+    L = 2000 + n
+    c = base.Cache(1, L, 16, 1, D, dtype, four)
+    k = torch.zeros(1, L, 1, D, dtype=dtype, device=DEV)
+    k[0, 0, 0, 0] = 12.0
+    v = (30 + base._q(1, L, 1, D, dtype)).contiguous()
+    v[0, 0] = 0
+    if four:
+        c.kw.update(k_scale=1.0, v_scale=1.0)
+        sd.append_kv4(k, v, c.k, c.v, c.table, base._i32([L]), **c.kw)
+    else:
+        at = torch.arange(L)
+        c.k[c.host_table[0].long()[at // 16].to(DEV), (at % 16).to(DEV)] = k[0]
+        c.v[c.host_table[0].long()[at // 16].to(DEV), (at % 16).to(DEV)] = v[0]
+    q = torch.zeros(B, n, hq, D, dtype=dtype, device=DEV)
+    q[..., 0] = 1.0
+    scale = 26 * np.log(2) / 12
+    r = sd.attend(q, c.k, c.v, c.table.expand(B, -1).contiguous(), base._i32([L] * B), scale=scale, with_lse=True, **c.kw)
+    torch.cuda.synchronize()
+    keys, values = c.rows(0, L)
+    out, lse, pv, av, qk = co.attend(base._np(q[0]), keys, values, co.visible(n, n, L, 0, 0), scale)
+    es = D * 2.0 ** -24 * qk
+    tol = ((2 * es + 2.0 ** -13)[..., None] + base.U[F16]) * pv + 2.0 ** -32 * av + base.U[dtype] * np.abs(out) + 2.0 ** -25
+    assert (np.abs(base._np(r["out"]) - out) <= tol).all(), (np.abs(base._np(r["out"]) - out).max(), tol.min())
+    assert (np.abs(base._np(r["lse"]) - lse) <= es + 2.0 ** -13 + 2.0 ** -22 * np.abs(lse)).all()
