@@ -897,7 +897,8 @@ int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype,
   P.Hq = q_heads;
   P.G = G;
   P.g_magic = ((uint64_t{1} << 40) + static_cast<uint64_t>(G) - 1) / static_cast<uint64_t>(G);
-  P.window = window;
+  // (a window beyond every position hides nothing, and the kernels' differences of positions stay ints)
+  P.window = window < static_cast<int64_t>(pages->max_pages) * pages->page_size + n ? window : 0;
   P.sinks = sinks;
   P.scale_log2 = scale * 1.4426950408889634f * P.pages.k_scale;
   P.out = out;

@@ -171,3 +171,14 @@ def test_many_small_weights_beside_a_large_one(sd, kernel, dtype, four, n, hq):
     tol = ((2 * es + 2.0 ** -13)[..., None] + base.U[F16]) * pv + 2.0 ** -32 * av + base.U[dtype] * np.abs(out) + 2.0 ** -25
     assert (np.abs(base._np(r["out"]) - out) <= tol).all(), (np.abs(base._np(r["out"]) - out).max(), tol.min())
     assert (np.abs(base._np(r["lse"]) - lse) <= es + 2.0 ** -13 + 2.0 ** -22 * np.abs(lse)).all()
+
+
+@pytest.mark.parametrize("window", [2 ** 31 - 1, 2 ** 31 - 30, 2 ** 30])
+@pytest.mark.parametrize("hq", [1, 4])
+def test_windows_beyond_every_position(sd, kernel, window, hq):
+    """New tokens that all see each other, under a window as wide as an int goes."""
+    n, D = 40, 64
+    c = base.Cache(3, 240, 16, 1, D, F16)
+    q = base._q(3, n, hq, D, F16)
+    base._run(sd, c, q, [n, n + 30, n + 200], F16, D, mask=np.ones((n, n), np.uint8), window=window, sinks=2)
+    base._run(sd, c, q, [n, n + 30, n + 200], F16, D, window=window)
