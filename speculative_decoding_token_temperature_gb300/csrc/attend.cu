@@ -123,7 +123,9 @@ __global__ void __launch_bounds__(32 * Stage<D, FOUR>::WARPS, 1) attend_kernel(c
 
     // this lane's slot of the steps from t on (SUB = 1: lanes 16..31 repeat 0..15), and its page
     auto slot_of = [&](int t) { return R.slot(t + (SUB == 1 ? 0 : lane / kStep)) + lane % kStep; };
-    auto wanted = [&](int t, int s) { return t + (SUB == 1 ? 0 : lane / kStep) < t_hi && s < R.end; };
+    auto wanted = [&](int t, int s) {
+      return t + (SUB == 1 ? 0 : lane / kStep) < t_hi && s < R.end && (s >= R.lo || s < R.sinks);
+    };
     auto entry = [&](int t) {
       const int s = slot_of(t);
       return wanted(t, s) ? __ldg(table + page_of(pg, s)) : 0;

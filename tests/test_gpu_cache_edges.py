@@ -182,3 +182,15 @@ def test_windows_beyond_every_position(sd, kernel, window, hq):
     q = base._q(3, n, hq, D, F16)
     base._run(sd, c, q, [n, n + 30, n + 200], F16, D, mask=np.ones((n, n), np.uint8), window=window, sinks=2)
     base._run(sd, c, q, [n, n + 30, n + 200], F16, D, window=window)
+
+
+@pytest.mark.parametrize("page", [1, 5])
+@pytest.mark.parametrize("window,sinks", [(3, 0), (21, 2)])
+def test_entries_behind_the_window_within_a_step(sd, kernel, page, window, sinks):
+    """Pages out of range between the first slots and the window, in the same 16 slots as visible ones."""
+    D, L, n = 64, 75, 2
+    c = base.Cache(1, L, page, 2, D, BF16)
+    for p in range(c.table.shape[1]):
+        if p * page >= sinks and (p + 1) * page <= L - n - (window - 1):
+            c.table[0, p] = -5 if p % 2 else 1 << 30
+    base._run(sd, c, base._q(1, n, 4, D, BF16), [L], BF16, D, window=window, sinks=sinks)
