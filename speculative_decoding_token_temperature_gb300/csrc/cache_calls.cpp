@@ -92,6 +92,11 @@ int integer(PyObject* o, const char* name) {
   if (over || v > INT32_MAX || v < INT32_MIN) value_error(std::string(name) + " does not fit an int");
   return static_cast<int>(v);
 }
+bool truth(PyObject* o) {
+  const int yes = PyObject_IsTrue(o);
+  if (yes < 0) throw python_error();
+  return yes != 0;
+}
 int dimension(int64_t v, const char* name) {
   if (v > INT32_MAX) value_error(std::string(name) + " does not fit an int");
   return static_cast<int>(v);
@@ -242,7 +247,7 @@ PyObject* rotate_qk(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const auto* wq = small<void>(a[6], "q_weight", dt, {D}, dev);
     const auto* wk = small<void>(a[7], "k_weight", dt, {D}, dev);
     const float eps = static_cast<float>(number(a[8]));
-    const int interleaved = PyObject_IsTrue(a[9]);
+    const int interleaved = truth(a[9]) ? 1 : 0;
     const bool paged = a[11] != Py_None || a[12] != Py_None || a[13] != Py_None;
     View vv;
     specdec_kv_pages pg{};
@@ -299,7 +304,7 @@ PyObject* read_kv4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     if (len.dim() != 1) value_error("context_len must be [B] int32");
     const int64_t B = len.size(0);
     const int n = integer(a[4], "n");
-    const at::ScalarType dt = PyObject_IsTrue(a[10]) ? at::kBFloat16 : at::kHalf;
+    const at::ScalarType dt = truth(a[10]) ? at::kBFloat16 : at::kHalf;
     const specdec_kv_pages pg = pages(a[0], a[1], a[2], B, dev, -1, a[6], a[7], a[8], a[9]);
     const auto* lens = small<int32_t>(a[3], "context_len", at::kInt, {B}, dev);
     const auto* ql = small<int32_t>(a[5], "query_len", at::kInt, {B}, dev);
@@ -337,7 +342,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const auto* depth = small<int32_t>(a[7], "depth", at::kInt, {n}, dev);
     const int window = integer(a[8], "window"), sinks = integer(a[9], "sinks");
     const float scale = a[10] == Py_None ? static_cast<float>(1.0 / std::sqrt(static_cast<double>(D))) : static_cast<float>(number(a[10]));
-    const bool with_lse = PyObject_IsTrue(a[15]) == 1;
+    const bool with_lse = truth(a[15]);
     const int Bi = dimension(B, "B"), ni = dimension(n, "n"), hi = dimension(hq, "q_heads"), Di = dimension(D, "D");
     const c10::cuda::OptionalCUDAGuard guard(dev);
     const cudaStream_t stream = c10::cuda::getCurrentCUDAStream(dev.index()).stream();

@@ -194,3 +194,14 @@ def test_entries_behind_the_window_within_a_step(sd, kernel, page, window, sinks
         if p * page >= sinks and (p + 1) * page <= L - n - (window - 1):
             c.table[0, p] = -5 if p % 2 else 1 << 30
     base._run(sd, c, base._q(1, n, 4, D, BF16), [L], BF16, D, window=window, sinks=sinks)
+
+
+def test_flags_without_a_truth_value_raise_their_error(sd):
+    c = base.Cache(1, 16, 16, 1, 64, BF16)
+    q, k = base._q(1, 1, 2, 64, BF16), base._q(1, 1, 1, 64, BF16)
+    many = torch.ones(2, dtype=torch.bool)
+    for call in (lambda: sd.attend(q, c.k, c.v, c.table, base._i32([3]), with_lse=many),
+                 lambda: sd.rotate_qk(q, k, sd.rotation_turns([1.0] * 32, DEV), base._i32([3]), interleaved=many)):
+        with pytest.raises(RuntimeError, match="ambiguous"):
+            call()
+    torch.cuda.synchronize()
