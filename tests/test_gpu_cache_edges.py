@@ -205,3 +205,24 @@ def test_flags_without_a_truth_value_raise_their_error(sd):
         with pytest.raises(RuntimeError, match="ambiguous"):
             call()
     torch.cuda.synchronize()
+
+
+def test_workspaces_of_many_streams_are_let_go(sd):
+    """The workspaces that calls leave do not grow with the streams they ran on."""
+    c = base.Cache(2, 400, 16, 1, 128, F16)
+    q, lens = base._q(2, 300, 1, 128, F16), base._i32([400, 390])
+    want = sd.attend(q, c.k, c.v, c.table, lens)["out"]
+    torch.cuda.synchronize()
+    held = []
+    streams = [torch.cuda.Stream() for _ in range(24)]
+    for s in streams:
+        r = sd.attend(q, c.k, c.v, c.table, lens, stream=s)
+        s.synchronize()
+        assert torch.equal(r["out"], want)
+        del r
+        held.append(torch.cuda.memory_allocated())
+    assert len({s.cuda_stream for s in streams}) == 24 and held[11] == held[23]
+    # one stream after another, without a wait: what is let go may still be in use
+    got = [sd.attend(q, c.k, c.v, c.table, lens, stream=s)["out"] for s in streams + streams]
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got)
