@@ -2,21 +2,21 @@
 
 Each .cu translation unit is compiled in parallel to an object, then linked into one
 shared library next to this file.  The CUDA runtime is linked statically, so loading
-the library (e.g. to list its symbols) does not need a GPU.  The host compiler builds
-`_cache_calls.so`, the Python side of the cache calls, beside it.
+the library (e.g. to list its symbols) does not need a GPU.  The library needs nvcc alone
+(`python build.py` in a Python without torch builds just that, for C callers); with torch, the
+host compiler builds `_cache_calls.so`, the Python side of the cache calls, beside it.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
 import hashlib
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
 import sysconfig
 from pathlib import Path
-
-import torch
 
 PKG = Path(__file__).resolve().parent
 ROOT = PKG.parent
@@ -43,21 +43,35 @@ def _sources():
     return sorted(CSRC.glob("*.cu"))
 
 
-def _fingerprint() -> str:
+def _digest(files, *words) -> str:
     h = hashlib.sha256()
-    for p in sorted(list(CSRC.glob("*")) + list(INCLUDE.glob("*.h"))):
-        if p.is_file():
-            h.update(p.name.encode())
-            h.update(p.read_bytes())
-    h.update(" ".join(ARCH_FLAGS + NVCC_FLAGS).encode())
-    h.update(os.uname().machine.encode())
-    h.update((torch.__version__ + sys.version).encode())
+    for p in sorted(files):
+        h.update(p.name.encode())
+        h.update(p.read_bytes())
+    for w in (*words, os.uname().machine):
+        h.update(w.encode())
     return h.hexdigest()
+
+
+def _fingerprint() -> str:
+    """Of what the library is made from: the CUDA sources and headers."""
+    files = [p for g in ("*.cu", "*.cuh", "*.h") for p in CSRC.glob(g)] + list(INCLUDE.glob("*.h"))
+    return _digest(files, " ".join(ARCH_FLAGS + NVCC_FLAGS))
+
+
+def _calls_fingerprint() -> str:
+    import torch
+    return _digest([CSRC / "cache_calls.cpp", *INCLUDE.glob("*.h")], torch.__version__, sys.version)
+
+
+def _current(so: Path, stamp: Path, fingerprint: str) -> bool:
+    return so.exists() and stamp.exists() and stamp.read_text() == fingerprint
 
 
 def _calls_command(out: Path) -> list:
     """The host compiler's command for the Python side of the cache calls (csrc/cache_calls.cpp),
     a CPython module on torch's C++ tensors, linked against the library next to it."""
+    import torch
     cuda = Path(_nvcc()).resolve().parents[1]
     root = Path(torch.__file__).resolve().parent
     lib = root / "lib"
@@ -68,11 +82,10 @@ def _calls_command(out: Path) -> list:
              "-ltorch_cpu", "-ltorch_python", "-ltorch", f"-Wl,-rpath,{lib}"])
 
 
-def build(verbose: bool = False, force: bool = False, extra_flags=None) -> Path:
-    """Compile every .cu under csrc/ and link libspecdec.so (skipped when up to date)."""
-    stamp = BUILD_DIR / "stamp"
-    fp = _fingerprint()
-    if not force and LIB_PATH.exists() and CALLS_PATH.exists() and stamp.exists() and stamp.read_text() == fp:
+def build_library(verbose: bool = False, force: bool = False, extra_flags=None) -> Path:
+    """Compile every .cu under csrc/ and link libspecdec.so (skipped when up to date).  Needs no torch."""
+    stamp, fp = BUILD_DIR / "stamp", _fingerprint()
+    if not force and _current(LIB_PATH, stamp, fp):
         return LIB_PATH
     BUILD_DIR.mkdir(exist_ok=True)
     nvcc = _nvcc()
@@ -88,32 +101,47 @@ def build(verbose: bool = False, force: bool = False, extra_flags=None) -> Path:
             print(r.stdout, r.stderr)
         return obj
 
-    calls_obj = BUILD_DIR / "cache_calls.o"
-
-    def compile_calls():
-        cmd = _calls_command(calls_obj)
-        cmd = [c for c in cmd if c != "-shared" and not c.startswith(("-l", "-L", "-Wl"))] + ["-c"]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed for cache_calls.cpp:\n{r.stderr}")
-
-    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1)) + 1) as ex:
-        calls = ex.submit(compile_calls)
+    with cf.ThreadPoolExecutor(max_workers=max(1, min(8, os.cpu_count() or 1))) as ex:
         objs = list(ex.map(compile_one, _sources()))
-        calls.result()
     tmp = LIB_PATH.with_suffix(".so.tmp")
     cmd = [nvcc, *ARCH_FLAGS, "-shared", "-cudart", "static", "-o", str(tmp), *map(str, objs)]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB_PATH)
+    stamp.write_text(fp)
+    return LIB_PATH
+
+
+def _compile_calls() -> Path:
+    obj = BUILD_DIR / "cache_calls.o"
+    BUILD_DIR.mkdir(exist_ok=True)
+    cmd = [c for c in _calls_command(obj) if c != "-shared" and not c.startswith(("-l", "-L", "-Wl"))] + ["-c"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for cache_calls.cpp:\n{r.stderr}")
+    return obj
+
+
+def _link_calls(obj: Path) -> None:
     tmp = CALLS_PATH.with_suffix(".so.tmp")
-    cmd = [str(calls_obj) if c == str(CSRC / "cache_calls.cpp") else c for c in _calls_command(tmp)]
+    cmd = [str(obj) if c == str(CSRC / "cache_calls.cpp") else c for c in _calls_command(tmp)]
     cmd += [f"-L{PKG}", "-lspecdec", "-Wl,-rpath,$ORIGIN"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link of {CALLS_PATH.name} failed:\n{r.stderr}")
     os.replace(tmp, CALLS_PATH)
+
+
+def build(verbose: bool = False, force: bool = False, extra_flags=None) -> Path:
+    """The library and the Python side of the cache calls, each skipped when up to date."""
+    stamp, fp = BUILD_DIR / "calls_stamp", _calls_fingerprint()
+    if not force and _current(CALLS_PATH, stamp, fp):
+        return build_library(verbose, force, extra_flags)
+    with cf.ThreadPoolExecutor(max_workers=1) as ex:
+        obj = ex.submit(_compile_calls)
+        build_library(verbose, force, extra_flags)
+        _link_calls(obj.result())
     stamp.write_text(fp)
     return LIB_PATH
 
@@ -135,8 +163,8 @@ def ptxas_report() -> str:
 
 
 if __name__ == "__main__":
-    import sys
     if "--ptxas" in sys.argv:
         print(ptxas_report())
     else:
-        print(build(verbose=True, force="--force" in sys.argv))
+        make = build if importlib.util.find_spec("torch") else build_library
+        print(make(verbose=True, force="--force" in sys.argv))
