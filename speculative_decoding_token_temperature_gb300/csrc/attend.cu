@@ -21,10 +21,10 @@
 // 16 rows of the tile, copied ahead with 16-byte asynchronous copies three stages deep; no barrier
 // until the warps join their rows through shared memory, once per segment.  It comes up faster than
 // the tensor-memory kernel (attend_tc.cuh), which takes all other calls, and reaches the same share of
-// HBM bandwidth on 16-bit pages: B=32, 8 key heads, 8000 slots at most, one token of 32 heads of 128
-// in 117 us, 5.6 TB/s, 0.83 of the measured copy rate.  Over 4-bit pages it is bound by the conversion of
+// HBM bandwidth on 16-bit pages: B=32, 8 key heads, 8000 slots at most, one token of 32 heads of 64
+// in 68 us, 4.8 TB/s, 0.71 of the measured copy rate.  Over 4-bit pages it is bound by the conversion of
 // codes (a conversion and a product for every two values, at 64 lanes a clock and SM): the same in
-// 99 us, 1.9 TB/s.
+// 66 us, 1.4 TB/s.
 
 #include <algorithm>
 

@@ -28,14 +28,14 @@
 //
 // Measured (32 query and 8 key heads of 128, key bytes against the copy rate, products against the
 // matrix rate):
-//  - 64 requests, 8 tokens, up to 8190 slots in 16 bits (32 rows to a key head): 222 us, 6.1 TB/s, 0.90 of
+//  - 64 requests, 8 tokens, up to 8190 slots in 16 bits (32 rows to a key head): 219 us, 6.2 TB/s, 0.91 of
 //    the measured copy rate; HBM bounds it.
-//  - 24 trees of 64 nodes, up to 12000 slots (256 rows): 200 us, 3.8 TB/s and 0.94 PFLOP/s, 0.56 of the
-//    measured copy and 0.49 of the matrix rate.  A pair of 128-by-128 tiles takes about 4200 clocks against 2050 of products: the chain scores,
+//  - 24 trees of 64 nodes, up to 12000 slots (256 rows): 204 us, 3.7 TB/s and 0.92 PFLOP/s, 0.55 of the
+//    measured copy and 0.48 of the matrix rate.  A pair of 128-by-128 tiles takes about 4200 clocks against 2050 of products: the chain scores,
 //    weights, products of one slot is longer than the other slot's products, for the exponentials
 //    (128 x 128 at 32 a clock and SM are 512 clocks) come with two reads of the scores and one store
 //    of the weights through tensor memory.
-//  - 16 requests, 8 tokens, up to 32003 slots in 4 bits: 163 us, 2.3 TB/s, DRAM traffic equal to the
+//  - 16 requests, 8 tokens, up to 32003 slots in 4 bits: 164 us, 2.3 TB/s, DRAM traffic equal to the
 //    cache's bytes.  A tile takes about 2400 clocks: its codes' conversion 790 at 64 lanes a clock, but
 //    with the copies in and the stores of the values (shared memory is busy for about 1500) the converting
 //    warps need 2000.
