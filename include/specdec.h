@@ -47,7 +47,8 @@ typedef enum {
   SPECDEC_F32 = 0,
   SPECDEC_BF16 = 1,
   SPECDEC_F16 = 2, /* the cache calls: queries, keys, values and 16-bit pages */
-  SPECDEC_KV4 = 3  /* the cache calls: pages held in 4 bits                    */
+  SPECDEC_KV4 = 3, /* the cache calls: pages held in 4 bits                    */
+  SPECDEC_KV8 = 4  /* the cache calls: pages held in 8 bits                    */
 } specdec_dtype;
 
 /* return codes */
@@ -69,6 +70,7 @@ typedef enum {
 #define SPECDEC_STATUS_TIMEOUT 128          /* a bounded wait inside a kernel gave up: not finished */
 #define SPECDEC_STATUS_BAD_CACHE 32         /* cache calls: a length or page out of range (the bit
                                                with which a path that leaves the cache is reported) */
+#define SPECDEC_STATUS_BAD_PENALTY 64       /* logits processing: a penalty that is not a number it takes */
 #define SPECDEC_STATUS_ERROR_MASK 0xFF
 #define SPECDEC_STATUS_ZERO_Q 256           /* warning: q_i(x_i) == 0; accepted iff p_i(x_i) > 0 */
 #define SPECDEC_STATUS_ZERO_RESIDUAL 512    /* warning: residual mass 0 after rounding; drew from p */
@@ -381,7 +383,13 @@ int specdec_compact_kv(void* cache, int64_t row_bytes, int64_t slot_stride, int6
  *     k_scales / v_scales hold head_dim / 16 E4M3 bytes per row at their own strides, one for
  *     each 16 values.  A value is code * scale * k_scale (v_scale for values).  k_scale and
  *     v_scale are positive and finite; they are not read for 16-bit pages.
- * Pointers and strides are multiples of 16 bytes (scales: of head_dim / 16 bytes); head_dim is
+ *   SPECDEC_KV8: a row is head_dim E4M3 codes.  The scale_block slots of a block share a scale for each
+ *     head, a power of two between 2^-15 and 2^7 held as its E8M0 byte (the exponent plus 127): k_scales /
+ *     v_scales hold it at page * scale_page_stride + (s % page_size / scale_block) * scale_slot_stride +
+ *     head * scale_head_stride (bytes, any).  A value is code * scale * k_scale (v_scale); before k_scale it is exact
+ *     in fp16.  page_size is a multiple of scale_block, that a multiple of 16.  specdec_compact_kv does not
+ *     know the scales: after a tree's round the accepted tokens are appended again at their slots.
+ * Pointers and strides are multiples of 16 bytes (4-bit pages' scales: of head_dim / 16 bytes); head_dim is
  * 64 or 128; max_pages * page_size < 2^31 - 256.
  *
  * Lengths, for each call below: context_len[b] counts sequence b's tokens including the new
@@ -394,14 +402,15 @@ int specdec_compact_kv(void* cache, int64_t row_bytes, int64_t slot_stride, int6
 typedef struct specdec_kv_pages {
   void* k;
   void* v;
-  void* k_scales; /* SPECDEC_KV4 only */
+  void* k_scales; /* SPECDEC_KV4 and SPECDEC_KV8 */
   void* v_scales;
   const int32_t* block_table; /* [B, max_pages], device */
   int64_t page_stride, slot_stride, head_stride;
-  int64_t scale_page_stride, scale_slot_stride, scale_head_stride; /* SPECDEC_KV4 only */
+  int64_t scale_page_stride, scale_slot_stride, scale_head_stride; /* SPECDEC_KV4 and SPECDEC_KV8 */
   int32_t num_pages, page_size, max_pages, kv_heads, head_dim;
-  int32_t format; /* SPECDEC_BF16, SPECDEC_F16 or SPECDEC_KV4 */
+  int32_t format; /* SPECDEC_BF16, SPECDEC_F16, SPECDEC_KV4 or SPECDEC_KV8 */
   float k_scale, v_scale;
+  int32_t scale_block; /* SPECDEC_KV8 only: slots that share a scale */
 } specdec_kv_pages;
 
 /* Norms of queries and keys for each head, the position rotation, and the write of keys and
@@ -450,8 +459,27 @@ int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B
                      const specdec_kv_pages* pages, specdec_dtype dtype, void* out_k, void* out_v,
                      int32_t* out_status, void* stream);
 
+/* Keys and values [B, n, kv_heads, D] (strides as above) written to 8-bit pages.
+ * With y = x * (1 / k_scale) in fp32: a block's scale is the smallest 2^e, e in [-15, 7], with max|y| <= 448 * 2^e
+ * over the new tokens that fall into it, and never below its scale of before when the block holds earlier tokens of
+ * the sequence (slots before the first new one); code = the E4M3 number nearest to y / 2^e (ties to the even code,
+ * saturated at 448).  Where a block's scale grows, the codes of its earlier tokens are rounded to the new scale: exact but
+ * for codes that become subnormal.  A value that is not finite is stored as NaN and does not count for the scale.
+ * Slots from a block's new tokens on are not looked at: rejected drafts are overwritten by appending again with the
+ * shorter context_len (a block keeps its scale then).  A sequence in error is left alone.  Two sequences must not write the
+ * same block.  B <= 65535. */
+int specdec_append_kv8(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                       specdec_dtype dtype, const int32_t* context_len, const int32_t* query_len, int B, int n,
+                       const specdec_kv_pages* pages, int32_t* out_status, void* stream);
+
+/* The values that 8-bit pages hold for the last query_len[b] tokens of each sequence, as
+ * specdec_read_kv4 gives them. */
+int specdec_read_kv8(const int32_t* context_len, const int32_t* query_len, int B, int n,
+                     const specdec_kv_pages* pages, specdec_dtype dtype, void* out_k, void* out_v,
+                     int32_t* out_status, void* stream);
+
 /* Attention of the new tokens over the cache, which holds their keys and values already
- * (specdec_rotate_qk, specdec_append_kv4).
+ * (specdec_rotate_qk, specdec_append_kv4, specdec_append_kv8).
  *
  * With P = context_len[b] - query_len[b], query i sees slot s when
  *   chain (tree_mask NULL):  s <= P + i
@@ -468,14 +496,14 @@ int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B
  * one of them +inf, gives NaN and lse NaN.
  *
  * q            [B, n, q_heads, D] of dtype (SPECDEC_BF16 or SPECDEC_F16), q_strides as above
- * pages        16-bit pages of the same dtype, or SPECDEC_KV4
+ * pages        16-bit pages of the same dtype, SPECDEC_KV4 or SPECDEC_KV8
  * out          [B, n, q_heads, D] contiguous
  * out_lse      [B, n, q_heads] fp32, optional: log of the sum of exp(scale * q . k_s)
  * A query that sees nothing gives zeros and lse -inf; one that sees a slot on a page outside
  * [0, num_pages) gives NaN, as does every query of a sequence whose lengths do not fit.  Pages
  * that no query sees (behind a window) are not read, and their entries are not looked at.
  * Scores, statistics and sums are fp32; the weights p are rounded to 16 bits (dtype, or fp16 for
- * 4-bit pages; in fp16 to 2^-32 of the row's largest where that is more) for the matrix products,
+ * 4-bit and 8-bit pages; in fp16 to 2^-32 of the row's largest where that is more) for the matrix products,
  * the output once at the end.
  * Every wait inside the kernels is bounded (one second); a call in which one runs out reports
  * SPECDEC_STATUS_TIMEOUT for every sequence, and its outputs do not count.
@@ -489,6 +517,50 @@ int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype,
                    const int32_t* context_len, const int32_t* query_len, const uint8_t* tree_mask,
                    const int32_t* depth, int B, int n, int q_heads, int window, int sinks, float scale, void* out,
                    float* out_lse, int32_t* out_status, void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------------------
+ * What is done to the target's logits before they are verified (SD 20.5, "Four ways to lose exactness": p is the
+ * distribution the target samples from, after its processing; every row of a round has its own history).
+ *
+ * Row i of a sequence follows the tokens generated so far and the drafts before it: tokens[b, 0 .. i-1] of a chain
+ * (parents NULL), or row 0 the root and row 1 + i node i with the tokens on the path from the root to node i,
+ * itself included.  With c the number of times t occurs among those (its entry of `counts` and the row's drafts),
+ * for each token t of the vocabulary:
+ *   x  = logits[b, i, t];  if c > 0 or t is in the prompt:  x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *   x  = x - frequency[b] * c - (c > 0 ? presence[b] : 0) + the bias listed for t
+ *   out[b, i, t] = x, or -inf where the row's mask has no bit for t.
+ * Computed in fp32 and rounded once.  A masked token is -inf whatever its logit holds (NaN too); a row whose mask leaves nothing
+ * is all -inf, which the verification calls report (SPECDEC_STATUS_EMPTY_ROW).
+ *
+ * logits       [B, rows, V] of dtype (SPECDEC_F32 or SPECDEC_BF16); out the same, or logits itself: in place
+ * tokens       [B, rows - 1] int32: drafts or node tokens; may be NULL (then they do not count, whatever rows is)
+ * parents      [rows - 1] int32, parent in [-1, i): a tree; NULL: a chain
+ * gammas       [B] int32 in [0, rows - 1], optional, chains only: the drafts that specdec_verify_chain_varlen verifies;
+ *              rows past gammas[b] are neither read nor written, and tokens from gammas[b] on may hold anything
+ * counts       [B, V] int32, optional: the low 31 bits are c without drafts, the sign bit says that t is in the prompt
+ *              (specdec_count_tokens)
+ * repetition, presence, frequency [B] fp32, each optional (NULL: 1, 0, 0); repetition is positive
+ * bias_tokens, bias_values [B, num_bias] int32 and fp32, optional (num_bias 0): negative tokens are skipped; of a token
+ *              that is listed twice the last entry counts
+ * mask         [B, rows, (V + 31) / 32] uint32, optional: bit t % 32 of word t / 32 is set where t is allowed
+ * out_status   [B] int32, optional: SPECDEC_STATUS_BAD_TOKEN (a token outside [0, V) that a row counts, a bias token
+ *              of V or more, gammas[b] out of range), SPECDEC_STATUS_BAD_TREE (a parent out of range), SPECDEC_STATUS_BAD_PENALTY (a repetition that is not
+ *              positive and finite, a presence or frequency that is not finite), else 0.  The rows of a sequence in error are NaN.
+ * rows <= 8192, B <= 65535, num_bias < 2^24, V < 2^31 - 65536. */
+int specdec_process_logits(const void* logits, specdec_dtype dtype, const int32_t* tokens, const int32_t* parents,
+                           const int32_t* gammas, const int32_t* counts, const float* repetition,
+                           const float* presence, const float* frequency, const int32_t* bias_tokens,
+                           const float* bias_values, int num_bias, const uint32_t* mask, int B, int rows, int V,
+                           void* out, int32_t* out_status, void* stream);
+
+/* The table of token counts that specdec_process_logits reads: for each of the first num_tokens[b] <= n tokens of
+ * sequence b (NULL: n), counts[b, t] grows by one, or, with prompt != 0, its sign bit is set.  Negative tokens are skipped, so a
+ * verification call's out_tokens can be counted as they are; so are tokens of V or more, which out_status reports
+ * (SPECDEC_STATUS_BAD_TOKEN), as num_tokens[b] outside [0, n] is clamped.  reset != 0: the sequence's entries are set to zero before.
+ * tokens [B, n] int32, rows token_stride elements apart; counts [B, V] int32, in place.
+ * n may be 0.  B <= 65535, V and n < 2^31 - 65536. */
+int specdec_count_tokens(int32_t* counts, const int32_t* tokens, int64_t token_stride, const int32_t* num_tokens, int B,
+                         int n, int V, int prompt, int reset, int32_t* out_status, void* stream);
 
 /* ------------------------------------------------------------------------------------
  * Tree-attention mask and position ids (SD 20.5, box "Token tree and tree attention").
@@ -531,7 +603,11 @@ int specdec_build_tree_mask(const int32_t* parents, int N, int prefix_len, uint8
 #define SPECDEC_KERNEL_APPEND_KV4 15       /* the 4-bit page write                       */
 #define SPECDEC_KERNEL_READ_KV4 16         /* 4-bit pages read back                      */
 #define SPECDEC_KERNEL_ATTEND 17           /* attention over pages, its join included    */
-#define SPECDEC_NUM_KERNELS 18
+#define SPECDEC_KERNEL_APPEND_KV8 18       /* the 8-bit page write                       */
+#define SPECDEC_KERNEL_READ_KV8 19         /* 8-bit pages read back                      */
+#define SPECDEC_KERNEL_PROCESS_LOGITS 20   /* penalties, biases and masks                */
+#define SPECDEC_KERNEL_COUNT_TOKENS 21     /* the table of token counts                  */
+#define SPECDEC_NUM_KERNELS 22
 
 int specdec_profile_start(int max_launches);
 int specdec_profile_read(double* total_ms, int* launches, int n);

@@ -1,5 +1,5 @@
 """fp64 CPU oracle of the cache calls -- test infrastructure only: the rotation with the page
-write, the 4-bit values and attention over pages, written from their definitions in
+write, the 4-bit and 8-bit values and attention over pages, written from their definitions in
 ``include/specdec.h``, one sequence, one head and one slot at a time where that is affordable."""
 from __future__ import annotations
 
@@ -46,6 +46,55 @@ def dequantise(codes, scales, tensor_scale: float) -> np.ndarray:
     table = np.concatenate((e4m3_values(), [np.nan]))
     s = np.where(scales & 128, -1.0, 1.0) * table[scales & 127]
     return v * np.repeat(s, 16, -1) * np.float32(tensor_scale)
+
+
+def block_exponent(amax: float) -> int:
+    """The smallest e in [-15, 7] with amax <= 448 * 2^e."""
+    for e in range(-15, 7):
+        if amax <= 448.0 * 2.0 ** e:
+            return e
+    return 7
+
+
+def encode8(y, e: int) -> np.ndarray:
+    """E4M3 bytes of y / 2^e: the nearest, ties to the even code, saturated; what is not finite is NaN (127)."""
+    y = np.asarray(y, np.float64)
+    grid = e4m3_values()
+    with np.errstate(invalid="ignore"):
+        a = np.minimum(np.abs(y) * 2.0 ** -e, 448.0)
+    up = np.clip(np.searchsorted(grid, np.where(np.isfinite(y), a, 0.0)), 1, 126)
+    below, above = a - grid[up - 1], grid[up] - a
+    code = np.where((above < below) | ((above == below) & (up % 2 == 0)), up, up - 1)
+    return np.where(np.isfinite(y), code + np.where(np.signbit(y), 128, 0), 127).astype(np.uint8)
+
+
+def decode8(codes, e) -> np.ndarray:
+    """The values of E4M3 bytes under scales 2^e, before the tensor's scale."""
+    codes = np.asarray(codes).astype(int)
+    table = np.concatenate((e4m3_values(), [np.nan]))
+    return np.where(codes & 128, -1.0, 1.0) * table[codes & 127] * 2.0 ** np.asarray(e, np.float64)
+
+
+def append8(codes, exps, x, first: int, block: int, tensor_scale: float):
+    """One sequence, one head, one of keys and values: codes [slots, D] and block exponents [blocks] with the new
+    tokens x [n, D] written from slot `first` on (copies)."""
+    codes, exps = np.array(codes), np.array(exps).astype(int)
+    with np.errstate(over="ignore"):
+        y = np.asarray(x, np.float32) * (np.float32(1.0) / np.float32(tensor_scale))
+    n = len(y)
+    for j in range(first // block, (first + n - 1) // block + 1 if n else 0):
+        lo, hi = max(first, j * block), min(first + n, (j + 1) * block)
+        here, raw = y[lo - first:hi - first], np.asarray(x, np.float64)[lo - first:hi - first]
+        ok = np.isfinite(raw)
+        e = block_exponent(float(np.abs(here[ok]).max()) if ok.any() else 0.0)
+        if lo > j * block:
+            e = max(e, exps[j])
+            if e != exps[j]:
+                codes[j * block:lo] = encode8(decode8(codes[j * block:lo], exps[j]), e)
+        exps[j] = e
+        value = np.where(ok, np.clip(np.where(ok, here, 0.0).astype(np.float64), -1e30, 1e30), np.nan)
+        codes[lo:hi] = encode8(value, e)
+    return codes, exps
 
 
 def rotate(x, pos: int, inv_freq, weight=None, eps: float = 1e-6, interleaved: bool = False):

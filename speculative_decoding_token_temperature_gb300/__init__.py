@@ -16,16 +16,19 @@ from pathlib import Path
 import torch
 
 from . import cache as _cache
-from .cache import append_kv4, attend, read_kv4, rotate_qk, rotation_turns
+from . import logits as _logits
+from .cache import append_kv4, append_kv8, attend, read_kv4, read_kv8, rotate_qk, rotation_turns
+from .logits import count_tokens, process_logits
 
 __all__ = [
     "SpecdecError", "verify_chain", "verify_greedy", "verify_tree", "build_tree_mask",
     "chain_workspace_bytes", "library_path", "load_library", "KernelTimer",
-    "F32", "BF16", "F16", "KV4", "GREEDY_TEMPERATURE",
-    "rotate_qk", "rotation_turns", "append_kv4", "read_kv4", "attend",
+    "F32", "BF16", "F16", "KV4", "KV8", "GREEDY_TEMPERATURE",
+    "rotate_qk", "rotation_turns", "append_kv4", "read_kv4", "append_kv8", "read_kv8", "attend",
+    "process_logits", "count_tokens",
 ]
 
-F32, BF16, F16, KV4 = 0, 1, 2, 3
+F32, BF16, F16, KV4, KV8 = 0, 1, 2, 3, 4
 GREEDY_TEMPERATURE = 1e-3
 STATUS_TIMEOUT = 128
 TREE_WITHOUT_REPLACEMENT = 1  # specdec_verify_tree_recursive: children drawn without replacement
@@ -46,13 +49,15 @@ STATUS_BAD_TREE = 32
 STATUS_BAD_TEMPERATURE = 64
 STATUS_TIMEOUT = 128
 STATUS_BAD_CACHE = 32
+STATUS_BAD_PENALTY = 64
 STATUS_ERROR_MASK = 0xFF
 STATUS_ZERO_Q = 256
 STATUS_ZERO_RESIDUAL = 512
 
 KERNEL_NAMES = ("chain_stats", "chain_sample", "tree_walk", "tree_mask", "chain_decide", "chain_finish",
                 "chain_seq", "block_decide", "block_finish", "block_fused", "tree_rr", "gumbel",
-                "gumbel_draft", "kv_compact", "rotate_qk", "append_kv4", "read_kv4", "attend")
+                "gumbel_draft", "kv_compact", "rotate_qk", "append_kv4", "read_kv4", "attend", "append_kv8", "read_kv8",
+                "process_logits", "count_tokens")
 
 
 class SpecdecError(RuntimeError):
@@ -128,6 +133,7 @@ def load_library():
     lib.specdec_get_test_hook.argtypes = [i32]
     lib.specdec_get_test_hook.restype = i32
     _cache.declare(lib)
+    _logits.declare(lib)
     _LIB = lib
     return lib
 

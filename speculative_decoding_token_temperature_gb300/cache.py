@@ -1,11 +1,13 @@
-"""The paged cache of the target's attention: rotation with the page write, 4-bit pages, and
+"""The paged cache of the target's attention: rotation with the page write, 4-bit and 8-bit pages, and
 attention of a round's tokens over the pages (the cache calls of ``include/specdec.h``).
 
 Pages are caller-owned CUDA tensors ``[num_pages, page_size, kv_heads, head_dim]`` of bfloat16
 or float16 (the layout ``compact_kv`` takes), or, held in 4 bits, uint8 codes
 ``[num_pages, page_size, kv_heads, head_dim / 2]`` with scales ``[..., head_dim / 16]`` (uint8
-or float8_e4m3fn bytes).  They may be views with any strides of whole 16-byte rows (scales:
-``head_dim / 16`` bytes), keys and values with the same strides.  Slot s of sequence b is
+or float8_e4m3fn bytes), or, held in 8 bits, float8_e4m3fn codes ``[num_pages, page_size, kv_heads, head_dim]``
+with scales ``[num_pages, blocks, kv_heads]`` (uint8 or float8_e8m0fnu bytes), one for each head and each
+``page_size / blocks`` slots, a multiple of 16.  They may be views with any strides of whole 16-byte rows (4-bit
+scales: ``head_dim / 16`` bytes; 8-bit scales: any), keys and values with the same strides.  Slot s of sequence b is
 entry ``s % page_size`` of page ``block_table[b, s // page_size]``.
 """
 from __future__ import annotations
@@ -15,7 +17,7 @@ import math
 
 import torch
 
-F16, KV4 = 2, 3
+F16, KV4, KV8 = 2, 3, 4
 _CODES = (torch.bfloat16, torch.float16)
 
 
@@ -25,7 +27,7 @@ class _KvPages(ctypes.Structure):
                                                  "scale_slot_stride", "scale_head_stride")]
                 + [(f, ctypes.c_int32) for f in ("num_pages", "page_size", "max_pages", "kv_heads", "head_dim",
                                                  "format")]
-                + [(f, ctypes.c_float) for f in ("k_scale", "v_scale")])
+                + [(f, ctypes.c_float) for f in ("k_scale", "v_scale")] + [("scale_block", ctypes.c_int32)])
 
 
 def declare(lib) -> None:
@@ -34,13 +36,16 @@ def declare(lib) -> None:
     st, pg = ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(_KvPages)
     lib.specdec_rotate_qk.argtypes = [vp, st, vp, st, vp, st, i32, vp, vp, f32, vp, i32, i32, vp, vp, vp, i32, i32,
                                       i32, i32, i32, vp, vp, pg, vp, vp]
-    lib.specdec_append_kv4.argtypes = [vp, st, vp, st, i32, vp, vp, i32, i32, pg, vp, vp]
-    lib.specdec_read_kv4.argtypes = [vp, vp, i32, i32, pg, i32, vp, vp, vp, vp]
+    for f in (lib.specdec_append_kv4, lib.specdec_append_kv8):
+        f.argtypes = [vp, st, vp, st, i32, vp, vp, i32, i32, pg, vp, vp]
+    for f in (lib.specdec_read_kv4, lib.specdec_read_kv8):
+        f.argtypes = [vp, vp, i32, i32, pg, i32, vp, vp, vp, vp]
     lib.specdec_attend_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
     lib.specdec_attend_workspace_bytes.restype = sz
     lib.specdec_attend.argtypes = [vp, st, i32, pg, vp, vp, vp, vp, i32, i32, i32, i32, i32, f32, vp, vp, vp, vp, sz,
                                    vp]
-    for f in (lib.specdec_rotate_qk, lib.specdec_append_kv4, lib.specdec_read_kv4, lib.specdec_attend):
+    for f in (lib.specdec_rotate_qk, lib.specdec_append_kv4, lib.specdec_read_kv4, lib.specdec_append_kv8, lib.specdec_read_kv8,
+              lib.specdec_attend):
         f.restype = i32
 
 
@@ -121,12 +126,38 @@ def read_kv4(k_pages, v_pages, block_table, context_len, n: int, *, k_scales, v_
 
 
 
+def append_kv8(k, v, k_pages, v_pages, block_table, context_len, *, k_scales, v_scales, k_scale: float = 1.0,
+               v_scale: float = 1.0, query_len=None, stream=None) -> dict:
+    """Keys and values [B, n, kv_heads, D] of the new tokens written to 8-bit pages, with a scale for each block of
+    slots and head (specdec_append_kv8).  A block's scale grows with the tokens appended to it, and its earlier codes
+    follow.  Returns status [B]."""
+    call = (_calls or _module()).append_kv8
+    if stream is None:
+        return call(k, v, k_pages, v_pages, block_table, context_len, query_len, k_scales, v_scales, k_scale, v_scale)
+    with torch.cuda.stream(stream):
+        return call(k, v, k_pages, v_pages, block_table, context_len, query_len, k_scales, v_scales, k_scale, v_scale)
+
+
+def read_kv8(k_pages, v_pages, block_table, context_len, n: int, *, k_scales, v_scales, k_scale: float = 1.0,
+             v_scale: float = 1.0, query_len=None, dtype=torch.bfloat16, stream=None) -> dict:
+    """The values that 8-bit pages hold for the last n tokens (query_len[b] <= n) of each
+    sequence (specdec_read_kv8): k, v [B, n, kv_heads, D] of dtype, and status [B]."""
+    if dtype not in _CODES:
+        raise ValueError("dtype must be bfloat16 or float16")
+    call = (_calls or _module()).read_kv8
+    brain = dtype is torch.bfloat16
+    if stream is None:
+        return call(k_pages, v_pages, block_table, context_len, n, query_len, k_scales, v_scales, k_scale, v_scale, brain)
+    with torch.cuda.stream(stream):
+        return call(k_pages, v_pages, block_table, context_len, n, query_len, k_scales, v_scales, k_scale, v_scale, brain)
+
+
 def attend(q, k_pages, v_pages, block_table, context_len, *, query_len=None, tree_mask=None, depth=None,
            window: int = 0, sinks: int = 0, scale=None, k_scales=None, v_scales=None, k_scale: float = 1.0,
            v_scale: float = 1.0, with_lse: bool = False, stream=None) -> dict:
     """Attention of the new tokens over a paged cache that holds their keys and values already
     (specdec_attend): chain or tree, a sliding window with a few first tokens that stay
-    visible, 16-bit or 4-bit pages.
+    visible, 16-bit, 8-bit or 4-bit pages.
 
     q [B, n, q_heads, D] bfloat16 or float16, a view with contiguous rows; context_len [B] int32,
     the new tokens included; query_len [B] int32 (default n); tree_mask [n, n] uint8 and depth [n]

@@ -53,15 +53,6 @@ __device__ __forceinline__ void load_matrices_t(uint32_t addr, uint32_t (&r)[4])
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
 }
-template <typename T>
-__device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
-  if constexpr (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value)
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-  else
-    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
-}
 // ---- one 16-bit or 4-bit step ------------------------------------------------------------
 
 // Sixteen slots' keys or values as staged: rows of D 16-bit values padded by 16 bytes (so that the
@@ -529,45 +520,8 @@ __global__ void __launch_bounds__(32 * Stage<D, FOUR>::WARPS, 1) attend_kernel(c
       }
     }
     __syncthreads();
-    const bool begins = w.u == w.item, ends = w.ends();
-    const int part = begins ? 1 : 0;  // a CTA has at most one part that goes on and one that began before
-    for (int f = tid; f < MR * (D / 4); f += THREADS) {
-      const int r = f / (D / 4), d = (f % (D / 4)) * 4;
-      if (r >= rows) continue;
-      float m = -kInf;
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) m = fmaxf(m, s_ml[k * MR + r].x);
-      const float base = m == -kInf ? 0.f : m;
-      float l = 0.f;
-      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < WARPS; ++k) {
-        const float2 ml = s_ml[k * MR + r];
-        const float a = ex2(ml.x - base);
-        const float4 x = *reinterpret_cast<const float4*>(s_o + (static_cast<size_t>(k) * MR + r) * D + d);
-        l += a * ml.y;
-        acc.x += a * x.x; acc.y += a * x.y; acc.z += a * x.z; acc.w += a * x.w;
-      }
-      if (begins && ends) {
-        const int i = query_of(P, row0 + r), head = h * P.G + row0 + r - i * P.G;
-        const int64_t at = (static_cast<int64_t>(b) * P.n + i) * P.Hq + head;
-        float inv = l == 0.f ? 0.f : pg.v_scale / l, lse = m * kLn2 + logf(l);
-        if (l == 0.f || i >= S.nq) { lse = -kInf; inv = 0.f; }
-        uint2 four = make_uint2(Half16<T>::pack(acc.x * inv, acc.y * inv), Half16<T>::pack(acc.z * inv, acc.w * inv));
-        if (i >= S.nq) four = make_uint2(0u, 0u);
-        if (!S.ok || (l == 0.f && sees_some(P, S.first, S.nq, i))) {
-          four = make_uint2(0x7fff7fffu, 0x7fff7fffu);
-          lse = __int_as_float(0x7fffffff);
-        }
-        *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + at * D + d) = four;
-        if (d == 0 && P.lse) P.lse[at] = lse;
-      } else {
-        const int64_t at = (cta * 2 + part) * MR + r;
-        *reinterpret_cast<float4*>(P.part_o + at * D + d) = acc;
-        if (d == 0) P.part_ml[at] = make_float2(m, l);
-      }
-    }
-    if (begins && !ends && tid == 0) P.split[cta] = w.split(share);
+    join_warps<T, D, MR, WARPS>(P, w, S, row0, rows, smem);
+    if (w.u == w.item && !w.ends() && tid == 0) P.split[cta] = w.split(share);
     if (!w.next()) break;
   }
 }
@@ -692,14 +646,14 @@ size_t attend_workspace_bytes(int n, int G, int D) {
 
 cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format, void* workspace, cudaStream_t stream) {
   const int64_t rows = static_cast<int64_t>(P.n) * P.G;
-  const bool four = format == SPECDEC_KV4;
+  const bool four = format == SPECDEC_KV4, eight = format == SPECDEC_KV8;
   const int hook = test_hook(SPECDEC_HOOK_ATTEND_KERNEL);
   P.ctas = attend_sms();
   if (P.ctas <= 0) return cudaErrorInvalidDevice;
   if (P.ctas > kMaxCtas) P.ctas = kMaxCtas;
   const bool items = P.pages.head_dim == 128 && static_cast<int64_t>(P.B) * P.pages.kv_heads >= P.ctas;
-  const bool tc = hook == 0 ? rows > kWarpRows || items : hook == 2;
-  const int mr = tc ? attend_tc_rows(rows) : kRows;
+  const bool tc = eight ? false : hook == 0 ? rows > kWarpRows || items : hook == 2;
+  const int mr = tc ? attend_tc_rows(rows) : eight ? attend8_rows(rows) : kRows;
   P.row_tiles = static_cast<int>((rows + mr - 1) / mr);
   // A row of CTAs for each key head, unless that leaves more than a sixteenth of the GPU out: a slot's heads
   // lie side by side, and are then read at about the same time (4-bit decode of 64 requests of 16000
@@ -716,7 +670,9 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   if (tc)
     if (cudaError_t e = four ? launch_attend_tc4(P, dt, mr, stream) : launch_attend_tc(P, dt, mr, stream); e != cudaSuccess)
       return e;
-  if (!tc)
+  if (!tc && eight)
+    if (cudaError_t e = launch_attend8(P, dt, mr, stream); e != cudaSuccess) return e;
+  if (!tc && !eight)
     if (cudaError_t e = dt == SPECDEC_BF16 ? launch_typed<__nv_bfloat16>(P, four, stream)
                                            : launch_typed<__half>(P, four, stream);
         e != cudaSuccess)

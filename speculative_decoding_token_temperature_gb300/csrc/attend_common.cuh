@@ -242,4 +242,64 @@ struct Walk {
   }
 };
 
+// The rows of a segment whose WARPS warps left (unnormalised output, running maximum and sum) in shared memory,
+// [WARPS][MR][D] and behind them [WARPS][MR]: written out where the segment is a whole item, else left as a part.
+template <typename T, int D, int MR, int WARPS>
+__device__ __forceinline__ void join_warps(const AttendParams& P, const Walk<MR>& w, const SeqLen& S, int row0, int rows, const char* smem) {
+  const Pages& pg = P.pages;
+  const int b = w.b, h = w.h;
+  const float* const s_o = reinterpret_cast<const float*>(smem);
+  const float2* const s_ml = reinterpret_cast<const float2*>(smem + WARPS * MR * D * 4);
+  const bool begins = w.u == w.item, ends = w.ends();
+  const int part = begins ? 1 : 0;  // a CTA has at most one part that goes on and one that began before
+  for (int f = threadIdx.x; f < MR * (D / 4); f += 32 * WARPS) {
+    const int r = f / (D / 4), d = (f % (D / 4)) * 4;
+    if (r >= rows) continue;
+    float m = -kInf;
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) m = fmaxf(m, s_ml[k * MR + r].x);
+    const float base = m == -kInf ? 0.f : m;
+    float l = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < WARPS; ++k) {
+      const float2 ml = s_ml[k * MR + r];
+      const float a = ex2(ml.x - base);
+      const float4 x = *reinterpret_cast<const float4*>(s_o + (static_cast<size_t>(k) * MR + r) * D + d);
+      l += a * ml.y;
+      acc.x += a * x.x; acc.y += a * x.y; acc.z += a * x.z; acc.w += a * x.w;
+    }
+    if (begins && ends) {
+      const int i = query_of(P, row0 + r), head = h * P.G + row0 + r - i * P.G;
+      const int64_t at = (static_cast<int64_t>(b) * P.n + i) * P.Hq + head;
+      float inv = l == 0.f ? 0.f : pg.v_scale / l, lse = m * kLn2 + logf(l);
+      if (l == 0.f || i >= S.nq) { lse = -kInf; inv = 0.f; }
+      uint2 four = make_uint2(Half16<T>::pack(acc.x * inv, acc.y * inv), Half16<T>::pack(acc.z * inv, acc.w * inv));
+      if (i >= S.nq) four = make_uint2(0u, 0u);
+      if (!S.ok || (l == 0.f && sees_some(P, S.first, S.nq, i))) {
+        four = make_uint2(0x7fff7fffu, 0x7fff7fffu);
+        lse = __int_as_float(0x7fffffff);
+      }
+      *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + at * D + d) = four;
+      if (d == 0 && P.lse) P.lse[at] = lse;
+    } else {
+      const int64_t at = (static_cast<int64_t>(blockIdx.x) * 2 + part) * MR + r;
+      *reinterpret_cast<float4*>(P.part_o + at * D + d) = acc;
+      if (d == 0) P.part_ml[at] = make_float2(m, l);
+    }
+  }
+}
+
+// ---- the warp-level kernels' matrix instruction ---------------------------------------------
+
+template <typename T>
+__device__ __forceinline__ void mma(float (&d)[4], const uint4& a, uint32_t b0, uint32_t b1) {
+  if constexpr (sizeof(T) == 2 && std::is_same<T, __nv_bfloat16>::value)
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+  else
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3]) : "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b0), "r"(b1));
+}
+
 }  // namespace specdec

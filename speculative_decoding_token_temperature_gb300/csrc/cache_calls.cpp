@@ -1,10 +1,10 @@
-// The Python side of the cache calls: argument checks, output allocation and the call of the C
+// The Python side of the cache calls and of the logits' processing: argument checks, output allocation and the call of the C
 // entry point, for torch tensors.
 //
 // A call marshals some twenty values for kernels that may take a few microseconds.  In Python
 // (attribute reads, ctypes conversions) that cost 25 us a call on a GB300 host; here, with the
-// tensors' fields at hand, it is a small part of the launch itself.  cache.py documents the calls and
-// passes their arguments on in order.
+// tensors' fields at hand, it is a small part of the launch itself.  cache.py and logits.py document the calls
+// and pass their arguments on in order.
 
 #include <Python.h>
 
@@ -104,20 +104,47 @@ int dimension(int64_t v, const char* name) {
 }
 
 c10::Device cuda_device(const at::Tensor& t, const char* name) {
-  if (!t.is_cuda()) value_error(std::string("the cache calls take CUDA tensors, ") + name + " is on " + t.device().str());
+  if (!t.is_cuda()) value_error(std::string("the call takes CUDA tensors, ") + name + " is on " + t.device().str());
   return t.device();
+}
+
+// The scales of 8-bit pages: [num_pages, page_size / scale_block, kv_heads] bytes, any strides.
+void block_scales(specdec_kv_pages& pg, PyObject* ks, PyObject* vs, int64_t num_pages, c10::Device device) {
+  void* sp[2];
+  int64_t st[2][3], blocks = 0;
+  for (int i = 0; i < 2; ++i) {
+    PyObject* o = i ? vs : ks;
+    const std::string name = i ? "v_scales" : "k_scales";
+    if (!THPVariable_Check(o)) value_error("pages held in 8 bits need " + name);
+    const at::Tensor& t = THPVariable_Unpack(o);
+    if ((t.scalar_type() != at::kByte && t.scalar_type() != at::kFloat8_e8m0fnu) || t.dim() != 3 || t.size(0) != num_pages ||
+        t.size(1) < 1 || (i && t.size(1) != blocks) || t.size(2) != pg.kv_heads || t.device() != device || pg.page_size % t.size(1) != 0)
+      value_error(name + " must be E8M0 bytes of shape (" + std::to_string(num_pages) + ", blocks of a page, " + std::to_string(pg.kv_heads) +
+                  ") on " + device.str() + ", got " + text(t.scalar_type()) + " " + text(t.sizes()) + " on " + t.device().str());
+    blocks = t.size(1);
+    for (int x = 0; x < 3; ++x) st[i][x] = t.size(x) == 1 ? 0 : t.stride(x);
+    sp[i] = t.data_ptr();
+  }
+  if (st[0][0] != st[1][0] || st[0][1] != st[1][1] || st[0][2] != st[1][2]) value_error("k_scales and v_scales must have the same strides");
+  pg.k_scales = sp[0];
+  pg.v_scales = sp[1];
+  pg.scale_page_stride = st[0][0];
+  pg.scale_slot_stride = st[0][1];
+  pg.scale_head_stride = st[0][2];
+  pg.scale_block = static_cast<int32_t>(pg.page_size / blocks);
+  pg.format = SPECDEC_KV8;
 }
 
 specdec_kv_pages pages(PyObject* ko, PyObject* vo, PyObject* table, int64_t B, c10::Device device, int64_t head_dim,
                        PyObject* ks, PyObject* vs, PyObject* k_scale, PyObject* v_scale) {
   const at::Tensor &k = tensor(ko, "k_pages"), &v = tensor(vo, "v_pages");
   const at::ScalarType dt = k.scalar_type();
-  const bool four = dt == at::kByte;
-  if ((!four && !half(dt)) || k.dim() != 4)
-    value_error("pages must be [num_pages, page_size, kv_heads, head_dim] of bfloat16 or float16, or uint8 codes [..., head_dim / 2]");
+  const bool four = dt == at::kByte, eight = dt == at::kFloat8_e4m3fn;
+  if ((!four && !eight && !half(dt)) || k.dim() != 4)
+    value_error("pages must be [num_pages, page_size, kv_heads, head_dim] of bfloat16, float16 or float8_e4m3fn, or uint8 codes [..., head_dim / 2]");
   if (v.scalar_type() != dt || v.sizes() != k.sizes() || k.device() != device || v.device() != device)
     value_error("k_pages and v_pages must have the same type and shape, on the call's device");
-  const int64_t unit = four ? 1 : 2;
+  const int64_t unit = four || eight ? 1 : 2;
   int64_t st[3], other[3];
   if (!strides(k, unit, st) || !strides(v, unit, other) || st[0] != other[0] || st[1] != other[1] || st[2] != other[2])
     value_error("k_pages and v_pages must have the same strides and a contiguous last dimension");
@@ -138,9 +165,15 @@ specdec_kv_pages pages(PyObject* ko, PyObject* vo, PyObject* table, int64_t B, c
   pg.block_table = small<int32_t>(table, "block_table", at::kInt, {B, per}, device);
   pg.max_pages = dimension(per, "max_pages");
   pg.k_scale = pg.v_scale = 1.f;
-  if (!four) {
+  if (!four && !eight) {
     if (ks != Py_None || vs != Py_None) value_error("16-bit pages have no scales");
     pg.format = code(dt);
+    return pg;
+  }
+  if (eight) {
+    block_scales(pg, ks, vs, k.size(0), device);
+    pg.k_scale = static_cast<float>(number(k_scale));
+    pg.v_scale = static_cast<float>(number(v_scale));
     return pg;
   }
   const int64_t want[4] = {k.size(0), k.size(1), k.size(2), pg.head_dim / 16};
@@ -290,7 +323,8 @@ PyObject* rotate_qk(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
 }
 
 // k, v, k_pages, v_pages, block_table, context_len, query_len, k_scales, v_scales, k_scale, v_scale
-PyObject* append_kv4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+template <decltype(&specdec_append_kv4) CALL_C>
+PyObject* append_few_bits(PyObject* const* a, Py_ssize_t n_args, const char* name) {
   return guarded(n_args, 11, [&]() -> PyObject* {
     const at::Tensor &k = tensor(a[0], "k"), &v = tensor(a[1], "v");
     const at::ScalarType dt = k.scalar_type();
@@ -304,17 +338,20 @@ PyObject* append_kv4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const auto* ql = small<int32_t>(a[6], "query_len", at::kInt, {B}, dev);
     const c10::cuda::OptionalCUDAGuard guard(dev);
     at::Tensor status = at::empty({B}, on(dev, at::kInt));
-    checked(specdec_append_kv4(kv.p, kv.st, vv.p, vv.st, code(dt), lens, ql, dimension(B, "B"), dimension(n, "n"), &pg,
+    checked(CALL_C(kv.p, kv.st, vv.p, vv.st, code(dt), lens, ql, dimension(B, "B"), dimension(n, "n"), &pg,
                                static_cast<int32_t*>(status.data_ptr()), c10::cuda::getCurrentCUDAStream(dev.index()).stream()),
-            "specdec_append_kv4");
+            name);
     Dict out;
     put(out.p, "status", std::move(status));
     return out.release();
   });
 }
+PyObject* append_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) { return append_few_bits<specdec_append_kv4>(a, n, "specdec_append_kv4"); }
+PyObject* append_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) { return append_few_bits<specdec_append_kv8>(a, n, "specdec_append_kv8"); }
 
 // k_pages, v_pages, block_table, context_len, n, query_len, k_scales, v_scales, k_scale, v_scale, bfloat16?
-PyObject* read_kv4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+template <decltype(&specdec_read_kv4) CALL_C>
+PyObject* read_few_bits(PyObject* const* a, Py_ssize_t n_args, const char* name) {
   return guarded(n_args, 11, [&]() -> PyObject* {
     const at::Tensor &k = tensor(a[0], "k_pages"), &len = tensor(a[3], "context_len");
     const c10::Device dev = cuda_device(k, "k_pages");
@@ -329,9 +366,9 @@ PyObject* read_kv4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t shape[4] = {B, n > 0 ? n : 0, pg.kv_heads, pg.head_dim};
     at::Tensor out_k = at::empty(at::IntArrayRef(shape, 4), on(dev, dt)), out_v = at::empty(at::IntArrayRef(shape, 4), on(dev, dt));
     at::Tensor status = at::empty({B}, on(dev, at::kInt));
-    checked(specdec_read_kv4(lens, ql, dimension(B, "B"), n, &pg, code(dt), out_k.data_ptr(), out_v.data_ptr(),
+    checked(CALL_C(lens, ql, dimension(B, "B"), n, &pg, code(dt), out_k.data_ptr(), out_v.data_ptr(),
                              static_cast<int32_t*>(status.data_ptr()), c10::cuda::getCurrentCUDAStream(dev.index()).stream()),
-            "specdec_read_kv4");
+            name);
     Dict out;
     put(out.p, "k", std::move(out_k));
     put(out.p, "v", std::move(out_v));
@@ -339,6 +376,8 @@ PyObject* read_kv4(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     return out.release();
   });
 }
+PyObject* read_kv4(PyObject*, PyObject* const* a, Py_ssize_t n) { return read_few_bits<specdec_read_kv4>(a, n, "specdec_read_kv4"); }
+PyObject* read_kv8(PyObject*, PyObject* const* a, Py_ssize_t n) { return read_few_bits<specdec_read_kv8>(a, n, "specdec_read_kv8"); }
 
 // q, k_pages, v_pages, block_table, context_len, query_len, tree_mask, depth, window, sinks, scale, k_scales, v_scales,
 // k_scale, v_scale, with_lse
@@ -351,7 +390,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
     const int64_t B = q.size(0), n = q.size(1), hq = q.size(2), D = q.size(3);
     const View qv = view(q, "q", dt, q.sizes(), dev);
     const specdec_kv_pages pg = pages(a[1], a[2], a[3], B, dev, D, a[11], a[12], a[13], a[14]);
-    if (pg.format != SPECDEC_KV4 && pg.format != code(dt))
+    if (pg.format != SPECDEC_KV4 && pg.format != SPECDEC_KV8 && pg.format != code(dt))
       value_error("q is " + text(dt) + ", the pages are " + text(THPVariable_Unpack(a[1]).scalar_type()));
     const auto* lens = small<int32_t>(a[4], "context_len", at::kInt, {B}, dev);
     const auto* ql = small<int32_t>(a[5], "query_len", at::kInt, {B}, dev);
@@ -379,8 +418,82 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
   });
 }
 
+// logits, tokens, parents, gammas, counts, repetition, presence, frequency, bias_tokens, bias_values, mask, out
+PyObject* process_logits(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded(n_args, 12, [&]() -> PyObject* {
+    const at::Tensor& x = tensor(a[0], "logits");
+    const at::ScalarType dt = x.scalar_type();
+    if (x.dim() != 3 || (dt != at::kFloat && dt != at::kBFloat16) || !x.is_contiguous())
+      value_error("logits must be contiguous [B, rows, V] bfloat16 or float32");
+    const c10::Device dev = cuda_device(x, "logits");
+    const int64_t B = x.size(0), rows = x.size(1), V = x.size(2);
+    const int64_t drafts = rows > 0 ? rows - 1 : 0;
+    const auto* tokens = small<int32_t>(a[1], "tokens", at::kInt, {B, drafts}, dev);
+    const bool has_tokens = a[1] != Py_None;
+    const auto* parents = small<int32_t>(a[2], "parents", at::kInt, {drafts}, dev);
+    if (a[2] != Py_None && !has_tokens) value_error("parents without tokens");
+    const auto* gammas = small<int32_t>(a[3], "gammas", at::kInt, {B}, dev);
+    if (a[2] != Py_None && gammas) value_error("gammas are for chains, parents for trees");
+    const auto* counts = small<int32_t>(a[4], "counts", at::kInt, {B, V}, dev);
+    const float* pen[3];
+    const char* const names[3] = {"repetition", "presence", "frequency"};
+    for (int i = 0; i < 3; ++i) pen[i] = small<float>(a[5 + i], names[i], at::kFloat, {B}, dev);
+    if ((a[8] == Py_None) != (a[9] == Py_None)) value_error("bias_tokens and bias_values come together");
+    int64_t K = 0;
+    if (a[8] != Py_None) {
+      const at::Tensor& bt = tensor(a[8], "bias_tokens");
+      if (bt.dim() != 2) value_error("bias_tokens must be [B, num_bias] int32");
+      K = bt.size(1);
+    }
+    const auto* bias_tokens = small<int32_t>(a[8], "bias_tokens", at::kInt, {B, K}, dev);
+    const auto* bias_values = small<float>(a[9], "bias_values", at::kFloat, {B, K}, dev);
+    const auto* mask = small<uint32_t>(a[10], "mask", at::kInt, {B, rows, (V + 31) / 32}, dev);
+    if (a[11] != Py_None) small<void>(a[11], "out", dt, x.sizes(), dev);
+    const c10::cuda::OptionalCUDAGuard guard(dev);
+    at::Tensor out = a[11] == Py_None ? at::empty({B, rows, V}, on(dev, dt)) : THPVariable_Unpack(a[11]);
+    at::Tensor status = at::empty({B}, on(dev, at::kInt));
+    checked(specdec_process_logits(x.data_ptr(), dt == at::kFloat ? SPECDEC_F32 : SPECDEC_BF16, tokens, drafts ? parents : nullptr, gammas, counts,
+                                   pen[0], pen[1], pen[2], bias_tokens, bias_values, dimension(K, "num_bias"), mask, dimension(B, "B"),
+                                   dimension(rows, "rows"), dimension(V, "V"), out.data_ptr(), static_cast<int32_t*>(status.data_ptr()),
+                                   c10::cuda::getCurrentCUDAStream(dev.index()).stream()),
+            "specdec_process_logits");
+    Dict result;
+    put(result.p, "logits", std::move(out));
+    put(result.p, "status", std::move(status));
+    return result.release();
+  });
+}
+
+// counts, tokens, num_tokens, prompt, reset
+PyObject* count_tokens(PyObject*, PyObject* const* a, Py_ssize_t n_args) {
+  return guarded(n_args, 5, [&]() -> PyObject* {
+    const at::Tensor &counts = tensor(a[0], "counts"), &tokens = tensor(a[1], "tokens");
+    if (counts.dim() != 2) value_error("counts must be [B, V] int32");
+    const c10::Device dev = cuda_device(counts, "counts");
+    const int64_t B = counts.size(0), V = counts.size(1);
+    auto* table = const_cast<int32_t*>(small<int32_t>(a[0], "counts", at::kInt, {B, V}, dev));
+    if (tokens.dim() != 2 || tokens.scalar_type() != at::kInt || tokens.size(0) != B || tokens.device() != dev ||
+        (tokens.size(1) > 1 && tokens.stride(1) != 1))
+      value_error("tokens must be [" + std::to_string(B) + ", n] int32 with contiguous rows on " + dev.str() + ", got " +
+                  text(tokens.scalar_type()) + " " + text(tokens.sizes()) + " on " + tokens.device().str());
+    const auto* num = small<int32_t>(a[2], "num_tokens", at::kInt, {B}, dev);
+    const bool prompt = truth(a[3]), reset = truth(a[4]);
+    const c10::cuda::OptionalCUDAGuard guard(dev);
+    at::Tensor status = at::empty({B}, on(dev, at::kInt));
+    checked(specdec_count_tokens(table, static_cast<const int32_t*>(tokens.data_ptr()), tokens.stride(0), num, dimension(B, "B"),
+                                 dimension(tokens.size(1), "n"), dimension(V, "V"), prompt ? 1 : 0, reset ? 1 : 0,
+                                 static_cast<int32_t*>(status.data_ptr()), c10::cuda::getCurrentCUDAStream(dev.index()).stream()),
+            "specdec_count_tokens");
+    Dict out;
+    put(out.p, "counts", counts);
+    put(out.p, "status", std::move(status));
+    return out.release();
+  });
+}
+
 #define CALL(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {CALL(rotate_qk), CALL(append_kv4), CALL(read_kv4), CALL(attend), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {CALL(rotate_qk), CALL(append_kv4), CALL(read_kv4), CALL(append_kv8), CALL(read_kv8),
+                         CALL(attend), CALL(process_logits), CALL(count_tokens), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_cache_calls", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -1,5 +1,5 @@
-// Host/device interface of the cache operators: rotation with the page write, the 4-bit
-// write and read, attention over pages.
+// Host/device interface of the cache operators: rotation with the page write, the 4-bit and
+// 8-bit writes and reads, attention over pages.
 #pragma once
 
 #include <cstddef>
@@ -23,6 +23,8 @@ struct Pages {
   int kv_heads, head_dim;
   float k_scale, v_scale;
   uint64_t page_magic;   // 2^64 / page_size, rounded up (0 for pages of one slot)
+  int scale_block;       // 8-bit pages: slots that share a scale
+  uint64_t block_magic;  // 2^64 / scale_block, rounded up
 };
 
 struct RotateParams {
@@ -40,7 +42,8 @@ struct RotateParams {
 };
 cudaError_t launch_rotate_qk(const RotateParams& P, specdec_dtype dt, cudaStream_t stream);
 
-struct Kv4Params {
+// The write and read of pages held in few bits.
+struct KvParams {
   const void *k, *v;  // append: [B, n, Hkv, D] inputs, strides in elements
   int64_t k_sb, k_st, k_sh, v_sb, v_st, v_sh;
   float k_inv, v_inv;   // append: 1 / the tensor-wide scales, rounded to fp32
@@ -50,8 +53,10 @@ struct Kv4Params {
   int32_t* out_status;
   Pages pages;
 };
-cudaError_t launch_append_kv4(const Kv4Params& P, specdec_dtype dt, cudaStream_t stream);
-cudaError_t launch_read_kv4(const Kv4Params& P, specdec_dtype dt, cudaStream_t stream);
+cudaError_t launch_append_kv4(const KvParams& P, specdec_dtype dt, cudaStream_t stream);
+cudaError_t launch_read_kv4(const KvParams& P, specdec_dtype dt, cudaStream_t stream);
+cudaError_t launch_append_kv8(const KvParams& P, specdec_dtype dt, cudaStream_t stream);
+cudaError_t launch_read_kv8(const KvParams& P, specdec_dtype dt, cudaStream_t stream);
 
 struct AttendParams {
   const void* q;  // [B, n, Hq, D]; strides in elements, the last is 1
@@ -78,6 +83,9 @@ struct AttendParams {
 int attend_tc_rows(int64_t rows);
 cudaError_t launch_attend_tc(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream);
 cudaError_t launch_attend_tc4(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream);
+// The warp-level kernel over 8-bit pages: the rows of its tile, and its launch.
+int attend8_rows(int64_t rows);
+cudaError_t launch_attend8(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream);
 size_t attend_workspace_bytes(int n, int G, int D);
 cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format, void* workspace,
                           cudaStream_t stream);

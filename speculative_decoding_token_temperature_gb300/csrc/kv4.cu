@@ -69,19 +69,6 @@ __device__ __forceinline__ uint2 quantise(const uint4& lo, const uint4& hi, floa
   return make_uint2(word[0], word[1]);
 }
 
-// Whether sequence b's lengths and the pages of its slots [first, len) are in range; every
-// thread of the CTA calls it, and gets the same answer.
-__device__ __forceinline__ bool sequence_fits(const SeqLen& S, const Pages& pg, int b) {
-  int bad = S.ok ? 0 : 1;
-  if (S.ok && S.nq > 0) {
-    const int32_t* table = pg.table + static_cast<int64_t>(b) * pg.max_pages;
-    const int p0 = page_of(pg, S.first), p1 = page_of(pg, S.len - 1);
-    for (int p = p0 + threadIdx.x; p <= p1; p += blockDim.x)
-      bad |= static_cast<unsigned>(__ldg(table + p)) >= static_cast<unsigned>(pg.num_pages);
-  }
-  return !__syncthreads_or(bad);
-}
-
 // A thread's column of PER values of a token (K's heads, then V's), and its tokens: i, i + rows, ...
 template <int PER>
 struct Column {
@@ -117,7 +104,7 @@ struct Slots {
 
 // grid (chunks of a sequence's tokens x chunks of a token's columns, B)
 template <typename T>
-__global__ void __launch_bounds__(kKv4Threads) append_kv4_kernel(const Kv4Params P) {
+__global__ void __launch_bounds__(kKv4Threads) append_kv4_kernel(const KvParams P) {
   const Pages& pg = P.pages;
   const int b = blockIdx.y;
   __shared__ Slots slots;
@@ -156,7 +143,7 @@ __global__ void __launch_bounds__(kKv4Threads) append_kv4_kernel(const Kv4Params
 
 // Read back by columns of 8 values: 4 bytes of codes and a scale in, 16 bytes out.
 template <typename T>
-__global__ void __launch_bounds__(kKv4Threads) read_kv4_kernel(const Kv4Params P) {
+__global__ void __launch_bounds__(kKv4Threads) read_kv4_kernel(const KvParams P) {
   const Pages& pg = P.pages;
   const int b = blockIdx.y;
   __shared__ Slots slots;
@@ -203,7 +190,7 @@ __global__ void __launch_bounds__(kKv4Threads) read_kv4_kernel(const Kv4Params P
   }
 }
 
-dim3 columns_grid(const Kv4Params& P, int per) {
+dim3 columns_grid(const KvParams& P, int per) {
   const int columns = 2 * P.pages.kv_heads * (P.pages.head_dim / per);
   const int tokens = kKv4Threads / (columns < kKv4Threads ? columns : kKv4Threads) * kSteps;
   return dim3(static_cast<unsigned>((P.n + tokens - 1) / tokens) * static_cast<unsigned>((columns + kKv4Threads - 1) / kKv4Threads),
@@ -212,13 +199,13 @@ dim3 columns_grid(const Kv4Params& P, int per) {
 
 }  // namespace
 
-cudaError_t launch_append_kv4(const Kv4Params& P, specdec_dtype dt, cudaStream_t stream) {
+cudaError_t launch_append_kv4(const KvParams& P, specdec_dtype dt, cudaStream_t stream) {
   const dim3 block(kKv4Threads);
   return dt == SPECDEC_BF16 ? launch_kernel(append_kv4_kernel<__nv_bfloat16>, columns_grid(P, kGroup4), block, 0, stream, 0, P)
                             : launch_kernel(append_kv4_kernel<__half>, columns_grid(P, kGroup4), block, 0, stream, 0, P);
 }
 
-cudaError_t launch_read_kv4(const Kv4Params& P, specdec_dtype dt, cudaStream_t stream) {
+cudaError_t launch_read_kv4(const KvParams& P, specdec_dtype dt, cudaStream_t stream) {
   const dim3 block(kKv4Threads);
   return dt == SPECDEC_BF16 ? launch_kernel(read_kv4_kernel<__nv_bfloat16>, columns_grid(P, 8), block, 0, stream, 0, P)
                             : launch_kernel(read_kv4_kernel<__half>, columns_grid(P, 8), block, 0, stream, 0, P);

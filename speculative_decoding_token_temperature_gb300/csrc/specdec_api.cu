@@ -13,6 +13,7 @@
 #include <cuda_runtime.h>
 
 #include "cache_ops.h"
+#include "logits_ops.h"
 #include "specdec.h"
 #include "specdec_internal.h"
 
@@ -703,10 +704,12 @@ int check_view(const void* p, const int64_t* st, const char* what) {
   return SPECDEC_OK;
 }
 
-int check_pages(const specdec_kv_pages* pg, bool four, specdec_dtype dt, Pages* out) {
+// Pages of the given format (SPECDEC_BF16, SPECDEC_F16, SPECDEC_KV4 or SPECDEC_KV8).
+int check_pages(const specdec_kv_pages* pg, specdec_dtype format, Pages* out) {
   if (!pg) return fail(SPECDEC_ERR_INVALID_ARG, "pages is null");
-  if (pg->format != (four ? SPECDEC_KV4 : dt)) return fail(SPECDEC_ERR_INVALID_ARG, "the pages' format does not fit the call");
-  if (!pg->k || !pg->v || !pg->block_table || (four && (!pg->k_scales || !pg->v_scales)))
+  if (pg->format != format) return fail(SPECDEC_ERR_INVALID_ARG, "the pages' format does not fit the call");
+  const bool four = format == SPECDEC_KV4, eight = format == SPECDEC_KV8;
+  if (!pg->k || !pg->v || !pg->block_table || ((four || eight) && (!pg->k_scales || !pg->v_scales)))
     return fail(SPECDEC_ERR_INVALID_ARG, "a required pointer of the pages is null");
   if (pg->num_pages <= 0 || pg->page_size <= 0 || pg->max_pages <= 0 || pg->kv_heads <= 0)
     return fail(SPECDEC_ERR_INVALID_ARG, "num_pages, page_size, max_pages and kv_heads must be positive");
@@ -720,6 +723,17 @@ int check_pages(const specdec_kv_pages* pg, bool four, specdec_dtype dt, Pages* 
     if (!aligned_to(pg->k_scales, u) || !aligned_to(pg->v_scales, u) ||
         !multiples(u, {pg->scale_page_stride, pg->scale_slot_stride, pg->scale_head_stride}))
       return fail(SPECDEC_ERR_UNSUPPORTED, "scales and their strides must be multiples of head_dim / 16 bytes (not negative)");
+  }
+  if (eight) {
+    if (pg->scale_block <= 0) return fail(SPECDEC_ERR_INVALID_ARG, "scale_block must be positive");
+    if (pg->scale_block % 16 != 0 || pg->page_size % pg->scale_block != 0)
+      return fail(SPECDEC_ERR_UNSUPPORTED, "page_size must be a multiple of scale_block, that a multiple of 16");
+    if (!multiples(1, {pg->scale_page_stride, pg->scale_slot_stride, pg->scale_head_stride}))
+      return fail(SPECDEC_ERR_UNSUPPORTED, "scale strides must not be negative");
+    if (!(1.f / pg->k_scale <= 3.4e38f && 1.f / pg->v_scale <= 3.4e38f))  // (NaN and 0 among them)
+      return fail(SPECDEC_ERR_INVALID_ARG, "k_scale and v_scale need finite reciprocals");
+  }
+  if (four || eight) {
     if (!(pg->k_scale > 0.f && pg->k_scale <= 3.4e38f && pg->v_scale > 0.f && pg->v_scale <= 3.4e38f))
       return fail(SPECDEC_ERR_INVALID_ARG, "k_scale and v_scale must be positive and finite");
   }
@@ -741,8 +755,65 @@ int check_pages(const specdec_kv_pages* pg, bool four, specdec_dtype dt, Pages* 
   o.max_pages = pg->max_pages;
   o.kv_heads = pg->kv_heads;
   o.head_dim = pg->head_dim;
-  o.k_scale = four ? pg->k_scale : 1.f;
-  o.v_scale = four ? pg->v_scale : 1.f;
+  o.k_scale = four || eight ? pg->k_scale : 1.f;
+  o.v_scale = four || eight ? pg->v_scale : 1.f;
+  o.scale_block = eight ? pg->scale_block : 0;
+  o.block_magic = eight ? ~uint64_t{0} / static_cast<uint64_t>(pg->scale_block) + 1 : 0;
+  return SPECDEC_OK;
+}
+
+// The writes and reads of pages held in few bits (SPECDEC_KV4, SPECDEC_KV8).
+int append_few_bits(specdec_dtype format, const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                    specdec_dtype dtype, const int32_t* context_len, const int32_t* query_len, int B, int n,
+                    const specdec_kv_pages* pages, int32_t* out_status, void* stream) {
+  if (!valid_half(dtype)) return fail(SPECDEC_ERR_INVALID_ARG, "dtype must be SPECDEC_BF16 or SPECDEC_F16");
+  if (B <= 0 || n <= 0 || !context_len) return fail(SPECDEC_ERR_INVALID_ARG, "B and n must be positive, context_len given");
+  KvParams P{};
+  if (int rc = check_view(k, k_strides, "k is null"); rc != SPECDEC_OK) return rc;
+  if (int rc = check_view(v, v_strides, "v is null"); rc != SPECDEC_OK) return rc;
+  if (int rc = check_pages(pages, format, &P.pages); rc != SPECDEC_OK) return rc;
+  if (B > 65535 || static_cast<int64_t>(n) * pages->kv_heads >= (1 << 26)) return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, or n * kv_heads above 2^26");
+  P.k = k;
+  P.v = v;
+  P.k_sb = k_strides[0]; P.k_st = k_strides[1]; P.k_sh = k_strides[2];
+  P.v_sb = v_strides[0]; P.v_st = v_strides[1]; P.v_sh = v_strides[2];
+  P.k_inv = 1.f / pages->k_scale;
+  P.v_inv = 1.f / pages->v_scale;
+  P.context_len = context_len;
+  P.query_len = query_len;
+  P.B = B;
+  P.n = n;
+  P.out_status = out_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool four = format == SPECDEC_KV4;
+  ProfScope prof(four ? SPECDEC_KERNEL_APPEND_KV4 : SPECDEC_KERNEL_APPEND_KV8, s);
+  if (cudaError_t e = four ? launch_append_kv4(P, dtype, s) : launch_append_kv8(P, dtype, s); e != cudaSuccess)
+    return fail_cuda(four ? "4-bit page write kernel" : "8-bit page write kernel", e);
+  return SPECDEC_OK;
+}
+
+int read_few_bits(specdec_dtype format, const int32_t* context_len, const int32_t* query_len, int B, int n,
+                  const specdec_kv_pages* pages, specdec_dtype dtype, void* out_k, void* out_v,
+                  int32_t* out_status, void* stream) {
+  if (!valid_half(dtype)) return fail(SPECDEC_ERR_INVALID_ARG, "dtype must be SPECDEC_BF16 or SPECDEC_F16");
+  if (B <= 0 || n <= 0 || !context_len || !out_k || !out_v)
+    return fail(SPECDEC_ERR_INVALID_ARG, "B and n must be positive, the pointers given");
+  KvParams P{};
+  if (int rc = check_pages(pages, format, &P.pages); rc != SPECDEC_OK) return rc;
+  if (!aligned16(out_k) || !aligned16(out_v)) return fail(SPECDEC_ERR_UNSUPPORTED, "outputs must be 16-byte aligned");
+  if (B > 65535 || static_cast<int64_t>(n) * pages->kv_heads >= (1 << 26)) return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, or n * kv_heads above 2^26");
+  P.k_out = out_k;
+  P.v_out = out_v;
+  P.context_len = context_len;
+  P.query_len = query_len;
+  P.B = B;
+  P.n = n;
+  P.out_status = out_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool four = format == SPECDEC_KV4;
+  ProfScope prof(four ? SPECDEC_KERNEL_READ_KV4 : SPECDEC_KERNEL_READ_KV8, s);
+  if (cudaError_t e = four ? launch_read_kv4(P, dtype, s) : launch_read_kv8(P, dtype, s); e != cudaSuccess)
+    return fail_cuda(four ? "4-bit page read kernel" : "8-bit page read kernel", e);
   return SPECDEC_OK;
 }
 
@@ -771,7 +842,7 @@ int specdec_rotate_qk(const void* q, const int64_t* q_strides, const void* k, co
     return fail(SPECDEC_ERR_UNSUPPORTED, "outputs and weights must be 16-byte aligned");
   RotateParams P{};
   if (pages) {
-    if (int rc = check_pages(pages, false, dtype, &P.pages); rc != SPECDEC_OK) return rc;
+    if (int rc = check_pages(pages, dtype, &P.pages); rc != SPECDEC_OK) return rc;
     if (pages->kv_heads != kv_heads || pages->head_dim != head_dim)
       return fail(SPECDEC_ERR_INVALID_ARG, "the pages' heads do not fit k");
   }
@@ -809,51 +880,25 @@ int specdec_rotate_qk(const void* q, const int64_t* q_strides, const void* k, co
 int specdec_append_kv4(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
                        specdec_dtype dtype, const int32_t* context_len, const int32_t* query_len, int B, int n,
                        const specdec_kv_pages* pages, int32_t* out_status, void* stream) {
-  if (!valid_half(dtype)) return fail(SPECDEC_ERR_INVALID_ARG, "dtype must be SPECDEC_BF16 or SPECDEC_F16");
-  if (B <= 0 || n <= 0 || !context_len) return fail(SPECDEC_ERR_INVALID_ARG, "B and n must be positive, context_len given");
-  Kv4Params P{};
-  if (int rc = check_view(k, k_strides, "k is null"); rc != SPECDEC_OK) return rc;
-  if (int rc = check_view(v, v_strides, "v is null"); rc != SPECDEC_OK) return rc;
-  if (int rc = check_pages(pages, true, dtype, &P.pages); rc != SPECDEC_OK) return rc;
-  if (B > 65535 || static_cast<int64_t>(n) * pages->kv_heads >= (1 << 26)) return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, or n * kv_heads above 2^26");
-  P.k = k;
-  P.v = v;
-  P.k_sb = k_strides[0]; P.k_st = k_strides[1]; P.k_sh = k_strides[2];
-  P.v_sb = v_strides[0]; P.v_st = v_strides[1]; P.v_sh = v_strides[2];
-  P.k_inv = 1.f / pages->k_scale;
-  P.v_inv = 1.f / pages->v_scale;
-  P.context_len = context_len;
-  P.query_len = query_len;
-  P.B = B;
-  P.n = n;
-  P.out_status = out_status;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  ProfScope prof(SPECDEC_KERNEL_APPEND_KV4, s);
-  if (cudaError_t e = launch_append_kv4(P, dtype, s); e != cudaSuccess) return fail_cuda("4-bit page write kernel", e);
-  return SPECDEC_OK;
+  return append_few_bits(SPECDEC_KV4, k, k_strides, v, v_strides, dtype, context_len, query_len, B, n, pages, out_status, stream);
 }
 
 int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B, int n,
                      const specdec_kv_pages* pages, specdec_dtype dtype, void* out_k, void* out_v,
                      int32_t* out_status, void* stream) {
-  if (!valid_half(dtype)) return fail(SPECDEC_ERR_INVALID_ARG, "dtype must be SPECDEC_BF16 or SPECDEC_F16");
-  if (B <= 0 || n <= 0 || !context_len || !out_k || !out_v)
-    return fail(SPECDEC_ERR_INVALID_ARG, "B and n must be positive, the pointers given");
-  Kv4Params P{};
-  if (int rc = check_pages(pages, true, dtype, &P.pages); rc != SPECDEC_OK) return rc;
-  if (!aligned16(out_k) || !aligned16(out_v)) return fail(SPECDEC_ERR_UNSUPPORTED, "outputs must be 16-byte aligned");
-  if (B > 65535 || static_cast<int64_t>(n) * pages->kv_heads >= (1 << 26)) return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, or n * kv_heads above 2^26");
-  P.k_out = out_k;
-  P.v_out = out_v;
-  P.context_len = context_len;
-  P.query_len = query_len;
-  P.B = B;
-  P.n = n;
-  P.out_status = out_status;
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  ProfScope prof(SPECDEC_KERNEL_READ_KV4, s);
-  if (cudaError_t e = launch_read_kv4(P, dtype, s); e != cudaSuccess) return fail_cuda("4-bit page read kernel", e);
-  return SPECDEC_OK;
+  return read_few_bits(SPECDEC_KV4, context_len, query_len, B, n, pages, dtype, out_k, out_v, out_status, stream);
+}
+
+int specdec_append_kv8(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
+                       specdec_dtype dtype, const int32_t* context_len, const int32_t* query_len, int B, int n,
+                       const specdec_kv_pages* pages, int32_t* out_status, void* stream) {
+  return append_few_bits(SPECDEC_KV8, k, k_strides, v, v_strides, dtype, context_len, query_len, B, n, pages, out_status, stream);
+}
+
+int specdec_read_kv8(const int32_t* context_len, const int32_t* query_len, int B, int n,
+                     const specdec_kv_pages* pages, specdec_dtype dtype, void* out_k, void* out_v,
+                     int32_t* out_status, void* stream) {
+  return read_few_bits(SPECDEC_KV8, context_len, query_len, B, n, pages, dtype, out_k, out_v, out_status, stream);
 }
 
 size_t specdec_attend_workspace_bytes(int B, int n, int q_heads, int kv_heads, int head_dim) {
@@ -875,8 +920,9 @@ int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype,
     return fail(SPECDEC_ERR_INVALID_ARG, "the workspace must be 256-byte aligned");
   if (int rc = check_view(q, q_strides, "q is null"); rc != SPECDEC_OK) return rc;
   AttendParams P{};
-  const bool four = pages && pages->format == SPECDEC_KV4;
-  if (int rc = check_pages(pages, four, dtype, &P.pages); rc != SPECDEC_OK) return rc;
+  const specdec_dtype format = pages && (pages->format == SPECDEC_KV4 || pages->format == SPECDEC_KV8)
+                                   ? static_cast<specdec_dtype>(pages->format) : dtype;
+  if (int rc = check_pages(pages, format, &P.pages); rc != SPECDEC_OK) return rc;
   if (q_heads % pages->kv_heads != 0) return fail(SPECDEC_ERR_INVALID_ARG, "q_heads must be a multiple of kv_heads");
   const int G = q_heads / pages->kv_heads;
   if (B >= (1 << 24) || static_cast<int64_t>(n) * G >= (1 << 24) || G >= (1 << 16))
@@ -906,8 +952,71 @@ int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype,
   P.out_status = out_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ProfScope prof(SPECDEC_KERNEL_ATTEND, s);
-  if (cudaError_t e = launch_attend(P, dtype, four ? SPECDEC_KV4 : dtype, workspace, s); e != cudaSuccess)
+  if (cudaError_t e = launch_attend(P, dtype, format, workspace, s); e != cudaSuccess)
     return fail_cuda("attention kernels", e);
+  return SPECDEC_OK;
+}
+
+int specdec_process_logits(const void* logits, specdec_dtype dtype, const int32_t* tokens, const int32_t* parents,
+                           const int32_t* gammas, const int32_t* counts, const float* repetition,
+                           const float* presence, const float* frequency, const int32_t* bias_tokens,
+                           const float* bias_values, int num_bias, const uint32_t* mask, int B, int rows, int V,
+                           void* out, int32_t* out_status, void* stream) {
+  if (!valid_dtype(dtype)) return fail(SPECDEC_ERR_INVALID_ARG, "dtype must be SPECDEC_F32 or SPECDEC_BF16");
+  if (B <= 0 || rows <= 0 || V <= 0 || num_bias < 0) return fail(SPECDEC_ERR_INVALID_ARG, "sizes must be positive");
+  if (!logits || !out) return fail(SPECDEC_ERR_INVALID_ARG, "a required pointer is null");
+  if (num_bias > 0 && (!bias_tokens || !bias_values)) return fail(SPECDEC_ERR_INVALID_ARG, "a list of biases has tokens and values");
+  if (parents && !tokens) return fail(SPECDEC_ERR_INVALID_ARG, "parents without tokens");
+  if (parents && gammas) return fail(SPECDEC_ERR_INVALID_ARG, "a number of drafts for each sequence is for chains");
+  const size_t es = elem_size(dtype);
+  if (!aligned_to(logits, es) || !aligned_to(out, es) || !aligned_to(mask, 4)) return fail(SPECDEC_ERR_UNSUPPORTED, "logits, out or mask is not aligned to its elements");
+  if (B > 65535 || rows > kMaxProcessRows || num_bias >= (1 << 24) || V >= INT32_MAX - 65536)
+    return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, more than 8192 rows, 2^24 biases, or a vocabulary above 2^31 - 65536");
+  ProcessParams P{};
+  P.logits = logits;
+  P.tokens = rows > 1 ? tokens : nullptr;
+  P.parents = rows > 1 ? parents : nullptr;
+  P.gammas = gammas;
+  P.counts = counts;
+  P.repetition = repetition;
+  P.presence = presence;
+  P.frequency = frequency;
+  P.bias_tokens = bias_tokens;
+  P.bias_values = bias_values;
+  P.num_bias = num_bias;
+  P.mask = mask;
+  P.words = static_cast<int>((static_cast<int64_t>(V) + 31) / 32);
+  P.B = B;
+  P.rows = rows;
+  P.V = V;
+  P.out = out;
+  P.out_status = out_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope prof(SPECDEC_KERNEL_PROCESS_LOGITS, s);
+  const bool vec = rows_vectorizable(logits, V, es) && rows_vectorizable(out, V, es);
+  if (cudaError_t e = launch_process_logits(P, dtype, vec, s); e != cudaSuccess) return fail_cuda("logits processing kernel", e);
+  return SPECDEC_OK;
+}
+
+int specdec_count_tokens(int32_t* counts, const int32_t* tokens, int64_t token_stride, const int32_t* num_tokens, int B,
+                         int n, int V, int prompt, int reset, int32_t* out_status, void* stream) {
+  if (B <= 0 || n < 0 || V <= 0) return fail(SPECDEC_ERR_INVALID_ARG, "B and V must be positive, n not negative");
+  if (!counts || (!tokens && n > 0)) return fail(SPECDEC_ERR_INVALID_ARG, "a required pointer is null");
+  if (token_stride < 0) return fail(SPECDEC_ERR_INVALID_ARG, "token_stride must not be negative");
+  if (B > 65535 || V >= INT32_MAX - 65536 || n >= INT32_MAX - 65536) return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, or a size above 2^31 - 65536");
+  CountParams P{};
+  P.counts = counts;
+  P.tokens = tokens;
+  P.token_stride = token_stride;
+  P.num_tokens = num_tokens;
+  P.B = B;
+  P.n = n;
+  P.V = V;
+  P.prompt = prompt;
+  P.out_status = out_status;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  ProfScope prof(SPECDEC_KERNEL_COUNT_TOKENS, s);
+  if (cudaError_t e = launch_count_tokens(P, reset != 0, s); e != cudaSuccess) return fail_cuda("token count kernel", e);
   return SPECDEC_OK;
 }
 
