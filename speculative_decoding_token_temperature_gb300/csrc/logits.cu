@@ -3,9 +3,12 @@
 //   x = l;  if c > 0 or the token is in the prompt:  x = x > 0 ? x / r : x * r
 //   y = x + (bias - (f c + p [c > 0])),  -inf where the row's mask has no bit
 // for every token of every row, c the token's count among what the row follows: the sequence's own (`counts`) and the
-// drafts before the row.  A token's bias and counts are the same for all rows of a sequence but for the few tokens that are
-// drafts, so a thread keeps them for its columns in registers and runs over the rows; a column that is some
-// draft's token takes a way of its own, which walks the row's drafts.
+// drafts before the row.
+//
+// Few tokens of a vocabulary have a count, a bias or are drafts; for all others y = l, or -inf.  So the call is a copy of the rows
+// under their masks, bound by HBM, in which a few elements are changed on the way.  A CTA takes a chunk of the vocabulary and some
+// rows of a sequence.  The rows come to shared memory by 16-byte asynchronous copies, kBatch at a time and two batches ahead, while
+// the CTA lists its chunk's tokens that change; those are changed in shared memory, and the words go out.
 
 #include <algorithm>
 
@@ -19,32 +22,22 @@ namespace {
 
 constexpr int kThreads = 256;
 
-template <typename T> struct Wide;  // 16 bytes of a row as fp32, and back
-template <> struct Wide<float> {
-  static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[4]) {
-    x[0] = __uint_as_float(w.x); x[1] = __uint_as_float(w.y); x[2] = __uint_as_float(w.z); x[3] = __uint_as_float(w.w);
-  }
-  static __device__ __forceinline__ uint4 pack(const float (&x)[4]) {
-    return make_uint4(__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]), __float_as_uint(x[3]));
-  }
-  static __device__ __forceinline__ float one(const float* p) { return *p; }
-  static __device__ __forceinline__ void put(float* p, float x) { *p = x; }
+template <typename T> struct Elem16;  // an element as fp32, and back
+template <> struct Elem16<float> {
+  static constexpr uint32_t kNone = 0xff800000u, kPair = 1;  // -inf in a word; elements of a word
+  static __device__ __forceinline__ float part(const uint32_t (&w)[4], int e) { return __uint_as_float(w[e]); }
+  static __device__ __forceinline__ float get(float x) { return x; }
+  static __device__ __forceinline__ float put(float x) { return x; }
 };
-__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {  // round to nearest even
-  uint32_t w;
-  asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(w) : "f"(hi), "f"(lo));
-  return w;
-}
-template <> struct Wide<uint16_t> {  // bf16
-  static __device__ __forceinline__ void unpack(const uint4& w, float (&x)[8]) {
-    x[0] = bf16_lo(w.x); x[1] = bf16_hi(w.x); x[2] = bf16_lo(w.y); x[3] = bf16_hi(w.y);
-    x[4] = bf16_lo(w.z); x[5] = bf16_hi(w.z); x[6] = bf16_lo(w.w); x[7] = bf16_hi(w.w);
+template <> struct Elem16<uint16_t> {  // bf16
+  static constexpr uint32_t kNone = 0xff80ff80u, kPair = 2;
+  static __device__ __forceinline__ uint16_t part(const uint32_t (&w)[4], int e) { return static_cast<uint16_t>(w[e / 2] >> (16 * (e % 2))); }
+  static __device__ __forceinline__ float get(uint16_t x) { return __uint_as_float(static_cast<uint32_t>(x) << 16); }
+  static __device__ __forceinline__ uint16_t put(float x) {  // round to nearest even
+    uint16_t w;
+    asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(w) : "f"(x));
+    return w;
   }
-  static __device__ __forceinline__ uint4 pack(const float (&x)[8]) {
-    return make_uint4(pack_bf16(x[0], x[1]), pack_bf16(x[2], x[3]), pack_bf16(x[4], x[5]), pack_bf16(x[6], x[7]));
-  }
-  static __device__ __forceinline__ float one(const uint16_t* p) { return __uint_as_float(static_cast<uint32_t>(*p) << 16); }
-  static __device__ __forceinline__ void put(uint16_t* p, float x) { *p = static_cast<uint16_t>(pack_bf16(x, 0.f)); }
 };
 
 struct Penalties {
@@ -54,109 +47,289 @@ struct Penalties {
   __device__ __forceinline__ float added(int c, float bias) const { return c > 0 ? bias - fmaf(frequency, static_cast<float>(c), presence) : bias; }
 };
 
-// A CTA takes a chunk of the vocabulary and some rows of a sequence.  grid (chunks, groups of rows, B); VEC: 16 bytes of a row
-// at a time, or one element where rows do not start on 16 bytes.
-template <typename T, int VEC>
+// Rows of a batch, and batches in flight.  256 x 8 rows of 128256 logits in bf16, 32 x 65 rows of 32001 under masks (us): 2, 2: 196,
+// 110; 4, 2: 215, 117; 4, 1: 211, 107; 2, 3: 195, 112; 2, 4: 229, 125.  (Rows held in registers, and the tokens changed in them
+// or in a pass of their own behind the copy: 217 to 275, 156 to 194.)
+constexpr int kBatch = 2, kStages = 2;
+
+__device__ __forceinline__ void copy_async16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_addr(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int LEFT>
+__device__ __forceinline__ void copy_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(LEFT) : "memory");
+}
+
+// The columns of a CTA: 16 bytes of a row for each thread, one less where rows do not start on 16 bytes (and a chunk then
+// touches a word more).
+template <typename T, bool ALIGNED>
+constexpr int kChunk = (ALIGNED ? kThreads : kThreads - 1) * (16 / static_cast<int>(sizeof(T)));
+
+// ALIGNED: every row of logits and out starts on 16 bytes.  grid (chunks, groups of rows, B)
+template <typename T, bool ALIGNED, bool MASKED>
 __global__ void __launch_bounds__(kThreads) process_kernel(const ProcessParams P) {
-  constexpr int NV = VEC == 1 ? 4 : 1, CHUNK = kThreads * VEC * NV;
-  __shared__ int s_bias[CHUNK];            // 1 + the entry of the bias list that counts for a token
-  __shared__ uint32_t s_mark[CHUNK / 32];  // tokens of drafts
-  extern __shared__ int s_draft[];         // [rows - 1] drafts, [rows - 1] their parents
+  constexpr int N = 16 / sizeof(T), CHUNK = kChunk<T, ALIGNED>, WORDS = kThreads * N / 32;
+  constexpr uint32_t kAll = (1u << N) - 1;
+  using E = Elem16<T>;
+  __shared__ __align__(16) T s_rows[kStages][kBatch][kThreads * N];
+  __shared__ __align__(16) int s_value[kThreads * N];  // by column: 1 + the entry of the bias list that counts, then what is added
+  __shared__ uint16_t s_list[kThreads * N];            // the columns that change
+  __shared__ uint32_t s_some[WORDS], s_mark[WORDS];    // the same as bits; columns that are some draft's token
+  __shared__ int s_sum[kThreads / 32], s_status;
+  extern __shared__ int s_draft[];                     // [rows - 1] drafts, [rows - 1] their parents
   int* const s_parent = s_draft + P.rows - 1;
-  const int b = blockIdx.z, lo = blockIdx.x * CHUNK, tid = threadIdx.x;
-  int bad = 0, gamma = P.rows - 1;
-  if (P.gammas) {
-    gamma = __ldg(P.gammas + b);
-    if (gamma < 0 || gamma >= P.rows) bad |= SPECDEC_STATUS_BAD_TOKEN;
+  const int b = blockIdx.z, lo = blockIdx.x * CHUNK, size = min(CHUNK, P.V - lo), tid = threadIdx.x, lane = tid % 32;
+  const int64_t row0 = static_cast<int64_t>(b) * P.rows;
+  const T* const logits = static_cast<const T*>(P.logits);
+
+  int gamma = P.rows - 1;
+  if (P.gammas) gamma = __ldg(P.gammas + b);
+  const bool counted = gamma >= 0 && gamma < P.rows;
+  const int r0 = blockIdx.y * P.group, r1 = min(r0 + P.group, counted ? gamma + 1 : P.rows);
+  // the chunk's part of row r, and how many elements past a 16-byte border it starts
+  auto from = [&](int r) { return logits + (row0 + r) * P.V + lo; };
+  auto to = [&](int r) { return static_cast<T*>(P.out) + (row0 + r) * P.V + lo; };
+  auto past = [&](const T* row) { return ALIGNED ? 0 : static_cast<int>(reinterpret_cast<uintptr_t>(row) / sizeof(T)) & (N - 1); };
+  auto bit = [&](int r, int t) -> bool {
+    return __ldg(reinterpret_cast<const uint8_t*>(P.mask + (row0 + r) * P.words) + (lo + t) / 8) >> ((lo + t) % 8) & 1u;
+  };
+  // This thread's word of a row is columns tid * N - past ..: the elements of it that are the chunk's, and those that the mask allows.
+  auto mine = [&](int off) -> uint32_t {
+    const int first = tid * N - off;
+    if (ALIGNED) return first < size ? kAll : 0u;
+    const uint32_t below = first >= 0 ? kAll : kAll & (kAll << -first), over = size - first >= N ? kAll : size > first ? (1u << (size - first)) - 1 : 0u;
+    return below & over;
+  };
+  auto look = [&](int r) -> uint32_t {
+    if (r >= r1) return 0u;
+    const int off = past(from(r));
+    uint32_t some = mine(off);
+    if constexpr (MASKED) {
+      if (some == 0) return 0u;
+      const uint8_t* const m = reinterpret_cast<const uint8_t*>(P.mask + (row0 + r) * P.words);
+      if constexpr (ALIGNED) {
+        some &= __ldg(m + (lo + tid * N) / 8) >> ((lo + tid * N) % 8);
+      } else {  // (a column below 0 belongs to another chunk or row: not looked at)
+        const int first = lo + tid * N - off, last = min(first + N, P.V) - 1;
+        uint32_t w = first >= 0 ? __ldg(m + first / 8) : 0u;
+        if (last / 8 != (first < 0 ? -1 : first / 8)) w |= static_cast<uint32_t>(__ldg(m + last / 8)) << (first < 0 ? 0 : 8);
+        some &= first >= 0 ? w >> (first % 8) : w << -first;
+      }
+    }
+    return some;
+  };
+  uint32_t allowed[kStages][kBatch];  // of the batches in flight
+  auto issue = [&](int r, int stage) {
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (allowed[stage][k] == 0) continue;
+      const T* const row = from(r + k);
+      const T* const at = row - past(row) + tid * N;
+      T* const dst = s_rows[stage][k] + tid * N;
+      if (ALIGNED || (at >= logits && at + N <= logits + static_cast<int64_t>(P.B) * P.rows * P.V)) {
+        copy_async16(dst, at);
+      } else {  // a word that reaches past the logits' ends
+#pragma unroll
+        for (int e = 0; e < N; ++e)
+          if (allowed[stage][k] >> e & 1u) dst[e] = at[e];
+      }
+    }
+    copy_commit();
+  };
+  // In place, and without masks, only the tokens that change are touched at all.
+  const bool staged = MASKED || P.out != P.logits;
+  if (staged) {  // (before the lists are there)
+#pragma unroll
+    for (int s = 0; s < kStages; ++s)
+#pragma unroll
+      for (int k = 0; k < kBatch; ++k) allowed[s][k] = look(r0 + s * kBatch + k);
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) issue(r0 + s * kBatch, s);
   }
-  const bool counted = bad == 0;
+
+  // ---- the tokens that change
   Penalties pen;
   pen.repetition = P.repetition ? __ldg(P.repetition + b) : 1.f;
   pen.presence = P.presence ? __ldg(P.presence + b) : 0.f;
   pen.frequency = P.frequency ? __ldg(P.frequency + b) : 0.f;
+  const int32_t* const counts = P.counts ? P.counts + static_cast<int64_t>(b) * P.V + lo : nullptr;
+  uint32_t some = 0;  // of the chunk's columns tid * N ...
+  if (counts) {
+    if (tid * N + N <= size && reinterpret_cast<uintptr_t>(counts) % 16 == 0) {
+#pragma unroll
+      for (int q = 0; q < N / 4; ++q) {
+        const int4 c = __ldg(reinterpret_cast<const int4*>(counts + tid * N) + q);
+        some |= ((c.x != 0 ? 1u : 0u) | (c.y != 0 ? 2u : 0u) | (c.z != 0 ? 4u : 0u) | (c.w != 0 ? 8u : 0u)) << (4 * q);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < N; ++e)
+        if (tid * N + e < size && __ldg(counts + tid * N + e) != 0) some |= 1u << e;
+    }
+  }
+  if (tid == 0) s_status = 0;
+#pragma unroll
+  for (int q = 0; q < N / 4; ++q) reinterpret_cast<int4*>(s_value)[tid + q * kThreads] = make_int4(0, 0, 0, 0);
+  if (tid < WORDS) s_some[tid] = s_mark[tid] = 0;
+  __syncthreads();
+  if (some) atomicOr(&s_some[tid * N / 32], some << (tid * N % 32));
+  int bad = counted ? 0 : SPECDEC_STATUS_BAD_TOKEN;
   if (!(pen.repetition > 0.f && pen.repetition < kInf && fabsf(pen.presence) < kInf && fabsf(pen.frequency) < kInf))
     bad |= SPECDEC_STATUS_BAD_PENALTY;
-  for (int k = tid; k < CHUNK; k += kThreads) s_bias[k] = 0;
-  for (int k = tid; k < CHUNK / 32; k += kThreads) s_mark[k] = 0;
-  __syncthreads();
   if (P.tokens && counted)
     for (int j = tid; j < gamma; j += kThreads) {
       const int t = __ldg(P.tokens + static_cast<int64_t>(b) * (P.rows - 1) + j);
       s_draft[j] = t;
-      if (static_cast<unsigned>(t) >= static_cast<unsigned>(P.V)) bad |= SPECDEC_STATUS_BAD_TOKEN;
-      else if (t >= lo && t - lo < CHUNK) atomicOr(&s_mark[(t - lo) / 32], 1u << ((t - lo) % 32));
+      if (static_cast<unsigned>(t) >= static_cast<unsigned>(P.V)) {
+        bad |= SPECDEC_STATUS_BAD_TOKEN;
+      } else if (t >= lo && t - lo < size) {
+        atomicOr(&s_some[(t - lo) / 32], 1u << ((t - lo) % 32));
+        atomicOr(&s_mark[(t - lo) / 32], 1u << ((t - lo) % 32));
+      }
       if (P.parents) {
         const int p = __ldg(P.parents + j);
         s_parent[j] = p;
         if (p < -1 || p >= j) bad |= SPECDEC_STATUS_BAD_TREE;
       }
     }
+  const float* const bias_values = P.bias_values + static_cast<int64_t>(b) * P.num_bias;
   for (int k = tid; k < P.num_bias; k += kThreads) {
     const int t = __ldg(P.bias_tokens + static_cast<int64_t>(b) * P.num_bias + k);
-    if (t >= P.V) bad |= SPECDEC_STATUS_BAD_TOKEN;
-    else if (t >= lo && t - lo < CHUNK) atomicMax(&s_bias[t - lo], k + 1);
+    if (t >= P.V) {
+      bad |= SPECDEC_STATUS_BAD_TOKEN;
+    } else if (t >= lo && t - lo < size) {
+      atomicMax(&s_value[t - lo], k + 1);
+      atomicOr(&s_some[(t - lo) / 32], 1u << ((t - lo) % 32));
+    }
   }
-  // (__syncthreads_or gives a truth value: one for each bit)
-  int status = 0;
-#pragma unroll
-  for (int bit : {SPECDEC_STATUS_BAD_TOKEN, SPECDEC_STATUS_BAD_TREE, SPECDEC_STATUS_BAD_PENALTY})
-    if (__syncthreads_or(bad & bit)) status |= bit;
+  if (bad) atomicOr(&s_status, bad);
+  __syncthreads();
+  const int status = s_status;
   if (blockIdx.x == 0 && blockIdx.y == 0 && tid == 0 && P.out_status) P.out_status[b] = status;
-
-  // this thread's columns: VEC from col(v) on
-  auto col = [&](int v) { return lo + (v * kThreads + tid) * VEC; };
-  float add[NV][VEC];
-  uint32_t seen[NV], mark[NV];  // bit e: column e is repeated, or some draft's token
-#pragma unroll
-  for (int v = 0; v < NV; ++v) {
-    seen[v] = mark[v] = 0;
-#pragma unroll
-    for (int e = 0; e < VEC; ++e) {
-      const int t = col(v) + e;
-      add[v][e] = 0.f;
-      if (t >= P.V) continue;
-      const int c = P.counts ? __ldg(P.counts + static_cast<int64_t>(b) * P.V + t) : 0, k = s_bias[t - lo];
-      add[v][e] = pen.added(c & 0x7fffffff, k ? __ldg(P.bias_values + static_cast<int64_t>(b) * P.num_bias + k - 1) : 0.f);
-      seen[v] |= (c != 0 ? 1u : 0u) << e;
-      mark[v] |= ((s_mark[(t - lo) / 32] >> ((t - lo) % 32)) & 1u) << e;
-    }
+  if (status) {  // nothing of the sequence counts
+    copy_wait<0>();
+    for (int r = r0; r < r1; ++r)
+      for (int t = tid; t < size; t += kThreads) to(r)[t] = E::put(__int_as_float(0x7fffffff));
+    return;
   }
-  // a column that is some draft's token
-  auto marked = [&](float x, int t, int row) {
-    int n = 0;
-    for (int j = row - 1; j >= 0; j = P.parents ? s_parent[j] : j - 1) n += s_draft[j] == t;
-    const int c = P.counts ? __ldg(P.counts + static_cast<int64_t>(b) * P.V + t) : 0, k = s_bias[t - lo];
-    const float bias = k ? __ldg(P.bias_values + static_cast<int64_t>(b) * P.num_bias + k - 1) : 0.f;
-    if (c != 0 || n > 0) x = pen.repeated(x);
-    return x + pen.added((c & 0x7fffffff) + n, bias);
-  };
-
-  const int r0 = blockIdx.y * P.group, r1 = min(r0 + P.group, counted ? gamma + 1 : P.rows);
-  for (int r = r0; r < r1; ++r) {
-    const int64_t row = static_cast<int64_t>(b) * P.rows + r;
-    const T* const src = static_cast<const T*>(P.logits) + row * P.V;
-    T* const dst = static_cast<T*>(P.out) + row * P.V;
-    const uint8_t* const mask = reinterpret_cast<const uint8_t*>(P.mask + (P.mask ? row * P.words : 0));
+  some = (s_some[tid * N / 32] >> (tid * N % 32)) & kAll;
+  int at = __popc(some);
 #pragma unroll
-    for (int v = 0; v < NV; ++v) {
-      const int t0 = col(v);
-      if (t0 >= P.V) continue;
-      uint32_t allowed = ~0u;
-      if (P.mask) allowed = __ldg(mask + t0 / 8) >> (t0 % 8);
-      float x[VEC];
-      if constexpr (VEC == 1) x[0] = Wide<T>::one(src + t0);
-      else Wide<T>::unpack(*reinterpret_cast<const uint4*>(src + t0), x);
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, at, o);
+    if (lane >= o) at += v;
+  }
+  if (lane == 31) s_sum[tid / 32] = at;
+  __syncthreads();
+  int listed = 0;
+  at -= __popc(some);
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) {
-        if (status) x[e] = __int_as_float(0x7fffffff);
-        else if (!((allowed >> e) & 1u)) x[e] = -kInf;
-        else if ((mark[v] >> e) & 1u) x[e] = marked(x[e], t0 + e, r);
-        else x[e] = ((seen[v] >> e) & 1u ? pen.repeated(x[e]) : x[e]) + add[v][e];
+  for (int w = 0; w < kThreads / 32; ++w) {
+    if (w < tid / 32) at += s_sum[w];
+    listed += s_sum[w];
+  }
+  // A column's part that all rows share: y = x * (x > 0 ? 1 / r : r) + add for a token that was there before, else x + add.
+  // (The reciprocal's rounding is that of the quotient: x * RN(1 / r) is within 2^-24 of x / r, and the sum rounds once.)
+  // Its entry says whether x is scaled, and whether its value is computed for each row: a draft's token, or a repetition so large
+  // or small that the reciprocal may be subnormal or infinite.
+  constexpr int kScaled = 0x8000, kOwn = 0x4000;
+  const bool usual = pen.repetition >= 0x1p-100f && pen.repetition <= 0x1p100f;
+  const float inverse = 1.f / pen.repetition;
+  for (; some != 0; some &= some - 1, ++at) {
+    const int t = tid * N + __ffs(some) - 1, c = counts ? __ldg(counts + t) : 0, k = s_value[t];
+    const bool own = (s_mark[t / 32] >> (t % 32) & 1u) != 0 || (c != 0 && !usual);
+    if (!own) s_value[t] = __float_as_int(pen.added(c & 0x7fffffff, k ? __ldg(bias_values + k - 1) : 0.f));
+    s_list[at] = static_cast<uint16_t>(t | (c != 0 ? kScaled : 0) | (own ? kOwn : 0));
+  }
+  // Changes entry j of the list in `rows` rows from r on, x the place of its column 0 in each.
+  auto change = [&](int j, int r, int rows, auto&& x) {
+    const int entry = s_list[j], t = entry & 0x3fff;
+    if (entry & kOwn) {
+      const int c = counts ? __ldg(counts + t) : 0, k = s_value[t];
+      const float bias = k ? __ldg(bias_values + k - 1) : 0.f;
+      const bool drafted = (s_mark[t / 32] >> (t % 32) & 1u) != 0;
+      for (int i = 0; i < rows; ++i) {
+        int n = 0;
+        if (drafted)  // (ends, whatever the parents)
+          for (int d = r + i - 1; d >= 0; d = P.parents ? min(s_parent[d], d - 1) : d - 1) n += s_draft[d] == lo + t;
+        T* const e = x(i) + t;
+        float v = E::get(*e);
+        if (c != 0 || n > 0) v = pen.repeated(v);
+        *e = E::put(v + pen.added((c & 0x7fffffff) + n, bias));
       }
-      if constexpr (VEC == 1) Wide<T>::put(dst + t0, x[0]);
-      else *reinterpret_cast<uint4*>(dst + t0) = Wide<T>::pack(x);
+    } else {
+      const float add = __int_as_float(s_value[t]);
+      const float up = entry & kScaled ? inverse : 1.f, down = entry & kScaled ? pen.repetition : 1.f;
+#pragma unroll
+      for (int i = 0; i < kBatch; ++i)
+        if (i < rows) {
+          T* const e = x(i) + t;
+          const float v = E::get(*e);
+          *e = E::put(fmaf(v, v > 0.f ? up : down, add));
+        }
     }
+  };
+  if (!staged) {
+    __syncthreads();
+    for (int r = r0; r < r1; r += kBatch)
+      for (int j = tid; j < listed; j += kThreads) change(j, r, min(kBatch, r1 - r), [&](int i) { return to(r + i); });
+    return;
   }
+
+  int stage = 0;
+  for (int r = r0; r < r1; r += kBatch) {
+    copy_wait<kStages - 1>();
+    __syncthreads();  // everybody's copies, and the list
+    for (int j = tid; j < listed; j += kThreads)
+      change(j, r, min(kBatch, r1 - r), [&](int i) { return s_rows[stage][i] + past(from(r + i)); });
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      if (r + k >= r1) break;
+      const T* const words = s_rows[stage][k];
+      const int off = past(from(r + k));
+      T* const dst = to(r + k);
+      uint32_t keep = 0;
+#pragma unroll
+      for (int s = 0; s < kStages; ++s)
+        if (s == stage) keep = allowed[s][k];
+      if (P.alike) {
+        const uint32_t there = mine(off);
+        if (there == 0) continue;
+        const uint4 in = *reinterpret_cast<const uint4*>(words + tid * N);
+        uint32_t w[4] = {in.x, in.y, in.z, in.w};
+        if constexpr (MASKED) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint32_t two = keep >> (q * E::kPair);
+            const uint32_t m = E::kPair == 1 ? 0u - (two & 1u) : ((two & 1u) * 0xffffu) | ((two >> 1 & 1u) * 0xffff0000u);
+            w[q] = (w[q] & m) | (E::kNone & ~m);
+          }
+        }
+        T* const word = dst + tid * N - off;
+        if (ALIGNED || there == kAll) {
+          __stcs(reinterpret_cast<uint4*>(word), make_uint4(w[0], w[1], w[2], w[3]));
+        } else {
+#pragma unroll
+          for (int e = 0; e < N; ++e)
+            if (there >> e & 1u) word[e] = static_cast<T>(E::part(w, e));
+        }
+      } else {
+        for (int t = tid; t < size; t += kThreads) dst[t] = !MASKED || bit(r + k, t) ? words[off + t] : E::put(-kInf);
+      }
+    }
+    if (!P.alike) __syncthreads();  // (else a thread's words are its own)
+#pragma unroll
+    for (int s = 0; s < kStages; ++s)
+      if (s == stage) {
+#pragma unroll
+        for (int k = 0; k < kBatch; ++k) allowed[s][k] = look(r + kStages * kBatch + k);
+        issue(r + kStages * kBatch, s);
+      }
+    stage = stage + 1 == kStages ? 0 : stage + 1;
+  }
+  copy_wait<0>();
 }
 
 // ---- the table of counts --------------------------------------------------------------------
@@ -191,52 +364,75 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const CountParams P) {
 
 // A sequence's table from nothing: a CTA counts the tokens of its chunk of the vocabulary in shared memory and writes the
 // chunk whole.  grid (chunks, B)
-constexpr int kCountChunk = 8192;
+constexpr int kCountChunk = 8192, kCountThreads = 512;
 
-__global__ void __launch_bounds__(kThreads) recount_kernel(const CountParams P) {
-  __shared__ int s_count[kCountChunk];
-  const int b = blockIdx.y, n = tokens_of(P, b), lo = blockIdx.x * kCountChunk;
+__global__ void __launch_bounds__(kCountThreads) recount_kernel(const CountParams P) {
+  __shared__ __align__(16) int s_count[kCountChunk];
+  const int b = blockIdx.y, n = tokens_of(P, b), lo = blockIdx.x * kCountChunk, tid = threadIdx.x;
   const int32_t* const tokens = P.tokens + b * P.token_stride;
-  for (int k = threadIdx.x; k < kCountChunk; k += kThreads) s_count[k] = 0;
+#pragma unroll
+  for (int k = 0; k < kCountChunk / 4 / kCountThreads; ++k) reinterpret_cast<int4*>(s_count)[tid + k * kCountThreads] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  for (int k = threadIdx.x; k < n; k += kThreads) {
-    const int t = __ldg(tokens + k);
-    if (t < lo || t >= P.V || t - lo >= kCountChunk) continue;
+  auto take = [&](int t) {
+    if (t < lo || t >= P.V || t - lo >= kCountChunk) return;
     if (P.prompt) s_count[t - lo] = kSign;
     else atomicAdd(&s_count[t - lo], 1);
+  };
+  // (whole words of four tokens, and what is before and behind them)
+  const int head = min(n, static_cast<int>((16 - reinterpret_cast<uintptr_t>(tokens) % 16) % 16 / 4)), words = (n - head) / 4;
+  if (tid < head) take(__ldg(tokens + tid));
+  if (head + 4 * words + tid < n) take(__ldg(tokens + head + 4 * words + tid));
+#pragma unroll 4
+  for (int k = tid; k < words; k += kCountThreads) {
+    const int4 t = __ldg(reinterpret_cast<const int4*>(tokens + head) + k);
+    take(t.x);
+    take(t.y);
+    take(t.z);
+    take(t.w);
   }
   __syncthreads();
   int* const out = P.counts + static_cast<int64_t>(b) * P.V + lo;
-  for (int k = threadIdx.x; k < kCountChunk && k < P.V - lo; k += kThreads) out[k] = s_count[k];
+  const int columns = min(kCountChunk, P.V - lo);
+  if (reinterpret_cast<uintptr_t>(out) % 16 == 0 && columns % 4 == 0) {
+    for (int k = tid; k < columns / 4; k += kCountThreads) reinterpret_cast<int4*>(out)[k] = reinterpret_cast<const int4*>(s_count)[k];
+  } else {
+    for (int k = tid; k < columns; k += kCountThreads) out[k] = s_count[k];
+  }
   if (blockIdx.x == 0 && P.out_status) report(P, b, n);
 }
 
-template <typename T, int VEC>
+template <typename T, bool ALIGNED, bool MASKED>
 cudaError_t process_shape(ProcessParams P, cudaStream_t stream) {
-  constexpr int CHUNK = kThreads * (VEC == 1 ? 4 : VEC);
+  constexpr int CHUNK = kChunk<T, ALIGNED>;
   const int64_t chunks = (static_cast<int64_t>(P.V) + CHUNK - 1) / CHUNK;
   const int64_t want = 8 * device_sm_count(), have = chunks * P.B;  // CTAs: all SMs full once
   const int groups = static_cast<int>(std::min<int64_t>(P.rows, std::max<int64_t>(1, (want + have - 1) / have)));
   P.group = (P.rows + groups - 1) / groups;
   const size_t smem = P.tokens ? static_cast<size_t>(P.rows - 1) * 2 * sizeof(int) : 0;
-  auto kernel = process_kernel<T, VEC>;
+  auto kernel = process_kernel<T, ALIGNED, MASKED>;
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kMaxProcessRows * 2 * static_cast<int>(sizeof(int))); e != cudaSuccess)
     return e;
   return launch_kernel(kernel, dim3(static_cast<unsigned>(chunks), static_cast<unsigned>((P.rows + P.group - 1) / P.group), static_cast<unsigned>(P.B)),
                        dim3(kThreads), smem, stream, 0, P);
 }
 
+template <typename T>
+cudaError_t process_typed(const ProcessParams& P, cudaStream_t stream) {
+  const bool aligned = P.alike && reinterpret_cast<uintptr_t>(P.logits) % 16 == 0 && static_cast<int64_t>(P.V) * sizeof(T) % 16 == 0;
+  if (aligned) return P.mask ? process_shape<T, true, true>(P, stream) : process_shape<T, true, false>(P, stream);
+  return P.mask ? process_shape<T, false, true>(P, stream) : process_shape<T, false, false>(P, stream);
+}
+
 }  // namespace
 
-cudaError_t launch_process_logits(const ProcessParams& P, specdec_dtype dt, bool vec, cudaStream_t stream) {
-  if (dt == SPECDEC_BF16) return vec ? process_shape<uint16_t, 8>(P, stream) : process_shape<uint16_t, 1>(P, stream);
-  return vec ? process_shape<float, 4>(P, stream) : process_shape<float, 1>(P, stream);
+cudaError_t launch_process_logits(const ProcessParams& P, specdec_dtype dt, cudaStream_t stream) {
+  return dt == SPECDEC_BF16 ? process_typed<uint16_t>(P, stream) : process_typed<float>(P, stream);
 }
 
 cudaError_t launch_count_tokens(const CountParams& P, bool reset, cudaStream_t stream) {
   if (reset)
     return launch_kernel(recount_kernel, dim3(static_cast<unsigned>((static_cast<int64_t>(P.V) + kCountChunk - 1) / kCountChunk), static_cast<unsigned>(P.B)),
-                         dim3(kThreads), 0, stream, 0, P);
+                         dim3(kCountThreads), 0, stream, 0, P);
   return launch_kernel(count_kernel, dim3(static_cast<unsigned>(std::max(1, (P.n + kThreads - 1) / kThreads)), static_cast<unsigned>(P.B)), dim3(kThreads), 0, stream, 0, P);
 }
 

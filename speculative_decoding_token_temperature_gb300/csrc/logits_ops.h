@@ -19,12 +19,12 @@ struct ProcessParams {
   const float* bias_values;
   const uint32_t* mask;  // [B, rows, words] or nullptr
   int num_bias, words, B, rows, V;
+  int alike;  // logits and out lie alike on 16 bytes
   int group;  // rows of a CTA
   void* out;
   int32_t* out_status;
 };
-// vec: every row starts on 16 bytes.
-cudaError_t launch_process_logits(const ProcessParams& P, specdec_dtype dt, bool vec, cudaStream_t stream);
+cudaError_t launch_process_logits(const ProcessParams& P, specdec_dtype dt, cudaStream_t stream);
 
 struct CountParams {
   int32_t* counts;  // [B, V]

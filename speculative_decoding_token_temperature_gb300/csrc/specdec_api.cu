@@ -993,8 +993,8 @@ int specdec_process_logits(const void* logits, specdec_dtype dtype, const int32_
   P.out_status = out_status;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   ProfScope prof(SPECDEC_KERNEL_PROCESS_LOGITS, s);
-  const bool vec = rows_vectorizable(logits, V, es) && rows_vectorizable(out, V, es);
-  if (cudaError_t e = launch_process_logits(P, dtype, vec, s); e != cudaSuccess) return fail_cuda("logits processing kernel", e);
+  P.alike = (reinterpret_cast<uintptr_t>(logits) - reinterpret_cast<uintptr_t>(out)) % 16 == 0;
+  if (cudaError_t e = launch_process_logits(P, dtype, s); e != cudaSuccess) return fail_cuda("logits processing kernel", e);
   return SPECDEC_OK;
 }
 
