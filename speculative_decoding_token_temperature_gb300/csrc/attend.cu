@@ -44,6 +44,7 @@ constexpr int kRows = 16;     // rows of a tile
 // 99 / 95; 32 rows 191 / 97.  64 values: 4 rows, B=4, 4000 slots 15.0 / 16.4; B=32, 8000 slots 67.8 / 68.3;
 // 4-bit pages 15.5 / 19.6 and 68.2 / 70.7; 16 rows, B=32, 8000 slots 68.8 / 68.4 and 72.3 / 70.6.
 constexpr int kWarpRows = 8;
+constexpr int kWarpRows8 = 32;  // over 8-bit pages
 
 __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -652,8 +653,8 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   if (P.ctas <= 0) return cudaErrorInvalidDevice;
   if (P.ctas > kMaxCtas) P.ctas = kMaxCtas;
   const bool items = P.pages.head_dim == 128 && static_cast<int64_t>(P.B) * P.pages.kv_heads >= P.ctas;
-  const bool tc = eight ? false : hook == 0 ? rows > kWarpRows || items : hook == 2;
-  const int mr = tc ? attend_tc_rows(rows) : eight ? attend8_rows(rows) : kRows;
+  const bool tc = hook == 0 ? (eight ? rows > kWarpRows8 : rows > kWarpRows || items) : hook == 2;
+  const int mr = tc ? std::max(attend_tc_rows(rows), eight ? 128 : 0) : eight ? attend8_rows(rows) : kRows;
   P.row_tiles = static_cast<int>((rows + mr - 1) / mr);
   // A row of CTAs for each key head, unless that leaves more than a sixteenth of the GPU out: a slot's heads
   // lie side by side, and are then read at about the same time (4-bit decode of 64 requests of 16000
@@ -668,7 +669,8 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   ws += round256(static_cast<size_t>(kMaxCtas) * 2 * mr * sizeof(float2));
   P.part_o = reinterpret_cast<float*>(ws);
   if (tc)
-    if (cudaError_t e = four ? launch_attend_tc4(P, dt, mr, stream) : launch_attend_tc(P, dt, mr, stream); e != cudaSuccess)
+    if (cudaError_t e = four ? launch_attend_tc4(P, dt, mr, stream) : eight ? launch_attend_tc8(P, dt, mr, stream) : launch_attend_tc(P, dt, mr, stream);
+        e != cudaSuccess)
       return e;
   if (!tc && eight)
     if (cudaError_t e = launch_attend8(P, dt, mr, stream); e != cudaSuccess) return e;

@@ -83,11 +83,12 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
     // Copies the steps from t on.  Comes back with the slots on pages out of range and this lane's step's scale
     // bytes (keys', then values').  A step's slots are not all wanted where the visible range begins or ends
     // inside it; those that are lie in one block.
+    // (Nothing is made of the bytes before they are used: it would wait for them.)
     struct Copied {
-      uint32_t bads, scales;
+      uint32_t bads, scale_k, scale_v;
     };
     auto prefetch = [&](int t, int stage, int page) -> Copied {
-      Copied got{0, 0};
+      Copied got{0, 0, 0};
       if (t < t_hi) {
         const int s = slot_of(t);
         const bool want = wanted(t, s);
@@ -100,7 +101,8 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
         const uint32_t present = __ballot_sync(0xffffffffu, there);
         if (there) {
           const int64_t so = page * pg.scale_page_stride + block_of(pg, in_page) * pg.scale_slot_stride + h * pg.scale_head_stride;
-          got.scales = __ldg(reinterpret_cast<const uint8_t*>(pg.k_scales) + so) | (__ldg(reinterpret_cast<const uint8_t*>(pg.v_scales) + so) << 8);
+          got.scale_k = __ldg(reinterpret_cast<const uint8_t*>(pg.k_scales) + so);
+          got.scale_v = __ldg(reinterpret_cast<const uint8_t*>(pg.v_scales) + so);
         }
         char* const base = stages + stage * St::kBytes;
         constexpr int CH = D / 16;     // 16-byte pieces of a row
@@ -243,9 +245,9 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
       int ek[SUB], ev[SUB];
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        const uint32_t mine = SUB == 1 || lane / kStep == u ? now.scales : 0u;
-        ek[u] = scale_exponent(__reduce_max_sync(0xffffffffu, mine & 0xffu));
-        ev[u] = scale_exponent(__reduce_max_sync(0xffffffffu, mine >> 8));
+        const bool mine = SUB == 1 || lane / kStep == u;
+        ek[u] = scale_exponent(__reduce_max_sync(0xffffffffu, mine ? now.scale_k : 0u));
+        ev[u] = scale_exponent(__reduce_max_sync(0xffffffffu, mine ? now.scale_v : 0u));
       }
 
       // S = Q K^T: lane (g, c) takes D/4 consecutive codes of keys g, g + 8, ...; a word is a k step

@@ -18,7 +18,8 @@
 //
 // Warps 0-15: rows (slot = warp / 8, columns = warp / 4 % 2, lanes = warp % 4).  Then the warps that
 // bring K and V: of 16-bit pages, 4 that copy rows asynchronously, 16 bytes at a time; of 4-bit
-// pages, 8 that turn copied codes into their fp16 values (exact: at most 6 significant bits).
+// pages, 8 that turn copied codes into their fp16 values (exact: at most 6 significant bits); of 8-bit pages, 8 that fetch codes a
+// tile ahead and store their fp16 values (exact: 4 significant bits).
 // Either way the tiles are 128-byte-swizzled and gathered row by row, so pages may have any size
 // and stride.  One warp issues the matrix instructions, one walks the items ahead of everybody, and
 // two bring query rows and, of 4-bit pages, the codes and scales.  The roles meet at mbarriers; every
@@ -69,19 +70,20 @@ struct Item {
 // Row tiles: 32 rows, each in the four quarters of tensor memory's lanes, or 128, or two of 128.
 enum Rows { kQuad, kOne, kTwo };
 
-template <int D, Rows ROWS, bool FOUR>
+template <int D, Rows ROWS, int BITS>
 struct Shape {
+  static constexpr bool FOUR = BITS == 4, EIGHT = BITS == 8;
   static constexpr bool TWO = ROWS == kTwo, QUAD = ROWS == kQuad;
   static constexpr int MR = QUAD ? 32 : TWO ? 256 : 128;
-  static constexpr int kCopyWarps = FOUR ? 8 : 4;
+  static constexpr int kCopyWarps = FOUR || EIGHT ? 8 : 4;
   static constexpr int kThreads = 32 * (kRowWarps + kCopyWarps + 4);
-  // Who is who among the warps from 16 on.  16-bit pages: 16 .. 19 copy.  4-bit pages: 16 .. 23 convert, two
+  // Who is who among the warps from 16 on.  16-bit pages: 16 .. 19 copy.  4-bit and 8-bit pages: 16 .. 23 convert, two
   // on each of an SM's four schedulers (warp % 4); with at most 32 rows, where a tile's copies are the
   // longer way, they keep off the scheduler of the two warps that copy.  (B=16, 16000 slots, D=128, us for
   // 32, 64 and 256 rows: 103, 120 and 266 two on each, 99, 127 and 279 on three schedulers.)
   static constexpr bool THREE = FOUR && QUAD;
-  static constexpr int kWalker = THREE ? 16 : FOUR ? 24 : 20, kMma = FOUR ? 27 : 23;
-  static constexpr int kQuery0 = THREE ? 20 : FOUR ? 25 : 21, kQuery1 = THREE ? 24 : FOUR ? 26 : 22;
+  static constexpr int kWalker = THREE ? 16 : 16 + kCopyWarps, kMma = 19 + kCopyWarps;
+  static constexpr int kQuery0 = THREE ? 20 : 17 + kCopyWarps, kQuery1 = THREE ? 24 : 18 + kCopyWarps;
   __device__ static constexpr int copy_index(int warp) {
     const int k = warp - kRowWarps;
     if (THREE) return k % 4 == 0 || k > 10 || k < 0 ? -1 : k / 4 * 3 + k % 4 - 1;  // 17, 18, 19, 21, 22, 23, 25, 26
@@ -98,8 +100,9 @@ struct Shape {
   static constexpr int kOffV = kOffK + RK * kTileBytes;
   static constexpr int kOffMl = kOffV + RV * kTileBytes;      // [2][2][128] (m, l) of slots and halves
   static constexpr int kOffRaw = kOffMl + 4 * 128 * 8;
-  static constexpr int kOffQScale = kOffRaw + RAW * kRawBytes;  // [2][MR] scales of query rows (4-bit pages)
-  static constexpr int kOffSum = kOffQScale + (FOUR ? 2 * MR * 4 : 0);  // [4][4][32][8] accumulators on their way, [32] 1 / l
+  static constexpr int kRawWarp = 16 * D;  // 8-bit pages: the codes of a converting warp's 16 keys, ahead of their conversion
+  static constexpr int kOffQScale = kOffRaw + (EIGHT ? kCopyWarps * kRawWarp : RAW * kRawBytes);  // [2][MR] scales of query rows (4-bit and 8-bit pages)
+  static constexpr int kOffSum = kOffQScale + (FOUR || EIGHT ? 2 * MR * 4 : 0);  // [4][4][32][8] accumulators on their way, [32] 1 / l
   static constexpr int kOffItem = kOffSum + (QUAD ? 4 * 4 * 32 * 8 * 4 + 32 * 4 : 0);
   static constexpr int kOffScan = kOffItem + kItems * sizeof(Item);
   static constexpr int kOffBad = (kOffScan + (kThreads / 32 + 3) * 8 + 15) / 16 * 16;
@@ -236,10 +239,12 @@ __device__ __forceinline__ uint64_t bits64(int lo, int hi) {
   return lo >= 64 ? 0ull : below & (~0ull << max(lo, 0));
 }
 
-template <typename T, int D, Rows ROWS, bool FOUR>
-__global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_kernel(const AttendParams P) {
-  using Sh = Shape<D, ROWS, FOUR>;
-  using M = typename std::conditional<FOUR, __half, T>::type;  // the matrix instructions' type
+template <typename T, int D, Rows ROWS, int BITS>
+__global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_kernel(const AttendParams P) {
+  using Sh = Shape<D, ROWS, BITS>;
+  constexpr bool FOUR = BITS == 4, EIGHT = BITS == 8;
+  constexpr bool BRAIN = BITS != 16 && !std::is_same<T, __half>::value;  // bf16 queries to be held in fp16
+  using M = typename std::conditional<BITS != 16, __half, T>::type;  // the matrix instructions' type
   constexpr int MR = Sh::MR, RK = Sh::RK, RV = Sh::RV, KT = D / 16, THREADS = Sh::kThreads;
   constexpr bool AHEAD = Sh::AHEAD, TWO = Sh::TWO, QUAD = Sh::QUAD;
   extern __shared__ __align__(1024) char smem[];
@@ -269,11 +274,11 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
   if (tid == 0) {
     // copied tiles: every copy lane's copies have landed, and a warp's part of s_bad is written
     for (int r = 0; r < RK; ++r) {
-      mbar_init(k_full + r, FOUR ? Sh::kCopyWarps : kTile + Sh::kCopyWarps);
+      mbar_init(k_full + r, FOUR || EIGHT ? Sh::kCopyWarps : kTile + Sh::kCopyWarps);
       mbar_init(k_empty + r, 1);
     }
     for (int r = 0; r < RV; ++r) {
-      mbar_init(v_full + r, FOUR ? Sh::kCopyWarps : kTile);
+      mbar_init(v_full + r, FOUR || EIGHT ? Sh::kCopyWarps : kTile);
       mbar_init(v_empty + r, 1);
     }
     for (int s = 0; s < 2; ++s) {
@@ -390,7 +395,111 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
       const int32_t* table = pg.table + static_cast<int64_t>(it.b) * pg.max_pages;
       const char* const k_head = pg.k + it.h * pg.head_stride;
       const char* const v_head = pg.v + it.h * pg.head_stride;
-      if constexpr (!FOUR) {
+      if constexpr (EIGHT) {
+        // Warp c brings slots 16 c ... of a tile, a step, whose slots are in one block; lane l looks up slot 16 c + l % 16.  The
+        // codes are copied ahead: keys' two tiles, to a slot of shared memory of the warp's own; values' once their tile's
+        // place is free, into that place, a row's codes in the first bytes of its row of the first 64 values, from where the
+        // warp takes them to registers.  A tile's keys are converted before the values of the tile before it, which
+        // are wanted later.  (Copies, not loads: a warp has few scoreboards, and a wait for a page or a scale then also waited for codes.)
+        constexpr int CH = D / 16, RPI = 32 / CH, LOADS = 16 / RPI;  // 16-byte pieces of a row of codes, rows at a time
+        char* const raw = smem + Sh::kOffRaw + cw * Sh::kRawWarp + lane * 16;
+        int page = 0, in_page = -1;  // of the next tile (-1: no query of the item sees the slot)
+        auto look_up = [&](int t) {
+          const int s = R.slot(t * kUnit + cw) + lane % kStep;
+          in_page = -1;
+          if (t < t_hi && s < it.end && (s >= it.lo || s < it.sinks)) {
+            const int logical = page_of(pg, s);
+            page = __ldg(table + logical);
+            in_page = s - logical * pg.page_size;
+          }
+        };
+        uint32_t bads = 0, present = 0, scale_k = 0, scale_v = 0;  // (nothing is made of the bytes before they are used: it would wait)
+        int64_t off = 0;
+        auto place = [&]() {  // what the looked-up slots give: where they are, and their block's scales
+          const bool want = in_page >= 0;
+          const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
+          const bool there = want && !bad;
+          bads = __ballot_sync(0xffffffffu, bad) & 0xffffu;
+          present = __ballot_sync(0xffffffffu, there);
+          off = there ? page * pg.page_stride + in_page * pg.slot_stride : 0;
+          scale_k = scale_v = 0;
+          if (there) {
+            const int64_t so = page * pg.scale_page_stride + block_of(pg, in_page) * pg.scale_slot_stride + it.h * pg.scale_head_stride;
+            scale_k = __ldg(reinterpret_cast<const uint8_t*>(pg.k_scales) + so);
+            scale_v = __ldg(reinterpret_cast<const uint8_t*>(pg.v_scales) + so);
+          }
+        };
+        auto copy = [&](uint32_t dst, int step, const char* head, int64_t at, uint32_t rows) {  // RPI rows every `step` bytes
+#pragma unroll
+          for (int j = 0; j < LOADS; ++j) {
+            const int row = j * RPI + lane / CH;
+            const int64_t o = __shfl_sync(0xffffffffu, at, row) + lane % CH * 16;
+            copy_async<16>(dst + j * step, head + o, (rows >> row) & 1u);
+          }
+          copy_commit();
+        };
+        auto place_of = [&](int kv, int n) { return smem + (kv ? Sh::kOffV : Sh::kOffK) + n % (kv ? RV : RK) * Sh::kTileBytes; };
+        auto wait_empty = [&](int kv, int n) {
+          wait_for((kv ? v_empty : k_empty) + n % (kv ? RV : RK), ((n / (kv ? RV : RK)) & 1) ^ 1, gave_up);
+          __syncwarp();
+        };
+        const int in_tile = (cw * 16 + lane / CH) * 128 + lane % CH * 16;  // this lane's first piece of the values' codes
+        uint4 codes[LOADS];
+        auto store = [&](int kv, int n, int e) {  // the codes' values to tile number n
+          char* const dst = place_of(kv, n);
+          const uint32_t s2 = power_f16x2(e);
+#pragma unroll
+          for (int j = 0; j < LOADS; ++j) {
+            uint32_t f[8];
+            e4m3x4_to_f16(codes[j].x, f[0], f[1]);
+            e4m3x4_to_f16(codes[j].y, f[2], f[3]);
+            e4m3x4_to_f16(codes[j].z, f[4], f[5]);
+            e4m3x4_to_f16(codes[j].w, f[6], f[7]);
+#pragma unroll
+            for (int x = 0; x < 8; ++x) f[x] = mul_f16x2(f[x], s2);
+            // (the lanes of a row's second half store their pieces the other way round: 8 lanes meet no bank conflict)
+            const int row = cw * 16 + j * RPI + lane / CH, piece = 2 * (lane % CH), turn = D == 128 ? lane % CH / 4 : 0;
+            const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
+            *reinterpret_cast<uint4*>(dst + tile_offset(row, piece + turn)) = turn ? hi : lo;
+            *reinterpret_cast<uint4*>(dst + tile_offset(row, piece + 1 - turn)) = turn ? lo : hi;
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive((kv ? v_full + n % RV : k_full + n % RK));
+        };
+        look_up(t_lo);
+        place();
+        look_up(t_lo + 1);
+        if (t_lo < t_hi) copy(smem_addr(raw), 512, k_head, off, present);
+        int ev = 0;  // the exponent of tile t's values
+        for (int t = t_lo - 1; t < t_hi; ++t) {
+          copy_wait<0>();
+          if (t >= t_lo) {
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < LOADS; ++j) codes[j] = *reinterpret_cast<const uint4*>(place_of(1, tile) + in_tile + j * RPI * 128);
+            __syncwarp();
+            store(1, tile, ev);
+            ++tile;
+          }
+          if (t + 1 >= t_hi) break;
+          // tile t + 1, which is number `tile` now
+          const int ek = scale_exponent(__reduce_max_sync(0xffffffffu, scale_k));
+          ev = scale_exponent(__reduce_max_sync(0xffffffffu, scale_v));
+          if (lane == 0) reinterpret_cast<uint16_t*>(s_bad)[(tile % kBadRing) * 8 + cw] = static_cast<uint16_t>(bads);
+#pragma unroll
+          for (int j = 0; j < LOADS; ++j) codes[j] = *reinterpret_cast<const uint4*>(raw + j * 512);  // (a lane's own copies)
+          const int64_t at = off;
+          const uint32_t rows = present;
+          place();
+          look_up(t + 3);
+          if (t + 2 < t_hi) copy(smem_addr(raw), 512, k_head, off, present);
+          wait_empty(0, tile);
+          store(0, tile, ek);
+          wait_empty(1, tile);
+          copy(smem_addr(place_of(1, tile) + in_tile), RPI * 128, v_head, at, rows);
+        }
+      } else if constexpr (!FOUR) {
         // lane l of warp c brings slot 32 c + l of a tile; its page is looked up a tile ahead
         int page = 0, in_page = -1;  // slot of the page (-1: no query of the item sees it)
         auto look_up = [&](int t) {
@@ -655,7 +764,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
       };
       auto target = [&](int r) { return smem + (TWO ? r / 128 * Sh::kTileBytes : 0) + tile_offset(r % 128, piece); };
       // (rows past the item's keep what was there: they only reach rows of S that nobody reads)
-      if (!FOUR && P.scale_log2 >= 0.f) {  // as they are
+      if (!FOUR && !BRAIN && P.scale_log2 >= 0.f) {  // as they are
         const int di = query_of(P, AT), dg = AT - di * P.G;
         const int64_t on = di * P.q_st + dg * P.q_sh, wrap = P.q_st - P.G * P.q_sh;
         const int i0 = query_of(P, row0 + t2 / CH);
@@ -684,8 +793,8 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
           for (int k = 0; k < AHEAD; ++k) {
             const int r = r0 + k * AT;
             uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
-            if constexpr (FOUR && !std::is_same<T, __half>::value) {
-              // bf16 queries over 4-bit pages: q / 2^(exponent of the row's largest value) is within
+            if constexpr (BRAIN) {
+              // bf16 queries over 4-bit or 8-bit pages: q / 2^(exponent of the row's largest value) is within
               // (-2, 2), and fp16 then holds it to 2^-25 of that value
               float a = 0.f;
 #pragma unroll
@@ -795,7 +904,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
         uint32_t r[2][16];
         float top = -kInf;
         const uint4 bads = *reinterpret_cast<const uint4*>(s_bad + (tile % kBadRing) * 4);
-        if (FOUR && !std::is_same<T, __half>::value && jobs == 0)
+        if (BRAIN && jobs == 0)
           c = fmaxf(c * s_qscale[(n & 1) * MR + (TWO ? slot * 128 : 0) + row], kLeast);
         uint32_t seen[2] = {~0u, ~0u};
         bool poisoned = false;  // the row sees a slot on a page out of range
@@ -988,6 +1097,11 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
 #pragma unroll
                 for (int x = 0; x < 16; ++x) acc[x] = __int_as_float(0x7fffffff);
               }
+            } else if constexpr (EIGHT) {  // only a code can be NaN
+              const uint8_t* v = reinterpret_cast<const uint8_t*>(pg.v + page * pg.page_stride + in_page * pg.slot_stride + it.h * pg.head_stride) + d;
+#pragma unroll
+              for (int x = 0; x < 16; ++x)
+                if ((v[x] & 0x7f) == 0x7f) acc[x] = __int_as_float(0x7fffffff);
             } else {
               const T* v = reinterpret_cast<const T*>(pg.v + page * pg.page_stride + in_page * pg.slot_stride + it.h * pg.head_stride) + d;
 #pragma unroll
@@ -1177,26 +1291,26 @@ __global__ void __launch_bounds__(Shape<D, ROWS, FOUR>::kThreads, 1) attend_tc_k
   if (tid == 0) P.gave_up[blockIdx.x] = *gave_up;
 }
 
-template <typename T, int D, Rows ROWS, bool FOUR>
+template <typename T, int D, Rows ROWS, int BITS>
 cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
-  using Sh = Shape<D, ROWS, FOUR>;
-  auto kernel = attend_tc_kernel<T, D, ROWS, FOUR>;
+  using Sh = Shape<D, ROWS, BITS>;
+  auto kernel = attend_tc_kernel<T, D, ROWS, BITS>;
   static_assert(Sh::kBytes <= 227 * 1024, "shared memory of a CTA");
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes); e != cudaSuccess)
     return e;
   return launch_kernel(kernel, dim3(P.ctas), dim3(Sh::kThreads), Sh::kBytes, stream, 1, P);
 }
 
-template <typename T, int D, bool FOUR>
+template <typename T, int D, int BITS>
 cudaError_t launch_rows(const AttendParams& P, int mr, cudaStream_t stream) {
-  return mr == 32    ? launch_shape<T, D, kQuad, FOUR>(P, stream)
-         : mr == 128 ? launch_shape<T, D, kOne, FOUR>(P, stream)
-                     : launch_shape<T, D, kTwo, FOUR>(P, stream);
+  if constexpr (BITS != 8)  // (up to 32 rows over 8-bit pages are the warp-level kernel's)
+    if (mr == 32) return launch_shape<T, D, kQuad, BITS>(P, stream);
+  return mr == 128 ? launch_shape<T, D, kOne, BITS>(P, stream) : launch_shape<T, D, kTwo, BITS>(P, stream);
 }
 
-template <typename T, bool FOUR>
+template <typename T, int BITS>
 cudaError_t launch_typed(const AttendParams& P, int mr, cudaStream_t stream) {
-  return P.pages.head_dim == 64 ? launch_rows<T, 64, FOUR>(P, mr, stream) : launch_rows<T, 128, FOUR>(P, mr, stream);
+  return P.pages.head_dim == 64 ? launch_rows<T, 64, BITS>(P, mr, stream) : launch_rows<T, 128, BITS>(P, mr, stream);
 }
 
 }  // namespace tc

@@ -4,7 +4,7 @@
 namespace specdec {
 
 cudaError_t launch_attend_tc4(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream) {
-  return dt == SPECDEC_BF16 ? tc::launch_typed<__nv_bfloat16, true>(P, mr, stream) : tc::launch_typed<__half, true>(P, mr, stream);
+  return dt == SPECDEC_BF16 ? tc::launch_typed<__nv_bfloat16, 4>(P, mr, stream) : tc::launch_typed<__half, 4>(P, mr, stream);
 }
 
 }  // namespace specdec
