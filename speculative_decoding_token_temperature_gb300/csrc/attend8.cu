@@ -7,11 +7,21 @@
 // fp16 with fp32 sums; the keys' scale goes into the scores' factor.  Queries in bf16 are held in fp16 relative to a power of
 // two of their row, to 2^-25 of its largest value.
 //
-// Codes go from the copied tile straight into the matrix instruction's registers: a key's row is read in the order that makes a
-// word the four codes of a step of the k index, two keys' words are interleaved by bytes for the product with V.
-// So shared memory carries the codes once in and once out, and a conversion serves all rows of the tile: 16 rows, or 32 whose
-// second 16 use the same registers of codes.
+// The products are transposed: S^T = K Q^T and O^T = V^T P^T with 16 slots (16 values) by 8 query rows to an instruction, so that 8 rows
+// cost half of what 16 do.  Codes go from the copied tile straight into the instruction's registers: a key's row is read in the order
+// that makes a word the four codes of a step of the k index, two slots' words are interleaved by bytes for the product with V;
+// the weights are turned by the matrix transposition of registers.  So shared memory carries the codes once in and once
+// out, and a conversion serves all rows of the tile: 8, 16 or 32.
+//
+// A row's reference m moves only when a score exceeds what it was set for by more than 2^8 (as in attend_tc.cuh; the
+// weights stay below 2^15): most steps then need no maximum across lanes and no rescaling.
+//
+// A step's 16 rows are a box of the pages' tensor (values, slots, heads, pages), which one TMA instruction brings, swizzled so that
+// the reads meet no bank conflicts; a warp looks up 32 steps at a time, a lane each.  (16-byte asynchronous copies by all
+// lanes, with a lookup for every step: 288 us for 64 requests of 8 tokens over up to 8190 slots, 485 us for one token of 96
+// requests over up to 16001; over half of the instructions were the copies'.)
 
+#include <cuda.h>
 #include "attend_common.cuh"
 #include "specdec_internal.h"
 
@@ -19,33 +29,76 @@ namespace specdec {
 
 namespace {
 
-// SUB steps of 16 slots as a warp takes them; RT tiles of 16 rows.
+#ifndef W1
+#define W1 12
+#define S1 2
+#define G1 2
+#define W2 8
+#define S2 2
+#define G2 3
+#define W4 8
+#define S4 1
+#define G4 5
+#endif
+// RT tiles of 8 rows.  Warps, each with a stream of slots of its own; SUB steps of 16 slots as a warp takes them; stages.
 template <int D, int RT>
 struct Stage8 {
-  static constexpr int WARPS = 8, SUB = RT, SLOTS = SUB * kStep, STAGES = 3, MR = 16 * RT;
-  // Rows of codes, padded so that the reads below meet no bank conflicts.
-  static constexpr int kPitchK = D == 128 ? D + 16 : D, kPitchV = D + 16;
-  static constexpr int kOffV = SLOTS * kPitchK, kBytes = SLOTS * (kPitchK + kPitchV);
+  static constexpr int WARPS = RT == 1 ? W1 : RT == 2 ? W2 : W4, SUB = RT == 1 ? S1 : RT == 2 ? S2 : S4;
+  static constexpr int STAGES = RT == 1 ? G1 : RT == 2 ? G2 : G4, MR = 8 * RT;
+  static constexpr int kBox = kStep * D, kBytes = 2 * SUB * kBox;  // keys, then values
   static constexpr int kStagesBytes = WARPS * STAGES * kBytes;
   static constexpr int kJoinBytes = WARPS * MR * (D * 4 + 8);  // the warps' rows, joined once per segment
   static constexpr int kOffQ = kStagesBytes > kJoinBytes ? kStagesBytes : kJoinBytes;
   static constexpr int kOffScale = kOffQ + MR * D * 2;
-  static constexpr int kSmem = kOffScale + MR * 4;
+  static constexpr int kOffBar = kOffScale + MR * 4;
+  static constexpr int kSmem = kOffBar + WARPS * STAGES * 8;
+  // Where the 16-byte piece `piece` of row `row` of a box lies: rows of D bytes, swizzled as the copies do.
+  __device__ static constexpr int at(int row, int piece) {
+    return row * D + ((D == 128 ? piece ^ (row & 7) : piece ^ (row >> 1 & 3)) << 4);
+  }
+};
+constexpr float kSlack = 8.f;  // log2 of how far a score may exceed what the reference was set for
+
+// An 8 x 8 matrix of 16-bit values, a register of two from each lane, transposed.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// The box of 16 slots of one head, (x, slot, head, page), to shared memory.
+__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int slot, int head, int page, uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(0), "r"(slot), "r"(head), "r"(page), "r"(smem_addr(bar))
+      : "memory");
+}
+
+struct Maps {
+  CUtensorMap k, v;
+  int heads, pages;  // 0: all heads, or pages, lie at the same place (a stride of 0): the coordinate is 0
 };
 
 template <typename T, int D, int RT>
-__global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(const AttendParams P) {
+__global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(const AttendParams P, const __grid_constant__ Maps maps) {
   using St = Stage8<D, RT>;
-  constexpr int MR = St::MR, WARPS = St::WARPS, SUB = St::SUB, SLOTS = St::SLOTS, STAGES = St::STAGES, THREADS = 32 * WARPS;
-  constexpr int KT = D / 16, NT = D / 8, N = 2 * SUB;  // k steps, tiles of 8 values, tiles of 8 slots
+  constexpr int MR = St::MR, WARPS = St::WARPS, SUB = St::SUB, STAGES = St::STAGES, THREADS = 32 * WARPS;
+  constexpr int KT = D / 16, MT = D / 16;  // k steps of the scores, tiles of 16 values
   constexpr bool BRAIN = !std::is_same<T, __half>::value;
-  extern __shared__ __align__(128) char smem[];
+  extern __shared__ __align__(1024) char smem[];
   __shared__ int64_t s_scan[WARPS + 3];
   const Pages& pg = P.pages;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32, g = lane / 4, c = lane % 4;
   const int64_t slots = static_cast<int64_t>(pg.max_pages) * pg.page_size;
   char* const stages = smem + warp * STAGES * St::kBytes;
   float* const s_rowscale = reinterpret_cast<float*>(smem + St::kOffScale);
+  uint64_t* const full = reinterpret_cast<uint64_t*>(smem + St::kOffBar) + warp * STAGES;  // a stage's copies have landed
+  if (lane == 0) {
+    for (int s = 0; s < STAGES; ++s) mbar_init(full + s, 1);
+    mbar_fence_init();
+  }
+  int issued = 0, taken = 0;  // stages filled and read by this warp so far
+  bool late = false;          // a bounded wait ran out
 
   // (the launch may overlap the end of the kernel before it: nothing above touches global memory)
   grid_dependency_wait();
@@ -68,70 +121,71 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
     const int t_lo = static_cast<int>(w.u - w.item) * kUnit;
     const int t_hi = min(static_cast<int>(w.seg_end() - w.item) * kUnit, R.steps);
     const int32_t* table = pg.table + static_cast<int64_t>(b) * pg.max_pages;
-    const char* const k_head = pg.k + h * pg.head_stride;
-    const char* const v_head = pg.v + h * pg.head_stride;
 
-    // this lane's slot of the steps from t on (SUB = 1: lanes 16..31 repeat 0..15), and its page
-    auto slot_of = [&](int t) { return R.slot(t + (SUB == 1 ? 0 : lane / kStep)) + lane % kStep; };
-    auto wanted = [&](int t, int s) {
-      return t + (SUB == 1 ? 0 : lane / kStep) < t_hi && s < R.end && (s >= R.lo || s < R.sinks);
+    // The warp's round n takes the steps first_step(n) ..; a look is 32 steps, a lane each.  (Every step has a slot that some
+    // query sees, and its 16 slots are on one page and in one block.)
+    auto first_step = [&](int n) { return t_lo + (n * WARPS + warp) * SUB; };
+    const int rounds = first_step(0) >= t_hi ? 0 : (t_hi - first_step(0) - 1) / (WARPS * SUB) + 1;
+    constexpr int LOOK = 32 / SUB;  // rounds of a look
+    struct Look {
+      int page, in_page;              // -1: no such step
+      uint32_t scale_k, scale_v;      // (nothing is made of the bytes before they are used: it would wait for them)
     };
-    auto entry = [&](int t) {
-      const int s = slot_of(t);
-      return wanted(t, s) ? __ldg(table + page_of(pg, s)) : 0;
-    };
-    // Copies the steps from t on.  Comes back with the slots on pages out of range and this lane's step's scale
-    // bytes (keys', then values').  A step's slots are not all wanted where the visible range begins or ends
-    // inside it; those that are lie in one block.
-    // (Nothing is made of the bytes before they are used: it would wait for them.)
-    struct Copied {
-      uint32_t bads, scale_k, scale_v;
-    };
-    auto prefetch = [&](int t, int stage, int page) -> Copied {
-      Copied got{0, 0, 0};
+    auto look_up = [&](int look) {
+      Look l{-1, 0, 0, 0};
+      const int t = first_step(look * LOOK + lane / SUB) + lane % SUB;
       if (t < t_hi) {
-        const int s = slot_of(t);
-        const bool want = wanted(t, s);
-        const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
-        const bool there = want && !bad;
-        const int in_page = s - page_of(pg, s) * pg.page_size;
-        const int64_t off = there ? page * pg.page_stride + in_page * pg.slot_stride : 0;
-        got.bads = __ballot_sync(0xffffffffu, bad);
-        if (SUB == 1) got.bads &= 0xffffu;
-        const uint32_t present = __ballot_sync(0xffffffffu, there);
-        if (there) {
-          const int64_t so = page * pg.scale_page_stride + block_of(pg, in_page) * pg.scale_slot_stride + h * pg.scale_head_stride;
-          got.scale_k = __ldg(reinterpret_cast<const uint8_t*>(pg.k_scales) + so);
-          got.scale_v = __ldg(reinterpret_cast<const uint8_t*>(pg.v_scales) + so);
-        }
-        char* const base = stages + stage * St::kBytes;
-        constexpr int CH = D / 16;     // 16-byte pieces of a row
-        constexpr int RPI = 32 / CH;   // rows a warp copies at a time
-#pragma unroll
-        for (int j = 0; j < SLOTS / RPI; ++j) {
-          const int row = j * RPI + lane / CH, piece = lane % CH;
-          const int64_t o = __shfl_sync(0xffffffffu, off, row) + piece * 16;
-          const bool ok = (present >> row) & 1u;
-          copy_async<16>(smem_addr(base + row * St::kPitchK + piece * 16), k_head + o, ok);
-          copy_async<16>(smem_addr(base + St::kOffV + row * St::kPitchV + piece * 16), v_head + o, ok);
-        }
+        const int s = R.slot(t), logical = page_of(pg, s);
+        l.page = __ldg(table + logical);
+        l.in_page = s - logical * pg.page_size;
+        if (l.page < 0) l.page = pg.num_pages;  // (out of range, and there)
       }
-      copy_commit();
-      return got;
+      return l;
     };
+    auto look_scales = [&](Look& l) {
+      if (static_cast<unsigned>(l.page) < static_cast<unsigned>(pg.num_pages)) {
+        const int64_t so = l.page * pg.scale_page_stride + block_of(pg, l.in_page) * pg.scale_slot_stride + h * pg.scale_head_stride;
+        l.scale_k = __ldg(reinterpret_cast<const uint8_t*>(pg.k_scales) + so);
+        l.scale_v = __ldg(reinterpret_cast<const uint8_t*>(pg.v_scales) + so);
+      }
+    };
+    Look now{}, next{};
+    // copies round n's steps (now is the look of the round that is taken, n the same or the next one)
+    auto issue = [&](int n, bool ahead) {
+      int page[SUB], in_page[SUB];
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) {
+        page[u] = __shfl_sync(0xffffffffu, ahead ? next.page : now.page, n % LOOK * SUB + u);
+        in_page[u] = __shfl_sync(0xffffffffu, ahead ? next.in_page : now.in_page, n % LOOK * SUB + u);
+      }
+      if (lane == 0) {
+        const int stage = issued % STAGES;
+        const uint32_t dst = smem_addr(stages + stage * St::kBytes);
+        uint32_t boxes = 0;
+#pragma unroll
+        for (int u = 0; u < SUB; ++u) boxes += static_cast<unsigned>(page[u]) < static_cast<unsigned>(pg.num_pages) ? 2 : 0;
+        fence_proxy_async_smem();  // (what was read of the stage)
+        mbar_expect_tx(full + stage, boxes * St::kBox);
+#pragma unroll
+        for (int u = 0; u < SUB; ++u)
+          if (static_cast<unsigned>(page[u]) < static_cast<unsigned>(pg.num_pages)) {
+            copy_box(dst + u * St::kBox, &maps.k, in_page[u], maps.heads ? h : 0, maps.pages ? page[u] : 0, full + stage);
+            copy_box(dst + (SUB + u) * St::kBox, &maps.v, in_page[u], maps.heads ? h : 0, maps.pages ? page[u] : 0, full + stage);
+          }
+      }
+      ++issued;
+    };
+    __syncthreads();  // the last segment's rows are written: its shared memory is free
+    if (!late) {
+      now = look_up(0);
+      next = look_up(1);
+#pragma unroll
+      for (int n = 0; n < STAGES - 1; ++n)
+        if (n < rounds) issue(n, false);
+      look_scales(now);
+    }
 
     // ---- the query rows, as the matrix instruction's fragments: [tile][k step][lane]
-    __syncthreads();  // the last segment's rows are written: its shared memory is free
-    int t_next = t_lo + warp * SUB;  // the next steps this warp copies
-    int page_next = entry(t_next);
-    Copied ring[STAGES - 1];
-#pragma unroll
-    for (int s = 0; s < STAGES - 1; ++s) {
-      const int page = page_next;
-      page_next = entry(t_next + WARPS * SUB);
-      ring[s] = prefetch(t_next, s, page);
-      t_next += WARPS * SUB;
-    }
     auto q_row = [&](int r) {
       const int i = query_of(P, row0 + r);
       return static_cast<const T*>(P.q) + b * P.q_sb + i * P.q_st + (h * P.G + row0 + r - i * P.G) * P.q_sh;
@@ -154,49 +208,44 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
       __syncthreads();
     }
     for (int f = tid; f < RT * KT * 32; f += THREADS) {
-      const int fg = f % 32 / 4, fc = f % 4, t = f / 32 % KT, rt = f / (32 * KT);
-      uint32_t a[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int r = 16 * rt + fg + (e & 1) * 8;  // a0, a2: row g; a1, a3: row g + 8
-        const int d = (D / 4) * fc + 4 * t + (e >> 1) * 2;  // the k index runs over D in the order the codes are read in
-        a[e] = r < rows ? __ldg(reinterpret_cast<const uint32_t*>(q_row(r) + d)) : 0u;
-        if constexpr (BRAIN) {
-          const float2 v = Half16<T>::to_f32(a[e]);
-          const float inv = 1.f / s_rowscale[r];
-          a[e] = Half16<__half>::pack(v.x * inv, v.y * inv);
-        }
+      const int r = f / (32 * KT) * 8 + f % 32 / 4, t = f / 32 % KT;
+      uint2 q = make_uint2(0u, 0u);  // the k index runs over D in the order the codes are read in
+      if (r < rows) q = __ldg(reinterpret_cast<const uint2*>(q_row(r) + (D / 4) * (f % 4) + 4 * t));
+      if constexpr (BRAIN) {
+        const float2 lo = Half16<T>::to_f32(q.x), hi = Half16<T>::to_f32(q.y);
+        const float inv = 1.f / s_rowscale[r];
+        q = make_uint2(Half16<__half>::pack(lo.x * inv, lo.y * inv), Half16<__half>::pack(hi.x * inv, hi.y * inv));
       }
-      reinterpret_cast<uint4*>(smem + St::kOffQ)[f] = make_uint4(a[0], a[1], a[2], a[3]);
+      reinterpret_cast<uint2*>(smem + St::kOffQ)[f] = q;
     }
     __syncthreads();
-    const uint4* const s_q = reinterpret_cast<const uint4*>(smem + St::kOffQ) + lane;
+    const uint2* const s_q = reinterpret_cast<const uint2*>(smem + St::kOffQ) + lane;
 
-    // this thread's rows: g and g + 8 of each tile
+    // this thread's rows: 2 c and 2 c + 1 of each tile
     int q_i[RT][2], q_pos[RT][2];
     float sc[RT][2], row_m[RT][2], row_l[RT][2];
-    float o[RT][NT][4];
+    float o[RT][MT][4];  // values (D/8) g + 2 m (of both rows) and the next one
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        q_i[r][e] = query_of(P, row0 + 16 * r + g + e * 8);
+        q_i[r][e] = query_of(P, row0 + 8 * r + 2 * c + e);
         q_pos[r][e] = S.first + (P.depth && q_i[r][e] < P.n ? node_depth(P, q_i[r][e]) : q_i[r][e]);
         sc[r][e] = P.scale_log2;
-        if constexpr (BRAIN) sc[r][e] *= s_rowscale[16 * r + g + e * 8];
+        if constexpr (BRAIN) sc[r][e] *= s_rowscale[8 * r + 2 * c + e];
         row_m[r][e] = -kInf;
         row_l[r][e] = 0.f;
       }
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int m = 0; m < MT; ++m)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) o[r][nt][e] = 0.f;
-    uint4 qf[RT == 1 ? KT : 1];  // (one tile: the fragments stay in registers)
-    if constexpr (RT == 1) {
+        for (int e = 0; e < 4; ++e) o[r][m][e] = 0.f;
+    uint2 qf[RT <= 2 ? RT * KT : 1];  // (up to two tiles: the fragments stay in registers)
+    if constexpr (RT <= 2) {
 #pragma unroll
-      for (int t = 0; t < KT; ++t) qf[t] = s_q[t * 32];
+      for (int t = 0; t < RT * KT; ++t) qf[t] = s_q[t * 32];
     }
     const int i0 = query_of(P, row0), i1 = min(query_of(P, row0 + rows - 1), S.nq - 1);
     const bool tree = P.tree_mask != nullptr;
@@ -223,223 +272,195 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
       return ok;
     };
 
-    int stage = 0;
-    for (int t = t_lo + warp * SUB; t < t_hi; t += WARPS * SUB) {
-      copy_wait<STAGES - 2>();
-      __syncwarp();
-      const Copied now = ring[0];
-      {
-        const int page = page_next;
-        page_next = entry(t_next + WARPS * SUB);
-        const Copied next = prefetch(t_next, stage == 0 ? STAGES - 1 : stage - 1, page);
-        t_next += WARPS * SUB;
-#pragma unroll
-        for (int k = 0; k + 2 < STAGES; ++k) ring[k] = ring[k + 1];
-        ring[STAGES - 2] = next;
+    for (int n = 0; n < rounds && !late; ++n) {
+      const int t = first_step(n), stage = taken % STAGES;
+      if (n > 0 && n % LOOK == 0) {
+        now = next;
+        next = look_up(n / LOOK + 1);
       }
-      const uint32_t bads = now.bads;
+      if (!__all_sync(0xffffffffu, mbar_wait(full + stage, (taken / STAGES) & 1))) {
+        late = true;
+        break;
+      }
+      ++taken;
+      // (every lane is done with the round before, whose stage is filled again)
+      if (n + STAGES - 1 < rounds) issue(n + STAGES - 1, (n + STAGES - 1) / LOOK != n / LOOK);
+      if (n % LOOK == LOOK / 2) look_scales(next);
       char* const kb = stages + stage * St::kBytes;
-      char* const vb = kb + St::kOffV;
-      stage = stage + 1 == STAGES ? 0 : stage + 1;
-      // the scales of the steps: from the largest byte of their lanes (slots that are not wanted give 0)
-      int ek[SUB], ev[SUB];
+      char* const vb = kb + SUB * St::kBox;
 #pragma unroll
       for (int u = 0; u < SUB; ++u) {
-        const bool mine = SUB == 1 || lane / kStep == u;
-        ek[u] = scale_exponent(__reduce_max_sync(0xffffffffu, mine ? now.scale_k : 0u));
-        ev[u] = scale_exponent(__reduce_max_sync(0xffffffffu, mine ? now.scale_v : 0u));
-      }
+        // the step's scales, and whether its page is out of range
+        const int lane_of = n % LOOK * SUB + u;
+        const int ek = scale_exponent(__shfl_sync(0xffffffffu, now.scale_k, lane_of)), ev = scale_exponent(__shfl_sync(0xffffffffu, now.scale_v, lane_of));
+        const bool bad = __shfl_sync(0xffffffffu, now.page, lane_of) >= pg.num_pages;
+        const char* const ks = kb + u * St::kBox;
+        const char* const vs = vb + u * St::kBox;
 
-      // S = Q K^T: lane (g, c) takes D/4 consecutive codes of keys g, g + 8, ...; a word is a k step
-      float s_acc[RT][N][4];
+        // S^T = K Q^T: lane (g, c) takes D/4 consecutive codes of keys g and g + 8; a word is a k step
+        float s[RT][4];  // slots g (of both rows) and g + 8
 #pragma unroll
-      for (int r = 0; r < RT; ++r)
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int n = 0; n < N; ++n)
+          for (int e = 0; e < 4; ++e) s[r][e] = 0.f;
 #pragma unroll
-          for (int e = 0; e < 4; ++e) s_acc[r][n][e] = 0.f;
+        for (int y = 0; y < D / 64; ++y) {
+          const uint4 lo = *reinterpret_cast<const uint4*>(ks + St::at(g, c * (D / 64) + y)), hi = *reinterpret_cast<const uint4*>(ks + St::at(g + 8, c * (D / 64) + y));
+          const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-      for (int y = 0; y < D / 64; ++y) {
-        uint4 word[N];
+          for (int z = 0; z < 4; ++z) {
+            uint4 a;
+            e4m3x4_to_f16(wl[z], a.x, a.z);
+            e4m3x4_to_f16(wh[z], a.y, a.w);
 #pragma unroll
-        for (int n = 0; n < N; ++n) word[n] = *reinterpret_cast<const uint4*>(kb + (g + 8 * n) * St::kPitchK + c * (D / 4) + 16 * y);
-#pragma unroll
-        for (int z = 0; z < 4; ++z) {
-          uint4 a[RT];
-#pragma unroll
-          for (int r = 0; r < RT; ++r) a[r] = RT == 1 ? qf[4 * y + z] : s_q[(r * KT + 4 * y + z) * 32];
-#pragma unroll
-          for (int n = 0; n < N; ++n) {
-            uint32_t b0, b1;
-            e4m3x4_to_f16(z == 0 ? word[n].x : z == 1 ? word[n].y : z == 2 ? word[n].z : word[n].w, b0, b1);
-#pragma unroll
-            for (int r = 0; r < RT; ++r) mma<__half>(s_acc[r][n], a[r], b0, b1);
+            for (int r = 0; r < RT; ++r) {
+              const uint2 q = RT <= 2 ? qf[RT <= 2 ? r * KT + 4 * y + z : 0] : s_q[(r * KT + 4 * y + z) * 32];
+              mma<__half>(s[r], a, q.x, q.y);
+            }
           }
         }
-      }
 
-      // scale and mask; a slot on a page out of range gives NaN to the rows that see it
-      bool whole = bads == 0;
+        // scale and mask; a slot on a page out of range gives NaN to the rows that see it
+        const bool whole = !bad && whole_step(t + u);
+        const float factor = power_f32(ek);
+        uint32_t seen = ~0u;  // bit 4 r + e
+        bool moves = false;
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) whole = whole && whole_step(t + u);
-      uint32_t seen[RT];  // bit 4 n + e: element e of key tile n is visible
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        seen[r] = 0;
-#pragma unroll
-        for (int n = 0; n < N; ++n) {
-          const float f = power_f32(ek[n / 2]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) s_acc[r][n][e] *= sc[r][e / 2] * f;
-        }
+          for (int e = 0; e < 4; ++e) s[r][e] *= sc[r][e % 2] * factor;
         if (!whole) {
+          seen = 0;
 #pragma unroll
-          for (int n = 0; n < N; ++n)
+          for (int r = 0; r < RT; ++r)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int key = 8 * n + 2 * c + (e & 1);
-              const bool ok = t + key / kStep < t_hi && sees(r, e / 2, R.slot(t + key / kStep) + key % kStep);
-              float v = s_acc[r][n][e];
-              if ((bads >> key) & 1u) v = __int_as_float(0x7fffffff);
-              s_acc[r][n][e] = ok ? v : -kInf;
-              seen[r] |= (ok ? 1u : 0u) << (4 * n + e);
+              const bool ok = t + u < t_hi && sees(r, e % 2, R.slot(t + u) + g + e / 2 * 8);
+              s[r][e] = !ok ? -kInf : bad ? __int_as_float(0x7fffffff) : s[r][e];
+              seen |= (ok ? 1u : 0u) << (4 * r + e);
             }
         }
-      }
-
-      // the running maximum and sum
-      uint4 p[RT][SUB];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        float alpha[2];
+        for (int r = 0; r < RT; ++r)
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float m = -kInf;
+          for (int e = 0; e < 2; ++e) moves = moves || fmaxf(s[r][e], s[r][2 + e]) - row_m[r][e] > kSlack + kBelow<__half>;
+        if (__any_sync(0xffffffffu, moves)) {  // (also where m is still -inf)
 #pragma unroll
-          for (int n = 0; n < N; ++n) m = fmaxf(m, fmaxf(s_acc[r][n][2 * x], s_acc[r][n][2 * x + 1]));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
-          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
-          const float top = fmaxf(row_m[r][x], m - kBelow<__half>);
-          const float base = top == -kInf ? 0.f : top;
-          alpha[x] = ex2(row_m[r][x] - base);
-          row_m[r][x] = top;
-          float sum = 0.f;
+          for (int r = 0; r < RT; ++r)
 #pragma unroll
-          for (int n = 0; n < N; ++n)
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(s[r][e], s[r][2 + e]);
 #pragma unroll
-            for (int y = 0; y < 2; ++y) {
-              s_acc[r][n][2 * x + y] = ex2(s_acc[r][n][2 * x + y] - base);
-              sum += s_acc[r][n][2 * x + y];
+              for (int x = 4; x < 32; x <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+              top = fmaxf(row_m[r][e], top - kBelow<__half>);
+              const float alpha = row_m[r][e] == top ? 1.f : ex2(row_m[r][e] - top);
+              row_m[r][e] = top;
+              row_l[r][e] *= alpha;
+#pragma unroll
+              for (int m = 0; m < MT; ++m) {
+                o[r][m][e] *= alpha;
+                o[r][m][2 + e] *= alpha;
+              }
             }
-          row_l[r][x] = row_l[r][x] * alpha[x] + sum;  // this lane's keys; joined at the end
         }
-        // P in fp16: a rounding of 2^-11 of each weight (below 2^-21 of the row's largest weight, of 2^-32 of that
-        // one); l keeps the unrounded weights
-#pragma unroll
-        for (int u = 0; u < SUB; ++u)
-          p[r][u] = make_uint4(Half16<__half>::pack(s_acc[r][2 * u][0], s_acc[r][2 * u][1]), Half16<__half>::pack(s_acc[r][2 * u][2], s_acc[r][2 * u][3]),
-                               Half16<__half>::pack(s_acc[r][2 * u + 1][0], s_acc[r][2 * u + 1][1]),
-                               Half16<__half>::pack(s_acc[r][2 * u + 1][2], s_acc[r][2 * u + 1][3]));
-        if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) o[r][nt][e] *= alpha[e / 2];
-        }
-      }
 
-      // A value that is not finite (a code of NaN) must not reach rows that do not see its slot (0 * NaN):
-      // steps that some row sees in part look for such codes, take them out of the product
-      // and add them to the rows that do see them.
-      uint32_t odd = 0;
-      if (!whole) {
-        for (int f = lane; f < SLOTS * (D / 16); f += 32) {
-          const uint4 x = *reinterpret_cast<const uint4*>(vb + (f / (D / 16)) * St::kPitchV + (f % (D / 16)) * 16);
-          const uint32_t any = __vcmpeq4(x.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(x.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
-                               __vcmpeq4(x.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(x.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
-          if (any) odd |= 1u << (f / (D / 16));
-        }
-        odd = __reduce_or_sync(0xffffffffu, odd);
-      }
-
-      // O += P V: lane (g, c) takes values (D/8) g ... of keys 2c, 2c+1, 2c+8, 2c+9; column g of tile
-      // nt stands for value (D/8) g + nt
+        // the weights.  P in fp16: a rounding of 2^-11 of each (below 2^-21 of the row's largest, of 2^-32 of
+        // that one); l keeps the unrounded ones
+        uint32_t w2[RT][2];  // slot g, then g + 8, of both rows
+        uint2 pf[RT];
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) {
+        for (int r = 0; r < RT; ++r) {
+          float pe[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) pe[e] = ex2(s[r][e] - (row_m[r][e % 2] == -kInf ? 0.f : row_m[r][e % 2]));
+          row_l[r][0] += pe[0] + pe[2];  // this lane's slots; joined at the end
+          row_l[r][1] += pe[1] + pe[3];
+          w2[r][0] = Half16<__half>::pack(pe[0], pe[1]);
+          w2[r][1] = Half16<__half>::pack(pe[2], pe[3]);
+          pf[r] = make_uint2(transpose8x8(w2[r][0]), transpose8x8(w2[r][1]));
+        }
+
+        // A value that is not finite (a code of NaN) must not reach rows that do not see its slot (0 * NaN):
+        // steps that some row sees in part look for such codes, take them out of the product
+        // and add them to the rows that do see them.
+        uint32_t odd = 0;
+        if (!whole) {
+          for (int f = lane; f < kStep * (D / 16); f += 32) {  // (rows of a box are whole, whatever the order of their pieces)
+            const uint4 x = *reinterpret_cast<const uint4*>(vs + f * 16);
+            const uint32_t any = __vcmpeq4(x.x & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(x.y & 0x7f7f7f7fu, 0x7f7f7f7fu) |
+                                 __vcmpeq4(x.z & 0x7f7f7f7fu, 0x7f7f7f7fu) | __vcmpeq4(x.w & 0x7f7f7f7fu, 0x7f7f7f7fu);
+            if (any) odd |= 1u << (f / (D / 16));
+          }
+          odd = __reduce_or_sync(0xffffffffu, odd);
+        }
+        const uint32_t keep0 = ((odd >> (2 * c)) & 1u ? 0u : 0xffffu) | ((odd >> (2 * c + 1)) & 1u ? 0u : 0xffff0000u);
+        const uint32_t keep1 = ((odd >> (2 * c + 8)) & 1u ? 0u : 0xffffu) | ((odd >> (2 * c + 9)) & 1u ? 0u : 0xffff0000u);
+
+        // O^T += V^T P^T: lane (g, c) takes values (D/8) g ... of slots 2c, 2c+1, 2c+8, 2c+9
         constexpr int W = D / 32;  // words of those codes
-        const uint32_t odd16 = odd >> (16 * u);
-        const uint32_t keep0 = ((odd16 >> (2 * c)) & 1u ? 0u : 0xffffu) | ((odd16 >> (2 * c + 1)) & 1u ? 0u : 0xffff0000u);
-        const uint32_t keep1 = ((odd16 >> (2 * c + 8)) & 1u ? 0u : 0xffffu) | ((odd16 >> (2 * c + 9)) & 1u ? 0u : 0xffff0000u);
         uint32_t word[4][W];
 #pragma unroll
         for (int k = 0; k < 4; ++k) {
-          const char* const row = vb + (16 * u + 2 * c + (k & 1) + (k >> 1) * 8) * St::kPitchV + g * (D / 8);
+          const int row = 2 * c + (k & 1) + (k >> 1) * 8;
+          const char* const from = vs + (D == 128 ? St::at(row, g) : St::at(row, g / 2) + g % 2 * 8);
           if constexpr (W == 4) {
-            const uint4 x = *reinterpret_cast<const uint4*>(row);
+            const uint4 x = *reinterpret_cast<const uint4*>(from);
             word[k][0] = x.x; word[k][1] = x.y; word[k][2] = x.z; word[k][3] = x.w;
           } else {
-            const uint2 x = *reinterpret_cast<const uint2*>(row);
+            const uint2 x = *reinterpret_cast<const uint2*>(from);
             word[k][0] = x.x; word[k][1] = x.y;
           }
         }
-        const uint32_t s2 = power_f16x2(ev[u]);
+        const uint32_t s2 = power_f16x2(ev);
 #pragma unroll
         for (int x = 0; x < W; ++x) {
           uint32_t f[2][4];
 #pragma unroll
-          for (int k = 0; k < 2; ++k) {  // pair the two keys' bytes
+          for (int k = 0; k < 2; ++k) {  // pair the two slots' bytes
             const uint32_t a = word[2 * k][x], bb = word[2 * k + 1][x];
             e4m3x4_to_f16(__byte_perm(a, bb, 0x5140), f[k][0], f[k][1]);
             e4m3x4_to_f16(__byte_perm(a, bb, 0x7362), f[k][2], f[k][3]);
 #pragma unroll
+            for (int e = 0; e < 4; ++e) f[k][e] = mul_f16x2(f[k][e], s2);
+          }
+          if (odd) {
+#pragma unroll
             for (int e = 0; e < 4; ++e) {
-              f[k][e] = mul_f16x2(f[k][e], s2);
-              if (odd) f[k][e] &= k == 0 ? keep0 : keep1;
+              f[0][e] &= keep0;
+              f[1][e] &= keep1;
             }
           }
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
+          for (int y = 0; y < 2; ++y)
 #pragma unroll
-            for (int r = 0; r < RT; ++r) mma<__half>(o[r][4 * x + e], p[r][u], f[0][e], f[1][e]);
+            for (int r = 0; r < RT; ++r)
+              mma<__half>(o[r][2 * x + y], make_uint4(f[0][2 * y], f[0][2 * y + 1], f[1][2 * y], f[1][2 * y + 1]), pf[r].x, pf[r].y);
         }
-      }
-      if (odd) {  // rare: what was taken out above, for the rows that see the slot
+        if (odd) {  // rare: what was taken out above, for the rows that see the slot
 #pragma unroll 1
-        for (uint32_t left = odd; left; left &= left - 1) {
-          const int key = __ffs(left) - 1, n = key / 8;
-          const int src = (lane & ~3) | ((key & 7) >> 1);
+          for (uint32_t left = odd; left; left &= left - 1) {
+            const int key = __ffs(left) - 1, src = (key & 7) * 4 + c;
+            const uint32_t vis = __shfl_sync(0xffffffffu, seen, src);
 #pragma unroll
-          for (int r = 0; r < RT; ++r)
+            for (int r = 0; r < RT; ++r) {
+              const uint32_t got = __shfl_sync(0xffffffffu, key < 8 ? w2[r][0] : w2[r][1], src);
+              const float2 p = Half16<__half>::to_f32(got);
 #pragma unroll
-            for (int x = 0; x < 2; ++x) {
-              uint32_t mine = 0;
+              for (int y = 0; y < 2; ++y) {
+                if (!((vis >> (4 * r + key / 8 * 2 + y)) & 1u)) continue;
+                const float py = y ? p.y : p.x;
 #pragma unroll
-              for (int u = 0; u < SUB; ++u) {
-                if (n == 2 * u) mine = x ? p[r][u].y : p[r][u].x;
-                if (n == 2 * u + 1) mine = x ? p[r][u].w : p[r][u].z;
-              }
-              const uint32_t got = __shfl_sync(0xffffffffu, mine, src);
-              const uint32_t vis = __shfl_sync(0xffffffffu, seen[r], src);
-              const float2 two = Half16<__half>::to_f32(got);
-              const float pk = key & 1 ? two.y : two.x;
-              if (!((vis >> (4 * n + 2 * x + (key & 1))) & 1u)) continue;
-#pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int y = 0; y < 2; ++y) {
-                  const int d = (D / 8) * (2 * c + y) + nt;
-                  const uint32_t byte = *reinterpret_cast<const uint8_t*>(vb + key * St::kPitchV + d);
-                  int e = ev[0];
-#pragma unroll
-                  for (int u = 1; u < SUB; ++u)
-                    if (key / kStep == u) e = ev[u];
-                  o[r][nt][2 * x + y] += pk * Half16<__half>::to_f32(mul_f16x2(e4m3x2_to_f16(byte), power_f16x2(e))).x;
+                for (int d = 0; d < 2 * MT; ++d) {
+                  const int at = (D / 8) * g + d;
+                  const uint32_t byte = *reinterpret_cast<const uint8_t*>(vs + St::at(key, at / 16) + at % 16);
+                  o[r][d / 2][d % 2 * 2 + y] += py * Half16<__half>::to_f32(mul_f16x2(e4m3x2_to_f16(byte), s2)).x;
                 }
+              }
             }
+          }
         }
       }
     }
-    copy_wait<0>();
 
     // ---- join the warps' rows
     __syncthreads();
@@ -448,25 +469,57 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
 #pragma unroll
     for (int r = 0; r < RT; ++r)
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        float l = row_l[r][x];
-        l += __shfl_xor_sync(0xffffffffu, l, 1);
-        l += __shfl_xor_sync(0xffffffffu, l, 2);
-        const int row = 16 * r + g + 8 * x;
-        if (c == 0) s_ml[warp * MR + row] = make_float2(row_m[r][x], l);
-        float* const dst = s_o + (static_cast<size_t>(warp) * MR + row) * D;
+      for (int e = 0; e < 2; ++e) {
+        float l = row_l[r][e];
 #pragma unroll
-        for (int y = 0; y < 2; ++y)
+        for (int x = 4; x < 32; x <<= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+        const int row = 8 * r + 2 * c + e;
+        if (g == 0) s_ml[warp * MR + row] = make_float2(row_m[r][e], l);
+        float* const dst = s_o + (static_cast<size_t>(warp) * MR + row) * D + (D / 8) * g;
 #pragma unroll
-          for (int nt = 0; nt < NT; nt += 4)
-            *reinterpret_cast<float4*>(dst + (D / 8) * (2 * c + y) + nt) =
-                make_float4(o[r][nt][2 * x + y], o[r][nt + 1][2 * x + y], o[r][nt + 2][2 * x + y], o[r][nt + 3][2 * x + y]);
+        for (int m = 0; m < MT; m += 2)
+          *reinterpret_cast<float4*>(dst + 2 * m) = make_float4(o[r][m][e], o[r][m][2 + e], o[r][m + 1][e], o[r][m + 1][2 + e]);
       }
     __syncthreads();
     join_warps<T, D, MR, WARPS>(P, w, S, row0, rows, smem);
     if (w.u == w.item && !w.ends() && tid == 0) P.split[cta] = w.split(share);
     if (!w.next()) break;
   }
+  if (late) {  // nothing of the call counts; what is still on its way lands first
+    for (; taken < issued; ++taken) mbar_wait(full + taken % STAGES, (taken / STAGES) & 1);
+    if (lane == 0) P.gave_up[cta] = 1;
+  }
+}
+
+// The pages' tensors of codes (values, slots, heads, pages), whose boxes of 16 slots of a head the kernel copies.
+using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeTiled encode_tiled() {  // (by the runtime's lookup: the library needs no link to the driver's)
+  static const EncodeTiled fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q{};
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+      return static_cast<EncodeTiled>(nullptr);
+    return reinterpret_cast<EncodeTiled>(f);
+  }();
+  return fn;
+}
+cudaError_t encode(const Pages& pg, Maps* maps) {
+  const EncodeTiled fn = encode_tiled();
+  if (!fn) return cudaErrorNotSupported;
+  maps->heads = pg.head_stride != 0;
+  maps->pages = pg.page_stride != 0;
+  const cuuint64_t D = static_cast<cuuint64_t>(pg.head_dim);
+  const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(pg.page_size), maps->heads ? static_cast<cuuint64_t>(pg.kv_heads) : 1,
+                              maps->pages ? static_cast<cuuint64_t>(pg.num_pages) : 1};
+  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(pg.slot_stride), static_cast<cuuint64_t>(maps->heads ? pg.head_stride : pg.slot_stride),
+                                 static_cast<cuuint64_t>(maps->pages ? pg.page_stride : pg.slot_stride)};
+  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), kStep, 1, 1}, one[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 2; ++i)
+    if (fn(i ? &maps->v : &maps->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? pg.v : pg.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
+           D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+      return cudaErrorInvalidValue;
+  return cudaSuccess;
 }
 
 template <typename T, int D, int RT>
@@ -476,18 +529,23 @@ cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
   static_assert(St::kSmem <= 227 * 1024 - 1024, "shared memory of a CTA");
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, St::kSmem); e != cudaSuccess)
     return e;
-  return launch_kernel(kernel, dim3(P.ctas), dim3(32 * St::WARPS), St::kSmem, stream, 1, P);
+  Maps maps;
+  if (cudaError_t e = encode(P.pages, &maps); e != cudaSuccess) return e;
+  return launch_kernel(kernel, dim3(P.ctas), dim3(32 * St::WARPS), St::kSmem, stream, 1, P, maps);
 }
 
+template <typename T, int D>
+cudaError_t launch_rows(const AttendParams& P, int mr, cudaStream_t stream) {
+  return mr == 8 ? launch_shape<T, D, 1>(P, stream) : mr == 16 ? launch_shape<T, D, 2>(P, stream) : launch_shape<T, D, 4>(P, stream);
+}
 template <typename T>
 cudaError_t launch_typed(const AttendParams& P, int mr, cudaStream_t stream) {
-  if (P.pages.head_dim == 64) return mr == 16 ? launch_shape<T, 64, 1>(P, stream) : launch_shape<T, 64, 2>(P, stream);
-  return mr == 16 ? launch_shape<T, 128, 1>(P, stream) : launch_shape<T, 128, 2>(P, stream);
+  return P.pages.head_dim == 64 ? launch_rows<T, 64>(P, mr, stream) : launch_rows<T, 128>(P, mr, stream);
 }
 
 }  // namespace
 
-int attend8_rows(int64_t rows) { return rows <= 16 ? 16 : 32; }
+int attend8_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
 
 cudaError_t launch_attend8(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream) {
   return dt == SPECDEC_BF16 ? launch_typed<__nv_bfloat16>(P, mr, stream) : launch_typed<__half>(P, mr, stream);

@@ -730,6 +730,8 @@ int check_pages(const specdec_kv_pages* pg, specdec_dtype format, Pages* out) {
       return fail(SPECDEC_ERR_UNSUPPORTED, "page_size must be a multiple of scale_block, that a multiple of 16");
     if (!multiples(1, {pg->scale_page_stride, pg->scale_slot_stride, pg->scale_head_stride}))
       return fail(SPECDEC_ERR_UNSUPPORTED, "scale strides must not be negative");
+    if (pg->slot_stride == 0 || (pg->page_stride | pg->slot_stride | pg->head_stride) >= int64_t{1} << 40)
+      return fail(SPECDEC_ERR_UNSUPPORTED, "strides of 8-bit pages must be below 2^40, of slots positive");
     if (!(1.f / pg->k_scale <= 3.4e38f && 1.f / pg->v_scale <= 3.4e38f))  // (NaN and 0 among them)
       return fail(SPECDEC_ERR_INVALID_ARG, "k_scale and v_scale need finite reciprocals");
   }
