@@ -21,8 +21,8 @@
 // lanes, with a lookup for every step: 288 us for 64 requests of 8 tokens over up to 8190 slots, 485 us for one token of 96
 // requests over up to 16001; over half of the instructions were the copies'.)
 
-#include <cuda.h>
 #include "attend_common.cuh"
+#include "boxes.cuh"
 #include "specdec_internal.h"
 
 namespace specdec {
@@ -65,19 +65,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
   asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
 }
-
-// The box of 16 slots of one head, (x, slot, head, page), to shared memory.
-__device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, int slot, int head, int page, uint64_t* bar) {
-  asm volatile(
-      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
-      "l"(map), "r"(0), "r"(slot), "r"(head), "r"(page), "r"(smem_addr(bar))
-      : "memory");
-}
-
-struct Maps {
-  CUtensorMap k, v;
-  int heads, pages;  // 0: all heads, or pages, lie at the same place (a stride of 0): the coordinate is 0
-};
 
 template <typename T, int D, int RT>
 __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(const AttendParams P, const __grid_constant__ Maps maps) {
@@ -127,27 +114,11 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
     auto first_step = [&](int n) { return t_lo + (n * WARPS + warp) * SUB; };
     const int rounds = first_step(0) >= t_hi ? 0 : (t_hi - first_step(0) - 1) / (WARPS * SUB) + 1;
     constexpr int LOOK = 32 / SUB;  // rounds of a look
-    struct Look {
-      int page, in_page;              // -1: no such step
-      uint32_t scale_k, scale_v;      // (nothing is made of the bytes before they are used: it would wait for them)
-    };
     auto look_up = [&](int look) {
-      Look l{-1, 0, 0, 0};
+      Look l;
       const int t = first_step(look * LOOK + lane / SUB) + lane % SUB;
-      if (t < t_hi) {
-        const int s = R.slot(t), logical = page_of(pg, s);
-        l.page = __ldg(table + logical);
-        l.in_page = s - logical * pg.page_size;
-        if (l.page < 0) l.page = pg.num_pages;  // (out of range, and there)
-      }
+      l.find(pg, table, R.slot(t), t < t_hi);
       return l;
-    };
-    auto look_scales = [&](Look& l) {
-      if (static_cast<unsigned>(l.page) < static_cast<unsigned>(pg.num_pages)) {
-        const int64_t so = l.page * pg.scale_page_stride + block_of(pg, l.in_page) * pg.scale_slot_stride + h * pg.scale_head_stride;
-        l.scale_k = __ldg(reinterpret_cast<const uint8_t*>(pg.k_scales) + so);
-        l.scale_v = __ldg(reinterpret_cast<const uint8_t*>(pg.v_scales) + so);
-      }
     };
     Look now{}, next{};
     // copies round n's steps (now is the look of the round that is taken, n the same or the next one)
@@ -182,7 +153,7 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
 #pragma unroll
       for (int n = 0; n < STAGES - 1; ++n)
         if (n < rounds) issue(n, false);
-      look_scales(now);
+      now.find_scales(pg, h);
     }
 
     // ---- the query rows, as the matrix instruction's fragments: [tile][k step][lane]
@@ -285,7 +256,7 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
       ++taken;
       // (every lane is done with the round before, whose stage is filled again)
       if (n + STAGES - 1 < rounds) issue(n + STAGES - 1, (n + STAGES - 1) / LOOK != n / LOOK);
-      if (n % LOOK == LOOK / 2) look_scales(next);
+      if (n % LOOK == LOOK / 2) next.find_scales(pg, h);
       char* const kb = stages + stage * St::kBytes;
       char* const vb = kb + SUB * St::kBox;
 #pragma unroll
@@ -491,37 +462,6 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
   }
 }
 
-// The pages' tensors of codes (values, slots, heads, pages), whose boxes of 16 slots of a head the kernel copies.
-using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
-                                 const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-EncodeTiled encode_tiled() {  // (by the runtime's lookup: the library needs no link to the driver's)
-  static const EncodeTiled fn = [] {
-    void* f = nullptr;
-    cudaDriverEntryPointQueryResult q{};
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
-      return static_cast<EncodeTiled>(nullptr);
-    return reinterpret_cast<EncodeTiled>(f);
-  }();
-  return fn;
-}
-cudaError_t encode(const Pages& pg, Maps* maps) {
-  const EncodeTiled fn = encode_tiled();
-  if (!fn) return cudaErrorNotSupported;
-  maps->heads = pg.head_stride != 0;
-  maps->pages = pg.page_stride != 0;
-  const cuuint64_t D = static_cast<cuuint64_t>(pg.head_dim);
-  const cuuint64_t dims[4] = {D, static_cast<cuuint64_t>(pg.page_size), maps->heads ? static_cast<cuuint64_t>(pg.kv_heads) : 1,
-                              maps->pages ? static_cast<cuuint64_t>(pg.num_pages) : 1};
-  const cuuint64_t strides[3] = {static_cast<cuuint64_t>(pg.slot_stride), static_cast<cuuint64_t>(maps->heads ? pg.head_stride : pg.slot_stride),
-                                 static_cast<cuuint64_t>(maps->pages ? pg.page_stride : pg.slot_stride)};
-  const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), kStep, 1, 1}, one[4] = {1, 1, 1, 1};
-  for (int i = 0; i < 2; ++i)
-    if (fn(i ? &maps->v : &maps->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? pg.v : pg.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-           D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
-      return cudaErrorInvalidValue;
-  return cudaSuccess;
-}
-
 template <typename T, int D, int RT>
 cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
   using St = Stage8<D, RT>;
@@ -530,7 +470,7 @@ cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, St::kSmem); e != cudaSuccess)
     return e;
   Maps maps;
-  if (cudaError_t e = encode(P.pages, &maps); e != cudaSuccess) return e;
+  if (cudaError_t e = encode_maps(P.pages, true, &maps); e != cudaSuccess) return e;
   return launch_kernel(kernel, dim3(P.ctas), dim3(32 * St::WARPS), St::kSmem, stream, 1, P, maps);
 }
 

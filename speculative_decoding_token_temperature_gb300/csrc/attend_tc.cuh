@@ -45,6 +45,7 @@
 #pragma once
 
 #include "attend_common.cuh"
+#include "boxes.cuh"
 
 namespace specdec {
 
@@ -90,7 +91,7 @@ struct Shape {
     return k >= 0 && k < kCopyWarps ? k : -1;
   }
   static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int RK = D == 64 ? 4 : (TWO || FOUR ? 2 : 3), RV = D == 64 ? 4 : 2;  // K tiles and V tiles staged
+  static constexpr int RK = D == 64 ? 4 : EIGHT && TWO ? 1 : (TWO || FOUR || EIGHT ? 2 : 3), RV = D == 64 ? 4 : 2;  // K tiles and V tiles staged
   // 4-bit pages: a tile's codes and scales (of K, then of V), copied ahead of their conversion
   static constexpr int kRawCodes = kTile * (D / 2), kRawScales = kTile * (D / 16), kRawBytes = 2 * (kRawCodes + kRawScales);
   // where the 16-byte piece of a row of codes lies: turned by the row, so that 8 rows meet no bank conflict
@@ -100,14 +101,15 @@ struct Shape {
   static constexpr int kOffV = kOffK + RK * kTileBytes;
   static constexpr int kOffMl = kOffV + RV * kTileBytes;      // [2][2][128] (m, l) of slots and halves
   static constexpr int kOffRaw = kOffMl + 4 * 128 * 8;
-  static constexpr int kRawWarp = 16 * D;  // 8-bit pages: the codes of a converting warp's 16 keys, ahead of their conversion
-  static constexpr int kOffQScale = kOffRaw + (EIGHT ? kCopyWarps * kRawWarp : RAW * kRawBytes);  // [2][MR] scales of query rows (4-bit and 8-bit pages)
+  // 8-bit pages: boxes of a converting warp's 16 slots, keys' and values' in turn, ahead of their conversion
+  static constexpr int kBox = 16 * D, BOXES = 3;
+  static constexpr int kOffQScale = kOffRaw + (EIGHT ? kCopyWarps * BOXES * kBox : RAW * kRawBytes);  // [2][MR] scales of query rows (4-bit and 8-bit pages)
   static constexpr int kOffSum = kOffQScale + (FOUR || EIGHT ? 2 * MR * 4 : 0);  // [4][4][32][8] accumulators on their way, [32] 1 / l
   static constexpr int kOffItem = kOffSum + (QUAD ? 4 * 4 * 32 * 8 * 4 + 32 * 4 : 0);
   static constexpr int kOffScan = kOffItem + kItems * sizeof(Item);
   static constexpr int kOffBad = (kOffScan + (kThreads / 32 + 3) * 8 + 15) / 16 * 16;
   static constexpr int kOffBar = kOffBad + kBadRing * 16;
-  static constexpr int kBars = 2 * (RK + RV + RAW) + 2 + 2 + 2 + 2 + 2 * kItems + 1;
+  static constexpr int kBars = 2 * (RK + RV + RAW) + 2 + 2 + 2 + 2 + 2 * kItems + 1 + (EIGHT ? kCopyWarps * BOXES : 0);
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kBytes = kOffMisc + 16;
 
@@ -239,8 +241,16 @@ __device__ __forceinline__ uint64_t bits64(int lo, int hi) {
   return lo >= 64 ? 0ull : below & (~0ull << max(lo, 0));
 }
 
+// What the kernel takes besides: the tensors of 8-bit pages.
+template <int BITS> struct Extra {
+  struct type {};
+};
+template <> struct Extra<8> {
+  using type = Maps;
+};
+
 template <typename T, int D, Rows ROWS, int BITS>
-__global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_kernel(const AttendParams P) {
+__global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_kernel(const AttendParams P, const __grid_constant__ typename Extra<BITS>::type extra) {
   using Sh = Shape<D, ROWS, BITS>;
   constexpr bool FOUR = BITS == 4, EIGHT = BITS == 8;
   constexpr bool BRAIN = BITS != 16 && !std::is_same<T, __half>::value;  // bf16 queries to be held in fp16
@@ -297,6 +307,8 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
       mbar_init(raw_full + r, 64 + 2);  // every lane's copies, and the two parts of s_bad
       mbar_init(raw_empty + r, Sh::kCopyWarps);
     }
+    if constexpr (EIGHT)
+      for (int r = 0; r < Sh::kCopyWarps * Sh::BOXES; ++r) mbar_init(raw_full + r, 1);  // (a converting warp's own)
     mbar_fence_init();
     *gave_up = 0;
     *s_odd = 0;
@@ -383,6 +395,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
     // ---- K and V
     const int cw = Sh::copy_index(warp);
     int tile = 0;
+    [[maybe_unused]] int boxes = 0;  // 8-bit pages: boxes of earlier items
     for (int n = 0;; ++n) {
       if (!__all_sync(0xffffffffu, wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up))) break;
       const Item it = items[n % kItems];
@@ -396,54 +409,19 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
       const char* const k_head = pg.k + it.h * pg.head_stride;
       const char* const v_head = pg.v + it.h * pg.head_stride;
       if constexpr (EIGHT) {
-        // Warp c brings slots 16 c ... of a tile, a step, whose slots are in one block; lane l looks up slot 16 c + l % 16.  The
-        // codes are copied ahead: keys' two tiles, to a slot of shared memory of the warp's own; values' once their tile's
-        // place is free, into that place, a row's codes in the first bytes of its row of the first 64 values, from where the
-        // warp takes them to registers.  A tile's keys are converted before the values of the tile before it, which
-        // are wanted later.  (Copies, not loads: a warp has few scoreboards, and a wait for a page or a scale then also waited for codes.)
-        constexpr int CH = D / 16, RPI = 32 / CH, LOADS = 16 / RPI;  // 16-byte pieces of a row of codes, rows at a time
-        char* const raw = smem + Sh::kOffRaw + cw * Sh::kRawWarp + lane * 16;
-        int page = 0, in_page = -1;  // of the next tile (-1: no query of the item sees the slot)
-        auto look_up = [&](int t) {
-          const int s = R.slot(t * kUnit + cw) + lane % kStep;
-          in_page = -1;
-          if (t < t_hi && s < it.end && (s >= it.lo || s < it.sinks)) {
-            const int logical = page_of(pg, s);
-            page = __ldg(table + logical);
-            in_page = s - logical * pg.page_size;
-          }
-        };
-        uint32_t bads = 0, present = 0, scale_k = 0, scale_v = 0;  // (nothing is made of the bytes before they are used: it would wait)
-        int64_t off = 0;
-        auto place = [&]() {  // what the looked-up slots give: where they are, and their block's scales
-          const bool want = in_page >= 0;
-          const bool bad = want && static_cast<unsigned>(page) >= static_cast<unsigned>(pg.num_pages);
-          const bool there = want && !bad;
-          bads = __ballot_sync(0xffffffffu, bad) & 0xffffu;
-          present = __ballot_sync(0xffffffffu, there);
-          off = there ? page * pg.page_stride + in_page * pg.slot_stride : 0;
-          scale_k = scale_v = 0;
-          if (there) {
-            const int64_t so = page * pg.scale_page_stride + block_of(pg, in_page) * pg.scale_slot_stride + it.h * pg.scale_head_stride;
-            scale_k = __ldg(reinterpret_cast<const uint8_t*>(pg.k_scales) + so);
-            scale_v = __ldg(reinterpret_cast<const uint8_t*>(pg.v_scales) + so);
-          }
-        };
-        auto copy = [&](uint32_t dst, int step, const char* head, int64_t at, uint32_t rows) {  // RPI rows every `step` bytes
-#pragma unroll
-          for (int j = 0; j < LOADS; ++j) {
-            const int row = j * RPI + lane / CH;
-            const int64_t o = __shfl_sync(0xffffffffu, at, row) + lane % CH * 16;
-            copy_async<16>(dst + j * step, head + o, (rows >> row) & 1u);
-          }
-          copy_commit();
-        };
+        // Warp c brings slots 16 c ... of a tile, a step: a box of keys and one of values.  A lane each looks up 32 tiles'
+        // steps, and boxes are copied three ahead, whatever tile's place is free, to shared memory of the warp's own.
+        // (16-byte copies by all lanes with a lookup for every tile, or values copied to their tile's place once that was free,
+        // which left the copy's latency in every tile's way: 271 us for the tree of the figures above, 286 to 293 us for 64
+        // requests of 8 tokens.)
+        constexpr int CH = D / 16, RPI = 32 / CH, LOADS = 16 / RPI, BOXES = Sh::BOXES;  // 16-byte pieces of a row of codes, rows at a time
+        char* const raw = smem + Sh::kOffRaw + cw * BOXES * Sh::kBox;
+        uint64_t* const full = raw_full + cw * BOXES;
         auto place_of = [&](int kv, int n) { return smem + (kv ? Sh::kOffV : Sh::kOffK) + n % (kv ? RV : RK) * Sh::kTileBytes; };
         auto wait_empty = [&](int kv, int n) {
           wait_for((kv ? v_empty : k_empty) + n % (kv ? RV : RK), ((n / (kv ? RV : RK)) & 1) ^ 1, gave_up);
           __syncwarp();
         };
-        const int in_tile = (cw * 16 + lane / CH) * 128 + lane % CH * 16;  // this lane's first piece of the values' codes
         uint4 codes[LOADS];
         auto store = [&](int kv, int n, int e) {  // the codes' values to tile number n
           char* const dst = place_of(kv, n);
@@ -467,38 +445,70 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
           __syncwarp();
           if (lane == 0) mbar_arrive((kv ? v_full + n % RV : k_full + n % RK));
         };
-        look_up(t_lo);
-        place();
-        look_up(t_lo + 1);
-        if (t_lo < t_hi) copy(smem_addr(raw), 512, k_head, off, present);
-        int ev = 0;  // the exponent of tile t's values
-        for (int t = t_lo - 1; t < t_hi; ++t) {
-          copy_wait<0>();
-          if (t >= t_lo) {
-            __syncwarp();
+        auto look_up = [&](int look) {
+          Look l;
+          const int t = t_lo + look * 32 + lane, s = R.slot(t * kUnit + cw);
+          l.find(pg, table, s, t < t_hi && s < it.end);
+          return l;
+        };
+        const int tiles = t_hi - t_lo;
+        Look now = look_up(0), next = look_up(1);
+        // The item's box n: tile n / 2's keys, then its values.  Number boxes + n of all; `at` is the look that `now` is.
+        auto fetch = [&](int n, int at) {
+          if (n >= 2 * tiles) return;
+          const int i = n / 2;
+          const int page = __shfl_sync(0xffffffffu, i / 32 == at ? now.page : next.page, i % 32);
+          const int in_page = __shfl_sync(0xffffffffu, i / 32 == at ? now.in_page : next.in_page, i % 32);
+          if (lane == 0) {
+            const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages) && !*gave_up;
+            const int slot = (boxes + n) % BOXES;
+            fence_proxy_async_smem();  // (what was read there)
+            mbar_expect_tx(full + slot, there ? Sh::kBox : 0);
+            if (there)
+              copy_box(smem_addr(raw + slot * Sh::kBox), n % 2 ? &extra.v : &extra.k, in_page, extra.heads ? it.h : 0, extra.pages ? page : 0, full + slot);
+          }
+        };
+        // box n's codes to registers (zeros for a step that is not there), and another box to its place
+        auto take = [&](int n, int at, bool there) {
+          const int slot = (boxes + n) % BOXES;
+          wait_for(full + slot, ((boxes + n) / BOXES) & 1, gave_up);
+          __syncwarp();
 #pragma unroll
-            for (int j = 0; j < LOADS; ++j) codes[j] = *reinterpret_cast<const uint4*>(place_of(1, tile) + in_tile + j * RPI * 128);
-            __syncwarp();
+          for (int j = 0; j < LOADS; ++j)
+            codes[j] = there ? *reinterpret_cast<const uint4*>(raw + slot * Sh::kBox + j * 512 + lane * 16) : make_uint4(0, 0, 0, 0);
+          __syncwarp();
+          fetch(n + BOXES, at);
+        };
+        for (int n = 0; n < BOXES; ++n) fetch(n, 0);
+        now.find_scales(pg, it.h);
+        int ev = 0;          // of the tile whose values are next
+        bool there = false;  // its step is
+        for (int i = -1; i < tiles; ++i) {
+          if (i >= 0) {
+            take(2 * i + 1, i / 32, there);
+            wait_empty(1, tile);
             store(1, tile, ev);
             ++tile;
           }
-          if (t + 1 >= t_hi) break;
-          // tile t + 1, which is number `tile` now
-          const int ek = scale_exponent(__reduce_max_sync(0xffffffffu, scale_k));
-          ev = scale_exponent(__reduce_max_sync(0xffffffffu, scale_v));
-          if (lane == 0) reinterpret_cast<uint16_t*>(s_bad)[(tile % kBadRing) * 8 + cw] = static_cast<uint16_t>(bads);
-#pragma unroll
-          for (int j = 0; j < LOADS; ++j) codes[j] = *reinterpret_cast<const uint4*>(raw + j * 512);  // (a lane's own copies)
-          const int64_t at = off;
-          const uint32_t rows = present;
-          place();
-          look_up(t + 3);
-          if (t + 2 < t_hi) copy(smem_addr(raw), 512, k_head, off, present);
+          const int k = i + 1;  // the tile whose keys are next, number `tile`
+          if (k >= tiles) break;
+          if (k > 0 && k % 32 == 0) {
+            now = next;
+            next = look_up(k / 32 + 1);
+          }
+          if (k % 32 == 16) next.find_scales(pg, it.h);
+          const int page = __shfl_sync(0xffffffffu, now.page, k % 32);
+          there = static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages);
+          take(2 * k, k / 32, there);
+          if (lane == 0) reinterpret_cast<uint16_t*>(s_bad)[(tile % kBadRing) * 8 + cw] = page >= pg.num_pages ? 0xffffu : 0u;
+          const int ek = scale_exponent(__shfl_sync(0xffffffffu, now.scale_k, k % 32));
+          ev = scale_exponent(__shfl_sync(0xffffffffu, now.scale_v, k % 32));
           wait_empty(0, tile);
           store(0, tile, ek);
-          wait_empty(1, tile);
-          copy(smem_addr(place_of(1, tile) + in_tile), RPI * 128, v_head, at, rows);
         }
+        boxes += 2 * tiles;
+        if (*gave_up && lane == 0)  // (what is still on its way lands first)
+          for (int n = max(0, boxes - BOXES); n < boxes; ++n) mbar_wait(full + n % BOXES, (n / BOXES) & 1);
       } else if constexpr (!FOUR) {
         // lane l of warp c brings slot 32 c + l of a tile; its page is looked up a tile ahead
         int page = 0, in_page = -1;  // slot of the page (-1: no query of the item sees it)
@@ -1298,7 +1308,10 @@ cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
   static_assert(Sh::kBytes <= 227 * 1024, "shared memory of a CTA");
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes); e != cudaSuccess)
     return e;
-  return launch_kernel(kernel, dim3(P.ctas), dim3(Sh::kThreads), Sh::kBytes, stream, 1, P);
+  typename Extra<BITS>::type extra{};
+  if constexpr (BITS == 8)
+    if (cudaError_t e = encode_maps(P.pages, false, &extra); e != cudaSuccess) return e;
+  return launch_kernel(kernel, dim3(P.ctas), dim3(Sh::kThreads), Sh::kBytes, stream, 1, P, extra);
 }
 
 template <typename T, int D, int BITS>
