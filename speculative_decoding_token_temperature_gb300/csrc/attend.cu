@@ -44,7 +44,10 @@ constexpr int kRows = 16;     // rows of a tile
 // 99 / 95; 32 rows 191 / 97.  64 values: 4 rows, B=4, 4000 slots 15.0 / 16.4; B=32, 8000 slots 67.8 / 68.3;
 // 4-bit pages 15.5 / 19.6 and 68.2 / 70.7; 16 rows, B=32, 8000 slots 68.8 / 68.4 and 72.3 / 70.6.
 constexpr int kWarpRows = 8;
-constexpr int kWarpRows8 = 32;  // over 8-bit pages
+// Over 8-bit pages (the warp-level kernel of attend8.cu, us here / there; 64 requests of up to 8190 slots, 8 key heads, heads of 128): 4 rows
+// 125 / 199, 8 rows 127 / 201, 12 rows 173 / 201, 16 rows 175 / 201, 24 rows 261 / 202, 32 rows 269 / 202; heads of 64: 16
+// rows 135 / 149, 32 rows 192 / 146; one request of 900 slots: 16 rows 17.8 / 18.2, 32 rows 21.1 / 19.6.  (24 and 32 rows here as a tile of 32.)
+constexpr int kWarpRows8 = 16;
 
 __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
@@ -654,7 +657,7 @@ cudaError_t launch_attend(AttendParams P, specdec_dtype dt, specdec_dtype format
   if (P.ctas > kMaxCtas) P.ctas = kMaxCtas;
   const bool items = P.pages.head_dim == 128 && static_cast<int64_t>(P.B) * P.pages.kv_heads >= P.ctas;
   const bool tc = hook == 0 ? (eight ? rows > kWarpRows8 : rows > kWarpRows || items) : hook == 2;
-  const int mr = tc ? std::max(attend_tc_rows(rows), eight ? 128 : 0) : eight ? attend8_rows(rows) : kRows;
+  const int mr = tc ? attend_tc_rows(rows) : eight ? attend8_rows(rows) : kRows;
   P.row_tiles = static_cast<int>((rows + mr - 1) / mr);
   // A row of CTAs for each key head, unless that leaves more than a sixteenth of the GPU out: a slot's heads
   // lie side by side, and are then read at about the same time (4-bit decode of 64 requests of 16000

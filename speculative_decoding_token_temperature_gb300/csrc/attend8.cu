@@ -1,4 +1,4 @@
-// Attention over 8-bit pages for a few rows to a key head (up to 32), on warp-level matrix instructions.
+// Attention over 8-bit pages for a few rows to a key head (up to 16), on warp-level matrix instructions.
 //
 // The formula, the items, the split of the work and the join are those of attend.cu.  Keys and values are
 // E4M3 codes, and the slots of a step of 16 lie in one block, so they share a scale 2^e for keys and one for values:
@@ -11,7 +11,7 @@
 // cost half of what 16 do.  Codes go from the copied tile straight into the instruction's registers: a key's row is read in the order
 // that makes a word the four codes of a step of the k index, two slots' words are interleaved by bytes for the product with V;
 // the weights are turned by the matrix transposition of registers.  So shared memory carries the codes once in and once
-// out, and a conversion serves all rows of the tile: 8, 16 or 32.
+// out, and a conversion serves all rows of the tile: 8 or 16.
 //
 // A row's reference m moves only when a score exceeds what it was set for by more than 2^8 (as in attend_tc.cuh; the
 // weights stay below 2^15): most steps then need no maximum across lanes and no rescaling.
@@ -29,22 +29,10 @@ namespace specdec {
 
 namespace {
 
-#ifndef W1
-#define W1 12
-#define S1 2
-#define G1 2
-#define W2 8
-#define S2 2
-#define G2 3
-#define W4 8
-#define S4 1
-#define G4 5
-#endif
 // RT tiles of 8 rows.  Warps, each with a stream of slots of its own; SUB steps of 16 slots as a warp takes them; stages.
 template <int D, int RT>
 struct Stage8 {
-  static constexpr int WARPS = RT == 1 ? W1 : RT == 2 ? W2 : W4, SUB = RT == 1 ? S1 : RT == 2 ? S2 : S4;
-  static constexpr int STAGES = RT == 1 ? G1 : RT == 2 ? G2 : G4, MR = 8 * RT;
+  static constexpr int WARPS = RT == 1 ? 12 : 8, SUB = 2, STAGES = RT == 1 ? 2 : 3, MR = 8 * RT;
   static constexpr int kBox = kStep * D, kBytes = 2 * SUB * kBox;  // keys, then values
   static constexpr int kStagesBytes = WARPS * STAGES * kBytes;
   static constexpr int kJoinBytes = WARPS * MR * (D * 4 + 8);  // the warps' rows, joined once per segment
@@ -135,7 +123,6 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
         uint32_t boxes = 0;
 #pragma unroll
         for (int u = 0; u < SUB; ++u) boxes += static_cast<unsigned>(page[u]) < static_cast<unsigned>(pg.num_pages) ? 2 : 0;
-        fence_proxy_async_smem();  // (what was read of the stage)
         mbar_expect_tx(full + stage, boxes * St::kBox);
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
@@ -146,7 +133,8 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
       }
       ++issued;
     };
-    __syncthreads();  // the last segment's rows are written: its shared memory is free
+    fence_proxy_async_smem();  // (the warps' rows that were written where boxes land now)
+    __syncthreads();           // the last segment's rows are written: its shared memory is free
     if (!late) {
       now = look_up(0);
       next = look_up(1);
@@ -213,11 +201,9 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
       for (int m = 0; m < MT; ++m)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[r][m][e] = 0.f;
-    uint2 qf[RT <= 2 ? RT * KT : 1];  // (up to two tiles: the fragments stay in registers)
-    if constexpr (RT <= 2) {
+    uint2 qf[RT * KT];
 #pragma unroll
-      for (int t = 0; t < RT * KT; ++t) qf[t] = s_q[t * 32];
-    }
+    for (int t = 0; t < RT * KT; ++t) qf[t] = s_q[t * 32];
     const int i0 = query_of(P, row0), i1 = min(query_of(P, row0 + rows - 1), S.nq - 1);
     const bool tree = P.tree_mask != nullptr;
     auto sees = [&](int r, int e, int s) {
@@ -285,7 +271,7 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
             e4m3x4_to_f16(wh[z], a.y, a.w);
 #pragma unroll
             for (int r = 0; r < RT; ++r) {
-              const uint2 q = RT <= 2 ? qf[RT <= 2 ? r * KT + 4 * y + z : 0] : s_q[(r * KT + 4 * y + z) * 32];
+              const uint2 q = qf[r * KT + 4 * y + z];
               mma<__half>(s[r], a, q.x, q.y);
             }
           }
@@ -476,7 +462,7 @@ cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
 
 template <typename T, int D>
 cudaError_t launch_rows(const AttendParams& P, int mr, cudaStream_t stream) {
-  return mr == 8 ? launch_shape<T, D, 1>(P, stream) : mr == 16 ? launch_shape<T, D, 2>(P, stream) : launch_shape<T, D, 4>(P, stream);
+  return mr == 8 ? launch_shape<T, D, 1>(P, stream) : launch_shape<T, D, 2>(P, stream);
 }
 template <typename T>
 cudaError_t launch_typed(const AttendParams& P, int mr, cudaStream_t stream) {
@@ -485,7 +471,7 @@ cudaError_t launch_typed(const AttendParams& P, int mr, cudaStream_t stream) {
 
 }  // namespace
 
-int attend8_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : 32; }
+int attend8_rows(int64_t rows) { return rows <= 8 ? 8 : 16; }
 
 cudaError_t launch_attend8(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream) {
   return dt == SPECDEC_BF16 ? launch_typed<__nv_bfloat16>(P, mr, stream) : launch_typed<__half>(P, mr, stream);

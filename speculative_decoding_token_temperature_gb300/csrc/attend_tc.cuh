@@ -51,7 +51,6 @@ namespace specdec {
 
 namespace tc {
 
-constexpr int kRowWarps = 16;
 constexpr int kTile = kUnit * kStep;  // 128 slots
 constexpr int kBadRing = 16;          // tiles whose out-of-range slots are remembered
 constexpr int kItems = 4;             // items the walk may be ahead
@@ -74,19 +73,23 @@ enum Rows { kQuad, kOne, kTwo };
 template <int D, Rows ROWS, int BITS>
 struct Shape {
   static constexpr bool FOUR = BITS == 4, EIGHT = BITS == 8;
-  static constexpr bool TWO = ROWS == kTwo, QUAD = ROWS == kQuad;
-  static constexpr int MR = QUAD ? 32 : TWO ? 256 : 128;
-  static constexpr int kCopyWarps = FOUR || EIGHT ? 8 : 4;
+  static constexpr bool TWO = ROWS == kTwo, QUAD = ROWS == kQuad && !EIGHT;
+  // 8-bit pages with at most 32 rows: one quarter of the lanes has them, and the warps of the others convert too
+  static constexpr bool FEW = ROWS == kQuad && EIGHT;
+  static constexpr int MR = ROWS == kQuad ? 32 : TWO ? 256 : 128;
+  static constexpr int kRowWarps = FEW ? 4 : 16;
+  static constexpr int kCopyWarps = FEW ? 16 : FOUR || EIGHT ? 8 : 4;
   static constexpr int kThreads = 32 * (kRowWarps + kCopyWarps + 4);
   // Who is who among the warps from 16 on.  16-bit pages: 16 .. 19 copy.  4-bit and 8-bit pages: 16 .. 23 convert, two
   // on each of an SM's four schedulers (warp % 4); with at most 32 rows, where a tile's copies are the
   // longer way, they keep off the scheduler of the two warps that copy.  (B=16, 16000 slots, D=128, us for
   // 32, 64 and 256 rows: 103, 120 and 266 two on each, 99, 127 and 279 on three schedulers.)
   static constexpr bool THREE = FOUR && QUAD;
-  static constexpr int kWalker = THREE ? 16 : 16 + kCopyWarps, kMma = 19 + kCopyWarps;
-  static constexpr int kQuery0 = THREE ? 20 : 17 + kCopyWarps, kQuery1 = THREE ? 24 : 18 + kCopyWarps;
+  static constexpr int kWalker = THREE ? 16 : kRowWarps + kCopyWarps, kMma = kWalker + (THREE ? 11 : 3);
+  static constexpr int kQuery0 = THREE ? 20 : kWalker + 1, kQuery1 = THREE ? 24 : kWalker + 2;
   __device__ static constexpr int copy_index(int warp) {
-    const int k = warp - kRowWarps;
+    const int k = warp - 16;
+    if (FEW) return k >= 4 ? -1 : k >= 0 ? 12 + k : warp % 4 == 0 ? -1 : warp / 4 * 3 + warp % 4 - 1;
     if (THREE) return k % 4 == 0 || k > 10 || k < 0 ? -1 : k / 4 * 3 + k % 4 - 1;  // 17, 18, 19, 21, 22, 23, 25, 26
     return k >= 0 && k < kCopyWarps ? k : -1;
   }
@@ -101,9 +104,14 @@ struct Shape {
   static constexpr int kOffV = kOffK + RK * kTileBytes;
   static constexpr int kOffMl = kOffV + RV * kTileBytes;      // [2][2][128] (m, l) of slots and halves
   static constexpr int kOffRaw = kOffMl + 4 * 128 * 8;
-  // 8-bit pages: boxes of a converting warp's 16 slots, keys' and values' in turn, ahead of their conversion
-  static constexpr int kBox = 16 * D, BOXES = 3;
-  static constexpr int kOffQScale = kOffRaw + (EIGHT ? kCopyWarps * BOXES * kBox : RAW * kRawBytes);  // [2][MR] scales of query rows (4-bit and 8-bit pages)
+  // 8-bit pages: boxes of a converting warp's 16 slots, keys' and values' in turn (FEW: a warp has the ones or the others),
+  // ahead of their conversion.  With at most 32 rows and heads of 128, 12 of them lie in the query tile behind its rows, which the
+  // products read for rows of scores that nobody reads.
+  static constexpr int kBox = 16 * D, BOXES = FEW && D == 128 ? 2 : 3, HOLES = FEW && D == 128 ? 12 : 0;
+  __device__ static constexpr int box_offset(int k) {
+    return k < HOLES ? k / 6 * (kTile * 128) + 32 * 128 + k % 6 * kBox : kOffRaw + (k - HOLES) * kBox;
+  }
+  static constexpr int kOffQScale = kOffRaw + (EIGHT ? (kCopyWarps * BOXES - HOLES) * kBox : RAW * kRawBytes);  // [2][MR] scales of query rows (4-bit and 8-bit pages)
   static constexpr int kOffSum = kOffQScale + (FOUR || EIGHT ? 2 * MR * 4 : 0);  // [4][4][32][8] accumulators on their way, [32] 1 / l
   static constexpr int kOffItem = kOffSum + (QUAD ? 4 * 4 * 32 * 8 * 4 + 32 * 4 : 0);
   static constexpr int kOffScan = kOffItem + kItems * sizeof(Item);
@@ -204,13 +212,16 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}" : "=r"(yes)::"memory");
   return yes != 0;
 }
-// Whether all row threads say yes (the barrier of all of them).
+// Whether all row threads say yes (the barrier of all of them), and the barrier alone.
+template <int THREADS>
 __device__ __forceinline__ bool rows_all(bool mine) {
   uint32_t all;
-  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.and.pred p, 1, 512, q;\nselp.u32 %0, 1, 0, p;\n}"
-               : "=r"(all) : "r"(mine ? 1u : 0u) : "memory");
+  asm volatile("{\n.reg .pred p, q;\nsetp.ne.u32 q, %1, 0;\nbarrier.cta.red.and.pred p, 1, %2, q;\nselp.u32 %0, 1, 0, p;\n}"
+               : "=r"(all) : "r"(mine ? 1u : 0u), "n"(THREADS) : "memory");
   return all != 0;
 }
+template <int THREADS>
+__device__ __forceinline__ void rows_sync() { asm volatile("bar.sync 1, %0;" ::"n"(THREADS) : "memory"); }
 // Whether either warp of a pair (64 threads) says yes.
 __device__ __forceinline__ bool pair_any(int barrier, bool mine) {
   uint32_t any;
@@ -256,7 +267,8 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
   constexpr bool BRAIN = BITS != 16 && !std::is_same<T, __half>::value;  // bf16 queries to be held in fp16
   using M = typename std::conditional<BITS != 16, __half, T>::type;  // the matrix instructions' type
   constexpr int MR = Sh::MR, RK = Sh::RK, RV = Sh::RV, KT = D / 16, THREADS = Sh::kThreads;
-  constexpr bool AHEAD = Sh::AHEAD, TWO = Sh::TWO, QUAD = Sh::QUAD;
+  constexpr bool AHEAD = Sh::AHEAD, TWO = Sh::TWO, QUAD = Sh::QUAD, FEW = Sh::FEW;
+  constexpr int ROW_THREADS = 32 * Sh::kRowWarps;
   extern __shared__ __align__(1024) char smem[];
   const Pages& pg = P.pages;
   const int tid = threadIdx.x, warp = tid / 32, lane = tid % 32;
@@ -284,23 +296,23 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
   if (tid == 0) {
     // copied tiles: every copy lane's copies have landed, and a warp's part of s_bad is written
     for (int r = 0; r < RK; ++r) {
-      mbar_init(k_full + r, FOUR || EIGHT ? Sh::kCopyWarps : kTile + Sh::kCopyWarps);
+      mbar_init(k_full + r, FOUR || EIGHT ? 8 : kTile + Sh::kCopyWarps);
       mbar_init(k_empty + r, 1);
     }
     for (int r = 0; r < RV; ++r) {
-      mbar_init(v_full + r, FOUR || EIGHT ? Sh::kCopyWarps : kTile);
+      mbar_init(v_full + r, FOUR || EIGHT ? 8 : kTile);
       mbar_init(v_empty + r, 1);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(s_full + s, 1);
-      mbar_init(p_full + s, kRowWarps / 2);
+      mbar_init(p_full + s, Sh::kRowWarps / 2);
       mbar_init(o_full + s, 1);
     }
     mbar_init(q_full, 64);
     mbar_init(q_empty, 1);
     for (int k = 0; k < kItems; ++k) {
       mbar_init(it_full + k, 1);
-      mbar_init(it_empty + k, kRowWarps + Sh::kCopyWarps + 1 + 2);
+      mbar_init(it_empty + k, Sh::kRowWarps + Sh::kCopyWarps + 1 + 2);
     }
     mbar_init(done, 1);
     for (int r = 0; r < Sh::RAW; ++r) {
@@ -415,31 +427,34 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
         // which left the copy's latency in every tile's way: 271 us for the tree of the figures above, 286 to 293 us for 64
         // requests of 8 tokens.)
         constexpr int CH = D / 16, RPI = 32 / CH, LOADS = 16 / RPI, BOXES = Sh::BOXES;  // 16-byte pieces of a row of codes, rows at a time
-        char* const raw = smem + Sh::kOffRaw + cw * BOXES * Sh::kBox;
+        const int step = cw % 8;  // (FEW: warps 0 .. 7 bring keys, 8 .. 15 values)
+        auto raw = [&](int slot) { return smem + Sh::box_offset(cw * BOXES + slot); };
         uint64_t* const full = raw_full + cw * BOXES;
         auto place_of = [&](int kv, int n) { return smem + (kv ? Sh::kOffV : Sh::kOffK) + n % (kv ? RV : RK) * Sh::kTileBytes; };
         auto wait_empty = [&](int kv, int n) {
           wait_for((kv ? v_empty : k_empty) + n % (kv ? RV : RK), ((n / (kv ? RV : RK)) & 1) ^ 1, gave_up);
           __syncwarp();
         };
-        uint4 codes[LOADS];
+        // A lane has two units of 8 codes in every RPI-th row, and their values are two 16-byte pieces of the tile's row.  With heads of
+        // 128 they are 8 apart, the later one first in odd rows; with heads of 64 they are neighbours.  (Neither the loads nor
+        // the stores meet bank conflicts.)
+        const int unit = lane % CH, odd_row = D == 128 ? lane / CH % 2 : 0;
+        const int unit0 = D == 128 ? unit + 8 * odd_row : 2 * unit, unit1 = D == 128 ? unit + 8 * (1 - odd_row) : 2 * unit + 1;
+        uint2 codes[LOADS][2];
         auto store = [&](int kv, int n, int e) {  // the codes' values to tile number n
           char* const dst = place_of(kv, n);
           const uint32_t s2 = power_f16x2(e);
 #pragma unroll
           for (int j = 0; j < LOADS; ++j) {
-            uint32_t f[8];
-            e4m3x4_to_f16(codes[j].x, f[0], f[1]);
-            e4m3x4_to_f16(codes[j].y, f[2], f[3]);
-            e4m3x4_to_f16(codes[j].z, f[4], f[5]);
-            e4m3x4_to_f16(codes[j].w, f[6], f[7]);
+            const int row = step * 16 + j * RPI + lane / CH;
 #pragma unroll
-            for (int x = 0; x < 8; ++x) f[x] = mul_f16x2(f[x], s2);
-            // (the lanes of a row's second half store their pieces the other way round: 8 lanes meet no bank conflict)
-            const int row = cw * 16 + j * RPI + lane / CH, piece = 2 * (lane % CH), turn = D == 128 ? lane % CH / 4 : 0;
-            const uint4 lo = make_uint4(f[0], f[1], f[2], f[3]), hi = make_uint4(f[4], f[5], f[6], f[7]);
-            *reinterpret_cast<uint4*>(dst + tile_offset(row, piece + turn)) = turn ? hi : lo;
-            *reinterpret_cast<uint4*>(dst + tile_offset(row, piece + 1 - turn)) = turn ? lo : hi;
+            for (int x = 0; x < 2; ++x) {
+              uint32_t f[4];
+              e4m3x4_to_f16(codes[j][x].x, f[0], f[1]);
+              e4m3x4_to_f16(codes[j][x].y, f[2], f[3]);
+              *reinterpret_cast<uint4*>(dst + tile_offset(row, x ? unit1 : unit0)) =
+                  make_uint4(mul_f16x2(f[0], s2), mul_f16x2(f[1], s2), mul_f16x2(f[2], s2), mul_f16x2(f[3], s2));
+            }
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -447,25 +462,27 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
         };
         auto look_up = [&](int look) {
           Look l;
-          const int t = t_lo + look * 32 + lane, s = R.slot(t * kUnit + cw);
+          const int t = t_lo + look * 32 + lane, s = R.slot(t * kUnit + step);
           l.find(pg, table, s, t < t_hi && s < it.end);
           return l;
         };
         const int tiles = t_hi - t_lo;
         Look now = look_up(0), next = look_up(1);
-        // The item's box n: tile n / 2's keys, then its values.  Number boxes + n of all; `at` is the look that `now` is.
+        // The item's box n: tile n / 2's keys, then its values (FEW: tile n's).  Number boxes + n of all; `at` is the look that
+        // `now` is.
+        constexpr int PER = FEW ? 1 : 2;
         auto fetch = [&](int n, int at) {
-          if (n >= 2 * tiles) return;
-          const int i = n / 2;
+          if (n >= PER * tiles) return;
+          const int i = n / PER;
           const int page = __shfl_sync(0xffffffffu, i / 32 == at ? now.page : next.page, i % 32);
           const int in_page = __shfl_sync(0xffffffffu, i / 32 == at ? now.in_page : next.in_page, i % 32);
           if (lane == 0) {
             const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages) && !*gave_up;
             const int slot = (boxes + n) % BOXES;
-            fence_proxy_async_smem();  // (what was read there)
             mbar_expect_tx(full + slot, there ? Sh::kBox : 0);
             if (there)
-              copy_box(smem_addr(raw + slot * Sh::kBox), n % 2 ? &extra.v : &extra.k, in_page, extra.heads ? it.h : 0, extra.pages ? page : 0, full + slot);
+              copy_box(smem_addr(raw(slot)), (FEW ? cw >= 8 : n % 2 != 0) ? &extra.v : &extra.k, in_page, extra.heads ? it.h : 0, extra.pages ? page : 0,
+                       full + slot);
           }
         };
         // box n's codes to registers (zeros for a step that is not there), and another box to its place
@@ -474,39 +491,61 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
           wait_for(full + slot, ((boxes + n) / BOXES) & 1, gave_up);
           __syncwarp();
 #pragma unroll
-          for (int j = 0; j < LOADS; ++j)
-            codes[j] = there ? *reinterpret_cast<const uint4*>(raw + slot * Sh::kBox + j * 512 + lane * 16) : make_uint4(0, 0, 0, 0);
-          __syncwarp();
+          for (int j = 0; j < LOADS; ++j) {
+            const char* const row = raw(slot) + (j * RPI + lane / CH) * D;
+            codes[j][0] = there ? *reinterpret_cast<const uint2*>(row + unit0 * 8) : make_uint2(0, 0);
+            codes[j][1] = there ? *reinterpret_cast<const uint2*>(row + unit1 * 8) : make_uint2(0, 0);
+          }
+          __syncwarp();  // (everybody has read the box)
           fetch(n + BOXES, at);
         };
         for (int n = 0; n < BOXES; ++n) fetch(n, 0);
         now.find_scales(pg, it.h);
-        int ev = 0;          // of the tile whose values are next
-        bool there = false;  // its step is
-        for (int i = -1; i < tiles; ++i) {
-          if (i >= 0) {
-            take(2 * i + 1, i / 32, there);
-            wait_empty(1, tile);
-            store(1, tile, ev);
-            ++tile;
-          }
-          const int k = i + 1;  // the tile whose keys are next, number `tile`
-          if (k >= tiles) break;
+        auto turn_to = [&](int k) {  // tile k is next
           if (k > 0 && k % 32 == 0) {
             now = next;
             next = look_up(k / 32 + 1);
           }
           if (k % 32 == 16) next.find_scales(pg, it.h);
-          const int page = __shfl_sync(0xffffffffu, now.page, k % 32);
-          there = static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages);
-          take(2 * k, k / 32, there);
-          if (lane == 0) reinterpret_cast<uint16_t*>(s_bad)[(tile % kBadRing) * 8 + cw] = page >= pg.num_pages ? 0xffffu : 0u;
-          const int ek = scale_exponent(__shfl_sync(0xffffffffu, now.scale_k, k % 32));
-          ev = scale_exponent(__shfl_sync(0xffffffffu, now.scale_v, k % 32));
-          wait_empty(0, tile);
-          store(0, tile, ek);
+        };
+        auto exponent = [&](int kv, int k) { return scale_exponent(__shfl_sync(0xffffffffu, kv ? now.scale_v : now.scale_k, k % 32)); };
+        auto remember_bad = [&](int page) {
+          if (lane == 0) reinterpret_cast<uint16_t*>(s_bad)[(tile % kBadRing) * 8 + step] = page >= pg.num_pages ? 0xffffu : 0u;
+        };
+        if constexpr (FEW) {
+          const int kv = cw / 8;
+          for (int i = 0; i < tiles; ++i, ++tile) {
+            turn_to(i);
+            const int page = __shfl_sync(0xffffffffu, now.page, i % 32), e = exponent(kv, i);
+            take(i, i / 32, static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages));
+            if (kv == 0) remember_bad(page);
+            wait_empty(kv, tile);
+            store(kv, tile, e);
+          }
+        } else {
+          int ev = 0;          // of the tile whose values are next
+          bool there = false;  // its step is
+          for (int i = -1; i < tiles; ++i) {
+            if (i >= 0) {
+              take(2 * i + 1, i / 32, there);
+              wait_empty(1, tile);
+              store(1, tile, ev);
+              ++tile;
+            }
+            const int k = i + 1;  // the tile whose keys are next, number `tile`
+            if (k >= tiles) break;
+            turn_to(k);
+            const int page = __shfl_sync(0xffffffffu, now.page, k % 32);
+            there = static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages);
+            take(2 * k, k / 32, there);
+            remember_bad(page);
+            const int ek = exponent(0, k);
+            ev = exponent(1, k);
+            wait_empty(0, tile);
+            store(0, tile, ek);
+          }
         }
-        boxes += 2 * tiles;
+        boxes += PER * tiles;
         if (*gave_up && lane == 0)  // (what is still on its way lands first)
           for (int n = max(0, boxes - BOXES); n < boxes; ++n) mbar_wait(full + n % BOXES, (n / BOXES) & 1);
       } else if constexpr (!FOUR) {
@@ -859,7 +898,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
     int tile_base = 0;  // tiles of earlier items
     for (int n = 0;; ++n) {
       // (all row threads are also done with the last item's accumulators and (m, l) here)
-      if (!rows_all(wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up))) break;
+      if (!rows_all<ROW_THREADS>(wait_for(it_full + n % kItems, (n / kItems) & 1, gave_up))) break;
       const volatile Item& it = items[n % kItems];
       const int row0 = it.row0 + (TWO ? slot * 128 : 0), rows = min(128, it.rows - (TWO ? slot * 128 : 0));  // may be <= 0
       const int tiles = it.tiles, t_lo = it.t_lo, first = it.first, end = it.end;
@@ -1046,7 +1085,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
           constexpr uint32_t em = std::is_same<M, __half>::value ? 0x7c00u : 0x7f80u;
           bool found = false;
 #pragma unroll 4
-          for (int f = (warp % 8) * 32 + lane; f < kTile * (D / 8); f += 256) {
+          for (int f = (FEW ? half : warp % 8) * 32 + lane; f < kTile * (D / 8); f += ROW_THREADS / 2) {
             uint4* const at = reinterpret_cast<uint4*>(vt + f * 16);
             uint32_t x[4] = {at->x, at->y, at->z, at->w};
             const uint32_t top2 = __vmaxu2(__vmaxu2(x[0] & 0x7fff7fffu, x[1] & 0x7fff7fffu), __vmaxu2(x[2] & 0x7fff7fffu, x[3] & 0x7fff7fffu));
@@ -1085,7 +1124,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
       if constexpr (TWO)
         asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
       else
-        asm volatile("bar.sync 1, 512;" ::: "memory");
+        rows_sync<ROW_THREADS>();
       fence_after();
       const bool whole_item = it.begins && it.ends;
       const int64_t token = static_cast<int64_t>(it.b) * P.n;
@@ -1195,7 +1234,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
               *reinterpret_cast<float4*>(to + ((piece + 1) ^ (lane & turn)) * 4) = make_float4(acc[8 * u + 4], acc[8 * u + 5], acc[8 * u + 6], acc[8 * u + 7]);
             }
             if ((d + 8 * u + 8) % per != 0) continue;
-            asm volatile("bar.sync 1, 512;" ::: "memory");
+            rows_sync<ROW_THREADS>();
             float2 v = make_float2(0.f, 0.f);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -1213,7 +1252,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
                 *reinterpret_cast<float2*>(P.part_o + (part0 + sum_row) * D + column) = v;
               }
             }
-            asm volatile("bar.sync 1, 512;" ::: "memory");
+            rows_sync<ROW_THREADS>();
           }
         }
       } else {
@@ -1316,9 +1355,9 @@ cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
 
 template <typename T, int D, int BITS>
 cudaError_t launch_rows(const AttendParams& P, int mr, cudaStream_t stream) {
-  if constexpr (BITS != 8)  // (up to 32 rows over 8-bit pages are the warp-level kernel's)
-    if (mr == 32) return launch_shape<T, D, kQuad, BITS>(P, stream);
-  return mr == 128 ? launch_shape<T, D, kOne, BITS>(P, stream) : launch_shape<T, D, kTwo, BITS>(P, stream);
+  return mr == 32    ? launch_shape<T, D, kQuad, BITS>(P, stream)
+         : mr == 128 ? launch_shape<T, D, kOne, BITS>(P, stream)
+                     : launch_shape<T, D, kTwo, BITS>(P, stream);
 }
 
 template <typename T, int BITS>

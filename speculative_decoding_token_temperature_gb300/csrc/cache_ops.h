@@ -79,7 +79,7 @@ struct AttendParams {
   float* part_o;     // workspace [ctas, 2, rows, D]: its unnormalised output
   Pages pages;
 };
-// The tensor-memory kernel: the rows of its tile (128 or 256 over 8-bit pages), and its launches for 16-bit, 4-bit and 8-bit pages.
+// The tensor-memory kernel: the rows of its tile, and its launches for 16-bit, 4-bit and 8-bit pages.
 int attend_tc_rows(int64_t rows);
 cudaError_t launch_attend_tc(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream);
 cudaError_t launch_attend_tc4(const AttendParams& P, specdec_dtype dt, int mr, cudaStream_t stream);
