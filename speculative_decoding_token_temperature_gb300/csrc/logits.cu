@@ -101,10 +101,12 @@ __global__ void __launch_bounds__(kThreads) process_kernel(const ProcessParams P
     const uint32_t below = first >= 0 ? kAll : kAll & (kAll << -first), over = size - first >= N ? kAll : size > first ? (1u << (size - first)) - 1 : 0u;
     return below & over;
   };
+  // (the first in the low byte, the second in the next)
   auto look = [&](int r) -> uint32_t {
     if (r >= r1) return 0u;
     const int off = past(from(r));
-    uint32_t some = mine(off);
+    const uint32_t there = mine(off);
+    uint32_t some = there;
     if constexpr (MASKED) {
       if (some == 0) return 0u;
       const uint8_t* const m = reinterpret_cast<const uint8_t*>(P.mask + (row0 + r) * P.words);
@@ -117,13 +119,14 @@ __global__ void __launch_bounds__(kThreads) process_kernel(const ProcessParams P
         some &= first >= 0 ? w >> (first % 8) : w << -first;
       }
     }
-    return some;
+    return there | some << 8;
   };
-  uint32_t allowed[kStages][kBatch];  // of the batches in flight
+  uint32_t looked[kStages][kBatch];  // of the batches in flight
   auto issue = [&](int r, int stage) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      if (allowed[stage][k] == 0) continue;
+      const uint32_t allowed = looked[stage][k] >> 8;
+      if (allowed == 0) continue;
       const T* const row = from(r + k);
       const T* const at = row - past(row) + tid * N;
       T* const dst = s_rows[stage][k] + tid * N;
@@ -132,7 +135,7 @@ __global__ void __launch_bounds__(kThreads) process_kernel(const ProcessParams P
       } else {  // a word that reaches past the logits' ends
 #pragma unroll
         for (int e = 0; e < N; ++e)
-          if (allowed[stage][k] >> e & 1u) dst[e] = at[e];
+          if (allowed >> e & 1u) dst[e] = at[e];
       }
     }
     copy_commit();
@@ -143,7 +146,7 @@ __global__ void __launch_bounds__(kThreads) process_kernel(const ProcessParams P
 #pragma unroll
     for (int s = 0; s < kStages; ++s)
 #pragma unroll
-      for (int k = 0; k < kBatch; ++k) allowed[s][k] = look(r0 + s * kBatch + k);
+      for (int k = 0; k < kBatch; ++k) looked[s][k] = look(r0 + s * kBatch + k);
 #pragma unroll
     for (int s = 0; s < kStages; ++s) issue(r0 + s * kBatch, s);
   }
@@ -290,12 +293,12 @@ __global__ void __launch_bounds__(kThreads) process_kernel(const ProcessParams P
       const T* const words = s_rows[stage][k];
       const int off = past(from(r + k));
       T* const dst = to(r + k);
-      uint32_t keep = 0;
+      uint32_t bits = 0;
 #pragma unroll
       for (int s = 0; s < kStages; ++s)
-        if (s == stage) keep = allowed[s][k];
+        if (s == stage) bits = looked[s][k];
       if (P.alike) {
-        const uint32_t there = mine(off);
+        const uint32_t there = bits & kAll, keep = bits >> 8;
         if (there == 0) continue;
         const uint4 in = *reinterpret_cast<const uint4*>(words + tid * N);
         uint32_t w[4] = {in.x, in.y, in.z, in.w};
@@ -324,7 +327,7 @@ __global__ void __launch_bounds__(kThreads) process_kernel(const ProcessParams P
     for (int s = 0; s < kStages; ++s)
       if (s == stage) {
 #pragma unroll
-        for (int k = 0; k < kBatch; ++k) allowed[s][k] = look(r + kStages * kBatch + k);
+        for (int k = 0; k < kBatch; ++k) looked[s][k] = look(r + kStages * kBatch + k);
         issue(r + kStages * kBatch, s);
       }
     stage = stage + 1 == kStages ? 0 : stage + 1;
@@ -364,32 +367,43 @@ __global__ void __launch_bounds__(kThreads) count_kernel(const CountParams P) {
 
 // A sequence's table from nothing: a CTA counts the tokens of its chunk of the vocabulary in shared memory and writes the
 // chunk whole.  grid (chunks, B)
-constexpr int kCountChunk = 8192, kCountThreads = 512;
+// (64 prompts of 4095 tokens, V=128256, us: 12.5; 512 threads 12.4, 1024 16.3; chunks of 4096 13.7, of 16384 12.4.)
+constexpr int kCountChunk = 8192, kCountThreads = 256;
 
 __global__ void __launch_bounds__(kCountThreads) recount_kernel(const CountParams P) {
   __shared__ __align__(16) int s_count[kCountChunk];
   const int b = blockIdx.y, n = tokens_of(P, b), lo = blockIdx.x * kCountChunk, tid = threadIdx.x;
   const int32_t* const tokens = P.tokens + b * P.token_stride;
+  // Whole words of four tokens, and what is before and behind them.  (The first words are on their way before the number of
+  // tokens is there: P.n are.)
+  constexpr int kFirst = 4;
+  const int head = min(P.n, static_cast<int>((16 - reinterpret_cast<uintptr_t>(tokens) % 16) % 16 / 4)), words = (P.n - head) / 4, rest = head + 4 * words;
+  int4 first[kFirst];
+#pragma unroll
+  for (int u = 0; u < kFirst; ++u) {
+    const int k = tid + u * kCountThreads;
+    first[u] = k < words ? __ldg(reinterpret_cast<const int4*>(tokens + head) + k) : make_int4(-1, -1, -1, -1);
+  }
+  const int single = tid < head ? tid : tid >= 32 && rest + tid - 32 < P.n ? rest + tid - 32 : -1;
+  const int one = single >= 0 ? __ldg(tokens + single) : -1;
 #pragma unroll
   for (int k = 0; k < kCountChunk / 4 / kCountThreads; ++k) reinterpret_cast<int4*>(s_count)[tid + k * kCountThreads] = make_int4(0, 0, 0, 0);
   __syncthreads();
-  auto take = [&](int t) {
-    if (t < lo || t >= P.V || t - lo >= kCountChunk) return;
+  auto take = [&](int k, int t) {  // token number k
+    if (k >= n || t < lo || t >= P.V || t - lo >= kCountChunk) return;
     if (P.prompt) s_count[t - lo] = kSign;
     else atomicAdd(&s_count[t - lo], 1);
   };
-  // (whole words of four tokens, and what is before and behind them)
-  const int head = min(n, static_cast<int>((16 - reinterpret_cast<uintptr_t>(tokens) % 16) % 16 / 4)), words = (n - head) / 4;
-  if (tid < head) take(__ldg(tokens + tid));
-  if (head + 4 * words + tid < n) take(__ldg(tokens + head + 4 * words + tid));
-#pragma unroll 4
-  for (int k = tid; k < words; k += kCountThreads) {
-    const int4 t = __ldg(reinterpret_cast<const int4*>(tokens + head) + k);
-    take(t.x);
-    take(t.y);
-    take(t.z);
-    take(t.w);
-  }
+  auto take4 = [&](int k, const int4& t) {
+    take(head + 4 * k, t.x);
+    take(head + 4 * k + 1, t.y);
+    take(head + 4 * k + 2, t.z);
+    take(head + 4 * k + 3, t.w);
+  };
+  if (single >= 0) take(single, one);
+#pragma unroll
+  for (int u = 0; u < kFirst; ++u) take4(tid + u * kCountThreads, first[u]);
+  for (int k = tid + kFirst * kCountThreads; k < words; k += kCountThreads) take4(k, __ldg(reinterpret_cast<const int4*>(tokens + head) + k));
   __syncthreads();
   int* const out = P.counts + static_cast<int64_t>(b) * P.V + lo;
   const int columns = min(kCountChunk, P.V - lo);
