@@ -419,8 +419,11 @@ template <typename T, bool ALIGNED, bool MASKED>
 cudaError_t process_shape(ProcessParams P, cudaStream_t stream) {
   constexpr int CHUNK = kChunk<T, ALIGNED>;
   const int64_t chunks = (static_cast<int64_t>(P.V) + CHUNK - 1) / CHUNK;
-  const int64_t want = 8 * device_sm_count(), have = chunks * P.B;  // CTAs: all SMs full once
-  const int groups = static_cast<int>(std::min<int64_t>(P.rows, std::max<int64_t>(1, (want + have - 1) / have)));
+  // Rows are split over CTAs until there are eight for an SM, four rows at least for each, as a chunk's list is made by every one.  (CTAs for an
+  // SM, us: 32 x 65 rows of 32001 under masks 4: 118, 8: 106, 12: 103, 30: 106; 16 x 8 rows of 128256 4: 21.5, 8: 23.1, 16:
+  // 26.6; 2 x 8 rows in fp32 4: 8.8, 8: 10.5, 12: 14.6.)
+  const int64_t want = 8 * device_sm_count(), have = chunks * P.B;
+  const int groups = static_cast<int>(std::min<int64_t>(std::max(1, P.rows / 4), (want + have - 1) / have));
   P.group = (P.rows + groups - 1) / groups;
   const size_t smem = P.tokens ? static_cast<size_t>(P.rows - 1) * 2 * sizeof(int) : 0;
   auto kernel = process_kernel<T, ALIGNED, MASKED>;
