@@ -387,7 +387,8 @@ int specdec_compact_kv(void* cache, int64_t row_bytes, int64_t slot_stride, int6
  *     head, a power of two between 2^-15 and 2^7 held as its E8M0 byte (the exponent plus 127): k_scales /
  *     v_scales hold it at page * scale_page_stride + (s % page_size / scale_block) * scale_slot_stride +
  *     head * scale_head_stride (bytes, any).  A value is code * scale * k_scale (v_scale); before k_scale it is exact
- *     in fp16.  page_size is a multiple of scale_block, that a multiple of 16.  specdec_compact_kv does not
+ *     in fp16.  page_size is a multiple of scale_block, that a multiple of 16; the pages' strides are below 2^40, that of
+ *     slots positive; k_scale and v_scale have finite reciprocals.  specdec_compact_kv does not
  *     know the scales: after a tree's round the accepted tokens are appended again at their slots.
  * Pointers and strides are multiples of 16 bytes (4-bit pages' scales: of head_dim / 16 bytes); head_dim is
  * 64 or 128; max_pages * page_size < 2^31 - 256.
@@ -532,7 +533,8 @@ int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype,
  * Computed in fp32 and rounded once.  A masked token is -inf whatever its logit holds (NaN too); a row whose mask leaves nothing
  * is all -inf, which the verification calls report (SPECDEC_STATUS_EMPTY_ROW).
  *
- * logits       [B, rows, V] of dtype (SPECDEC_F32 or SPECDEC_BF16); out the same, or logits itself: in place
+ * logits       [B, rows, V] of dtype (SPECDEC_F32 or SPECDEC_BF16); out the same, or logits itself: in place (one that overlaps
+ *              it otherwise is refused)
  * tokens       [B, rows - 1] int32: drafts or node tokens; may be NULL (then they do not count, whatever rows is)
  * parents      [rows - 1] int32, parent in [-1, i): a tree; NULL: a chain
  * gammas       [B] int32 in [0, rows - 1], optional, chains only: the drafts that specdec_verify_chain_varlen verifies;

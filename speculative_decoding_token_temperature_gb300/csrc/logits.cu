@@ -257,9 +257,10 @@ __global__ void __launch_bounds__(kThreads) process_kernel(const ProcessParams P
         if (drafted)  // (ends, whatever the parents)
           for (int d = r + i - 1; d >= 0; d = P.parents ? min(s_parent[d], d - 1) : d - 1) n += s_draft[d] == lo + t;
         T* const e = x(i) + t;
-        float v = E::get(*e);
-        if (c != 0 || n > 0) v = pen.repeated(v);
-        *e = E::put(v + pen.added((c & 0x7fffffff) + n, bias));
+        const float v = E::get(*e), add = pen.added((c & 0x7fffffff) + n, bias);
+        const bool repeated = c != 0 || n > 0;
+        // (as a token that is counted is computed, bit for bit: a history's result does not depend on where its tokens stand)
+        *e = E::put(usual || !repeated ? fmaf(v, !repeated ? 1.f : v > 0.f ? inverse : pen.repetition, add) : pen.repeated(v) + add);
       }
     } else {
       const float add = __int_as_float(s_value[t]);

@@ -974,6 +974,9 @@ int specdec_process_logits(const void* logits, specdec_dtype dtype, const int32_
   if (!aligned_to(logits, es) || !aligned_to(out, es) || !aligned_to(mask, 4)) return fail(SPECDEC_ERR_UNSUPPORTED, "logits, out or mask is not aligned to its elements");
   if (B > 65535 || rows > kMaxProcessRows || num_bias >= (1 << 24) || V >= INT32_MAX - 65536)
     return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, more than 8192 rows, 2^24 biases, or a vocabulary above 2^31 - 65536");
+  const uintptr_t from = reinterpret_cast<uintptr_t>(logits), to = reinterpret_cast<uintptr_t>(out);
+  if (from != to && (from > to ? from - to : to - from) < static_cast<uintptr_t>(B) * rows * V * es)
+    return fail(SPECDEC_ERR_INVALID_ARG, "out must be logits itself or lie apart from it");
   ProcessParams P{};
   P.logits = logits;
   P.tokens = rows > 1 ? tokens : nullptr;

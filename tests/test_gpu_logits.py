@@ -316,3 +316,37 @@ def test_streams_and_graphs(sd, V):
     torch.cuda.synchronize()
     assert not out["status"].any() and int(table.sum()) == 3 * 4 * 3
     _check(out["logits"], {**x, "counts": table})
+
+
+def test_outputs_that_overlap_the_logits_raise(sd):
+    buf = torch.zeros(2 * 3 * 100 + 8, device=DEV)
+    with pytest.raises(RuntimeError):
+        sd.process_logits(buf[:600].view(2, 3, 100), out=buf[8:].view(2, 3, 100))
+
+
+def test_many_rows_past_32_bits(sd):
+    """The most rows, over more than 2^31 logits: each equals the row of a call of its own, whose counts hold the drafts."""
+    B, rows, V = 2, 8192, 140001
+    g = torch.Generator(device=DEV).manual_seed(1)
+    x = torch.randn(B, rows, V, generator=g, device=DEV, dtype=BF16)
+    t = torch.randint(0, V, (B, rows - 1), generator=g, device=DEV, dtype=torch.int32)
+    t[:, ::5], t[:, -1] = 7, V - 1
+    kw = dict(repetition=torch.tensor([1.5, 0.75], device=DEV), presence=torch.tensor([0.5, -1.0], device=DEV),
+              frequency=torch.tensor([0.25, 0.125], device=DEV))
+    r = sd.process_logits(x, tokens=t, **kw)
+    assert not r["status"].any()
+    for i in (0, 1, 2, 4096, rows - 2, rows - 1):
+        counts = torch.zeros(B, V, dtype=torch.int32, device=DEV)
+        for b in range(B):
+            counts[b] = torch.bincount(t[b, :i].long(), minlength=V)[:V].int()
+        assert torch.equal(sd.process_logits(x[:, i:i + 1].contiguous(), counts=counts, **kw)["logits"], r["logits"][:, i:i + 1]), i
+
+
+@pytest.mark.parametrize("reset", [False, True])
+def test_counts_past_32_bits(sd, reset):
+    B, V = 17000, 128256
+    counts = torch.full((B, V), 3 if reset else 0, dtype=torch.int32, device=DEV)
+    t = torch.tensor([5, V - 1, 5], dtype=torch.int32, device=DEV).expand(B, 3)
+    assert not sd.count_tokens(counts, t, reset=reset)["status"].any()
+    assert (counts[:, 5] == 2).all() and (counts[:, V - 1] == 1).all()
+    assert int(counts.sum(dtype=torch.int64)) == 3 * B

@@ -40,6 +40,15 @@ def test_process_refuses_mixed_and_misaligned(sd):
     assert _process(sd, a, mask=a + 2) == 2
 
 
+@pytest.mark.parametrize("shift", [-600, -4, 4, 300, 596])
+def test_process_refuses_outputs_that_overlap_the_logits(sd, shift):
+    a, keep = _fake()  # 3 rows of 100 bfloat16: 600 bytes
+    assert _process(sd, a, out=a + shift, B=0) == 1
+    if abs(shift) < 600:
+        assert _process(sd, a, out=a + shift) == 1
+        assert "lie apart" in sd.load_library().specdec_last_error().decode()
+
+
 @pytest.mark.parametrize("change,code", [(dict(counts=None), 1), (dict(tokens=None), 1), (dict(B=0), 1), (dict(n=-1), 1), (dict(V=0), 1), (dict(stride=-1), 1),
                                          (dict(B=70000), 2), (dict(V=2 ** 31 - 65536), 2), (dict(n=2 ** 31 - 65536), 2)])
 def test_count_refuses_bad_arguments(sd, change, code):
