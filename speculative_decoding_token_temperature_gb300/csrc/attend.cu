@@ -1,4 +1,4 @@
-// Attention of a round's query tokens over a paged cache, in 16 or in 4 bits.
+// Attention of a round's query tokens over a paged cache, in 16, 8 or 4 bits.
 //
 //   out_i = sum_j p_ij v_j,  p_ij = 2^(s_ij - m) / sum_j 2^(s_ij - m),  s_ij = c q_i.k_j
 // over the slots j that query i sees, c = scale * log2(e).  One pass over the keys keeps a
@@ -16,7 +16,7 @@
 // border leaves parts in the workspace, which a second kernel, started while the first one runs, joins in
 // a fixed order: the result depends on the number of CTAs only.
 //
-// Two kernels do the first part.  The one here is for a few rows (kWarpRows): m16n8k16 matrix
+// Two kernels do the first part (over 8-bit pages the first of them is attend8.cu's).  The one here is for a few rows (kWarpRows): m16n8k16 matrix
 // instructions, each of 8 warps with a stream of slots of its own (every 8th step of a segment) and all
 // 16 rows of the tile, copied ahead with 16-byte asynchronous copies three stages deep; no barrier
 // until the warps join their rows through shared memory, once per segment.  It comes up faster than

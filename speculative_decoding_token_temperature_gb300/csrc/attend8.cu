@@ -16,6 +16,10 @@
 // A row's reference m moves only when a score exceeds what it was set for by more than 2^8 (as in attend_tc.cuh; the
 // weights stay below 2^15): most steps then need no maximum across lanes and no rescaling.
 //
+// One token of 96 requests over up to 16001 slots (8 rows to a key head): 310 us, 6.3 TB/s, 0.93 of the measured copy rate: HBM
+// bounds it.  64 requests of 2 tokens over up to 8190 slots (8 rows) 127 us, 0.79; of 4 tokens (16 rows) 175 us, 0.57: two row
+// tiles leave registers for two warps to a scheduler only.
+//
 // A step's 16 rows are a box of the pages' tensor (values, slots, heads, pages), which one TMA instruction brings, swizzled so that
 // the reads meet no bank conflicts; a warp looks up 32 steps at a time, a lane each.  (16-byte asynchronous copies by all
 // lanes, with a lookup for every step: 288 us for 64 requests of 8 tokens over up to 8190 slots, 485 us for one token of 96
@@ -29,6 +33,8 @@ namespace specdec {
 
 namespace {
 
+// (Warps, steps, stages for 8 rows, us for the 96 requests above: 12, 2, 2: 312; 16, 1, 3: 332; 12, 1, 4: 340; 8, 2, 3: 359.  For 16
+// rows, 64 requests: 8, 2, 3: 175; 8, 1, 5: 185; 12, 1, 4: 202; 10, 1, 5: 223.)
 // RT tiles of 8 rows.  Warps, each with a stream of slots of its own; SUB steps of 16 slots as a warp takes them; stages.
 template <int D, int RT>
 struct Stage8 {
@@ -123,6 +129,7 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
         uint32_t boxes = 0;
 #pragma unroll
         for (int u = 0; u < SUB; ++u) boxes += static_cast<unsigned>(page[u]) < static_cast<unsigned>(pg.num_pages) ? 2 : 0;
+        fence_proxy_async_smem();  // (the warp's reads of the stage, which its vote ordered before this)
         mbar_expect_tx(full + stage, boxes * St::kBox);
 #pragma unroll
         for (int u = 0; u < SUB; ++u)

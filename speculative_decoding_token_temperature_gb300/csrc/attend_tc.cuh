@@ -16,10 +16,11 @@
 // unrounded weights, in fp32.  Two threads hold a row, 64 columns each: the chain scores -> weights -> products of a
 // slot is what bounds a short tile, and this halves its longest link.
 //
-// Warps 0-15: rows (slot = warp / 8, columns = warp / 4 % 2, lanes = warp % 4).  Then the warps that
+// Warps 0-15: rows (slot = warp / 8, columns = warp / 4 % 2, lanes = warp % 4; over 8-bit pages with at most 32 rows, which lie
+// in one quarter of the lanes, those of that quarter alone, and the others convert too).  Then the warps that
 // bring K and V: of 16-bit pages, 4 that copy rows asynchronously, 16 bytes at a time; of 4-bit
-// pages, 8 that turn copied codes into their fp16 values (exact: at most 6 significant bits); of 8-bit pages, 8 that fetch codes a
-// tile ahead and store their fp16 values (exact: 4 significant bits).
+// pages, 8 that turn copied codes into their fp16 values (exact: at most 6 significant bits); of 8-bit pages, 8
+// (16) that copy boxes of codes ahead and store their fp16 values (exact: 4 significant bits).
 // Either way the tiles are 128-byte-swizzled and gathered row by row, so pages may have any size
 // and stride.  One warp issues the matrix instructions, one walks the items ahead of everybody, and
 // two bring query rows and, of 4-bit pages, the codes and scales.  The roles meet at mbarriers; every
@@ -40,6 +41,10 @@
 //    cache's bytes.  A tile takes about 2400 clocks: its codes' conversion 790 at 64 lanes a clock, but
 //    with the copies in and the stores of the values (shared memory is busy for about 1500) the converting
 //    warps need 2000.
+//  - 64 requests, 8 tokens, up to 8190 slots in 8 bits (32 rows): 199 us, 3.4 TB/s, 0.50 of the measured copy rate.  With
+//    clock counters in it, at 202 us, a tile took about 2800 clocks and the warps that convert keys, which hold
+//    everybody up, 2300 of them (480 read, 770 store and fence, the rest the way from box to box); those for values waited 1100.
+//    By count, not measured, shared memory is busy for about 1800.  The trees of 64 nodes in 8 bits: 276 us, 204 in 16 bits.
 //  - 35 rows, a window of 1024 slots, 96 requests: 60 us, 3.5 TB/s: an item is 9 tiles, and its first,
 //    partial tile, the way out of its rows and the next one's queries cost about 4 more.
 #pragma once
@@ -67,7 +72,7 @@ struct Item {
   int clean_lo, clean_hi;        // tiles that every row of the item sees whole: others' values are scanned
 };
 
-// Row tiles: 32 rows, each in the four quarters of tensor memory's lanes, or 128, or two of 128.
+// Row tiles: 32 rows, each in the four quarters of tensor memory's lanes (over 8-bit pages in one), or 128, or two of 128.
 enum Rows { kQuad, kOne, kTwo };
 
 template <int D, Rows ROWS, int BITS>
@@ -479,6 +484,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
           if (lane == 0) {
             const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages) && !*gave_up;
             const int slot = (boxes + n) % BOXES;
+            fence_proxy_async_smem();  // (the warp's reads, which its barrier ordered before this)
             mbar_expect_tx(full + slot, there ? Sh::kBox : 0);
             if (there)
               copy_box(smem_addr(raw(slot)), (FEW ? cw >= 8 : n % 2 != 0) ? &extra.v : &extra.k, in_page, extra.heads ? it.h : 0, extra.pages ? page : 0,

@@ -434,6 +434,21 @@ def test_bad_pages_reach_the_rows_that_see_them(sd, kernel):
     assert torch.isfinite(r["out"][1]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [1, 3, 8, 40])
+def test_a_pool_of_one_page_and_heads_at_one_place(sd, kernel, D, n):
+    """Dimensions whose stride does not count, and one whose stride is zero: shared keys and values, or scales."""
+    c = Cache(1, 100, 112, 16, 4, D, seed=n)
+    p = int(c.host_table[0, 0])
+    c.k, c.v, c.ks, c.vs = (t[p:p + 1] for t in (c.k, c.v, c.ks, c.vs))
+    c.N, c.host_table, c.table = 1, torch.zeros(1, 1, dtype=torch.int32), torch.zeros(1, 1, dtype=torch.int32, device=DEV)
+    c.kw.update(k_scales=c.ks, v_scales=c.vs)
+    base._run(sd, c, base._q(1, n, 8, D, BF16), [100], BF16, D, what="one page", scale=0.05)
+    c.k, c.v, c.ks, c.vs = (t[:, :, 1:2].expand(t.shape) for t in (c.k, c.v, c.ks, c.vs))
+    c.kw.update(k_scales=c.ks, v_scales=c.vs)
+    base._run(sd, c, base._q(1, n, 8, D, BF16), [100], BF16, D, what="one head", scale=0.05)
+
+
 # ---- streams, graphs, repetition ------------------------------------------------------------
 
 @pytest.mark.parametrize("n", [1, 6, 40])
