@@ -463,7 +463,7 @@ cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, St::kSmem); e != cudaSuccess)
     return e;
   Maps maps;
-  if (cudaError_t e = encode_maps(P.pages, true, &maps); e != cudaSuccess) return e;
+  if (cudaError_t e = encode_maps(P.pages, true, true, &maps); e != cudaSuccess) return e;
   return launch_kernel(kernel, dim3(P.ctas), dim3(32 * St::WARPS), St::kSmem, stream, 1, P, maps);
 }
 

@@ -75,11 +75,15 @@ struct Item {
 // Row tiles: 32 rows, each in the four quarters of tensor memory's lanes (over 8-bit pages in one), or 128, or two of 128.
 enum Rows { kQuad, kOne, kTwo };
 
-template <int D, Rows ROWS, int BITS>
+// PIECES: of E4M3 codes that a query's values are held in (FEW)
+template <int D, Rows ROWS, int BITS, int PIECES>
 struct Shape {
   static constexpr bool FOUR = BITS == 4, EIGHT = BITS == 8;
   static constexpr bool TWO = ROWS == kTwo, QUAD = ROWS == kQuad && !EIGHT;
-  // 8-bit pages with at most 32 rows: one quarter of the lanes has them, and the warps of the others convert too
+  // 8-bit pages with at most 32 rows: one quarter of the lanes has them, and the warps of the others convert too.  Keys are not
+  // converted: the scores are products of codes, the queries' in pieces.  (64 requests of 8 tokens: 173 us, 199 with the keys
+  // converted.  With more rows the pieces' products cost more than that saves: 202 against 183 us for 128 rows, 279 against 271
+  // for 256, in fp16, whose pieces are three, 352 against 217.)
   static constexpr bool FEW = ROWS == kQuad && EIGHT;
   static constexpr int MR = ROWS == kQuad ? 32 : TWO ? 256 : 128;
   static constexpr int kRowWarps = FEW ? 4 : 16;
@@ -98,30 +102,32 @@ struct Shape {
     if (THREE) return k % 4 == 0 || k > 10 || k < 0 ? -1 : k / 4 * 3 + k % 4 - 1;  // 17, 18, 19, 21, 22, 23, 25, 26
     return k >= 0 && k < kCopyWarps ? k : -1;
   }
-  static constexpr int kTileBytes = kTile * D * 2;
-  static constexpr int RK = D == 64 ? 4 : EIGHT && TWO ? 1 : (TWO || FOUR || EIGHT ? 2 : 3), RV = D == 64 ? 4 : 2;  // K tiles and V tiles staged
+  static constexpr int kTileBytes = kTile * D * 2, kCodeBytes = kTile * D;
+  static constexpr int kKeyBytes = FEW ? kCodeBytes : kTileBytes, kQueryBytes = FEW ? PIECES * kCodeBytes : kTileBytes;  // (of 128 rows)
+  static constexpr int RK = D == 64 || FEW ? 4 : EIGHT && TWO ? 1 : (TWO || FOUR || EIGHT ? 2 : 3), RV = D == 64 ? 4 : 2;  // K tiles and V tiles staged
   // 4-bit pages: a tile's codes and scales (of K, then of V), copied ahead of their conversion
   static constexpr int kRawCodes = kTile * (D / 2), kRawScales = kTile * (D / 16), kRawBytes = 2 * (kRawCodes + kRawScales);
   // where the 16-byte piece of a row of codes lies: turned by the row, so that 8 rows meet no bank conflict
   __device__ static constexpr int raw_piece(int row, int piece) { return piece ^ ((row >> (D == 128 ? 1 : 2)) & (D / 32 - 1)); }
   static constexpr int RAW = !FOUR ? 0 : D == 64 ? 3 : TWO ? 1 : QUAD ? 2 : 3;
-  static constexpr int kOffK = (TWO ? 2 : 1) * kTileBytes;
-  static constexpr int kOffV = kOffK + RK * kTileBytes;
+  static constexpr int kOffK = (TWO ? 2 : 1) * kQueryBytes;
+  static constexpr int kOffV = kOffK + RK * kKeyBytes;
   static constexpr int kOffMl = kOffV + RV * kTileBytes;      // [2][2][128] (m, l) of slots and halves
   static constexpr int kOffRaw = kOffMl + 4 * 128 * 8;
-  // 8-bit pages: boxes of a converting warp's 16 slots, keys' and values' in turn (FEW: a warp has the ones or the others),
-  // ahead of their conversion.  With at most 32 rows and heads of 128, 12 of them lie in the query tile behind its rows, which the
-  // products read for rows of scores that nobody reads.
-  static constexpr int kBox = 16 * D, BOXES = FEW && D == 128 ? 2 : 3, HOLES = FEW && D == 128 ? 12 : 0;
+  // 8-bit pages: boxes of a converting warp's 16 slots, keys' and values' in turn (FEW: values'), ahead of their conversion.
+  // With at most 32 rows and heads of 128, 6 of them lie behind the rows of each piece of the query tile, which the products read
+  // for rows of scores that nobody reads.
+  static constexpr int kBox = 16 * D, BOXES = FEW && D == 128 ? 2 : 3, HOLES = FEW && D == 128 ? 6 * PIECES : 0;
   __device__ static constexpr int box_offset(int k) {
-    return k < HOLES ? k / 6 * (kTile * 128) + 32 * 128 + k % 6 * kBox : kOffRaw + (k - HOLES) * kBox;
+    return k < HOLES ? k / 6 * kCodeBytes + 32 * 128 + k % 6 * kBox : kOffRaw + (k - HOLES) * kBox;
   }
   static constexpr int kOffQScale = kOffRaw + (EIGHT ? (kCopyWarps * BOXES - HOLES) * kBox : RAW * kRawBytes);  // [2][MR] scales of query rows (4-bit and 8-bit pages)
   static constexpr int kOffSum = kOffQScale + (FOUR || EIGHT ? 2 * MR * 4 : 0);  // [4][4][32][8] accumulators on their way, [32] 1 / l
   static constexpr int kOffItem = kOffSum + (QUAD ? 4 * 4 * 32 * 8 * 4 + 32 * 4 : 0);
   static constexpr int kOffScan = kOffItem + kItems * sizeof(Item);
   static constexpr int kOffBad = (kOffScan + (kThreads / 32 + 3) * 8 + 15) / 16 * 16;
-  static constexpr int kOffBar = kOffBad + kBadRing * 16;
+  static constexpr int kOffPower = kOffBad + kBadRing * 16;  // [kBadRing][8] scales of a tile's steps of keys (FEW)
+  static constexpr int kOffBar = kOffPower + (FEW ? kBadRing * 8 * 4 : 0);
   static constexpr int kBars = 2 * (RK + RV + RAW) + 2 + 2 + 2 + 2 + 2 * kItems + 1 + (EIGHT ? kCopyWarps * BOXES : 0);
   static constexpr int kOffMisc = kOffBar + kBars * 8;
   static constexpr int kBytes = kOffMisc + 16;
@@ -153,6 +159,16 @@ __device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint3
       "{\n.reg .pred p;\n.reg .b64 da, db;\nmov.b64 da, {%1, %5};\nmov.b64 db, {%2, %5};\nsetp.ne.u32 p, %4, 0;\n"
       "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate),
       "r"(kDescHigh)
+      : "memory");
+}
+// The same for 8-bit codes: E4M3, K-major rows of D bytes, swizzled over the row.
+template <int D>
+__device__ __forceinline__ void mma_codes(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
+  constexpr uint32_t high = D == 128 ? kDescHigh : (512u >> 4) | (1u << 14) | (4u << 29);
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b64 da, db;\nmov.b64 da, {%1, %5};\nmov.b64 db, {%2, %5};\nsetp.ne.u32 p, %4, 0;\n"
+      "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], da, db, %3, p;\n}" ::"r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate),
+      "n"(high)
       : "memory");
 }
 __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate) {
@@ -240,6 +256,11 @@ __device__ __forceinline__ bool pair_any(int barrier, bool mine) {
 __device__ __forceinline__ uint32_t tile_offset(int row, int piece) {
   return (piece >> 3) * (kTile * 128) + row * 128 + (((piece & 7) ^ (row & 7)) << 4);
 }
+// The same for rows of D codes (FEW).
+template <int D>
+__device__ __forceinline__ uint32_t code_offset(int row, int piece) {
+  return row * D + ((D == 128 ? piece ^ (row & 7) : piece ^ (row >> 1 & 3)) << 4);
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float y;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
@@ -265,14 +286,23 @@ template <> struct Extra<8> {
   using type = Maps;
 };
 
+// E4M3 has 4 significant bits, bf16 8 and fp16 11: with that many pieces, each the code nearest to what the ones before left, a query's values
+// are exact down to where pieces become subnormal (kQueryTop).
+template <typename T>
+constexpr int kPieces = std::is_same<T, __half>::value ? 3 : 2;
+// Queries are scaled so that a row's largest value is within [kQueryTop, 2 kQueryTop): the smallest code is 2^-9, so what is lost is at most
+// 2^-17 of that value.
+constexpr float kQueryTop = 128.f;
+
 template <typename T, int D, Rows ROWS, int BITS>
-__global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_kernel(const AttendParams P, const __grid_constant__ typename Extra<BITS>::type extra) {
-  using Sh = Shape<D, ROWS, BITS>;
+__global__ void __launch_bounds__(Shape<D, ROWS, BITS, kPieces<T>>::kThreads, 1) attend_tc_kernel(const AttendParams P, const __grid_constant__ typename Extra<BITS>::type extra) {
+  using Sh = Shape<D, ROWS, BITS, kPieces<T>>;
   constexpr bool FOUR = BITS == 4, EIGHT = BITS == 8;
-  constexpr bool BRAIN = BITS != 16 && !std::is_same<T, __half>::value;  // bf16 queries to be held in fp16
+  constexpr bool FEW = Sh::FEW;
+  constexpr bool BRAIN = FEW || (BITS != 16 && !std::is_same<T, __half>::value);  // queries are scaled: to be held in codes, or bf16 in fp16
   using M = typename std::conditional<BITS != 16, __half, T>::type;  // the matrix instructions' type
   constexpr int MR = Sh::MR, RK = Sh::RK, RV = Sh::RV, KT = D / 16, THREADS = Sh::kThreads;
-  constexpr bool AHEAD = Sh::AHEAD, TWO = Sh::TWO, QUAD = Sh::QUAD, FEW = Sh::FEW;
+  constexpr bool AHEAD = Sh::AHEAD, TWO = Sh::TWO, QUAD = Sh::QUAD;
   constexpr int ROW_THREADS = 32 * Sh::kRowWarps;
   extern __shared__ __align__(1024) char smem[];
   const Pages& pg = P.pages;
@@ -296,6 +326,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
   volatile int* const gave_up = reinterpret_cast<int*>(smem + Sh::kOffMisc) + 1;
   volatile int* const s_odd = reinterpret_cast<int*>(smem + Sh::kOffMisc) + 2;  // a masked value that is not finite
   Item* const items = reinterpret_cast<Item*>(smem + Sh::kOffItem);
+  [[maybe_unused]] float* const s_power = reinterpret_cast<float*>(smem + Sh::kOffPower);
   float* const s_qscale = reinterpret_cast<float*>(smem + Sh::kOffQScale);
 
   if (tid == 0) {
@@ -425,14 +456,136 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
       const int32_t* table = pg.table + static_cast<int64_t>(it.b) * pg.max_pages;
       const char* const k_head = pg.k + it.h * pg.head_stride;
       const char* const v_head = pg.v + it.h * pg.head_stride;
-      if constexpr (EIGHT) {
+      if constexpr (FEW) {
+        // Warp c brings slots 16 c ... of a tile, a step: warps 0 .. 7 of the CTA's even tiles, 8 .. 15 of its odd ones.  Keys
+        // stay codes: their box goes to its place in the tile, swizzled as the matrix instructions read it, and its scale to the
+        // rows' threads.  Values become fp16: boxes of them are copied ahead to shared memory of the warp's own, whatever tile's place
+        // is free.  A lane each looks up 32 tiles' steps.
+        constexpr int CH = D / 16, RPI = 32 / CH, LOADS = 16 / RPI, BOXES = Sh::BOXES;  // 16-byte pieces of a row of codes, rows at a time
+        constexpr int EVERY = 2;  // this warp's tiles: mine, mine + EVERY ...
+        // How many tiles ahead keys are sent: their place is free once the scores of tile i + KEYS_AHEAD - RK are there.
+        constexpr int KEYS_AHEAD = RK - EVERY;
+        static_assert(KEYS_AHEAD % EVERY == 0, "a warp's own tiles");
+        // (by the CTA's number of a tile, so that a warp passes over none of its stages: a wait tells apart one round of a
+        // barrier from the next, not from the one after)
+        const int step = cw % 8, tile0 = tile, tiles = t_hi - t_lo, mine = (cw / 8 + tile0) % EVERY;
+        auto raw = [&](int slot) { return smem + Sh::box_offset(cw * BOXES + slot); };
+        uint64_t* const full = raw_full + cw * BOXES;
+        // A lane has two units of 8 codes in every RPI-th row, and their values are two 16-byte pieces of the tile's row.  With heads of
+        // 128 they are 8 apart, the later one first in odd rows; with heads of 64 they are neighbours.  (Neither the loads nor
+        // the stores meet bank conflicts.)
+        const int unit = lane % CH, odd_row = D == 128 ? lane / CH % 2 : 0;
+        const int unit0 = D == 128 ? unit + 8 * odd_row : 2 * unit, unit1 = D == 128 ? unit + 8 * (1 - odd_row) : 2 * unit + 1;
+        uint2 codes[LOADS][2];
+        auto store = [&](int i, int e) {  // the codes' values to tile i
+          const int n = tile0 + i;
+          wait_for(v_empty + n % RV, ((n / RV) & 1) ^ 1, gave_up);
+          __syncwarp();
+          char* const dst = smem + Sh::kOffV + n % RV * Sh::kTileBytes;
+          const uint32_t s2 = power_f16x2(e);
+#pragma unroll
+          for (int j = 0; j < LOADS; ++j) {
+            const int row = step * 16 + j * RPI + lane / CH;
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+              uint32_t f[4];
+              e4m3x4_to_f16(codes[j][x].x, f[0], f[1]);
+              e4m3x4_to_f16(codes[j][x].y, f[2], f[3]);
+              *reinterpret_cast<uint4*>(dst + tile_offset(row, x ? unit1 : unit0)) =
+                  make_uint4(mul_f16x2(f[0], s2), mul_f16x2(f[1], s2), mul_f16x2(f[2], s2), mul_f16x2(f[3], s2));
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(v_full + n % RV);
+        };
+        auto look_up = [&](int look) {
+          Look l;
+          const int t = t_lo + look * 32 + lane, s = R.slot(t * kUnit + step);
+          l.find(pg, table, s, t < t_hi && s < it.end);
+          return l;
+        };
+        int at = 0;  // the look that `now` is
+        bool scaled = false;  // the next one's scales have been asked for
+        Look now = look_up(0), next = look_up(1);
+        auto box = [&](int i, uint64_t* bar, const CUtensorMap* map, char* dst) {  // tile i's, by lane 0
+          const int page = __shfl_sync(0xffffffffu, i / 32 == at ? now.page : next.page, i % 32);
+          const int in_page = __shfl_sync(0xffffffffu, i / 32 == at ? now.in_page : next.in_page, i % 32);
+          if (lane == 0) {
+            const bool there = static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages) && !*gave_up;
+            mbar_expect_tx(bar, there ? Sh::kBox : 0);
+            if (there) copy_box(smem_addr(dst), map, in_page, extra.heads ? it.h : 0, extra.pages ? page : 0, bar);
+          }
+        };
+        auto fetch = [&](int n) {  // this warp's box n of values in the item; number boxes + n of all
+          const int i = n * EVERY + mine, slot = (boxes + n) % BOXES;
+          if (i >= tiles) return;
+          fence_proxy_async_smem();  // (the warp's reads, which its barrier ordered before this)
+          box(i, full + slot, &extra.v, raw(slot));
+        };
+        // box n's codes to registers (zeros for a step that is not there), and another box to its place
+        auto take = [&](int n, bool there) {
+          const int slot = (boxes + n) % BOXES;
+          wait_for(full + slot, ((boxes + n) / BOXES) & 1, gave_up);
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < LOADS; ++j) {
+            const char* const row = raw(slot) + (j * RPI + lane / CH) * D;
+            codes[j][0] = there ? *reinterpret_cast<const uint2*>(row + unit0 * 8) : make_uint2(0, 0);
+            codes[j][1] = there ? *reinterpret_cast<const uint2*>(row + unit1 * 8) : make_uint2(0, 0);
+          }
+          __syncwarp();  // (everybody has read the box)
+          fetch(n + BOXES);
+        };
+        // Tile i's keys.  (Of a step that is not there the place keeps what it held, for scores that nobody uses.)
+        auto send = [&](int i) {
+          if (i >= tiles) return;
+          const int n = tile0 + i, stage = n % RK;
+          const int page = __shfl_sync(0xffffffffu, i / 32 == at ? now.page : next.page, i % 32);
+          const uint32_t scale = __shfl_sync(0xffffffffu, i / 32 == at ? now.scale_k : next.scale_k, i % 32);
+          wait_for(k_empty + stage, ((n / RK) & 1) ^ 1, gave_up);
+          __syncwarp();
+          if (lane == 0) {
+            reinterpret_cast<uint16_t*>(s_bad)[n % kBadRing * 8 + step] = page >= pg.num_pages ? 0xffffu : 0u;
+            s_power[n % kBadRing * 8 + step] = power_f32(scale_exponent(scale));
+          }
+          box(i, k_full + stage, &extra.k, smem + Sh::kOffK + stage * Sh::kKeyBytes + step * Sh::kBox);
+        };
+        for (int n = 0; n < BOXES; ++n) fetch(n);
+        now.find_scales(pg, it.h);
+        for (int i = mine; i < KEYS_AHEAD; i += EVERY) send(i);
+        int n = 0;
+        for (int i = mine; i < tiles; i += EVERY, ++n) {
+          if (i / 32 != at) {
+            now = next;
+            next = look_up(++at + 1);
+            scaled = false;
+          }
+          if (!scaled && i % 32 >= 16) {
+            next.find_scales(pg, it.h);
+            scaled = true;
+          }
+          send(i + KEYS_AHEAD);
+          const int page = __shfl_sync(0xffffffffu, now.page, i % 32);
+          const int e = scale_exponent(__shfl_sync(0xffffffffu, now.scale_v, i % 32));
+          take(n, static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages));
+          store(i, e);
+        }
+        boxes += n;
+        tile += tiles;
+        if (*gave_up && lane == 0) {  // (what is still on its way lands first)
+          for (int x = max(0, boxes - BOXES); x < boxes; ++x) mbar_wait(full + x % BOXES, (x / BOXES) & 1);
+          for (int x = max(tile0, tile - RK); x < tile; ++x)
+            if ((x - tile0) % EVERY == mine) mbar_wait(k_full + x % RK, (x / RK) & 1);
+        }
+      } else if constexpr (EIGHT) {
         // Warp c brings slots 16 c ... of a tile, a step: a box of keys and one of values.  A lane each looks up 32 tiles'
         // steps, and boxes are copied three ahead, whatever tile's place is free, to shared memory of the warp's own.
         // (16-byte copies by all lanes with a lookup for every tile, or values copied to their tile's place once that was free,
         // which left the copy's latency in every tile's way: 271 us for the tree of the figures above, 286 to 293 us for 64
         // requests of 8 tokens.)
         constexpr int CH = D / 16, RPI = 32 / CH, LOADS = 16 / RPI, BOXES = Sh::BOXES;  // 16-byte pieces of a row of codes, rows at a time
-        const int step = cw % 8;  // (FEW: warps 0 .. 7 bring keys, 8 .. 15 values)
+        const int step = cw;
         auto raw = [&](int slot) { return smem + Sh::box_offset(cw * BOXES + slot); };
         uint64_t* const full = raw_full + cw * BOXES;
         auto place_of = [&](int kv, int n) { return smem + (kv ? Sh::kOffV : Sh::kOffK) + n % (kv ? RV : RK) * Sh::kTileBytes; };
@@ -473,12 +626,10 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
         };
         const int tiles = t_hi - t_lo;
         Look now = look_up(0), next = look_up(1);
-        // The item's box n: tile n / 2's keys, then its values (FEW: tile n's).  Number boxes + n of all; `at` is the look that
-        // `now` is.
-        constexpr int PER = FEW ? 1 : 2;
+        // The item's box n: tile n / 2's keys, then its values.  Number boxes + n of all; `at` is the look that `now` is.
         auto fetch = [&](int n, int at) {
-          if (n >= PER * tiles) return;
-          const int i = n / PER;
+          if (n >= 2 * tiles) return;
+          const int i = n / 2;
           const int page = __shfl_sync(0xffffffffu, i / 32 == at ? now.page : next.page, i % 32);
           const int in_page = __shfl_sync(0xffffffffu, i / 32 == at ? now.in_page : next.in_page, i % 32);
           if (lane == 0) {
@@ -487,7 +638,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
             fence_proxy_async_smem();  // (the warp's reads, which its barrier ordered before this)
             mbar_expect_tx(full + slot, there ? Sh::kBox : 0);
             if (there)
-              copy_box(smem_addr(raw(slot)), (FEW ? cw >= 8 : n % 2 != 0) ? &extra.v : &extra.k, in_page, extra.heads ? it.h : 0, extra.pages ? page : 0,
+              copy_box(smem_addr(raw(slot)), n % 2 != 0 ? &extra.v : &extra.k, in_page, extra.heads ? it.h : 0, extra.pages ? page : 0,
                        full + slot);
           }
         };
@@ -518,40 +669,28 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
         auto remember_bad = [&](int page) {
           if (lane == 0) reinterpret_cast<uint16_t*>(s_bad)[(tile % kBadRing) * 8 + step] = page >= pg.num_pages ? 0xffffu : 0u;
         };
-        if constexpr (FEW) {
-          const int kv = cw / 8;
-          for (int i = 0; i < tiles; ++i, ++tile) {
-            turn_to(i);
-            const int page = __shfl_sync(0xffffffffu, now.page, i % 32), e = exponent(kv, i);
-            take(i, i / 32, static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages));
-            if (kv == 0) remember_bad(page);
-            wait_empty(kv, tile);
-            store(kv, tile, e);
+        int ev = 0;          // of the tile whose values are next
+        bool there = false;  // its step is
+        for (int i = -1; i < tiles; ++i) {
+          if (i >= 0) {
+            take(2 * i + 1, i / 32, there);
+            wait_empty(1, tile);
+            store(1, tile, ev);
+            ++tile;
           }
-        } else {
-          int ev = 0;          // of the tile whose values are next
-          bool there = false;  // its step is
-          for (int i = -1; i < tiles; ++i) {
-            if (i >= 0) {
-              take(2 * i + 1, i / 32, there);
-              wait_empty(1, tile);
-              store(1, tile, ev);
-              ++tile;
-            }
-            const int k = i + 1;  // the tile whose keys are next, number `tile`
-            if (k >= tiles) break;
-            turn_to(k);
-            const int page = __shfl_sync(0xffffffffu, now.page, k % 32);
-            there = static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages);
-            take(2 * k, k / 32, there);
-            remember_bad(page);
-            const int ek = exponent(0, k);
-            ev = exponent(1, k);
-            wait_empty(0, tile);
-            store(0, tile, ek);
-          }
+          const int k = i + 1;  // the tile whose keys are next, number `tile`
+          if (k >= tiles) break;
+          turn_to(k);
+          const int page = __shfl_sync(0xffffffffu, now.page, k % 32);
+          there = static_cast<unsigned>(page) < static_cast<unsigned>(pg.num_pages);
+          take(2 * k, k / 32, there);
+          remember_bad(page);
+          const int ek = exponent(0, k);
+          ev = exponent(1, k);
+          wait_empty(0, tile);
+          store(0, tile, ek);
         }
-        boxes += PER * tiles;
+        boxes += 2 * tiles;
         if (*gave_up && lane == 0)  // (what is still on its way lands first)
           for (int n = max(0, boxes - BOXES); n < boxes; ++n) mbar_wait(full + n % BOXES, (n / BOXES) & 1);
       } else if constexpr (!FOUR) {
@@ -650,7 +789,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
     // ---- matrix instructions, from one elected thread.  The whole warp runs the loops, on values that
     // are the same in all lanes: the operands' descriptors then live in uniform registers, as the
     // instructions take them (from a thread's own registers each one cost about 80 clocks to issue).
-    constexpr uint32_t id_s = instr_desc<M>(kTile, false), id_o = instr_desc<M>(D, true);
+    constexpr uint32_t id_s = FEW ? (1u << 4) | (kTile >> 3) << 17 | (128u >> 4) << 24 : instr_desc<M>(kTile, false), id_o = instr_desc<M>(D, true);
     const bool leader = elect_one();
     const uint32_t base = __shfl_sync(0xffffffffu, tmem, 0);
     int k_tile = 0, v_tile = 0;
@@ -674,13 +813,19 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
         }
         fence_after();
         const uint32_t a = desc_low(smem_addr(smem + (TWO ? slot * Sh::kTileBytes : 0)), 16);
-        const uint32_t b = desc_low(smem_addr(smem + Sh::kOffK + stage * Sh::kTileBytes), 16);
+        const uint32_t b = desc_low(smem_addr(smem + Sh::kOffK + stage * Sh::kKeyBytes), 16);
         const uint32_t d = base + slot * 128;
         if (leader) {
+          if constexpr (FEW) {  // every piece of the queries times the keys' codes, 32 values at a time
 #pragma unroll
-          for (int k = 0; k < KT; ++k) {
-            const uint32_t o = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
-            mma_ss(d, a + o, b + o, id_s, k > 0 ? 1u : 0u);
+            for (int k = 0; k < kPieces<T> * (D / 32); ++k)
+              mma_codes<D>(d, a + ((k / (D / 32) * Sh::kCodeBytes + k % (D / 32) * 32) >> 4), b + ((k % (D / 32) * 32) >> 4), id_s, k > 0 ? 1u : 0u);
+          } else {
+#pragma unroll
+            for (int k = 0; k < KT; ++k) {
+              const uint32_t o = ((k >> 2) * (kTile * 128) + (k & 3) * 32) >> 4;
+              mma_ss(d, a + o, b + o, id_s, k > 0 ? 1u : 0u);
+            }
           }
           mma_commit(s_full + slot);
           if (!TWO || slot == 1) mma_commit(k_empty + stage);
@@ -837,6 +982,51 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
           }
         }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(q_full)) : "memory");
+      } else if (EIGHT && !FEW) {
+        // All rows on their way at once, then each piece scaled in place by the lane that copied it.  (Four rows at a time through
+        // registers, each a wait for global memory: the trees of the figures above 271 us.)
+        const int di = query_of(P, AT), dg = AT - di * P.G;
+        const int64_t on = di * P.q_st + dg * P.q_sh, wrap = P.q_st - P.G * P.q_sh;
+        const int i0 = query_of(P, row0 + t2 / CH);
+        int g = row0 + t2 / CH - i0 * P.G;
+        const T* from = q_item + i0 * P.q_st + g * P.q_sh + piece * 8;
+#pragma unroll 8
+        for (int r = t2 / CH; r < rows; r += AT) {
+          copy_async<16>(smem_addr(target(r)), from, true);
+          from += on;
+          g += dg;
+          if (g >= P.G) {
+            g -= P.G;
+            from += wrap;
+          }
+        }
+        copy_commit();
+        copy_wait<0>();
+        const uint32_t flip = P.scale_log2 < 0.f ? 0x80008000u : 0u;  // the scale's sign goes into the queries
+#pragma unroll 4
+        for (int r = t2 / CH; r - t2 / CH < rows; r += AT) {  // (rows past the item's are read, not written)
+          uint4* const place = reinterpret_cast<uint4*>(target(r));
+          const uint4 x = *place;
+          uint32_t y[4] = {x.x, x.y, x.z, x.w};
+          if constexpr (BRAIN) {
+            const uint32_t a2 = __vmaxu2(__vmaxu2(x.x & 0x7fff7fffu, x.y & 0x7fff7fffu), __vmaxu2(x.z & 0x7fff7fffu, x.w & 0x7fff7fffu));
+            uint32_t a = max(a2 & 0xffffu, a2 >> 16);
+#pragma unroll
+            for (int o = CH / 2; o > 0; o >>= 1) a = max(a, __shfl_xor_sync(0xffffffffu, a, o));
+            const int e8 = a >> 7;
+            const bool usual = e8 != 0 && e8 != 0xff;
+            if (piece == 0 && r < rows) s_qscale[(n & 1) * MR + r] = usual ? __int_as_float(e8 << 23) : 1.f;
+            const float down = usual ? __int_as_float(e8 == 254 ? 1 << 22 : (254 - e8) << 23) : 1.f;  // the reciprocal
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = Half16<T>::to_f32(y[e]);
+              y[e] = Half16<__half>::pack(f.x * down, f.y * down);
+            }
+          }
+          if (r < rows) *place = make_uint4(y[0] ^ flip, y[1] ^ flip, y[2] ^ flip, y[3] ^ flip);
+        }
+        fence_proxy_async_smem();
+        mbar_arrive(q_full);
       } else {
         constexpr int AHEAD = 4;
         for (int r0 = t2 / CH; r0 - t2 / CH < rows; r0 += AHEAD * AT) {
@@ -849,8 +1039,8 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
             const int r = r0 + k * AT;
             uint32_t y[4] = {x[k].x, x[k].y, x[k].z, x[k].w};
             if constexpr (BRAIN) {
-              // bf16 queries over 4-bit or 8-bit pages: q / 2^(exponent of the row's largest value) is within
-              // (-2, 2), and fp16 then holds it to 2^-25 of that value
+              // q / 2^(exponent of the row's largest value) is within (-2, 2), and fp16 then holds a bf16 query to 2^-25 of that
+              // value (FEW: kQueryTop)
               float a = 0.f;
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
@@ -861,22 +1051,54 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
               for (int o = CH / 2; o > 0; o >>= 1) a = fmaxf(a, __shfl_xor_sync(0xffffffffu, a, o));
               const int e8 = (__float_as_int(a) >> 23) & 0xff;
               const float up = (e8 == 0 || e8 == 0xff) ? 1.f : __int_as_float(e8 << 23);
-              if (piece == 0 && r < rows) s_qscale[(n & 1) * MR + r] = up;
+              if (piece == 0 && r < rows) s_qscale[(n & 1) * MR + r] = FEW ? up * (1.f / kQueryTop) : up;
               const float down = 1.f / up;
+              if constexpr (FEW) {
+                float left[8];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                const float2 f = Half16<T>::to_f32(y[e]);
-                y[e] = Half16<__half>::pack(f.x * down, f.y * down);
+                for (int e = 0; e < 4; ++e) {
+                  const float2 f = Half16<T>::to_f32(y[e]);
+                  left[2 * e] = f.x * down * (P.scale_log2 < 0.f ? -kQueryTop : kQueryTop);
+                  left[2 * e + 1] = f.y * down * (P.scale_log2 < 0.f ? -kQueryTop : kQueryTop);
+                }
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                  if (!(fabsf(left[e]) < kInf)) left[e] = __int_as_float(0x7fffffff);  // (every score of the row is undefined)
+#pragma unroll
+                for (int k = 0; k < kPieces<T>; ++k) {
+                  uint32_t w[2];
+#pragma unroll
+                  for (int x = 0; x < 2; ++x) {
+                    w[x] = to_e4m3x2(left[4 * x], left[4 * x + 1]) | to_e4m3x2(left[4 * x + 2], left[4 * x + 3]) << 16;
+                    uint32_t lo, hi;
+                    e4m3x4_to_f16(w[x], lo, hi);
+                    const float2 f = Half16<__half>::to_f32(lo), g = Half16<__half>::to_f32(hi);
+                    left[4 * x] -= f.x;
+                    left[4 * x + 1] -= f.y;
+                    left[4 * x + 2] -= g.x;
+                    left[4 * x + 3] -= g.y;
+                  }
+                  if (r < rows)
+                    *reinterpret_cast<uint2*>(smem + k * Sh::kCodeBytes + code_offset<D>(r, piece / 2) + piece % 2 * 8) = make_uint2(w[0], w[1]);
+                }
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  const float2 f = Half16<T>::to_f32(y[e]);
+                  y[e] = Half16<__half>::pack(f.x * down, f.y * down);
+                }
               }
             }
-            if (P.scale_log2 < 0.f) {  // the scale's sign goes into the queries
+            if constexpr (!FEW) {
+              if (P.scale_log2 < 0.f) {  // the scale's sign goes into the queries
 #pragma unroll
-              for (int e = 0; e < 4; ++e) y[e] ^= 0x80008000u;
-            }
-            if (r < rows) {
+                for (int e = 0; e < 4; ++e) y[e] ^= 0x80008000u;
+              }
+              if (r < rows) {
 #pragma unroll
-              for (int q = 0; q < (QUAD ? 4 : 1); ++q)
-                *reinterpret_cast<uint4*>(target(r + 32 * q)) = make_uint4(y[0], y[1], y[2], y[3]);
+                for (int q = 0; q < (QUAD ? 4 : 1); ++q)
+                  *reinterpret_cast<uint4*>(target(r + 32 * q)) = make_uint4(y[0], y[1], y[2], y[3]);
+              }
             }
           }
         }
@@ -961,6 +1183,9 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
         const uint4 bads = *reinterpret_cast<const uint4*>(s_bad + (tile % kBadRing) * 4);
         if (BRAIN && jobs == 0)
           c = fmaxf(c * s_qscale[(n & 1) * MR + (TWO ? slot * 128 : 0) + row], kLeast);
+        // what a step's scores are multiplied with: c, times the scale of its keys (FEW)
+        const float* const power = s_power + tile % kBadRing * 8 + half * 4;
+        auto factor = [&](int ch) { return FEW ? fmaxf(c * power[ch], kLeast) : c; };
         uint32_t seen[2] = {~0u, ~0u};
         bool poisoned = false;  // the row sees a slot on a page out of range
         partial = partial || (rows > 0 && (bads.x | bads.y | bads.z | bads.w) != 0);
@@ -1011,11 +1236,13 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
             for (int x = 0; x < 2; ++x) {
               tmem_load_wait(r[x]);
               mask_scores(2 * h2 + x, r[x]);
+              float most = FEW ? -kInf : top;
 #pragma unroll
-              for (int e = 0; e < 16; e += 2) top = max3(top, __uint_as_float(r[x][e]), __uint_as_float(r[x][e + 1]));
+              for (int e = 0; e < 16; e += 2) most = max3(most, __uint_as_float(r[x][e]), __uint_as_float(r[x][e + 1]));
+              top = FEW ? fmaxf(top, most * factor(2 * h2 + x)) : most;
             }
           }
-          top *= c;
+          if (!FEW) top *= c;
         }
         if (AHEAD && jobs > 0) {  // the last products have read their weights and added to the accumulator
           wait_for(o_full + slot, o_phase, gave_up);
@@ -1046,7 +1273,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
           // go to columns 8 ch ..., scores 16 ch ... are in columns 16 ch ...
           const float base = m == -kInf ? 0.f : m;
           // (two at a time: packed fp32 products and sums, rounded as the scalar ones)
-          const unsigned long long c2 = f2pack(c, c), base2 = f2pack(-base, -base);
+          const unsigned long long base2 = f2pack(-base, -base);
           unsigned long long sum2[2] = {0ull, 0ull};
           if constexpr (!QUAD) tmem_load(s_at, r[0]);
 #pragma unroll
@@ -1057,6 +1284,8 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
               mask_scores(ch, r[ch & 1]);
             }
             uint32_t p[8];
+            const float cx = factor(ch);
+            const unsigned long long c2 = f2pack(cx, cx);
 #pragma unroll
             for (int e = 0; e < 16; e += 2) {
               float x0, x1;
@@ -1348,14 +1577,14 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS>::kThreads, 1) attend_tc_k
 
 template <typename T, int D, Rows ROWS, int BITS>
 cudaError_t launch_shape(const AttendParams& P, cudaStream_t stream) {
-  using Sh = Shape<D, ROWS, BITS>;
+  using Sh = Shape<D, ROWS, BITS, kPieces<T>>;
   auto kernel = attend_tc_kernel<T, D, ROWS, BITS>;
   static_assert(Sh::kBytes <= 227 * 1024, "shared memory of a CTA");
   if (cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Sh::kBytes); e != cudaSuccess)
     return e;
   typename Extra<BITS>::type extra{};
   if constexpr (BITS == 8)
-    if (cudaError_t e = encode_maps(P.pages, false, &extra); e != cudaSuccess) return e;
+    if (cudaError_t e = encode_maps(P.pages, Sh::FEW, false, &extra); e != cudaSuccess) return e;
   return launch_kernel(kernel, dim3(P.ctas), dim3(Sh::kThreads), Sh::kBytes, stream, 1, P, extra);
 }
 

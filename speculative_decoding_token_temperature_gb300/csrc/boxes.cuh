@@ -27,7 +27,7 @@ __device__ __forceinline__ void copy_box(uint32_t dst, const CUtensorMap* map, i
 }
 
 // (By the runtime's lookup of the driver's function: the library needs no link to the driver's.)
-inline cudaError_t encode_maps(const Pages& pg, bool swizzled, Maps* maps) {
+inline cudaError_t encode_maps(const Pages& pg, bool swizzled_k, bool swizzled_v, Maps* maps) {
   using Encode = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
                               const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
   static const Encode encode = [] {
@@ -46,10 +46,10 @@ inline cudaError_t encode_maps(const Pages& pg, bool swizzled, Maps* maps) {
   const cuuint64_t strides[3] = {static_cast<cuuint64_t>(pg.slot_stride), static_cast<cuuint64_t>(maps->heads ? pg.head_stride : pg.slot_stride),
                                  static_cast<cuuint64_t>(maps->pages ? pg.page_stride : pg.slot_stride)};
   const cuuint32_t box[4] = {static_cast<cuuint32_t>(D), kBoxSlots, 1, 1}, one[4] = {1, 1, 1, 1};
-  const CUtensorMapSwizzle swizzle = !swizzled ? CU_TENSOR_MAP_SWIZZLE_NONE : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const CUtensorMapSwizzle rows = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
   for (int i = 0; i < 2; ++i)
     if (encode(i ? &maps->v : &maps->k, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, i ? pg.v : pg.k, dims, strides, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE,
-               swizzle, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+               (i ? swizzled_v : swizzled_k) ? rows : CU_TENSOR_MAP_SWIZZLE_NONE, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
       return cudaErrorInvalidValue;
   return cudaSuccess;
 }
