@@ -45,8 +45,8 @@ constexpr int kRows = 16;     // rows of a tile
 // 4-bit pages 15.5 / 19.6 and 68.2 / 70.7; 16 rows, B=32, 8000 slots 68.8 / 68.4 and 72.3 / 70.6.
 constexpr int kWarpRows = 8;
 // Over 8-bit pages (the warp-level kernel of attend8.cu, us here / there; 64 requests of up to 8190 slots, 8 key heads, heads of 128): 4 rows
-// 125 / 199, 8 rows 127 / 201, 12 rows 173 / 201, 16 rows 175 / 201, 24 rows 261 / 202, 32 rows 269 / 202; heads of 64: 16
-// rows 135 / 149, 32 rows 192 / 146; one request of 900 slots: 16 rows 17.8 / 18.2, 32 rows 21.1 / 19.6.  (24 and 32 rows here as a tile of 32.)
+// 126 / 179, 8 rows 128 / 178, 12 rows 173 / 178, 16 rows 175 / 178, 24 rows 318 / 179; heads of 64: 16 rows 135 / 150, 32 rows
+// 251 / 146; one request of 900 slots: 16 rows 17.8 / 18.2, 32 rows 17.8 / 19.7.  (24 and 32 rows here as two tiles of 16.)
 constexpr int kWarpRows8 = 16;
 
 __device__ __forceinline__ void load_matrices(uint32_t addr, uint32_t (&r)[4]) {

@@ -20,7 +20,8 @@
 // in one quarter of the lanes, those of that quarter alone, and the others convert too).  Then the warps that
 // bring K and V: of 16-bit pages, 4 that copy rows asynchronously, 16 bytes at a time; of 4-bit
 // pages, 8 that turn copied codes into their fp16 values (exact: at most 6 significant bits); of 8-bit pages, 8
-// (16) that copy boxes of codes ahead and store their fp16 values (exact: 4 significant bits).
+// that copy boxes of codes ahead and store their fp16 values (exact: 4 significant bits), or, with at most 32 rows, 16 that do
+// so with values only and copy keys to their tile as they are.
 // Either way the tiles are 128-byte-swizzled and gathered row by row, so pages may have any size
 // and stride.  One warp issues the matrix instructions, one walks the items ahead of everybody, and
 // two bring query rows and, of 4-bit pages, the codes and scales.  The roles meet at mbarriers; every
@@ -41,10 +42,9 @@
 //    cache's bytes.  A tile takes about 2400 clocks: its codes' conversion 790 at 64 lanes a clock, but
 //    with the copies in and the stores of the values (shared memory is busy for about 1500) the converting
 //    warps need 2000.
-//  - 64 requests, 8 tokens, up to 8190 slots in 8 bits (32 rows): 199 us, 3.4 TB/s, 0.50 of the measured copy rate.  With
-//    clock counters in it, at 202 us, a tile took about 2800 clocks and the warps that convert keys, which hold
-//    everybody up, 2300 of them (480 read, 770 store and fence, the rest the way from box to box); those for values waited 1100.
-//    By count, not measured, shared memory is busy for about 1800.  The trees of 64 nodes in 8 bits: 276 us, 204 in 16 bits.
+//  - 64 requests, 8 tokens, up to 8190 slots in 8 bits (32 rows): 176 us, 3.9 TB/s, 0.57 of the measured copy rate.  The trees of 64
+//    nodes in 8 bits: 244 us (219 with queries in fp16, which are not scaled; 201 in 16 bits).  In neither are the matrix
+//    pipe, the issue slots or shared memory full.
 //  - 35 rows, a window of 1024 slots, 96 requests: 60 us, 3.5 TB/s: an item is 9 tiles, and its first,
 //    partial tile, the way out of its rows and the next one's queries cost about 4 more.
 #pragma once
@@ -81,7 +81,7 @@ struct Shape {
   static constexpr bool FOUR = BITS == 4, EIGHT = BITS == 8;
   static constexpr bool TWO = ROWS == kTwo, QUAD = ROWS == kQuad && !EIGHT;
   // 8-bit pages with at most 32 rows: one quarter of the lanes has them, and the warps of the others convert too.  Keys are not
-  // converted: the scores are products of codes, the queries' in pieces.  (64 requests of 8 tokens: 173 us, 199 with the keys
+  // converted: the scores are products of codes, the queries' in pieces.  (64 requests of 8 tokens: 175 us, 199 with the keys
   // converted.  With more rows the pieces' products cost more than that saves: 202 against 183 us for 128 rows, 279 against 271
   // for 256, in fp16, whose pieces are three, 352 against 217.)
   static constexpr bool FEW = ROWS == kQuad && EIGHT;

@@ -365,6 +365,54 @@ def test_scales_next_to_zero_and_below(sd, kernel, n, scale):
     base._run(sd, c, base._q(2, n, 4, 128, BF16, std=0.1), [n, 299], BF16, 128, scale=scale)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F16])
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("n", [3, 8, 40])
+def test_queries_with_a_few_large_values(sd, kernel, dtype, D, n):
+    """Rows of a few values 2^10 times the others', and of values of every magnitude.  Where queries are held in E4M3 pieces a
+    value is off by at most 2^-17 of the row's largest (the largest is scaled into [128, 256), and what the pieces leave is at most half
+    the smallest code, 2^-10): a score by 2^-17 scale max|q| sum|k| more, which counts like its other errors, twice for an
+    output.  (1 + d for e^d is off by less than d^2, here below d / 32: 2.0625 instead of 2.)"""
+    B, hq, hkv, scale = 2, 8, 2, 2.0 ** -13
+    c = Cache(B, 300, 32, 16, hkv, D, seed=n)
+    q = base._q(B, n, hq, D, F16 if dtype == F16 else torch.float32)
+    q = q.float() * 2.0 ** -6
+    q[..., ::31] *= 2.0 ** 10
+    g = torch.Generator().manual_seed(n)
+    q[:, :, 1::2] = q[:, :, 1::2] * 2.0 ** torch.randint(-6, 5, (B, n, hq // 2, D), generator=g).to(DEV)
+    q = q.to(dtype)
+    lens = [n + 20, 300]
+    r = sd.attend(q, c.k, c.v, c.table, base._i32(lens), scale=scale, with_lse=True, **c.kw)
+    torch.cuda.synchronize()
+    assert not r["status"].any()
+    for b, L in enumerate(lens):
+        k, v = c.rows(b, L)
+        out, lse, pv, av, qk = co.attend(base._np(q[b]), k, v, co.visible(n, n, L, 0, 0), scale)
+        most = np.repeat(np.abs(k).sum(-1).max(0), hq // hkv)
+        eq = scale * 2.0 ** -17 * np.abs(base._np(q[b])).max(-1) * most
+        es = D * 2.0 ** -24 * qk + eq
+        assert eq.max() < 1 / 32
+        tol = ((2.0625 * es + 2.0 ** -13)[..., None] + base.U[F16]) * pv + 2.0 ** -25 * av + base.U[dtype] * np.abs(out) + 1e-30
+        assert (np.abs(base._np(r["out"][b]) - out) <= tol).all(), (np.abs(base._np(r["out"][b]) - out).max(), tol.min())
+        assert (np.abs(base._np(r["lse"][b]) - lse) <= es + 2.0 ** -13 + 2.0 ** -22 * np.abs(lse)).all()
+
+
+@pytest.mark.parametrize("n", [3, 8, 40])
+def test_queries_that_are_not_finite(sd, kernel, n):
+    """An infinity or a NaN in a row of queries: the row is undefined, the others are not."""
+    for dtype in (BF16, F16):
+        c = Cache(1, 200, 32, 16, 2, 64)
+        q = base._q(1, n, 8, 64, dtype)
+        want = sd.attend(q, c.k, c.v, c.table, base._i32([200]), scale=0.01, with_lse=True, **c.kw)
+        q[0, 1, 2, 5], q[0, 0, 7, 63], q[0, n - 1, 4, 0] = float("inf"), float("-inf"), float("nan")
+        r = sd.attend(q, c.k, c.v, c.table, base._i32([200]), scale=0.01, with_lse=True, **c.kw)
+        torch.cuda.synchronize()
+        odd = torch.zeros(n, 8, dtype=torch.bool, device=DEV)
+        odd[1, 2] = odd[0, 7] = odd[n - 1, 4] = True
+        assert torch.isnan(r["out"][0][odd]).all() and torch.isnan(r["lse"][0][odd]).all()
+        assert torch.equal(r["out"][0][~odd], want["out"][0][~odd]) and torch.equal(r["lse"][0][~odd], want["lse"][0][~odd])
+
+
 def test_long_rows_split_over_the_gpu(sd, kernel):
     """Few rows over a long cache: many CTAs share a row, and their parts are joined."""
     c = Cache(1, 40000, 64, 64, 1, 128)
