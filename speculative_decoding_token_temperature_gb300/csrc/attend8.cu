@@ -151,7 +151,9 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
       now.find_scales(pg, h);
     }
 
-    // ---- the query rows, as the matrix instruction's fragments: [tile][k step][lane]
+    // ---- the query rows, as the matrix instruction's fragments: [tile][k step][lane].  Rows that are no token's are zeros, whatever
+    // a padded batch's queries hold: they take part in the vote on references, which may change another row's rounding.
+    const int there = static_cast<int>(min(static_cast<int64_t>(rows), max(static_cast<int64_t>(S.nq) * P.G - row0, int64_t{0})));
     auto q_row = [&](int r) {
       const int i = query_of(P, row0 + r);
       return static_cast<const T*>(P.q) + b * P.q_sb + i * P.q_st + (h * P.G + row0 + r - i * P.G) * P.q_sh;
@@ -159,7 +161,7 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
     if constexpr (BRAIN) {  // a row's power-of-two scale
       for (int r = warp; r < MR; r += WARPS) {
         float a = 0.f;
-        if (r < rows)
+        if (r < there)
           for (int d = 2 * lane; d < D; d += 64) {
             const float2 f = Half16<T>::to_f32(__ldg(reinterpret_cast<const uint32_t*>(q_row(r) + d)));
             a = fmaxf(a, fmaxf(fabsf(f.x), fabsf(f.y)));
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
     for (int f = tid; f < RT * KT * 32; f += THREADS) {
       const int r = f / (32 * KT) * 8 + f % 32 / 4, t = f / 32 % KT;
       uint2 q = make_uint2(0u, 0u);  // the k index runs over D in the order the codes are read in
-      if (r < rows) q = __ldg(reinterpret_cast<const uint2*>(q_row(r) + (D / 4) * (f % 4) + 4 * t));
+      if (r < there) q = __ldg(reinterpret_cast<const uint2*>(q_row(r) + (D / 4) * (f % 4) + 4 * t));
       if constexpr (BRAIN) {
         const float2 lo = Half16<T>::to_f32(q.x), hi = Half16<T>::to_f32(q.y);
         const float inv = 1.f / s_rowscale[r];

@@ -1164,6 +1164,9 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS, kPieces<T>>::kThreads, 1)
       };
 
       const bool active = QUAD || quarter * 32 < rows;  // a warp without rows leaves its lanes as they are
+      // Rows that are no token's have no say in when references move: what their lanes hold is an earlier item's or call's, or
+      // padding, and must not reach another row, not even its rounding.
+      const bool votes = me < it.nq;
       // (never 0, not by underflow either, so that a masked score stays infinite; the sign is in the
       // staged queries)
       constexpr float kLeast = 1.4e-45f;
@@ -1251,7 +1254,7 @@ __global__ void __launch_bounds__(Shape<D, ROWS, BITS, kPieces<T>>::kThreads, 1)
           fence_after();
         }
         if (active) {
-          if (pair_any(pair, top - m > kSlack + kBelow<M>)) {  // (also where m is still -inf) the reference moves
+          if (pair_any(pair, votes && top - m > kSlack + kBelow<M>)) {  // (also where m is still -inf) the reference moves
             s_ml[(slot * 2 + half) * 128 + spot].x = top;
             asm volatile("bar.sync %0, 64;" ::"r"(pair) : "memory");
             top = fmaxf(m, fmaxf(top, s_ml[(slot * 2 + (half ^ 1)) * 128 + spot].x) - kBelow<M>);
