@@ -129,7 +129,7 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
         uint32_t boxes = 0;
 #pragma unroll
         for (int u = 0; u < SUB; ++u) boxes += static_cast<unsigned>(page[u]) < static_cast<unsigned>(pg.num_pages) ? 2 : 0;
-        fence_proxy_async_smem();  // (the warp's reads of the stage, which its vote ordered before this)
+        fence_proxy_async_smem();  // (the warp's reads of the stage, which its barrier ordered before this)
         mbar_expect_tx(full + stage, boxes * St::kBox);
 #pragma unroll
         for (int u = 0; u < SUB; ++u)
@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(32 * Stage8<D, RT>::WARPS, 1) attend8_kernel(c
         break;
       }
       ++taken;
-      // (every lane is done with the round before, whose stage is filled again)
+      __syncwarp();  // every lane has read the round before, whose stage is filled again (votes and shuffles order no memory)
       if (n + STAGES - 1 < rounds) issue(n + STAGES - 1, (n + STAGES - 1) / LOOK != n / LOOK);
       if (n % LOOK == LOOK / 2) next.find_scales(pg, h);
       char* const kb = stages + stage * St::kBytes;
