@@ -531,7 +531,8 @@ int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype,
  *   x  = logits[b, i, t];  if c > 0 or t is in the prompt:  x = x > 0 ? x / repetition[b] : x * repetition[b]
  *   x  = x - frequency[b] * c - (c > 0 ? presence[b] : 0) + the bias listed for t
  *   out[b, i, t] = x, or -inf where the row's mask has no bit for t.
- * Computed in fp32 and rounded once.  A masked token is -inf whatever its logit holds (NaN too); a row whose mask leaves nothing
+ * Computed in fp32, each step rounded to nearest: the quotient or product; the penalties (frequency * c + presence once); the bias
+ * less them; the sum.  A bf16 result is rounded once more.  A masked token is -inf whatever its logit holds (NaN too); a row whose mask leaves nothing
  * is all -inf, which the verification calls report (SPECDEC_STATUS_EMPTY_ROW).
  *
  * logits       [B, rows, V] of dtype (SPECDEC_F32 or SPECDEC_BF16); out the same, or logits itself: in place (one that overlaps

@@ -42,7 +42,11 @@ template <> struct Elem16<uint16_t> {  // bf16
 
 struct Penalties {
   float repetition, presence, frequency;
-  __device__ __forceinline__ float repeated(float x) const { return x > 0.f ? __fdiv_rn(x, repetition) : x * repetition; }
+  // a token's value: the quotient or product, then the sum, each rounded to nearest (not contracted into one rounding, so that every
+  // place where a value is computed gives the same bits)
+  __device__ __forceinline__ float value(float x, bool repeated, float add) const {
+    return __fadd_rn(!repeated ? x : x > 0.f ? __fdiv_rn(x, repetition) : __fmul_rn(x, repetition), add);
+  }
   // what is added for c occurrences
   __device__ __forceinline__ float added(int c, float bias) const { return c > 0 ? bias - fmaf(frequency, static_cast<float>(c), presence) : bias; }
 };
@@ -232,16 +236,12 @@ __global__ void __launch_bounds__(kThreads) process_kernel(const ProcessParams P
     if (w < tid / 32) at += s_sum[w];
     listed += s_sum[w];
   }
-  // A column's part that all rows share: y = x * (x > 0 ? 1 / r : r) + add for a token that was there before, else x + add.
-  // (The reciprocal's rounding is that of the quotient: x * RN(1 / r) is within 2^-24 of x / r, and the sum rounds once.)
-  // Its entry says whether x is scaled, and whether its value is computed for each row: a draft's token, or a repetition so large
-  // or small that the reciprocal may be subnormal or infinite.
+  // What is added to a column is the same in all rows, unless the token is some draft's.  An entry says whether the token was there
+  // before (kScaled: x is divided, or multiplied), and whether it is a draft's (kOwn: counted anew for each row).
   constexpr int kScaled = 0x8000, kOwn = 0x4000;
-  const bool usual = pen.repetition >= 0x1p-100f && pen.repetition <= 0x1p100f;
-  const float inverse = 1.f / pen.repetition;
   for (; some != 0; some &= some - 1, ++at) {
     const int t = tid * N + __ffs(some) - 1, c = counts ? __ldg(counts + t) : 0, k = s_value[t];
-    const bool own = (s_mark[t / 32] >> (t % 32) & 1u) != 0 || (c != 0 && !usual);
+    const bool own = (s_mark[t / 32] >> (t % 32) & 1u) != 0;
     if (!own) s_value[t] = __float_as_int(pen.added(c & 0x7fffffff, k ? __ldg(bias_values + k - 1) : 0.f));
     s_list[at] = static_cast<uint16_t>(t | (c != 0 ? kScaled : 0) | (own ? kOwn : 0));
   }
@@ -251,26 +251,19 @@ __global__ void __launch_bounds__(kThreads) process_kernel(const ProcessParams P
     if (entry & kOwn) {
       const int c = counts ? __ldg(counts + t) : 0, k = s_value[t];
       const float bias = k ? __ldg(bias_values + k - 1) : 0.f;
-      const bool drafted = (s_mark[t / 32] >> (t % 32) & 1u) != 0;
       for (int i = 0; i < rows; ++i) {
-        int n = 0;
-        if (drafted)  // (ends, whatever the parents)
-          for (int d = r + i - 1; d >= 0; d = P.parents ? min(s_parent[d], d - 1) : d - 1) n += s_draft[d] == lo + t;
+        int n = 0;  // (ends, whatever the parents)
+        for (int d = r + i - 1; d >= 0; d = P.parents ? min(s_parent[d], d - 1) : d - 1) n += s_draft[d] == lo + t;
         T* const e = x(i) + t;
-        const float v = E::get(*e), add = pen.added((c & 0x7fffffff) + n, bias);
-        const bool repeated = c != 0 || n > 0;
-        // (as a token that is counted is computed, bit for bit: a history's result does not depend on where its tokens stand)
-        *e = E::put(usual || !repeated ? fmaf(v, !repeated ? 1.f : v > 0.f ? inverse : pen.repetition, add) : pen.repeated(v) + add);
+        *e = E::put(pen.value(E::get(*e), c != 0 || n > 0, pen.added((c & 0x7fffffff) + n, bias)));
       }
     } else {
       const float add = __int_as_float(s_value[t]);
-      const float up = entry & kScaled ? inverse : 1.f, down = entry & kScaled ? pen.repetition : 1.f;
 #pragma unroll
       for (int i = 0; i < kBatch; ++i)
         if (i < rows) {
           T* const e = x(i) + t;
-          const float v = E::get(*e);
-          *e = E::put(fmaf(v, v > 0.f ? up : down, add));
+          *e = E::put(pen.value(E::get(*e), (entry & kScaled) != 0, add));
         }
     }
   };
