@@ -505,8 +505,9 @@ int specdec_read_kv8(const int32_t* context_len, const int32_t* query_len, int B
  * that no query sees (behind a window) are not read, and their entries are not looked at.
  * Scores, statistics and sums are fp32; the weights p are rounded to 16 bits (dtype, or fp16 for
  * 4-bit and 8-bit pages; in fp16 to 2^-32 of the row's largest where that is more) for the matrix products,
- * the output once at the end.  Over 8-bit pages with 17 to 32 query rows to a key head the queries are held to 2^-17 of a
- * row's largest value (values above 2^-10 of it in bf16, and above 2^-7 in fp16, are exact).
+ * the output once at the end.  Over 8-bit and 4-bit pages bf16 queries are held in fp16, to 2^-25 of a row's largest value;
+ * over 8-bit pages with 17 to 32 query rows to a key head queries of either type are held to 2^-17 of a
+ * row's largest value (values from 2^-9 of it up in bf16, and from 2^-6 up in fp16, are exact).
  * Every wait inside the kernels is bounded (one second); a call in which one runs out reports
  * SPECDEC_STATUS_TIMEOUT for every sequence, and its outputs do not count.
  * The workspace (specdec_attend_workspace_bytes) follows the rules at the top.  The split of the
