@@ -7,7 +7,7 @@ keys are normed, rotated to the nodes' positions and written to the cache pages
 ancestors (`attend` with `build_tree_mask`), the logits of the last layer are penalised for what each node's path
 repeats (`process_logits`, where asked for) and verified (`verify_tree`), the emitted tokens are counted
 (`count_tokens`), and the accepted branch's entries are gathered (`compact_kv`; in 8 bits, whose blocks share
-scales, they are appended again).
+scales, they are appended again, to the block as it was before the nodes: a rejected node leaves no mark).
 
     python examples/verify_round.py [--four-bit | --eight-bit] [--window 256 --sinks 4] [--repetition 1.3]
 """
@@ -63,6 +63,7 @@ class ToyTarget:
         depth = tree["depth"] if tree else None
         x = self.embed[tokens.long()]
         self.new = []  # the new tokens' keys and values of every layer
+        self.open = []  # 8-bit pages, a tree's step: the block (here a page) that its first node falls into, as it was before
         for qkv, out, cache in zip(self.qkv, self.out, self.cache):
             y = (x @ qkv).view(B, n, self.heads + 2 * self.kv_heads, self.D)
             q, k, v = y.split([self.heads, self.kv_heads, self.kv_heads], 2)
@@ -71,6 +72,10 @@ class ToyTarget:
                 r = sd.rotate_qk(q, k, self.turns, context_len, **norms)
                 append = sd.append_kv4 if self.four else sd.append_kv8
                 self.new.append((r["k"], v))
+                if self.eight and tree:
+                    page = ((context_len - n) // cache["k_pages"].shape[1]).clamp(max=self.table.shape[1] - 1).long()
+                    page = self.table.gather(1, page[:, None])[:, 0].long()
+                    self.open.append((page, {name: t.view(torch.uint8)[page] for name, t in cache.items()}))
                 append(r["k"], v, cache["k_pages"], cache["v_pages"], self.table, context_len,
                        k_scales=cache["k_scales"], v_scales=cache["v_scales"], **self.scales)
             else:
@@ -85,7 +90,9 @@ class ToyTarget:
         if self.eight:
             count = num_accepted.clamp(min=0)
             at = path.clamp(min=0).long()[:, :, None, None]
-            for (k, v), cache in zip(self.new, self.cache):
+            for (k, v), (page, before), cache in zip(self.new, self.open, self.cache):
+                for name, t in before.items():
+                    cache[name].view(torch.uint8)[page] = t
                 k, v = (t.gather(1, at.expand(-1, -1, *t.shape[2:])) for t in (k, v))
                 sd.append_kv8(k, v, cache["k_pages"], cache["v_pages"], self.table, prefix_len + count, query_len=count,
                               k_scales=cache["k_scales"], v_scales=cache["v_scales"], **self.scales)

@@ -467,7 +467,11 @@ int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B
  * saturated at 448).  Where a block's scale grows, the codes of its earlier tokens are rounded to the new scale: exact but
  * for codes that become subnormal.  A value that is not finite is stored as NaN and does not count for the scale.
  * Slots from a block's new tokens on are not looked at: rejected drafts are overwritten by appending again with the
- * shorter context_len (a block keeps its scale then).  A sequence in error is left alone.  Two sequences must not write the
+ * shorter context_len (a block keeps its scale then).  So a rejected draft leaves a mark: the scale s that it raised stays until
+ * the block is begun again, and accepted tokens of the block, those before it and those after, are off by up to 2^-9 s (times k_scale)
+ * from what they would be without it, where they are below 2^-6 s.  A caller whose accepted tokens must not depend on rejected ones
+ * keeps the codes and scale bytes of the block of slot context_len[b] - query_len[b] before drafts are appended, puts them back once the drafts
+ * are verified, and appends the accepted ones again at their slots.  A sequence in error is left alone.  Two sequences must not write the
  * same block.  B <= 65535. */
 int specdec_append_kv8(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
                        specdec_dtype dtype, const int32_t* context_len, const int32_t* query_len, int B, int n,

@@ -130,7 +130,8 @@ def append_kv8(k, v, k_pages, v_pages, block_table, context_len, *, k_scales, v_
                v_scale: float = 1.0, query_len=None, stream=None) -> dict:
     """Keys and values [B, n, kv_heads, D] of the new tokens written to 8-bit pages, with a scale for each block of
     slots and head (specdec_append_kv8).  A block's scale grows with the tokens appended to it, and its earlier codes
-    follow.  Returns status [B]."""
+    follow; it stays when a draft that raised it is rejected, unless the caller puts the block back as it was (its codes
+    and scales) before the accepted tokens are appended again.  Returns status [B]."""
     call = (_calls or _module()).append_kv8
     if stream is None:
         return call(k, v, k_pages, v_pages, block_table, context_len, query_len, k_scales, v_scales, k_scale, v_scale)
