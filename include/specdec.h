@@ -362,6 +362,8 @@ int specdec_gumbel_noise(uint64_t seed, int B, int rows, int V, float* out_noise
  * that sequence is left alone.  Freeing emptied pages is the allocator's business.
  * 16-byte aligned layouts move 16-byte words, others bytes.  All pointers are device
  * pointers; strides and sizes in bytes.
+ * Slots move as the bytes they are and hold their values whole.  SPECDEC_KV8 pages are not such a cache: a code's scale is
+ * its block's and stays where it is (specdec_append_kv8 appends their accepted tokens again).
  */
 int specdec_compact_kv(void* cache, int64_t row_bytes, int64_t slot_stride, int64_t seq_stride,
                        int64_t num_slots, const int32_t* block_table, int block_size, int max_blocks,

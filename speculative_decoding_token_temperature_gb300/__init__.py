@@ -531,7 +531,12 @@ def compact_kv(cache, prefix_len, path, num_accepted, *, block_table=None, strea
     cache: a device tensor [B, S, ...] (contiguous per sequence) or, with block_table
     [B, max_blocks] int32, a page pool [num_blocks, block_size, ...]; the trailing
     dimensions are one slot.  prefix_len [B], path [B, D], num_accepted [B] int32 (the tree
-    verifier's outputs).  Returns new_len [B] and status [B]."""
+    verifier's outputs).  Returns new_len [B] and status [B].
+
+    Slots move as the bytes they are, so a slot has to hold its value whole: 16-bit pages, 4-bit pages (codes
+    and scales, a call each), E4M3 codes under one scale for the tensor.  The pages of ``append_kv8`` are not moved by this call: a
+    code's scale is its block's, which stays where it is, and a branch that crosses blocks would be read under
+    another scale.  Their accepted tokens are appended again (``examples/verify_round.py``)."""
     lib = load_library()
     if not cache.is_contiguous():
         raise ValueError("cache must be contiguous")

@@ -106,3 +106,31 @@ def test_tree_rounds_do_not_depend_on_rejected_nodes(example):
             for (x, s), (y, t) in zip(codes[b], left[0][1][b]):
                 assert torch.equal(x, y) and torch.equal(s, t)
     assert same >= B
+
+
+def test_compaction_moves_codes_and_appending_again_moves_values(sd):
+    """compact_kv moves slots as bytes, as its documentation says: right for codes under one scale, not for blocks with scales of
+    their own, whose accepted branch is appended again."""
+    B, hkv, D, block, first, n = 1, 1, 64, 16, 16, 20
+    c = kv8.Cache(B, 64, 32, block, hkv, D, seed=2)
+    prefix = kv8._new(B, first, hkv, D, torch.float16, seed=3)
+    _append(sd, c, prefix, prefix, [first], [first])
+    nodes = kv8._new(B, n, hkv, D, torch.float16, seed=4)
+    nodes[:, 16:] *= 64  # the nodes of the second block: another scale
+    _append(sd, c, nodes, nodes, [first + n], [n])
+    path = torch.tensor([[2, 7, 18]], dtype=torch.int32, device="cuda")
+    before, start = c.codes("k", 0, first + n), _state(c)
+    r = sd.compact_kv(c.k, base._i32([first]), path, base._i32([3]), block_table=c.table)
+    torch.cuda.synchronize()
+    assert r["new_len"].tolist() == [first + 3] and not r["status"].any()
+    assert np.array_equal(c.codes("k", 0, first + 3), before[[*range(first), first + 2, first + 7, first + 18]])
+    want = base._np(nodes[0, [2, 7, 18]])
+    moved = c.rows(0, first + 3)[0][first:]
+    assert np.abs(moved - want)[2].max() > 16 * np.abs(want[:2]).max()  # the large node's codes under a small node's scale
+    for w in NAMES:
+        getattr(c, w).view(torch.uint8).copy_(start[w])
+    kept = nodes[:, [2, 7, 18]].contiguous()
+    _append(sd, c, kept, kept, [first + 3], [3])
+    for x in c.rows(0, first + 3):
+        again = x[first:]
+        assert (np.abs(again - want) <= 2.0 ** -4 * np.abs(want) + 2.0 ** -9 * np.abs(want).max()).all()
