@@ -8,9 +8,11 @@
 // again only where they become subnormal).  The range of e is what fp16 holds exactly: 448 * 2^7 is below 65504, and
 // the smallest code, 2^-9, times 2^-15 is 2^-24.
 //
-// 64 x 8 new tokens of 8 key heads of 128 are written in 6.2 us and 64 x 71 read back in 9.7 us; 4 x 2045 are written in 16.3 us
-// (50 MB, 3.1 TB/s) and 4 x 2060 read back in 13.9 us (50 MB, 3.6 TB/s): bound by the ramp of so short a kernel, a chain of
-// dependent loads (lengths, pages, scales), rather than by bytes.
+// Calls one after another, 8 key heads of 128: 64 x 8 new tokens are written in 6.2 us (3.5 on the device, the rest is the host's)
+// and 64 x 71 read back in 9.5 us: launches and a chain of dependent loads (lengths, pages, scales, codes).  4 x 2045 are written in 16.6 us
+// (15.2 on the device; 50 MB, 3.3 TB/s) and 4 x 2060 read back in 13.8 us (50 MB, 3.7 TB/s), about twice what the copy rate would
+// allow.  What holds these up is not measured; the write's CTAs go through that chain once each for four units of
+// a few KB, and each of a read's store instructions fills half of the sectors that it touches.
 
 #include "cache_device.cuh"
 #include "specdec_device.cuh"
@@ -238,11 +240,13 @@ cudaError_t append_shape(const KvParams& P, cudaStream_t stream) {
     const int64_t per = kThreads / unit;
     return launch_kernel(kernel, dim3(static_cast<unsigned>((units + per - 1) / per), static_cast<unsigned>(P.B)), dim3(kThreads), 0, stream, 0, P);
   };
-  // A unit's pieces, and its threads: up to four pieces a thread, for a CTA's way to its first byte (lengths, pages, scales) costs more
-  // than its bytes.  4 x 2045 tokens of 8 heads of 128, a scale for 16 tokens (256 pieces): 16.3 us with 64 threads, 17.4 with 32, 24.3
-  // with 128, 36.8 with 256; 64 x 8 tokens (128 pieces): 6.2 us with 64, 5.8 with 32, 8.0 with 128.
+  // A unit's pieces, and its threads: about four pieces a thread, for a CTA's way to its first byte (lengths, pages, scales) costs more
+  // than its bytes.  Device time of 32, 64 and 256 threads, us (8 key heads; graphs of calls): 64 x 8 tokens, heads of 128 (128 pieces) 3.5,
+  // 4.3, 8.9; 4 x 2045 tokens, heads of 64, a scale for 16 tokens (128) 7.8, 11.9, 33.6; the same with heads of 128 (256) 16.8, 15.2, 35.2;
+  // 64 x 16 tokens (256) 5.4, 5.0, 9.5; a scale for 32 tokens (512) 17.9, 17.3, 20.6, of one request of 300 tokens 6.7, 4.4, 3.1; a scale
+  // for 64 (1024) 27.2, 18.5, 13.6, for 256 (4096) 90.9, 48.9, 18.4.  (Between 256 and 1024 pieces long batches would like 64, short ones 256.)
   const int threads = rows * (D / 8);
-  if (threads <= 64) return launch(append_kv8_kernel<T, D, 32>, 32);
+  if (threads <= 128) return launch(append_kv8_kernel<T, D, 32>, 32);
   if (threads <= 256) return launch(append_kv8_kernel<T, D, 64>, 64);
   return launch(append_kv8_kernel<T, D, 256>, 256);
 }
