@@ -474,7 +474,7 @@ int specdec_read_kv4(const int32_t* context_len, const int32_t* query_len, int B
  * from what they would be without it, where they are below 2^-6 s.  A caller whose accepted tokens must not depend on rejected ones
  * keeps the codes and scale bytes of the block of slot context_len[b] - query_len[b] before drafts are appended, puts them back once the drafts
  * are verified, and appends the accepted ones again at their slots.  A sequence in error is left alone.  Two sequences must not write the
- * same block.  B <= 65535. */
+ * same block; strides of zero (of more than one page, block or head) are refused here.  B <= 65535. */
 int specdec_append_kv8(const void* k, const int64_t* k_strides, const void* v, const int64_t* v_strides,
                        specdec_dtype dtype, const int32_t* context_len, const int32_t* query_len, int B, int n,
                        const specdec_kv_pages* pages, int32_t* out_status, void* stream);

@@ -774,6 +774,12 @@ int append_few_bits(specdec_dtype format, const void* k, const int64_t* k_stride
   if (int rc = check_view(k, k_strides, "k is null"); rc != SPECDEC_OK) return rc;
   if (int rc = check_view(v, v_strides, "v is null"); rc != SPECDEC_OK) return rc;
   if (int rc = check_pages(pages, format, &P.pages); rc != SPECDEC_OK) return rc;
+  if (format == SPECDEC_KV8) {  // (pages that are only read may have strides of zero; two heads' scales written to one byte would race)
+    const bool one_head = pages->kv_heads == 1, one_page = pages->num_pages == 1, one_block = pages->page_size == pages->scale_block;
+    if ((!one_page && (pages->page_stride == 0 || pages->scale_page_stride == 0)) || (!one_block && pages->scale_slot_stride == 0) ||
+        (!one_head && (pages->head_stride == 0 || pages->scale_head_stride == 0)))
+      return fail(SPECDEC_ERR_INVALID_ARG, "pages that are written need a place of their own for each page, block and head (a stride is 0)");
+  }
   if (B > 65535 || static_cast<int64_t>(n) * pages->kv_heads >= (1 << 26)) return fail(SPECDEC_ERR_UNSUPPORTED, "B above 65535, or n * kv_heads above 2^26");
   P.k = k;
   P.v = v;
