@@ -557,7 +557,9 @@ int specdec_attend(const void* q, const int64_t* q_strides, specdec_dtype dtype,
  * out_status   [B] int32, optional: SPECDEC_STATUS_BAD_TOKEN (a token outside [0, V) that a row counts, a bias token
  *              of V or more, gammas[b] out of range), SPECDEC_STATUS_BAD_TREE (a parent out of range), SPECDEC_STATUS_BAD_PENALTY (a repetition that is not
  *              positive and finite, a presence or frequency that is not finite), else 0.  The rows of a sequence in error are NaN.
- * rows <= 8192, B <= 65535, num_bias < 2^24, V < 2^31 - 65536. */
+ * rows <= 8192, B <= 65535, num_bias < 2^24, V < 2^31 - 65536.  Meant for a round's tens of rows: a draft's token is counted
+ * along the path of each row, so that thousands of different drafts take tens of milliseconds; every few thousand tokens
+ * of the vocabulary the list of biases is read once. */
 int specdec_process_logits(const void* logits, specdec_dtype dtype, const int32_t* tokens, const int32_t* parents,
                            const int32_t* gammas, const int32_t* counts, const float* repetition,
                            const float* presence, const float* frequency, const int32_t* bias_tokens,

@@ -31,20 +31,20 @@
 //
 // Measured (32 query and 8 key heads of 128, key bytes against the copy rate, products against the
 // matrix rate):
-//  - 64 requests, 8 tokens, up to 8190 slots in 16 bits (32 rows to a key head): 219 us, 6.2 TB/s, 0.91 of
+//  - 64 requests, 8 tokens, up to 8190 slots in 16 bits (32 rows to a key head): 222 us, 6.1 TB/s, 0.90 of
 //    the measured copy rate; HBM bounds it.
-//  - 24 trees of 64 nodes, up to 12000 slots (256 rows): 204 us, 3.7 TB/s and 0.92 PFLOP/s, 0.55 of the
-//    measured copy and 0.48 of the matrix rate.  A pair of 128-by-128 tiles takes about 4200 clocks against 2050 of products: the chain scores,
+//  - 24 trees of 64 nodes, up to 12000 slots (256 rows): 207 us, 3.7 TB/s and 0.91 PFLOP/s, 0.54 of the
+//    measured copy and 0.47 of the matrix rate.  A pair of 128-by-128 tiles takes about 4200 clocks against 2050 of products: the chain scores,
 //    weights, products of one slot is longer than the other slot's products, for the exponentials
 //    (128 x 128 at 32 a clock and SM are 512 clocks) come with two reads of the scores and one store
 //    of the weights through tensor memory.
-//  - 16 requests, 8 tokens, up to 32003 slots in 4 bits: 164 us, 2.3 TB/s, DRAM traffic equal to the
+//  - 16 requests, 8 tokens, up to 32003 slots in 4 bits: 163 us, 2.3 TB/s, DRAM traffic equal to the
 //    cache's bytes.  A tile takes about 2400 clocks: its codes' conversion 790 at 64 lanes a clock, but
 //    with the copies in and the stores of the values (shared memory is busy for about 1500) the converting
 //    warps need 2000.
 //  - 64 requests, 8 tokens, up to 8190 slots in 8 bits (32 rows): 176 us, 3.9 TB/s, 0.57 of the measured copy rate.  The trees of 64
-//    nodes in 8 bits: 244 us (219 with queries in fp16, which are not scaled; 201 in 16 bits).  In neither are the matrix
-//    pipe, the issue slots or shared memory full.
+//    nodes in 8 bits: 242 us (218 with queries in fp16, which are not scaled; 207 in 16 bits).  In neither are the matrix
+//    pipe, the issue slots or shared memory full.  64 requests of 16 tokens (64 rows) 277 us, of 32 (128 rows) 302, of 64 (256) 414.
 //  - 35 rows, a window of 1024 slots, 96 requests: 60 us, 3.5 TB/s: an item is 9 tiles, and its first,
 //    partial tile, the way out of its rows and the next one's queries cost about 4 more.
 #pragma once
@@ -82,8 +82,8 @@ struct Shape {
   static constexpr bool TWO = ROWS == kTwo, QUAD = ROWS == kQuad && !EIGHT;
   // 8-bit pages with at most 32 rows: one quarter of the lanes has them, and the warps of the others convert too.  Keys are not
   // converted: the scores are products of codes, the queries' in pieces.  (64 requests of 8 tokens: 175 us, 199 with the keys
-  // converted.  With more rows the pieces' products cost more than that saves: 202 against 183 us for 128 rows, 279 against 271
-  // for 256, in fp16, whose pieces are three, 352 against 217.)
+  // converted.  With more rows the pieces' products cost more than that saves, when both were built: 24 x 64 tokens over up to 12000
+  // slots, 128 rows 202 against 183 us (174 now), 256 rows 279 against 271 (242 now), in fp16, whose pieces are three, 352 against 217.)
   static constexpr bool FEW = ROWS == kQuad && EIGHT;
   static constexpr int MR = ROWS == kQuad ? 32 : TWO ? 256 : 128;
   static constexpr int kRowWarps = FEW ? 4 : 16;

@@ -9,6 +9,11 @@
 // under their masks, bound by HBM, in which a few elements are changed on the way.  A CTA takes a chunk of the vocabulary and some
 // rows of a sequence.  The rows come to shared memory by 16-byte asynchronous copies, kBatch at a time and two batches ahead, while
 // the CTA lists its chunk's tokens that change; those are changed in shared memory, and the words go out.
+//
+// 256 x 8 rows of 128256 in bf16: 203 us, 0.86 of the measured copy rate; in place, where listed tokens alone are read and written, by single
+// elements, 247 us against a floor of 69.  32 x 65 rows of 32001 under masks 107 us (floor 41), of 32000 83.  A draft's token is
+// counted anew for each row, along the row's whole path: nothing at a round's tens of rows, but 1 x 1024 rows of different drafts take 0.2 ms (a
+// chain) to 0.6 ms (a path of a tree), 8192 58 to 187 ms.
 
 #include <algorithm>
 
@@ -53,7 +58,7 @@ struct Penalties {
 
 // Rows of a batch, and batches in flight.  256 x 8 rows of 128256 logits in bf16, 32 x 65 rows of 32001 under masks (us): 2, 2: 196,
 // 110; 4, 2: 215, 117; 4, 1: 211, 107; 2, 3: 195, 112; 2, 4: 229, 125.  (Rows held in registers, and the tokens changed in them
-// or in a pass of their own behind the copy: 217 to 275, 156 to 194.)
+// or in a pass of their own behind the copy: 217 to 275, 156 to 194.  All of these with products by a reciprocal; with quotients 2, 2: 203, 107.)
 constexpr int kBatch = 2, kStages = 2;
 
 __device__ __forceinline__ void copy_async16(void* dst, const void* src) {
@@ -414,8 +419,9 @@ cudaError_t process_shape(ProcessParams P, cudaStream_t stream) {
   constexpr int CHUNK = kChunk<T, ALIGNED>;
   const int64_t chunks = (static_cast<int64_t>(P.V) + CHUNK - 1) / CHUNK;
   // Rows are split over CTAs until there are eight for an SM, four rows at least for each, as a chunk's list is made by every one.  (CTAs for an
-  // SM, us: 32 x 65 rows of 32001 under masks 4: 118, 8: 106, 12: 103, 30: 106; 16 x 8 rows of 128256 4: 21.5, 8: 23.1, 16:
-  // 26.6; 2 x 8 rows in fp32 4: 8.8, 8: 10.5, 12: 14.6.)
+  // SM, us: 32 x 65 rows of 32001 under masks 2: 146, 4: 121, 8: 107, 12: 104, 30: 107; 4 x 65 such rows 28.3, 21.4, 23.4, 23.5, 23.4; 256 x 8
+  // and 16 x 8 rows of 128256 203 and 21.5 with any.  Rows at least: 2 x 8 rows of 128256 in fp32 2: 10.4, 4: 8.5, 8: 10.5; 1 x 8 in bf16 8.4,
+  // 9.4, 12.5; 32 x 65 under masks 107 with any.)
   const int64_t want = 8 * device_sm_count(), have = chunks * P.B;
   const int groups = static_cast<int>(std::min<int64_t>(std::max(1, P.rows / 4), (want + have - 1) / have));
   P.group = (P.rows + groups - 1) / groups;
