@@ -63,7 +63,7 @@ class ToyTarget:
         depth = tree["depth"] if tree else None
         x = self.embed[tokens.long()]
         self.new = []  # the new tokens' keys and values of every layer
-        self.open = []  # 8-bit pages, a tree's step: the block (here a page) that its first node falls into, as it was before
+        self.open = []  # 8-bit pages: the block (here a page) that the first new token falls into, as it was before
         for qkv, out, cache in zip(self.qkv, self.out, self.cache):
             y = (x @ qkv).view(B, n, self.heads + 2 * self.kv_heads, self.D)
             q, k, v = y.split([self.heads, self.kv_heads, self.kv_heads], 2)
@@ -72,7 +72,7 @@ class ToyTarget:
                 r = sd.rotate_qk(q, k, self.turns, context_len, **norms)
                 append = sd.append_kv4 if self.four else sd.append_kv8
                 self.new.append((r["k"], v))
-                if self.eight and tree:
+                if self.eight:
                     page = ((context_len - n) // cache["k_pages"].shape[1]).clamp(max=self.table.shape[1] - 1).long()
                     page = self.table.gather(1, page[:, None])[:, 0].long()
                     self.open.append((page, {name: t.view(torch.uint8)[page] for name, t in cache.items()}))
